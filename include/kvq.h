@@ -1,5 +1,6 @@
 /*
- * kvq.h -- C ABI of the GB300 (sm_103a) attention-prologue kernels.
+ * kvq.h -- C ABI of the GB300 (sm_103a) attention-prologue kernels, and of the
+ * paged grouped-query cache and attention that follow them (further below).
  *
  * Two operators of the memory-bound per-token prologue that runs between the
  * QKV projection and attention in LLM serving:
@@ -88,7 +89,8 @@ typedef enum kvq_status {
   KVQ_ERR_UNSUPPORTED = 3, /* head_dim / rotary_dim / is_neox outside the set above */
   KVQ_ERR_ALIGN = 4,       /* a pointer is not aligned as required below */
   KVQ_ERR_CUDA = 5,        /* the kernel launch itself failed */
-  KVQ_ERR_VALUE = 6        /* eps negative or not finite; q_out partly overlaps q */
+  KVQ_ERR_VALUE = 6        /* eps negative or not finite; scale not finite; an
+                              output overlaps an input */
 } kvq_status;
 
 /*
@@ -263,6 +265,177 @@ kvq_status dsv4_qnorm_rope_kv_rope_quant_insert_checked(
 kvq_status dsv4_kv_cache_gather_checked(const uint8_t* kv_cache, int64_t num_blocks,
                                         int block_size, const int64_t* slots, int64_t num_rows,
                                         void* out, int32_t* error_count, kvq_stream_t stream);
+
+/*
+ * Paged grouped-query operators: what a decode step or a prompt chunk of a
+ * model with grouped-query heads runs after its QKV projection (or after
+ * fused_qk_norm_rope above, then with rotary_dim 0).
+ *
+ *   kv_cache     bf16 [num_pages, 2, num_heads_kv, page_size, head_dim],
+ *                contiguous, 16-byte aligned: of each page the keys of every
+ *                kv head, then the values.  Slot s is offset s % page_size of
+ *                page s / page_size.
+ *   head_dim     64, 128 or 256; page_size 1 .. 65536; num_pages below 2^31.
+ *   num_heads_q  a multiple of num_heads_kv; query head h reads kv head
+ *                h / (num_heads_q / num_heads_kv).
+ *   page_table   int32 [num_requests, table_width]: the pages of each request
+ *                in order; entries past a request's length are not read.
+ *                table_width at most 2^24.
+ *   requests     int32 [num_tokens]: the request of each token; NULL: token t
+ *                is request t (num_requests >= num_tokens).
+ *   lens         int32 [num_tokens]: how many keys of its request each token
+ *                sees (several tokens of one request, each seeing one more
+ *                key, are a causal chunk).  0 is allowed.
+ *   q            bf16, rows of num_heads_q * head_dim contiguous values,
+ *                q_stride elements apart (a multiple of 8; q may be a view
+ *                into packed QKV); 16-byte aligned.
+ *   error_count  int32 device counter or NULL.  All indices are checked
+ *                against the sizes given, and what lies outside is rejected,
+ *                never followed: a position or slot as documented with each
+ *                operator; a page id outside the cache (its keys are not
+ *                there); a request outside the table or a negative length
+ *                (the token has no keys of its own); a length past
+ *                table_width * page_size (cut to it).  Then something is
+ *                added to *error_count: one per rejected token or entry in
+ *                the append and the bounds, an unspecified positive number
+ *                in the others.
+ * Everything in the general contract above holds: no allocation, no
+ * synchronisation, host-side validation, programmatic dependent launch.  The
+ * two attentions take a workspace of at least the bytes their _workspace
+ * function returns (16-byte aligned; nothing in it has to be kept or set
+ * between calls; two calls that may run at the same time, or two graphs that
+ * may be replayed at the same time, need one each).
+ * No counterpart in the source pages, which end at the attention prologue:
+ * the operators continue it for the packed-QKV layout.
+ */
+
+/*
+ * paged_kv_rope_append -- rotary embedding of the Q and K heads of packed QKV,
+ * and the K and V heads written into the paged cache, in one pass.
+ *
+ *   qkv           bf16 [num_tokens, (Hq + 2 Hkv) * head_dim], contiguous,
+ *                 16-byte aligned (layout as in fused_qk_norm_rope).  K and V
+ *                 rows are read only.
+ *   q_out         bf16 [num_tokens, Hq, head_dim], 16-byte aligned: the
+ *                 rotated query rows; NULL: in place in qkv.  A q_out that
+ *                 overlaps qkv is KVQ_ERR_VALUE.
+ *   cos_sin_cache, max_pos, rotary_dim, is_neox, positions  as in
+ *                 fused_qk_norm_rope_ex (max_pos: rows of the table).
+ *                 rotary_dim 0: no rotation; cos_sin_cache and positions are
+ *                 not read and may be NULL.
+ *   slot_mapping  int64 [num_tokens]; -1 = no cache write.
+ * A token with a position outside the table is left out entirely (q row and
+ * cache unchanged) and counted; one with a slot outside the cache (and not
+ * -1) gets its q row but no cache write, and is counted.  No two tokens may
+ * have the same slot (the entry would be a mixture).
+ * fp32 arithmetic, one rounding: out_a = a cos - b sin, out_b = b cos + a sin.
+ */
+kvq_status paged_kv_rope_append(void* qkv, void* q_out, int64_t num_tokens, int num_heads_q,
+                                int num_heads_kv, int head_dim, const float* cos_sin_cache,
+                                int64_t max_pos, int rotary_dim, int is_neox,
+                                const int64_t* positions, const int64_t* slot_mapping,
+                                void* kv_cache, int64_t num_pages, int page_size,
+                                int32_t* error_count, kvq_stream_t stream);
+
+/*
+ * paged_kv_page_bounds -- per listed page, kv head and dim, the smallest and
+ * the largest key of the page's first lens[i] tokens (for
+ * paged_kv_block_select).
+ *
+ *   pages   int64 [num_listed]; -1 = nothing (a fixed-size list in a graph).
+ *   lens    int32 [num_listed], 0 .. page_size; 0 = nothing.
+ *   bounds  bf16 [num_pages, num_heads_kv, 2, head_dim], 16-byte aligned: the
+ *           minima, then the maxima.  Entries of pages not listed are left
+ *           as they are.  Exact (no rounding); a NaN key gives NaN.
+ * A page or length outside its range is skipped and counted.  A page may be
+ * listed twice with the same length; with two lengths either may win.
+ */
+kvq_status paged_kv_page_bounds(const void* kv_cache, int64_t num_pages, int num_heads_kv,
+                                int page_size, int head_dim, const int64_t* pages,
+                                const int32_t* lens, int64_t num_listed, void* bounds,
+                                int32_t* error_count, kvq_stream_t stream);
+
+/*
+ * paged_kv_block_select -- for each token and kv head the topk cache blocks
+ * with the highest score; a block is a page of the token's request, and
+ * n = ceil(lens / page_size) of them compete.
+ *
+ *   score of block j = sum over the group's query heads h and the dims d of
+ *     max(q_hd lo_jd, q_hd hi_jd),  lo/hi the block's bounds: an upper bound
+ *     of the group's summed logits on any key of the block.
+ *   keep_first, keep_last  blocks at the start and at the end of the range
+ *                that are selected ahead of every score.
+ *   blocks       int32 [num_tokens, num_heads_kv, topk], written: the
+ *                selected block indices in ascending order, then -1.
+ * The selection is that of exact arithmetic: fp32 scores too close to call
+ * are computed again in fp64, and of equal scores the lower index wins.  A
+ * NaN score, and a block whose page lies outside the cache, rank with -inf.
+ * n <= topk selects all n without reading bounds.  table_width at most 16384
+ * (else KVQ_ERR_UNSUPPORTED).
+ */
+kvq_status paged_kv_block_select(const void* q, int64_t q_stride, int64_t num_tokens,
+                                 int num_heads_q, int num_heads_kv, int head_dim,
+                                 const void* bounds, int64_t num_pages, int page_size,
+                                 const int32_t* page_table, int64_t num_requests,
+                                 int64_t table_width, const int32_t* requests,
+                                 const int32_t* lens, int topk, int keep_first, int keep_last,
+                                 int32_t* blocks, int32_t* error_count, kvq_stream_t stream);
+
+/*
+ * paged_block_sparse_attention -- attention of each token over the keys of
+ * the blocks listed for it and its kv head (as paged_kv_block_select writes
+ * them).
+ *
+ *   blocks   int32 [num_tokens, num_heads_kv, topk]: block indices into the
+ *            request's pages, -1 = none (anywhere in the list).  A block
+ *            listed twice is attended to twice.  Keys at or past lens[t] are
+ *            not there; an index that is negative (but for -1) or starts at
+ *            or past lens[t] is rejected.
+ *   scale    factor of the logits (finite), e.g. 1 / sqrt(head_dim).
+ *   out      bf16 [num_tokens, num_heads_q, head_dim], 16-byte aligned, not
+ *            overlapping q.  A token without any key gets zeros.
+ * out = softmax(scale q K^T) V per query head.  Scores, softmax statistics
+ * and sums in fp32; the softmax numerators are rounded to bf16 for the
+ * product with V, the output once at the end.
+ */
+int64_t paged_block_sparse_attention_workspace(int64_t num_tokens, int num_heads_q,
+                                               int num_heads_kv, int head_dim, int page_size,
+                                               int topk);
+kvq_status paged_block_sparse_attention(const void* q, int64_t q_stride, int64_t num_tokens,
+                                        int num_heads_q, int num_heads_kv, int head_dim,
+                                        const void* kv_cache, int64_t num_pages, int page_size,
+                                        const int32_t* page_table, int64_t num_requests,
+                                        int64_t table_width, const int32_t* requests,
+                                        const int32_t* lens, const int32_t* blocks, int topk,
+                                        float scale, void* out, void* workspace,
+                                        int64_t workspace_bytes, int32_t* error_count,
+                                        kvq_stream_t stream);
+
+/*
+ * paged_shared_prefix_attention -- attention of a batch whose requests all
+ * begin with the same prefix: every token sees the prefix_len keys of
+ * prefix_pages and then the first lens[t] keys of its own request's pages.
+ * The prefix is read once for the whole batch, its product taken over all of
+ * the batch's query rows together.
+ *
+ *   prefix_pages  int32 [ceil(prefix_len / page_size)]; the last one may be
+ *                 partly filled.  prefix_len 0 .. 2^31 - 1 (a host value), at
+ *                 most 2^24 pages.
+ *   scale, out, arithmetic  as paged_block_sparse_attention.  table_width 0
+ *                 (no keys but the prefix's) is allowed.
+ */
+int64_t paged_shared_prefix_attention_workspace(int64_t num_tokens, int num_heads_q,
+                                                int num_heads_kv, int head_dim, int page_size,
+                                                int64_t prefix_len, int64_t table_width);
+kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_t num_tokens,
+                                         int num_heads_q, int num_heads_kv, int head_dim,
+                                         const void* kv_cache, int64_t num_pages, int page_size,
+                                         const int32_t* prefix_pages, int64_t prefix_len,
+                                         const int32_t* page_table, int64_t num_requests,
+                                         int64_t table_width, const int32_t* requests,
+                                         const int32_t* lens, float scale, void* out,
+                                         void* workspace, int64_t workspace_bytes,
+                                         int32_t* error_count, kvq_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* kvq_status_string(kvq_status status);

@@ -67,6 +67,24 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.dsv4_kv_cache_gather_checked.argtypes = [_P, _I64, _I, _P, _I64, _P, _P, _P]
     L.dsv4_kv_cache_gather.restype = _I
     L.dsv4_kv_cache_gather.argtypes = [_P, _I, _P, _I64, _P, _P]
+    L.paged_kv_rope_append.restype = _I
+    L.paged_kv_rope_append.argtypes = [_P, _P, _I64, _I, _I, _I, _P, _I64, _I, _I, _P, _P, _P,
+                                       _I64, _I, _P, _P]
+    L.paged_kv_page_bounds.restype = _I
+    L.paged_kv_page_bounds.argtypes = [_P, _I64, _I, _I, _I, _P, _P, _I64, _P, _P, _P]
+    L.paged_kv_block_select.restype = _I
+    L.paged_kv_block_select.argtypes = [_P, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I64, _I64,
+                                        _P, _P, _I, _I, _I, _P, _P, _P]
+    L.paged_block_sparse_attention_workspace.restype = _I64
+    L.paged_block_sparse_attention_workspace.argtypes = [_I64, _I, _I, _I, _I, _I]
+    L.paged_block_sparse_attention.restype = _I
+    L.paged_block_sparse_attention.argtypes = [_P, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I64,
+                                               _I64, _P, _P, _P, _I, _F, _P, _P, _I64, _P, _P]
+    L.paged_shared_prefix_attention_workspace.restype = _I64
+    L.paged_shared_prefix_attention_workspace.argtypes = [_I64, _I, _I, _I, _I, _I64, _I64]
+    L.paged_shared_prefix_attention.restype = _I
+    L.paged_shared_prefix_attention.argtypes = [_P, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I64,
+                                                _P, _I64, _I64, _P, _P, _F, _P, _P, _I64, _P, _P]
     L.kvq_status_string.restype = ctypes.c_char_p
     L.kvq_status_string.argtypes = [_I]
     L.kvq_last_cuda_error.restype = _I
@@ -302,6 +320,211 @@ def dsv4_kv_cache_gather(kv_cache, slots, out=None, stream=None, errors=None):
                  _cuda(slots, torch.int64, "slots"), n, _cuda(out, torch.bfloat16, "out"),
                  _counter(errors), _stream(stream, dev))
     _check(st, "dsv4_kv_cache_gather")
+    return out
+
+
+def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox,
+                         positions, slot_mapping, kv_cache, q_out=None, stream=None,
+                         rotary_dim=None, errors=None) -> None:
+    """RoPE of the Q and K heads of ``qkv`` [T, (Hq+2Hkv)*head_dim] and the K
+    and V heads written to ``kv_cache`` (bf16 [num_pages, 2, Hkv, page_size,
+    head_dim]) at ``slot_mapping`` (int64 [T], -1 = none), in one pass.  The
+    rotated query rows go to ``q_out`` (bf16 [T, Hq, head_dim]) or stay in
+    place.  ``cos_sin_cache`` None: no rotation (after fused_qk_norm_rope);
+    ``rotary_dim`` defaults to the table's width.  Tokens with a position
+    outside the table are left out, slots outside the cache not written; both
+    are counted in ``errors`` (int32 CUDA tensor) when given."""
+    if qkv.dim() != 2 or qkv.shape[1] != (num_heads_q + 2 * num_heads_kv) * head_dim:
+        raise ValueError("qkv must be [T, (Hq+2*Hkv)*head_dim]")
+    T = qkv.shape[0]
+    _paged_cache(kv_cache, num_heads_kv, head_dim)
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must hold one value per token")
+    if q_out is not None and q_out.shape != (T, num_heads_q, head_dim):
+        raise ValueError("q_out must be [T, Hq, head_dim]")
+    if cos_sin_cache is None:
+        if rotary_dim:
+            raise ValueError("rotary_dim without a cos_sin_cache")
+        rotary_dim = rows = 0
+        cs = pos = None
+        positions = None
+    else:
+        if rotary_dim is None:
+            rotary_dim = cos_sin_cache.shape[1]
+        if cos_sin_cache.dim() != 2 or cos_sin_cache.shape[1] != rotary_dim or rotary_dim == 0:
+            raise ValueError("cos_sin_cache must be [max_pos, rotary_dim]")
+        if positions.numel() != T:
+            raise ValueError("positions must hold one value per token")
+        rows = cos_sin_cache.shape[0]
+        cs = _cuda(cos_sin_cache, torch.float32, "cos_sin_cache")
+        pos = _cuda(positions, torch.int64, "positions")
+    dev = _device(qkv, q_out, cos_sin_cache, positions, slot_mapping, kv_cache, errors)
+    st = _on(dev, lib().paged_kv_rope_append, _cuda(qkv, torch.bfloat16, "qkv"),
+             None if q_out is None else _cuda(q_out, torch.bfloat16, "q_out"), T, num_heads_q,
+             num_heads_kv, head_dim, cs, rows, int(rotary_dim), int(bool(is_neox)), pos,
+             _cuda(slot_mapping, torch.int64, "slot_mapping"),
+             _cuda(kv_cache, torch.bfloat16, "kv_cache"), kv_cache.shape[0], kv_cache.shape[3],
+             None if errors is None else _counter(errors), _stream(stream, dev))
+    _check(st, "paged_kv_rope_append")
+
+
+def _paged_cache(kv_cache, num_heads_kv=None, head_dim=None) -> None:
+    if kv_cache.dim() != 5 or kv_cache.shape[1] != 2:
+        raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim]")
+    if num_heads_kv is not None and (kv_cache.shape[2] != num_heads_kv
+                                     or kv_cache.shape[4] != head_dim):
+        raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim] of the "
+                         "call's Hkv and head_dim")
+
+
+def paged_kv_page_bounds(kv_cache, pages, lens, bounds, stream=None, errors=None):
+    """Writes the smallest and largest key per dim of the first ``lens``
+    (int32 [n]) tokens of each listed page (int64 [n], -1 = none) into
+    ``bounds`` (bf16 [num_pages, Hkv, 2, head_dim]), and returns ``bounds``."""
+    _paged_cache(kv_cache)
+    N, _, Hkv, page, D = kv_cache.shape
+    if pages.dim() != 1 or lens.shape != pages.shape:
+        raise ValueError("pages and lens must be 1-D, of one length")
+    if bounds.shape != (N, Hkv, 2, D):
+        raise ValueError("bounds must be [num_pages, Hkv, 2, head_dim]")
+    dev = _device(kv_cache, pages, lens, bounds, errors)
+    st = _on(dev, lib().paged_kv_page_bounds, _cuda(kv_cache, torch.bfloat16, "kv_cache"), N, Hkv,
+             page, D, _cuda(pages, torch.int64, "pages"), _cuda(lens, torch.int32, "lens"),
+             pages.shape[0], _cuda(bounds, torch.bfloat16, "bounds"),
+             None if errors is None else _counter(errors), _stream(stream, dev))
+    _check(st, "paged_kv_page_bounds")
+    return bounds
+
+
+def _paged_q(q, head_dim, name="q"):
+    """Address and token stride of bf16 [T, Hq, D] whose heads are contiguous
+    (a token's rows may be a view into packed QKV)."""
+    if q.dim() != 3 or q.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [T, Hq, {head_dim}]")
+    if q.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: expected {torch.bfloat16}, got {q.dtype}")
+    if not (q.is_cuda or (q.device.type == "cpu" and q.is_pinned())):
+        raise ValueError(f"{name}: expected a CUDA tensor or a pinned host tensor")
+    T, Hq, D = q.shape
+    if q.is_contiguous() or T == 0:
+        return q.data_ptr(), Hq * D
+    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return q.data_ptr(), (q.stride(0) if T > 1 else Hq * D)
+
+
+def _requests(T, page_table, lens, requests):
+    """Addresses of the request arrays of a call with T tokens."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [num_requests, table_width]")
+    if lens.numel() != T or (requests is not None and requests.numel() != T):
+        raise ValueError("lens and requests must hold one value per token")
+    if requests is None and page_table.shape[0] < T:
+        raise ValueError("page_table must have a row per token when requests is not given")
+    return (_cuda(page_table, torch.int32, "page_table"), page_table.shape[0],
+            page_table.shape[1],
+            None if requests is None else _cuda(requests, torch.int32, "requests"),
+            _cuda(lens, torch.int32, "lens"))
+
+
+def paged_kv_block_select(q, bounds, page_table, lens, page_size, topk, keep_first=0,
+                          keep_last=0, out=None, requests=None, stream=None, errors=None):
+    """int32 [T, Hkv, topk]: for each token of ``q`` [T, Hq, D] and kv head the
+    blocks (pages of the token's request) with the highest scores from
+    ``bounds`` (paged_kv_page_bounds), ascending, then -1.  ``page_table``
+    int32 [requests, width]; ``lens`` int32 [T]: keys each token sees;
+    ``requests`` int32 [T] (default: token t is request t); ``keep_first`` /
+    ``keep_last`` blocks are always selected."""
+    if bounds.dim() != 4 or bounds.shape[2] != 2:
+        raise ValueError("bounds must be [num_pages, Hkv, 2, head_dim]")
+    N, Hkv, _, D = bounds.shape
+    q_ptr, q_stride = _paged_q(q, D)
+    T, Hq = q.shape[0], q.shape[1]
+    table = _requests(T, page_table, lens, requests)
+    if out is None:
+        out = torch.empty((T, Hkv, topk), dtype=torch.int32, device=q.device)
+    if out.shape != (T, Hkv, topk):
+        raise ValueError("out must be [T, Hkv, topk]")
+    dev = _device(q, bounds, page_table, lens, requests, out, errors)
+    st = _on(dev, lib().paged_kv_block_select, q_ptr, q_stride, T, Hq, Hkv, D,
+             _cuda(bounds, torch.bfloat16, "bounds"), N, int(page_size), *table, int(topk),
+             int(keep_first), int(keep_last), _cuda(out, torch.int32, "out"),
+             None if errors is None else _counter(errors), _stream(stream, dev))
+    _check(st, "paged_kv_block_select")
+    return out
+
+
+def _attention_buffers(q, out, workspace, need):
+    """out and workspace of an attention call, allocated where not given; a
+    tensor of one call that must live until its kernels have run is torch's
+    to keep (its allocator reuses memory in stream order)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        return out, None, None, 0
+    return (out, workspace, _cuda(workspace, workspace.dtype, "workspace"),
+            workspace.numel() * workspace.element_size())
+
+
+def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=None, out=None,
+                                 requests=None, workspace=None, stream=None, errors=None):
+    """bf16 [T, Hq, D]: attention of each token of ``q`` over the keys of the
+    cache blocks listed for it (``blocks`` int32 [T, Hkv, topk], -1 = none, as
+    paged_kv_block_select returns them) that lie below ``lens[t]``.  ``scale``
+    defaults to 1/sqrt(D).  ``workspace``: a tensor of at least
+    ``paged_block_sparse_attention_workspace`` bytes, allocated per call if
+    not given."""
+    _paged_cache(kv_cache)
+    N, _, Hkv, page, D = kv_cache.shape
+    q_ptr, q_stride = _paged_q(q, D)
+    T, Hq = q.shape[0], q.shape[1]
+    if blocks.dim() != 3 or blocks.shape[0] != T or blocks.shape[1] != Hkv:
+        raise ValueError("blocks must be [T, Hkv, topk]")
+    topk = blocks.shape[2]
+    table = _requests(T, page_table, lens, requests)
+    L = lib()
+    need = L.paged_block_sparse_attention_workspace(T, Hq, Hkv, D, page, topk)
+    out, workspace, ws, ws_bytes = _attention_buffers(q, out, workspace, need)
+    dev = _device(q, kv_cache, page_table, blocks, lens, requests, out, workspace, errors)
+    st = _on(dev, L.paged_block_sparse_attention, q_ptr, q_stride, T, Hq, Hkv, D,
+             _cuda(kv_cache, torch.bfloat16, "kv_cache"), N, page, *table,
+             _cuda(blocks, torch.int32, "blocks"), topk,
+             float(D ** -0.5 if scale is None else scale), _cuda(out, torch.bfloat16, "out"), ws,
+             ws_bytes, None if errors is None else _counter(errors), _stream(stream, dev))
+    _check(st, "paged_block_sparse_attention")
+    return out
+
+
+def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_table, lens,
+                                  scale=None, out=None, requests=None, workspace=None,
+                                  stream=None, errors=None):
+    """bf16 [T, Hq, D]: attention of each token of ``q`` over the shared
+    ``prefix_len`` keys of ``prefix_pages`` (int32) and the first ``lens[t]``
+    keys of its own request's pages (``page_table``).  The prefix is read once
+    for the whole batch.  Other arguments as paged_block_sparse_attention."""
+    _paged_cache(kv_cache)
+    N, _, Hkv, page, D = kv_cache.shape
+    q_ptr, q_stride = _paged_q(q, D)
+    T, Hq = q.shape[0], q.shape[1]
+    prefix_len = int(prefix_len)
+    if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page < prefix_len:
+        raise ValueError("prefix_pages must be 1-D and hold prefix_len keys")
+    table = _requests(T, page_table, lens, requests)
+    L = lib()
+    need = L.paged_shared_prefix_attention_workspace(T, Hq, Hkv, D, page, prefix_len,
+                                                     page_table.shape[1])
+    out, workspace, ws, ws_bytes = _attention_buffers(q, out, workspace, need)
+    dev = _device(q, kv_cache, prefix_pages, page_table, lens, requests, out, workspace, errors)
+    st = _on(dev, L.paged_shared_prefix_attention, q_ptr, q_stride, T, Hq, Hkv, D,
+             _cuda(kv_cache, torch.bfloat16, "kv_cache"), N, page,
+             _cuda(prefix_pages, torch.int32, "prefix_pages"), prefix_len, *table,
+             float(D ** -0.5 if scale is None else scale), _cuda(out, torch.bfloat16, "out"), ws,
+             ws_bytes, None if errors is None else _counter(errors), _stream(stream, dev))
+    _check(st, "paged_shared_prefix_attention")
     return out
 
 

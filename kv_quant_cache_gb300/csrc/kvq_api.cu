@@ -78,11 +78,7 @@ int64_t current_threshold() {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-kvq_status finish_launch(cudaError_t e) {
-  if (e == cudaSuccess) return KVQ_OK;
-  t_last_cuda_error = static_cast<int>(e);
-  return KVQ_ERR_CUDA;
-}
+kvq_status finish_launch(cudaError_t e) { return kvq::report_launch(e); }
 
 constexpr int64_t kIndexLimit = (int64_t)1 << 31;
 
@@ -119,6 +115,12 @@ namespace {
 std::atomic<uint32_t> g_stage_wait_limit{1u << 22};
 std::atomic<bool> g_programmatic_launch{true};
 }  // namespace
+
+kvq_status report_launch(cudaError_t e) {
+  if (e == cudaSuccess) return KVQ_OK;
+  t_last_cuda_error = static_cast<int>(e);
+  return KVQ_ERR_CUDA;
+}
 
 bool programmatic_launch() { return g_programmatic_launch.load(std::memory_order_relaxed); }
 
@@ -362,10 +364,10 @@ const char* kvq_status_string(kvq_status status) {
     case KVQ_OK: return "ok";
     case KVQ_ERR_NULL: return "a required pointer is NULL";
     case KVQ_ERR_SHAPE: return "invalid count or size";
-    case KVQ_ERR_UNSUPPORTED: return "unsupported head_dim / rotary_dim / is_neox";
+    case KVQ_ERR_UNSUPPORTED: return "unsupported head_dim / rotary_dim / is_neox / table width";
     case KVQ_ERR_ALIGN: return "pointer not aligned as required";
     case KVQ_ERR_CUDA: return "CUDA launch failed (see kvq_last_cuda_error)";
-    case KVQ_ERR_VALUE: return "eps not finite / negative, or q_out partly overlaps q";
+    case KVQ_ERR_VALUE: return "eps or scale not finite, eps negative, or an output overlaps an input";
   }
   return "unknown kvq_status";
 }

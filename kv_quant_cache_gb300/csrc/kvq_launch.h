@@ -7,7 +7,12 @@
 
 #include <atomic>
 
+#include "kvq.h"
+
 namespace kvq {
+
+// KVQ_OK, or KVQ_ERR_CUDA with the error kept for kvq_last_cuda_error.
+kvq_status report_launch(cudaError_t e);
 
 struct QkArgs {
   void* qkv;
