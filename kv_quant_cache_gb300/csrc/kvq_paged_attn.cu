@@ -517,6 +517,19 @@ int64_t prefix_tiles(int64_t num_tokens, int num_q, int num_kv) {
   return (num_tokens * (num_q / num_kv) + kRows - 1) / kRows;
 }
 
+// Parts of the prefix on the small matrix instruction, and of the tokens' own
+// keys (0: there are none).
+int prefix_slots(int64_t num_tokens, int num_q, int num_kv, int page_size, int64_t prefix_len) {
+  if (prefix_len == 0) return 0;
+  return splits_for(prefix_tiles(num_tokens, num_q, num_kv) * num_kv,
+                    (prefix_len + page_size - 1) / page_size, page_size);
+}
+
+int own_slots(int64_t num_tokens, int num_q, int num_kv, int page_size, int table_width) {
+  if (table_width == 0) return 0;
+  return splits_for(own_ctas(num_tokens, num_q, num_kv), table_width, page_size);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, void* out,
@@ -559,15 +572,17 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
 int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int64_t prefix_len,
                               int table_width) {
-  const int64_t pages = (prefix_len + page_size - 1) / page_size;
-  const int s1 = prefix_len == 0 ? 0
-                                 : splits_for(prefix_tiles(num_tokens, num_heads_q, num_heads_kv) *
-                                                  num_heads_kv,
-                                              pages, page_size);
-  const int s2 = table_width == 0 ? 0
-                                  : splits_for(own_ctas(num_tokens, num_heads_q, num_heads_kv),
-                                               table_width, page_size);
-  return partials_bytes(s1 + s2, num_tokens * num_heads_q, head_dim);
+  const int64_t slots =
+      prefix_slots(num_tokens, num_heads_q, num_heads_kv, page_size, prefix_len);
+  int64_t tiles = 0;
+  if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len))
+    tiles = prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size,
+                              prefix_len).parts;
+  // either kernel may run: which one depends on where the cache lies
+  return partials_bytes((slots > tiles ? slots : tiles) +
+                            own_slots(num_tokens, num_heads_q, num_heads_kv, page_size,
+                                      table_width),
+                        num_tokens * num_heads_q, head_dim);
 }
 
 cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
@@ -575,27 +590,34 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   AttnParams p = common(x, a.kv_cache, a.scale);
   p.prefix_pages = a.prefix_pages;
   p.prefix_len = a.prefix_len;
-  const int64_t tiles = prefix_tiles(x.num_tokens, x.num_heads_q, x.num_heads_kv);
-  p.row_tiles = (int)tiles;
-  const int64_t pre_ctas = tiles * x.num_heads_kv;
-  const int64_t own = own_ctas(x.num_tokens, x.num_heads_q, x.num_heads_kv);
-  const int64_t pages = (a.prefix_len + x.page_size - 1) / x.page_size;
-  const int s1 = a.prefix_len == 0 ? 0 : splits_for(pre_ctas, pages, x.page_size);
-  const int s2 = x.table_width == 0 ? 0 : splits_for(own, x.table_width, x.page_size);
   const int64_t rows = (int64_t)x.num_tokens * x.num_heads_q;
+  CUtensorMap map;
+  const bool tiles = prefix_tiles_fit(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
+                                      x.page_size, a.prefix_len) &&
+                     prefix_tiles_map(a, &map);
+  const int s1 = tiles ? prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv,
+                                           x.head_dim, x.page_size, a.prefix_len).parts
+                       : prefix_slots(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
+                                      a.prefix_len);
+  const int s2 = own_slots(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
+                           x.table_width);
   p.parts = partials_at(a.workspace, s1 + s2, rows, x.head_dim);
-  if (s1) {
+  cudaError_t e = cudaSuccess;
+  if (tiles) {
+    e = launch_prefix_tiles(a, map, p.parts, stream);
+  } else if (s1) {
+    p.row_tiles = (int)prefix_tiles(x.num_tokens, x.num_heads_q, x.num_heads_kv);
     p.splits = s1;
     p.first_slot = 0;
-    const cudaError_t e = launch_attn_dim<kPrefix>(p, x.head_dim, pre_ctas, stream);
-    if (e != cudaSuccess) return e;
+    e = launch_attn_dim<kPrefix>(p, x.head_dim, (int64_t)p.row_tiles * x.num_heads_kv, stream);
   }
-  if (s2) {
+  if (e == cudaSuccess && s2) {
     p.splits = s2;
     p.first_slot = s1;
-    const cudaError_t e = launch_attn_dim<kOwn>(p, x.head_dim, own, stream);
-    if (e != cudaSuccess) return e;
+    e = launch_attn_dim<kOwn>(p, x.head_dim, own_ctas(x.num_tokens, x.num_heads_q, x.num_heads_kv),
+                              stream);
   }
+  if (e != cudaSuccess) return e;
   return launch_attn_join(p.parts, s1 + s2, x.head_dim, a.out, stream);
 }
 

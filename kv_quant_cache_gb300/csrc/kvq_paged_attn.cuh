@@ -9,6 +9,8 @@
 // left is zero.  o_i and l_i are fp32.
 #pragma once
 
+#include <cuda.h>
+
 #include "kvq_device.cuh"
 #include "kvq_paged.h"
 
@@ -38,5 +40,21 @@ inline Partials partials_at(void* workspace, int64_t slots, int64_t rows, int he
 // Joins the parts into out bf16 [rows][D].
 cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, void* out,
                              cudaStream_t stream);
+
+// The prefix on the tensor cores (kvq_paged_prefix.cu): sizes it takes, the
+// parts it makes of the prefix, the tensor map of the cache (false where it
+// cannot be copied that way: not memory of the current device, no pages), and
+// the launch (partials slots 0 .. parts - 1).
+struct PrefixTilesPlan {
+  int share;  // blocks of 128 keys of a part
+  int parts;
+};
+bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
+                      int page_size, int64_t prefix_len);
+PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_heads_kv,
+                                  int head_dim, int page_size, int64_t prefix_len);
+bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map);
+cudaError_t launch_prefix_tiles(const PrefixAttnArgs& a, const CUtensorMap& map,
+                                const Partials& parts, cudaStream_t stream);
 
 }  // namespace kvq

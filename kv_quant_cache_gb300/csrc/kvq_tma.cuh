@@ -115,6 +115,16 @@ __device__ __forceinline__ void tile_load_3d(uint32_t dst, const CUtensorMap* tm
       : "memory");
 }
 
+// The same for a 4-D tensor map.
+__device__ __forceinline__ void tile_load_4d(uint32_t dst, const CUtensorMap* tmap, int c0,
+                                             int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
 // Orders this thread's earlier shared-memory accesses before later
 // bulk-copy writes to the same stage.
 __device__ __forceinline__ void fence_proxy_async() {
@@ -173,6 +183,18 @@ inline bool encode_bf16_3d(CUtensorMap* map, const void* base, const cuuint64_t 
   const cuuint32_t elem[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
             elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A 4-D bf16 tensor map whose boxes land with the 128-byte swizzle (box[0] is
+// 64 elements).
+inline bool encode_bf16_4d_swizzled(CUtensorMap* map, const void* base, const cuuint64_t dims[4],
+                                    const cuuint64_t strides[3], const cuuint32_t box[4]) {
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
