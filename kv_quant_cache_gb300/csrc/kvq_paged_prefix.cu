@@ -13,7 +13,7 @@
 //     reference m of a row only moves when a score exceeds it by more than
 //     2^8; until then weights above 1 are as exact as those below, and O is
 //     seldom rescaled;
-//   * warp 8, one thread: issues the matrix instructions.  While one tile's
+//   * warp 8, one lane: issues the matrix instructions.  While one tile's
 //     softmax runs, the other tile's products do;
 //   * warp 9: loads K and V, two blocks ahead, by tensor-map copies (a page,
 //     or 128 keys of one, at a time; 128-byte swizzle).  A block that ends
@@ -41,6 +41,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9;
 // third group keeps 64 (256 x 208 + 128 x 64 = 61440 of 64512).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 64;
 constexpr int kMaxPages = 2048;       // pages of a part
+constexpr int kEarly = 3;             // quarters of a block whose P is handed over early
 constexpr float kRescaleAt = 8.f;     // log2 by which a score may exceed m
 
 struct PrefixParams {
@@ -72,19 +73,40 @@ struct Layout {
   static constexpr int kV = kK + 2 * kTile;
   static constexpr int kList = kV + 2 * kTile;
   static constexpr int kBars = kList + kMaxPages * 4;
-  static constexpr int kEnd = kBars + 16 * 8 + 32;
+  static constexpr int kEnd = kBars + 24 * 8 + 32;
   static constexpr int kSmem = kEnd + 1024;          // room to align the base
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
 // mbarriers, by index
 enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 9, kPFull = 11,
-       kPvDone = 13, kDrain = 15 };
+       kPvDone = 13, kPEarly = 15, kDrain = 17, kBarriers = 18 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 values at a time: (a.x, a.y) * m + c and a + b.
+union Pair {
+  float f[2];
+  unsigned long long u;
+};
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair m, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(m.u), "l"(c.u));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
 }
 
 // Where 16-byte fragment c of row r lies in a swizzled 128-row tile.
@@ -107,13 +129,13 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   uint8_t* smem = raw + (base - tma::smem_addr(raw));
   int* list = reinterpret_cast<int*>(smem + L::kList);
   const uint32_t bars = base + L::kBars;
-  int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 16 * 8);
+  int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 24 * 8);
   volatile int* dead = shared_state;      // a wait ran out
   int* any_bad = shared_state + 1;        // a listed page lies outside the cache
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_state + 2);
   auto bar = [&](int i) { return bars + 8u * i; };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int kv_head = blockIdx.x / p.row_tiles;
   const int64_t row0 = (int64_t)(blockIdx.x % p.row_tiles) * (2 * kTileRows);
   const int64_t rows_left = p.rows - row0;
@@ -125,8 +147,10 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   const int listed = ((key1 - 1) >> p.page_shift) - page0 + 1;
 
   if (threadIdx.x == 0) {
-    const int counts[16] = {1, 1, 1, 1, 1, 1, 1, 1, 8, 1, 1, 4, 4, 1, 1, 1};
-    for (int i = 0; i < 16; ++i) tma::mbar_init(bar(i), counts[i]);
+    for (int i = 0; i < kBarriers; ++i) {
+      const bool by_warps = (i >= kPFull && i < kPFull + 2) || (i >= kPEarly && i < kPEarly + 2);
+      tma::mbar_init(bar(i), i == kQFull ? 8 : by_warps ? 4 : 1);
+    }
     tma::mbar_init_fence();
     *dead = 0;
     *any_bad = 0;
@@ -146,7 +170,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -177,7 +201,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     bool ok = true;
     if (tile < tiles) {
       for (int j = 0; j < n; ++j) {
-        ok = __all_sync(kFullMask, tc::wait(bar(kSFull + tile), j & 1, dead));
+        ok = tc::wait_warp(bar(kSFull + tile), j & 1, dead);
         if (!ok) break;
         tc::fence_after();
         uint32_t s[4][32];
@@ -208,7 +232,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           m = top;
           if (j > 0) {
             // O is at rest once the previous block's product is done
-            ok = __all_sync(kFullMask, tc::wait(bar(kPvDone + tile), (j - 1) & 1, dead));
+            ok = tc::wait_warp(bar(kPvDone + tile), (j - 1) & 1, dead);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll
@@ -223,28 +247,41 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           }
         }
         const float shift = m == -INFINITY ? 0.f : -m * p.scale_log2;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const Pair scale2 = pair(p.scale_log2, p.scale_log2), shift2 = pair(shift, shift);
+        Pair sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float a = ex2(fmaf(__uint_as_float(s[c][2 * k]), p.scale_log2, shift));
-            const float b = ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), p.scale_log2, shift));
-            sum[2 * (k & 1)] += a;
-            sum[2 * (k & 1) + 1] += b;
-            w[k] = pack_bf16x2(a, b);
+          for (int k = 0; k < 16; k += 2) {
+            Pair a = fma2(pair(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])),
+                          scale2, shift2);
+            Pair b = fma2(pair(__uint_as_float(s[c][2 * k + 2]), __uint_as_float(s[c][2 * k + 3])),
+                          scale2, shift2);
+            a = pair(ex2(a.f[0]), ex2(a.f[1]));
+            b = pair(ex2(b.f[0]), ex2(b.f[1]));
+            sum0 = add2(sum0, a);
+            sum1 = add2(sum1, b);
+            w[k] = pack_bf16x2(a.f[0], a.f[1]);
+            w[k + 1] = pack_bf16x2(b.f[0], b.f[1]);
           }
           tc::st16(s_at + 16 * c, w);
+          if (c == kEarly - 1) {  // the products of the first keys may begin
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(kPEarly + tile));
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum0 = add2(sum0, sum1);
+        l += sum0.f[0] + sum0.f[1];
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(kPFull + tile));
       }
       // ---- the partial -----------------------------------------------------------------
-      if (ok) ok = __all_sync(kFullMask, tc::wait(bar(kPvDone + tile), (n - 1) & 1, dead));
+      if (ok) ok = tc::wait_warp(bar(kPvDone + tile), (n - 1) & 1, dead);
       tc::fence_after();
       const int r = tile * kTileRows + (warp & 3) * 32 + lane;
       const int64_t t = (row0 + r) / p.group;
@@ -275,54 +312,62 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   }
   if (warp == kMmaWarp) {
     // ---- the matrix instructions -------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t qk = tc::instr_desc(kKeys, false), pv = tc::instr_desc(D, true);
-      auto scores = [&](int tile, int stage) {
-        const uint32_t a = base + L::kQ + tile * L::kTile, b = base + L::kK + stage * L::kTile;
+    constexpr uint32_t qk = tc::instr_desc(kKeys, false), pv = tc::instr_desc(D, true);
+    const uint64_t q_desc = tc::smem_desc(base + L::kQ, 16);
+    const uint64_t k_desc = tc::smem_desc(base + L::kK, 16);
+    const uint64_t v_desc = tc::smem_desc(base + L::kV, 128 * 128);
+    auto scores = [&](int tile, int stage) {
+      const uint64_t a = q_desc + (uint32_t)(tile * (L::kTile >> 4));
+      const uint64_t b = k_desc + (uint32_t)(stage * (L::kTile >> 4));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-          tc::mma_ss(tmem + 128 * tile, tc::smem_desc(a + off, 16), tc::smem_desc(b + off, 16), qk,
-                     k > 0);
-        }
-        tc::commit(bar(kSFull + tile));
-      };
-      bool ok = tc::wait(bar(kQFull), 0, dead) && tc::wait(bar(kKFull), 0, dead);
-      if (ok) {
-        tc::fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-        tc::commit(bar(kKEmpty));
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+        tc::mma_ss(tmem + 128 * tile, a + off, b + off, qk, k > 0);
       }
-      for (int j = 0; ok && j < n; ++j) {
-        const int stage = j & 1, next = (j + 1) & 1;
-        const bool more = j + 1 < n;
-        ok = tc::wait(bar(kVFull + stage), (j >> 1) & 1, dead) &&
-             (!more || tc::wait(bar(kKFull + next), ((j + 1) >> 1) & 1, dead));
-        for (int t = 0; ok && t < tiles; ++t) {
-          ok = tc::wait(bar(kPFull + t), j & 1, dead);
-          if (!ok) break;
-          tc::fence_after();
-          const uint32_t v = base + L::kV + stage * L::kTile;
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k,
-                       tc::smem_desc(v + k * (16 * 128), 128 * 128), pv, j > 0 || k > 0);
-          tc::commit(bar(kPvDone + t));
-          // the next scores go over P, which the products above read first:
-          // matrix instructions of one thread run in order
-          if (more) scores(t, next);
-        }
-        if (!ok) break;
-        tc::commit(bar(kVEmpty + stage));
-        if (more) tc::commit(bar(kKEmpty + next));
-      }
-      if (!ok) {  // nothing may be in flight when the tensor memory goes
-        tc::commit(bar(kDrain));
-        for (uint32_t i = 0; i < (1u << 22) && !tma::mbar_test(bar(kDrain), 0); ++i) {
-        }
-      }
+      tc::commit(bar(kSFull + tile));
+    };
+    bool ok = tc::wait_warp(bar(kQFull), 0, dead) && tc::wait_warp(bar(kKFull), 0, dead);
+    if (ok) {
+      tc::fence_after();
+      for (int t = 0; t < tiles; ++t) scores(t, 0);
+      tc::commit(bar(kKEmpty));
     }
-    __syncwarp();
+    for (int j = 0; ok && j < n; ++j) {
+      const int stage = j & 1, next = (j + 1) & 1;
+      const bool more = j + 1 < n;
+      ok = tc::wait_warp(bar(kVFull + stage), (j >> 1) & 1, dead) &&
+           (!more || tc::wait_warp(bar(kKFull + next), ((j + 1) >> 1) & 1, dead));
+      for (int t = 0; ok && t < tiles; ++t) {
+        const uint64_t v = v_desc + (uint32_t)(stage * (L::kTile >> 4));
+        ok = tc::wait_warp(bar(kPEarly + t), j & 1, dead);
+        if (!ok) break;
+        tc::fence_after();
+#pragma unroll
+        for (int k = 0; k < 2 * kEarly; ++k)
+          tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4), pv,
+                     j > 0 || k > 0);
+        ok = tc::wait_warp(bar(kPFull + t), j & 1, dead);
+        if (!ok) break;
+        tc::fence_after();
+#pragma unroll
+        for (int k = 2 * kEarly; k < kKeys / 16; ++k)
+          tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4), pv,
+                     true);
+        tc::commit(bar(kPvDone + t));
+        // the next scores go over P, which the products above read first:
+        // matrix instructions of one thread run in order
+        if (more) scores(t, next);
+      }
+      if (!ok) break;
+      tc::commit(bar(kVEmpty + stage));
+      if (more) tc::commit(bar(kKEmpty + next));
+    }
+    if (!ok) {  // nothing may be in flight when the tensor memory goes
+      tc::commit(bar(kDrain));
+      for (uint32_t i = 0; i < (1u << 22) && !tma::mbar_test(bar(kDrain), 0); ++i) {
+      }
+      __syncwarp();
+    }
   } else if (warp == kLoadWarp) {
     // ---- the loads ---------------------------------------------------------------------
     const int page_size = 1 << p.page_shift;
@@ -341,8 +386,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         const uint32_t full = bar((kv ? kVFull : kKFull) + stage);
         const uint32_t dst = base + (kv ? L::kV : L::kK) + stage * L::kTile;
         if (j >= 2) {
-          ok = __all_sync(kFullMask, tc::wait(bar((kv ? kVEmpty : kKEmpty) + stage),
-                                              ((j >> 1) - 1) & 1, dead));
+          ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + stage), ((j >> 1) - 1) & 1, dead);
           if (!ok) break;
         }
         if (whole) {

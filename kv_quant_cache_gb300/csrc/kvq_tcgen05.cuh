@@ -13,21 +13,27 @@ namespace kvq {
 namespace tc {
 
 // ---- waits -------------------------------------------------------------------
-// No wait is endless: after kPolls polls or kNs nanoseconds the waiter raises
+// No wait is endless: after kPolls polls or kClocks cycles the waiter raises
 // the CTA's `dead` flag and returns false, and every other waiter of the CTA
-// that polls sees the flag.
+// that polls sees the flag.  (The cycle counter, not the nanosecond timer: a
+// read of that one takes longer than most waits.)
 constexpr uint32_t kPolls = 1u << 24;
-constexpr uint64_t kNs = 1000000000;  // 1 s
+constexpr long long kClocks = 2000000000;  // about 1 s
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* dead) {
   if (tma::mbar_test(bar, parity)) return true;
-  const uint64_t t0 = tma::global_ns();
+  const long long t0 = clock64();
   for (uint32_t i = 1; i < kPolls; ++i) {
     if (tma::mbar_test(bar, parity)) return true;
-    if ((i & 63u) == 0 && (*dead || tma::global_ns() - t0 > kNs)) break;
+    if ((i & 63u) == 0 && (*dead || clock64() - t0 > kClocks)) break;
   }
   *dead = 1;
   return false;
+}
+
+// The same by a whole warp, which stays converged.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* dead) {
+  return __all_sync(kFullMask, wait(bar, parity, dead));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -114,22 +120,28 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool k_rows_b) {
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// D[tmem] (+)= A B, one K = 16 step; issued by one thread.
+// D[tmem] (+)= A B, one K = 16 step.  The whole warp calls, converged, and one
+// elected lane issues (always the same one, which commit() relies on): the
+// operands then are warp-uniform for the compiler.  Issued from a branch of
+// one lane instead, each instruction took about 75 cycles to prepare, longer
+// than it takes to run.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
@@ -137,7 +149,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // Arrives on `bar` once all matrix instructions issued so far are done.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar)
       : "memory");
 }
 
