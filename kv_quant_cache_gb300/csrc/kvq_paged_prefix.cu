@@ -8,17 +8,18 @@
 //   P = 2^(S scale log2(e) - m), rounded once to bf16, over S's columns,
 //   O += P V    [128 x D], fp32 in tensor memory, P read from there.
 // Warps have one role each:
-//   * warps 0-3 and 4-7: the softmax of tile 0 and tile 1.  A thread owns a
-//     row (its tensor-memory lane), so maximum and sum need no shuffle.  The
-//     reference m of a row only moves when a score exceeds it by more than
-//     2^8; until then weights above 1 are as exact as those below, and O is
-//     seldom rescaled;
-//   * warp 8, one lane: issues the matrix instructions.  While one tile's
+//   * warps 0-7 and 8-15: the softmax of tile 0 and tile 1.  Two threads own
+//     a row (its tensor-memory lane), 64 keys each, and exchange only their
+//     maxima.  (One thread a row: 1500 cycles a block instead of about half,
+//     and the tensor cores waited.)  The reference m of a row only moves when
+//     a score exceeds it by more than 2^8; until then weights above 1 are as
+//     exact as those below, and O is seldom rescaled;
+//   * warp 16, one lane: issues the matrix instructions.  While one tile's
 //     softmax runs, the other tile's products do;
-//   * warp 9: loads K and V, two blocks ahead, by tensor-map copies (a page,
-//     or 128 keys of one, at a time; 128-byte swizzle).  A block that ends
-//     past the prefix, or that lists a page outside the cache, is copied by
-//     the warp's own loads instead, with zeros in V where there is no key;
+//   * warps 17 and 18: load K and V, two blocks ahead, by tensor-map copies (a
+//     page, or 128 keys of one, at a time; 128-byte swizzle).  A block that
+//     ends past the prefix, or that lists a page outside the cache, is copied
+//     by the warp's own loads instead, with zeros in V where there is no key;
 //     the softmax gives those places weight 0.
 // The result is a partial (normalised O and log2 of the weight sum) for the
 // join with the other parts and with each token's own keys.
@@ -35,13 +36,12 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;            // keys of a block
-constexpr int kThreads = 384;         // three groups of four warps
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-// Registers of a thread: 384 x 168 at launch; the softmax groups take 208, the
-// third group keeps 64 (256 x 208 + 128 x 64 = 61440 of 64512).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 64;
+constexpr int kThreads = 640;         // five groups of four warps
+constexpr int kMmaWarp = 16, kLoadWarp = 17;  // 17: K, 18: V
+// Registers of a thread: 640 x 96 at launch; the softmax groups take 104, the
+// last group keeps 56 (512 x 104 + 128 x 56 = 60416 of 61440).
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
 constexpr int kMaxPages = 2048;       // pages of a part
-constexpr int kEarly = 3;             // quarters of a block whose P is handed over early
 constexpr float kRescaleAt = 8.f;     // log2 by which a score may exceed m
 
 struct PrefixParams {
@@ -72,7 +72,8 @@ struct Layout {
   static constexpr int kK = 2 * kTile;
   static constexpr int kV = kK + 2 * kTile;
   static constexpr int kList = kV + 2 * kTile;
-  static constexpr int kBars = kList + kMaxPages * 4;
+  static constexpr int kTops = kList + kMaxPages * 4;  // [2 blocks][2 halves][256 rows]
+  static constexpr int kBars = kTops + 4096;
   static constexpr int kEnd = kBars + 24 * 8 + 32;
   static constexpr int kSmem = kEnd + 1024;          // room to align the base
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -80,11 +81,17 @@ struct Layout {
 
 // mbarriers, by index
 enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 9, kPFull = 11,
-       kPvDone = 13, kPEarly = 15, kDrain = 17, kBarriers = 18 };
+       kPvDone = 15, kDrain = 17, kBarriers = 18 };  // kPFull + 2 tile + part
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -109,6 +116,18 @@ __device__ __forceinline__ Pair add2(Pair a, Pair b) {
   return r;
 }
 
+// Barrier of the two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+// Its arrival alone, by a warp that gives up (`dead` is set): the other one's
+// next pair_sync, its last before it fails in a wait of its own, passes.
+__device__ __forceinline__ void pair_leave(int id) {
+  __threadfence_block();
+  asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+}
+
 // Where 16-byte fragment c of row r lies in a swizzled 128-row tile.
 __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -128,6 +147,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (base - tma::smem_addr(raw));
   int* list = reinterpret_cast<int*>(smem + L::kList);
+  volatile float* tops = reinterpret_cast<float*>(smem + L::kTops);
   const uint32_t bars = base + L::kBars;
   int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 24 * 8);
   volatile int* dead = shared_state;      // a wait ran out
@@ -148,8 +168,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBarriers; ++i) {
-      const bool by_warps = (i >= kPFull && i < kPFull + 2) || (i >= kPEarly && i < kPEarly + 2);
-      tma::mbar_init(bar(i), i == kQFull ? 8 : by_warps ? 4 : 1);
+      tma::mbar_init(bar(i), i == kQFull ? 16 : i >= kPFull && i < kPFull + 4 ? 8 : 1);
     }
     tma::mbar_init_fence();
     *dead = 0;
@@ -172,12 +191,12 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
 
-  if (warp < 8) {
+  if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ---------------------------------------------------------------------
-    // all 256 threads bring in Q, tile after tile
+    // all 512 threads bring in Q, tile after tile
     constexpr int FRAGS = D / 8;
-    for (int i = threadIdx.x; i < tiles * kTileRows * FRAGS; i += 256) {
+    for (int i = threadIdx.x; i < tiles * kTileRows * FRAGS; i += 512) {
       const int r = i / FRAGS, c = i % FRAGS;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < rows_left) {
@@ -192,9 +211,12 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bar(kQFull));
 
-    const int tile = warp >> 2;
+    const int tile = warp >> 3, half = (warp >> 2) & 1;
+    const int r = tile * kTileRows + (warp & 3) * 32 + lane;  // the thread's row
+    const int pair_bar = 1 + tile * 4 + (warp & 3);           // its two warps' barrier
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
-    const uint32_t s_at = at + 128 * tile, o_at = at + 256 + 128 * tile;
+    const uint32_t s_at = at + 128 * tile + 64 * half, p_at = at + 128 * tile + 32 * half;
+    const uint32_t o_at = at + 256 + 128 * tile + (D / 2) * half;
     const bool ragged_end = ((key1 - key0) & (kKeys - 1)) != 0;
     const bool bad = *any_bad != 0;
     float m = -INFINITY, l = 0.f;
@@ -204,16 +226,16 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         ok = tc::wait_warp(bar(kSFull + tile), j & 1, dead);
         if (!ok) break;
         tc::fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld32(s[c], s_at + 32 * c);
+        uint32_t s[2][32];
+        tc::ld32(s[0], s_at);
+        tc::ld32(s[1], s_at + 32);
         tc::wait_ld();
         if (bad || (ragged_end && j == n - 1)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const int key = key0 + j * kKeys + 32 * c + k;
+              const int key = key0 + j * kKeys + 64 * half + 32 * c + k;
               if (key >= key1 || list[(key >> p.page_shift) - page0] < 0)
                 s[c][k] = 0xff800000u;  // -inf
             }
@@ -221,11 +243,19 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         float top4[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          top4[c] = __uint_as_float(s[c][0]);
+          const uint32_t* x = s[c >> 1] + 16 * (c & 1);
+          top4[c] = __uint_as_float(x[0]);
 #pragma unroll
-          for (int k = 1; k < 32; ++k) top4[c] = fmaxf(top4[c], __uint_as_float(s[c][k]));
+          for (int k = 1; k < 15; k += 2)
+            top4[c] = max3(top4[c], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
         }
-        const float top = fmaxf(m, fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])));
+        float top = max3(top4[0], top4[1], max3(top4[2], top4[3], __uint_as_float(s[0][15])));
+        top = max3(top, __uint_as_float(s[0][31]),
+                   fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31])));
+        // the row's maximum over both halves; from here on both have read S
+        tops[(j & 1) * 512 + half * 256 + r] = top;
+        pair_sync(pair_bar);
+        top = fmaxf(m, fmaxf(top, tops[(j & 1) * 512 + (half ^ 1) * 256 + r]));
         if (__any_sync(kFullMask, (top - m) * p.scale_log2 > kRescaleAt)) {
           const float f = top == m ? 1.f : ex2((m - top) * p.scale_log2);
           l *= f;
@@ -235,8 +265,8 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
             ok = tc::wait_warp(bar(kPvDone + tile), (j - 1) & 1, dead);
             if (!ok) break;
             tc::fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
               uint32_t o[32];
               tc::ld32(o, o_at + 32 * c);
               tc::wait_ld();
@@ -250,7 +280,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         const Pair scale2 = pair(p.scale_log2, p.scale_log2), shift2 = pair(shift, shift);
         Pair sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
@@ -265,32 +295,35 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
             w[k] = pack_bf16x2(a.f[0], a.f[1]);
             w[k + 1] = pack_bf16x2(b.f[0], b.f[1]);
           }
-          tc::st16(s_at + 16 * c, w);
-          if (c == kEarly - 1) {  // the products of the first keys may begin
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(kPEarly + tile));
-          }
+          tc::st16(p_at + 16 * c, w);
+          // each half's first 32 keys are handed over before the others are done
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(kPFull + 2 * tile + c));
         }
         sum0 = add2(sum0, sum1);
         l += sum0.f[0] + sum0.f[1];
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(kPFull + tile));
       }
       // ---- the partial -----------------------------------------------------------------
       if (ok) ok = tc::wait_warp(bar(kPvDone + tile), (n - 1) & 1, dead);
       tc::fence_after();
-      const int r = tile * kTileRows + (warp & 3) * 32 + lane;
+      // the halves' sums; not the slots of the last block's maxima
+      if (ok) {
+        tops[(n & 1) * 512 + half * 256 + r] = l;
+        pair_sync(pair_bar);
+        l += tops[(n & 1) * 512 + (half ^ 1) * 256 + r];
+        ok = *dead == 0;
+      } else {
+        pair_leave(pair_bar);
+      }
       const int64_t t = (row0 + r) / p.group;
       const int64_t row = t * p.num_q + kv_head * p.group + (row0 + r - t * p.group);
       const int64_t slot = p.first_slot + blockIdx.y;
       const float f = l == 0.f ? 0.f : 1.f / l;
-      float* out = p.parts.o + (slot * p.parts.rows + row) * D;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      float* out = p.parts.o + (slot * p.parts.rows + row) * D + (D / 2) * half;
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];
         tc::ld32(o, o_at + 32 * c);
         tc::wait_ld();
@@ -302,7 +335,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
                             __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
         }
       }
-      if (r < rows_left)
+      if (half == 0 && r < rows_left)
         p.parts.lse[slot * p.parts.rows + row] =
             !ok ? NAN : l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m * p.scale_log2);
     }
@@ -339,20 +372,18 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
            (!more || tc::wait_warp(bar(kKFull + next), ((j + 1) >> 1) & 1, dead));
       for (int t = 0; ok && t < tiles; ++t) {
         const uint64_t v = v_desc + (uint32_t)(stage * (L::kTile >> 4));
-        ok = tc::wait_warp(bar(kPEarly + t), j & 1, dead);
-        if (!ok) break;
-        tc::fence_after();
+        for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
+          ok = tc::wait_warp(bar(kPFull + 2 * t + c), j & 1, dead);
+          if (!ok) break;
+          tc::fence_after();
 #pragma unroll
-        for (int k = 0; k < 2 * kEarly; ++k)
-          tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4), pv,
-                     j > 0 || k > 0);
-        ok = tc::wait_warp(bar(kPFull + t), j & 1, dead);
+          for (int i = 0; i < 4; ++i) {
+            const int k = 4 * (i >> 1) + 2 * c + (i & 1);
+            tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4), pv,
+                       j > 0 || c > 0 || i > 0);
+          }
+        }
         if (!ok) break;
-        tc::fence_after();
-#pragma unroll
-        for (int k = 2 * kEarly; k < kKeys / 16; ++k)
-          tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4), pv,
-                     true);
         tc::commit(bar(kPvDone + t));
         // the next scores go over P, which the products above read first:
         // matrix instructions of one thread run in order
@@ -368,65 +399,61 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       }
       __syncwarp();
     }
-  } else if (warp == kLoadWarp) {
-    // ---- the loads ---------------------------------------------------------------------
+  } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    // ---- the loads: one warp for K, one for V --------------------------------------------
+    const int kv = warp - kLoadWarp;
     const int page_size = 1 << p.page_shift;
     const int box = min(page_size, kKeys), pieces = kKeys / box;
+    const int head = kv * p.num_kv + kv_head;
     const int64_t head_elems = (int64_t)page_size * D;
-    int last_k = -1, last_v = -1;  // blocks whose copies were started
+    int last = -1;  // latest block whose copies were started
     bool ok = true;
-    for (int j = 0; ok && j < n; ++j) {
+    for (int j = 0; j < n; ++j) {
       const int stage = j & 1, first = key0 + j * kKeys;
-      bool whole = first + kKeys <= key1;
-      for (int i = lane; whole && i < pieces; i += 32)
-        whole = list[((first + i * box) >> p.page_shift) - page0] >= 0;
-      whole = __all_sync(kFullMask, whole);
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t full = bar((kv ? kVFull : kKFull) + stage);
-        const uint32_t dst = base + (kv ? L::kV : L::kK) + stage * L::kTile;
-        if (j >= 2) {
-          ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + stage), ((j >> 1) - 1) & 1, dead);
-          if (!ok) break;
-        }
-        if (whole) {
-          if (lane == 0) {
-            tma::mbar_arrive_expect_tx(full, L::kTile);
-            for (int i = 0; i < pieces; ++i) {
-              const int key = first + i * box;
-#pragma unroll
-              for (int b = 0; b < L::kBlocks; ++b)
-                tma::tile_load_4d(dst + b * (128 * 128) + i * box * 128, &p.map, 64 * b,
-                                  key & (page_size - 1), kv * p.num_kv + kv_head,
-                                  list[(key >> p.page_shift) - page0], full);
-            }
-          }
-          if (kv) last_v = j; else last_k = j;
-        } else {
-          constexpr int FRAGS = D / 8, RPW = 32 / FRAGS;
-#pragma unroll 4
-          for (int r = lane / FRAGS; r < kKeys; r += RPW) {
-            const int key = first + r, c = lane % FRAGS;
-            const int page = key < key1 ? list[(key >> p.page_shift) - page0] : -1;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (page >= 0)
-              v = __ldg(reinterpret_cast<const uint4*>(
-                  p.cache + ((int64_t)page * 2 * p.num_kv + kv * p.num_kv + kv_head) * head_elems +
-                  (int64_t)(key & (page_size - 1)) * D + 8 * c));
-            st_shared16(dst + tile_offset(r, c), v);
-          }
-          tma::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(full);
-        }
-        __syncwarp();
+      const uint32_t full = bar((kv ? kVFull : kKFull) + stage);
+      const uint32_t dst = base + (kv ? L::kV : L::kK) + stage * L::kTile;
+      // lane i has piece i of the block
+      const int key = first + lane * box;
+      const int page = lane < pieces && key < key1 ? list[(key >> p.page_shift) - page0] : -1;
+      const bool whole = first + kKeys <= key1 &&
+                         __all_sync(kFullMask, lane >= pieces || page >= 0);
+      if (j >= 2) {
+        ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + stage), ((j >> 1) - 1) & 1, dead);
+        if (!ok) break;
       }
+      if (whole) {
+        if (lane == 0) tma::mbar_arrive_expect_tx(full, L::kTile);
+        __syncwarp();
+        if (lane < pieces) {
+#pragma unroll
+          for (int b = 0; b < L::kBlocks; ++b)
+            tma::tile_load_4d(dst + b * (128 * 128) + lane * box * 128, &p.map, 64 * b,
+                              key & (page_size - 1), head, page, full);
+        }
+        last = j;
+      } else {
+        constexpr int FRAGS = D / 8, RPW = 32 / FRAGS;
+#pragma unroll 4
+        for (int r = lane / FRAGS; r < kKeys; r += RPW) {
+          const int k = first + r, c = lane % FRAGS;
+          const int from = k < key1 ? list[(k >> p.page_shift) - page0] : -1;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (from >= 0)
+            v = __ldg(reinterpret_cast<const uint4*>(
+                p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
+                (int64_t)(k & (page_size - 1)) * D + 8 * c));
+          st_shared16(dst + tile_offset(r, c), v);
+        }
+        tma::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(full);
+      }
+      __syncwarp();
     }
-    if (!ok) {  // let the copies in flight land before the CTA may end
-      for (uint32_t i = 0; last_k >= 0 && i < (1u << 22); ++i)
-        if (tma::mbar_test(bar(kKFull + (last_k & 1)), (last_k >> 1) & 1)) break;
-      for (uint32_t i = 0; last_v >= 0 && i < (1u << 22); ++i)
-        if (tma::mbar_test(bar(kVFull + (last_v & 1)), (last_v >> 1) & 1)) break;
+    if (!ok && last >= 0) {  // let the copies in flight land before the CTA may end
+      const uint32_t full = bar((kv ? kVFull : kKFull) + (last & 1));
+      for (uint32_t i = 0; i < (1u << 22) && !tma::mbar_test(full, (last >> 1) & 1); ++i) {
+      }
     }
   }
   __syncthreads();
