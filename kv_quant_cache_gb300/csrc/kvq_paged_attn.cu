@@ -3,11 +3,15 @@
 // own keys of each token of shared-prefix attention, and the prefix itself
 // where few rows share it.
 //
-// One CTA takes up to 16 query rows that see the same keys (the heads of one
-// kv head's group) and one part of their key range.  It first lists the
-// part's pages in shared memory ({page, valid keys}), so that no table lookup
-// stands between a page and its loads.  Then each of its warps works alone,
-// on every kWarps-th group of 16 keys, with an online softmax of its own:
+// One cluster of 1..8 CTAs takes up to 16 query rows of one kv head and the
+// pages that any of them sees, its CTAs a part each.  The rows are either the
+// heads of one token's group (block-sparse), or 16 consecutive (token, head of
+// the group) pairs: then the prefix's pages are seen by all rows and a token's
+// own pages by its rows alone, in one sweep and one softmax.  A CTA first
+// lists its part's pages in shared memory ({page, valid keys, whose}), so that
+// no table lookup stands between a page and its loads.  Then each of its warps
+// works alone, on every kWarps-th group of 16 keys, with an online softmax of
+// its own:
 //   * K and V rows of the group come in by 16-byte asynchronous copies,
 //     kStages groups deep, into a shared-memory ring that only this warp
 //     uses, so there is no CTA barrier in the loop; a 16-byte fragment c of
@@ -18,48 +22,55 @@
 //     bf16 (the row sum adds the unrounded fp32 values);
 //   * keys past a page's valid count are neither read nor weighted: their
 //     rows are filled with zeros and their scores set to -inf.
-// The warps' states are joined in shared memory at the end.  With one part
-// per row the CTA writes the output, otherwise a partial for the join kernel.
+// The warps' states are joined in shared memory, the CTAs' through the
+// cluster's shared memory (one launch, no workspace).  Only where a cluster
+// per 16 rows would leave most of the GPU idle on a long range is the range
+// split further, into partials for the join kernel.
 //
 // Bound by the reading of K and V: 16 rows of products per key row are a few
 // per cent of the tensor pipes, which is why the small matrix instruction is
 // enough here and one tile of 16 rows is as cheap as one row.
+#include <cooperative_groups.h>
+
 #include "kvq_paged_attn.cuh"
 #include "kvq_tma.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kvq {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMaxCluster = 8;
 constexpr int kRows = 16;         // query rows of a CTA
 constexpr int kGroup = 16;        // keys of one step of a warp
 constexpr int kMaxPages = 2048;   // pages a CTA can list
 
-enum KeySource { kSparse = 0, kOwn = 1, kPrefix = 2 };
+// Whose a listed page is: of all rows, or of the rows of one token of the tile.
+constexpr int kAllRows = 31;
+constexpr int kValidBits = 20;  // valid keys of a page: at most 2^16
 
 struct AttnParams {
   const __nv_bfloat16* q;
   int64_t q_stride;
   const __nv_bfloat16* cache;
   int num_q, num_kv, group;  // group = num_q / num_kv
-  int chunks;                // CTAs a group of heads takes (ceil(group / 16))
+  int tiles;                 // row tiles of a kv head (of a token and kv head: block-sparse)
   int num_tokens;
   int64_t num_pages;
   int page_size;
-  // kSparse, kOwn: the request's pages
   const int* table;
   int num_requests, table_width;
   const int* requests;
   const int* lens;
-  // kSparse
+  // block-sparse
   const int* blocks;
   int topk;
-  // kPrefix
+  // shared prefix
   const int* prefix_pages;
-  int64_t prefix_len;
-  int row_tiles;  // tiles of 16 rows of one kv head
+  int prefix_len;
   float scale_log2;
-  int splits;
+  int cluster, splits;
   int first_slot;      // partials slot of split 0
   Partials parts;      // used unless direct
   __nv_bfloat16* out;  // direct
@@ -101,6 +112,16 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Clears the values of keys outside `keep` in a V fragment: registers 0 and 2
+// hold keys 2(lane%4) and the next, registers 1 and 3 those 8 further.
+__device__ __forceinline__ void keep_keys(uint32_t b[4], uint32_t keep, int lane) {
+  const uint32_t k = keep >> (2 * (lane & 3));
+  const uint32_t lo = (k & 1 ? 0xffffu : 0u) | (k & 2 ? 0xffff0000u : 0u);
+  const uint32_t hi = (k & 0x100 ? 0xffffu : 0u) | (k & 0x200 ? 0xffff0000u : 0u);
+  b[0] &= lo, b[2] &= lo;
+  b[1] &= hi, b[3] &= hi;
+}
+
 template <int D>
 struct Shape {
   static constexpr int kStages = D == 256 ? 2 : 3;
@@ -109,111 +130,132 @@ struct Shape {
   static constexpr int kRing = kStages * kStage;      // of one warp
   static constexpr int kList = kMaxPages * 8;         // {page, valid keys}
   static constexpr int kState = kWarps * kRows * 8;   // {m, l} per warp and row
-  static constexpr int kSmem = kWarps * kRing + kList + kState;
+  static constexpr int kLse = kRows * 4;              // of the CTA's part, per row
+  static constexpr int kSmem = kWarps * kRing + kList + kState + kLse;
   static_assert(kRing >= kRows * D * 4, "a warp's output fits in its ring");
 };
 
-template <int D, int SOURCE>
+// SPARSE: the rows of one token's group and the blocks selected for them;
+// otherwise a tile of (token, head) pairs, the prefix and their own keys.
+template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParams p) {
   using S = Shape<D>;
   extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
   grid_dependency_sync(p.trigger_from);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int2* list = reinterpret_cast<int2*>(smem + kWarps * S::kRing);
   float2* state = reinterpret_cast<float2*>(smem + kWarps * S::kRing + S::kList);
+  float* part_lse = reinterpret_cast<float*>(smem + kWarps * S::kRing + S::kList + S::kState);
+  const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
+  const int unit = blockIdx.x / p.cluster;
 
-  // ---- which rows, which keys --------------------------------------------------
-  // rows of this CTA: row r is head head0 + r of token t (kSparse, kOwn), or
-  // row tile * 16 + r of the (token, head of the group) pairs (kPrefix)
-  int kv_head, t = 0, head0 = 0, rows;
-  int64_t flat0 = 0;
-  if (SOURCE == kPrefix) {
-    kv_head = blockIdx.x / p.row_tiles;
-    flat0 = (int64_t)(blockIdx.x % p.row_tiles) * kRows;
-    const int64_t left = (int64_t)p.num_tokens * p.group - flat0;
-    rows = left < kRows ? (int)left : kRows;
-  } else {
-    const int chunk = blockIdx.x % p.chunks;
-    const int tg = blockIdx.x / p.chunks;
-    kv_head = tg % p.num_kv;
-    t = tg / p.num_kv;
-    head0 = kv_head * p.group + chunk * kRows;
-    rows = min(kRows, p.group - chunk * kRows);
-  }
-  // keys of the whole range (a page or a selected block counts page_size)
-  int64_t keys;
-  int req = 0, len = 0;
-  bool rejected = false;
-  if (SOURCE == kPrefix) {
-    keys = p.prefix_len;
-  } else {
-    req = p.requests ? __ldg(p.requests + t) : t;
-    len = __ldg(p.lens + t);
-    const int64_t room = (int64_t)p.table_width * p.page_size;
-    if (req < 0 || req >= p.num_requests || len < 0 || len > room) {
-      rejected = true;
-      if (len > room) len = (int)room;
-      if (req < 0 || req >= p.num_requests || len < 0) len = 0;
-    }
-    keys = SOURCE == kSparse ? (len > 0 ? (int64_t)p.topk * p.page_size : 0) : len;
-  }
-  // this split's share, in whole pages
-  const int64_t pages = (keys + p.page_size - 1) / p.page_size;
-  const int64_t share = (pages + p.splits - 1) / p.splits;
-  const int64_t page0 = share * blockIdx.y;
-  const int listed = (int)max((int64_t)0, min(share, pages - page0));
-  for (int i = threadIdx.x; i < listed; i += kWarps * 32) {
-    int2 e = make_int2(0, 0);
-    const int64_t at = page0 + i;
-    if (SOURCE == kPrefix) {
-      e.x = __ldg(p.prefix_pages + at);
-      e.y = (int)min((int64_t)p.page_size, keys - at * p.page_size);
-    } else if (SOURCE == kOwn) {
-      e.x = __ldg(p.table + (int64_t)req * p.table_width + at);
-      e.y = (int)min((int64_t)p.page_size, keys - at * p.page_size);
-    } else {
-      const int b = __ldg(p.blocks + ((int64_t)t * p.num_kv + kv_head) * p.topk + at);
-      if (b >= 0 && (int64_t)b * p.page_size < len) {
-        e.x = __ldg(p.table + (int64_t)req * p.table_width + b);
-        e.y = min(p.page_size, len - b * p.page_size);
-      } else if (b != -1) {
-        rejected = true;
-      }
-    }
-    if (e.y > 0 && (e.x < 0 || e.x >= p.num_pages)) {
-      rejected = true;
-      e = make_int2(0, 0);
-    }
-    list[i] = e;
-  }
-  if (rejected && p.errors && (SOURCE == kPrefix || threadIdx.x < listed || threadIdx.x == 0))
-    atomicAdd(p.errors, 1);
+  // ---- which rows -----------------------------------------------------------------
+  // row r is row flat0 + r of the kv head's (token, head of the group) pairs
+  const int tile = unit % p.tiles;
+  const int per = unit / p.tiles;
+  const int kv_head = SPARSE ? per % p.num_kv : per;
+  const int64_t flat0 = SPARSE ? (int64_t)(per / p.num_kv) * p.group + tile * kRows
+                               : (int64_t)tile * kRows;
+  const int64_t flat_end = SPARSE ? (int64_t)(per / p.num_kv + 1) * p.group
+                                  : (int64_t)p.num_tokens * p.group;
+  const int rows = (int)min((int64_t)kRows, flat_end - flat0);
+  const int t0 = (int)(flat0 / p.group);  // the first row's token
+  auto row_of = [&](int r) {              // token * num_q + head
+    const int64_t t = (flat0 + r) / p.group;
+    return t * p.num_q + kv_head * p.group + (flat0 + r - t * p.group);
+  };
 
   // ---- Q fragments ---------------------------------------------------------------
   // a lane holds rows lane/4 and lane/4 + 8, dims 16k + 2(lane%4) + {0, 1, 8, 9}
   uint32_t qf[D / 16][4];
-  int64_t out_row[2];  // token * num_q + head of the lane's two rows, -1: no row
+  int64_t out_row[2];  // -1: no row
+  int mine[2];         // the row's token, less t0
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = (lane >> 2) + 8 * i;
-    out_row[i] = -1;
-    const __nv_bfloat16* src = nullptr;
-    if (r < rows) {
-      int64_t tok = t;
-      int head = head0 + r;
-      if (SOURCE == kPrefix) {
-        tok = (flat0 + r) / p.group;
-        head = kv_head * p.group + (int)(flat0 + r - tok * p.group);
-      }
-      out_row[i] = tok * p.num_q + head;
-      src = p.q + tok * p.q_stride + (int64_t)head * D + 2 * (lane & 3);
-    }
+    out_row[i] = r < rows ? row_of(r) : -1;
+    const int64_t tok = r < rows ? (flat0 + r) / p.group : t0;
+    mine[i] = r < rows ? (int)(tok - t0) : -1;
+    const __nv_bfloat16* src =
+        p.q + tok * p.q_stride + (out_row[i] - tok * p.num_q) * D + 2 * (lane & 3);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      qf[k][i] = src ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k)) : 0u;
-      qf[k][2 + i] = src ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8)) : 0u;
+      qf[k][i] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k)) : 0u;
+      qf[k][2 + i] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8)) : 0u;
     }
   }
+
+  // ---- which pages -----------------------------------------------------------------
+  // every warp: lane i has token t0 + i of the tile (block-sparse: lane 0 alone)
+  const int tokens = (int)((flat0 + rows - 1) / p.group) - t0 + 1;
+  bool rejected = false;
+  int req = 0, len = 0;
+  if (lane < tokens) {
+    req = p.requests ? __ldg(p.requests + t0 + lane) : t0 + lane;
+    len = __ldg(p.lens + t0 + lane);
+    const int64_t room = (int64_t)p.table_width * p.page_size;
+    if (req < 0 || req >= p.num_requests || len < 0) {
+      rejected = true;
+      req = len = 0;
+    } else if (len > room) {
+      rejected = true;
+      len = (int)room;
+    }
+  }
+  // pages of the lane's token, and where they end in the tile's list
+  const int own = SPARSE ? (lane == 0 && len > 0 ? p.topk : 0)
+                   : (int)(((int64_t)len + p.page_size - 1) / p.page_size);
+  int64_t end = own;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFullMask, end, o);
+    if (lane >= o) end += v;
+  }
+  const int prefix = SPARSE ? 0 : (int)(((int64_t)p.prefix_len + p.page_size - 1) / p.page_size);
+  const int64_t pages = prefix + __shfl_sync(kFullMask, end, 15);
+  const int64_t parts = (int64_t)p.cluster * p.splits;
+  const int64_t share = (pages + parts - 1) / parts;
+  const int64_t page0 = share * ((int64_t)blockIdx.y * p.cluster + rank);
+  const int listed = (int)max((int64_t)0, min(share, pages - page0));
+  for (int i0 = 0; i0 < listed; i0 += kWarps * 32) {
+    const int i = i0 + threadIdx.x;
+    const int64_t at = page0 + i - prefix;  // among the tokens' own pages
+    // the token whose pages hold `at`: the number of tokens that end before
+    int tok = 0;
+    if (!SPARSE) {
+      for (int k = 0; k + 1 < tokens; ++k) tok += at >= __shfl_sync(kFullMask, end, k);
+    }
+    const int64_t skip = __shfl_sync(kFullMask, end, max(tok - 1, 0));
+    const int r = __shfl_sync(kFullMask, req, tok), n = __shfl_sync(kFullMask, len, tok);
+    int page = 0, valid = 0, whose = kAllRows;
+    if (i < listed) {
+      if (SPARSE) {
+        const int b =
+            __ldg(p.blocks + ((int64_t)t0 * p.num_kv + kv_head) * p.topk + page0 + i);
+        if (b >= 0 && (int64_t)b * p.page_size < n) {
+          page = __ldg(p.table + (int64_t)r * p.table_width + b);
+          valid = min(p.page_size, n - b * p.page_size);
+        } else if (b != -1) {
+          rejected = true;
+        }
+      } else if (at < 0) {
+        page = __ldg(p.prefix_pages + page0 + i);
+        valid = (int)min((int64_t)p.page_size, p.prefix_len - (page0 + i) * p.page_size);
+      } else {
+        const int64_t k = at - (tok > 0 ? skip : 0);
+        page = __ldg(p.table + (int64_t)r * p.table_width + k);
+        valid = (int)min((int64_t)p.page_size, n - k * p.page_size);
+        whose = tok;
+      }
+      if (valid > 0 && (page < 0 || page >= p.num_pages)) {
+        rejected = true;
+        valid = 0;
+      }
+      list[i] = make_int2(page, valid | whose << kValidBits);
+    }
+  }
+  if (rejected && p.errors && (warp == 0 || lane >= tokens || listed > 0)) atomicAdd(p.errors, 1);
   __syncthreads();
 
   // ---- the warp's groups of keys ---------------------------------------------------
@@ -230,7 +272,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
       const int at = (k0 + lane) / p.page_size;
       const int off = k0 + lane - at * p.page_size;
       const int2 e = list[at];
-      if (off < e.y) row = ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)off * D;
+      if (off < (e.y & ((1 << kValidBits) - 1)))
+        row = ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)off * D;
     }
     const uint32_t stage = ring + (i % S::kStages) * S::kStage;
     constexpr int FRAGS = D / 8;          // 16-byte fragments of a row
@@ -260,79 +303,115 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
     issue(i + S::kStages - 1);
     cp_wait<S::kStages - 1>();
     __syncwarp();
-    // which of the step's keys exist: bit r of the warp's ballot
+    // whose the step's keys are: lane r < 16 for key r, -2 where there is none
     const int k0 = (i * kWarps + warp) * kGroup;
-    bool there = false;
+    int whose = -2;
     if (lane < kGroup && k0 + lane < total) {
       const int at = (k0 + lane) / p.page_size;
-      there = k0 + lane - at * p.page_size < list[at].y;
+      const int e = list[at].y;
+      if (k0 + lane - at * p.page_size < (e & ((1 << kValidBits) - 1))) whose = e >> kValidBits;
     }
-    const uint32_t mask = __ballot_sync(kFullMask, there);
-    if (mask == 0) {
+    uint32_t todo = __ballot_sync(kFullMask, whose != -2);
+    if (todo == 0) {
       __syncwarp();
       continue;
     }
     const uint32_t kt = ring + (i % S::kStages) * S::kStage, vt = kt + S::kTile;
-    float s[2][4] = {};
+    float raw[2][4] = {};
     {
       const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t b[4];
         ldmatrix4(b, kt + r * (2 * D) + (((2 * k + half) ^ (r & 7)) << 4));
-        mma16816(s[0], qf[k], b[0], b[1]);
-        mma16816(s[1], qf[k], b[2], b[3]);
+        mma16816(raw[0], qf[k], b[0], b[1]);
+        mma16816(raw[1], qf[k], b[2], b[3]);
       }
     }
-    // scores in units of log2: s * scale * log2(e); keys that do not exist -inf
-    float top[2] = {m[0], m[1]};
+    // one round for all keys that the same rows see: a single one but where
+    // small pages of several tokens share the step
+    const int first_seen_by = __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
+    const bool mixed = !SPARSE && __any_sync(kFullMask, whose != -2 && whose != first_seen_by);
+    while (todo) {
+      const int seen_by = SPARSE ? kAllRows : __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
+      const uint32_t mask = SPARSE ? todo : __ballot_sync(kFullMask, whose == seen_by);
+      todo &= ~mask;
+      bool sees[2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+      for (int h = 0; h < 2; ++h) sees[h] = SPARSE || seen_by == kAllRows || seen_by == mine[h];
+      // scores in units of log2: s * scale * log2(e); keys not seen -inf
+      float s[2][4];
+      float top[2] = {m[0], m[1]};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = 8 * n + 2 * (lane & 3) + (k & 1);
-        s[n][k] = (mask >> key) & 1 ? s[n][k] * p.scale_log2 : -INFINITY;
-        top[k >> 1] = fmaxf(top[k >> 1], s[n][k]);
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 8 * n + 2 * (lane & 3) + (k & 1);
+          s[n][k] = sees[k >> 1] && ((mask >> key) & 1) ? raw[n][k] * p.scale_log2 : -INFINITY;
+          top[k >> 1] = fmaxf(top[k >> 1], s[n][k]);
+        }
       }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 1));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 2));
-    }
-    if (__any_sync(kFullMask, top[0] != m[0] || top[1] != m[1])) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
-        const float f = top[h] == m[h] ? 1.f : exp2f(m[h] - top[h]);
-        l[h] *= f;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
-        m[h] = top[h];
+        top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 2));
       }
-    }
-    uint32_t pf[4];
+      if (__any_sync(kFullMask, top[0] != m[0] || top[1] != m[1])) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float e[4];
+        for (int h = 0; h < 2; ++h) {
+          // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
+          const float f = top[h] == m[h] ? 1.f : exp2f(m[h] - top[h]);
+          l[h] *= f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float ref = m[k >> 1] == -INFINITY ? 0.f : m[k >> 1];
-        e[k] = exp2f(s[n][k] - ref);
+          for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+          m[h] = top[h];
+        }
       }
-      l[0] += e[0] + e[1];
-      l[1] += e[2] + e[3];
-      pf[2 * n] = pack_bf16x2(e[0], e[1]);
-      pf[2 * n + 1] = pack_bf16x2(e[2], e[3]);
-    }
-    {
+      uint32_t pf[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float ref = m[k >> 1] == -INFINITY ? 0.f : m[k >> 1];
+          e[k] = exp2f(s[n][k] - ref);
+        }
+        l[0] += e[0] + e[1];
+        l[1] += e[2] + e[3];
+        pf[2 * n] = pack_bf16x2(e[0], e[1]);
+        pf[2 * n + 1] = pack_bf16x2(e[2], e[3]);
+      }
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+      if (SPARSE || seen_by == kAllRows) {
+        // zeros in V where there is no key, and every row sees the others
+        // (in a mixed step the others' keys have weight 0 here, but a NaN
+        // value of theirs would not stay out: they are cleared)
+        const uint32_t keep = mixed ? mask : 0xffffu;
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        uint32_t b[4];
-        ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
-        mma16816(o[2 * n], pf, b[0], b[1]);
-        mma16816(o[2 * n + 1], pf, b[2], b[3]);
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
+          if (!SPARSE && mixed) keep_keys(b, keep, lane);
+          mma16816(o[2 * n], pf, b[0], b[1]);
+          mma16816(o[2 * n + 1], pf, b[2], b[3]);
+        }
+      } else {
+        // other tokens' rows keep their sums whatever these values are (a
+        // zero weight times an infinite or NaN value would reach them)
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
+          if (mixed) keep_keys(b, mask, lane);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float x[4] = {o[2 * n + u][0], o[2 * n + u][1], o[2 * n + u][2], o[2 * n + u][3]};
+            mma16816(x, pf, b[2 * u], b[2 * u + 1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (sees[k >> 1]) o[2 * n + u][k] = x[k];
+          }
+        }
       }
     }
     __syncwarp();  // the stage is read before its next copies start
@@ -362,35 +441,69 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
       *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
-    if (!p.direct && warp == 0 && (lane & 3) == 0 && out_row[h] >= 0)
-      p.parts.lse[(int64_t)(p.first_slot + blockIdx.y) * p.parts.rows + out_row[h]] =
-          sum == 0.f ? -INFINITY : ref + log2f(sum);
+    if (warp == 0 && (lane & 3) == 0)
+      part_lse[r] = sum == 0.f ? -INFINITY : ref + log2f(sum);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-    const int r = i / (D / 4), c = 4 * (i % (D / 4));
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the CTA's part: the sum of its warps', which are scaled to one reference
+  const bool joined = p.cluster > 1;
+  const int slice = joined ? (rows * (D / 4) + p.cluster - 1) / p.cluster : rows * (D / 4);
+  float4* own_o = reinterpret_cast<float4*>(smem);
+  auto warps_sum = [&](int i) {
+    float4 v = own_o[i];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 u = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + w * S::kRing) + r * D + c);
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 u = *reinterpret_cast<const float4*>(smem + w * S::kRing + 16 * i);
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
-    int64_t tok = t;
-    int head = head0 + r;
-    if (SOURCE == kPrefix) {
-      tok = (flat0 + r) / p.group;
-      head = kv_head * p.group + (int)(flat0 + r - tok * p.group);
+    return v;
+  };
+  if (joined) {
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) own_o[i] = warps_sum(i);
+    cluster.sync();
+  }
+  // each CTA of the cluster writes a slice of the rows
+  for (int i = rank * slice + threadIdx.x; i < min((rank + 1) * slice, rows * (D / 4));
+       i += kWarps * 32) {
+    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+    float4 v;
+    float lse;
+    if (joined) {
+      float part[kMaxCluster], top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        part[k] = k < p.cluster ? cluster.map_shared_rank(part_lse, k)[r] : -INFINITY;
+        top = fmaxf(top, part[k]);
+      }
+      const float ref = top == -INFINITY ? 0.f : top;
+      v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (part[k] == -INFINITY) continue;  // a part without a key
+        const float w = exp2f(part[k] - ref);
+        const float4 u = cluster.map_shared_rank(own_o, k)[i];
+        sum += w;
+        v.x = fmaf(w, u.x, v.x), v.y = fmaf(w, u.y, v.y);
+        v.z = fmaf(w, u.z, v.z), v.w = fmaf(w, u.w, v.w);
+      }
+      const float f = sum == 0.f ? 0.f : 1.f / sum;
+      v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+      lse = sum == 0.f ? -INFINITY : ref + log2f(sum);
+    } else {
+      v = warps_sum(i);
+      lse = part_lse[r];
     }
-    const int64_t row = tok * p.num_q + head;
+    const int64_t row = row_of(r);
     if (p.direct) {
       *reinterpret_cast<uint2*>(p.out + row * D + c) =
           make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     } else {
       const int64_t slot = p.first_slot + blockIdx.y;
       *reinterpret_cast<float4*>(p.parts.o + (slot * p.parts.rows + row) * D + c) = v;
+      if (c == 0) p.parts.lse[slot * p.parts.rows + row] = lse;
     }
   }
+  if (joined) cluster.sync();  // no CTA ends while its part is being read
 }
 
 // ---- the join of the parts -------------------------------------------------------------
@@ -447,41 +560,51 @@ cudaError_t launch_join(const JoinParams& in, cudaStream_t stream) {
 
 // ---- launch ------------------------------------------------------------------------------
 
-// Parts a range of up to `pages` pages is split into when `ctas` CTAs would
-// each take a whole one: enough CTAs for two on each of the 152 SMs, none
-// with less than 4 groups of keys a warp, and none with more pages than fit
-// its list.
-int splits_for(int64_t ctas, int64_t pages, int page_size) {
-  const int64_t least = (pages + kMaxPages - 1) / kMaxPages;
-  const int64_t most = pages * page_size / (kGroup * kWarps * 4);
-  int64_t s = (2 * 152 + ctas - 1) / ctas;
-  if (s > most) s = most;
-  if (s < least) s = least;
-  if (s > pages) s = pages;
-  return s < 1 ? 1 : (int)s;
+// How a launch of `units` row tiles over up to `pages` pages each is spread.
+struct Spread {
+  int cluster, splits;
+};
+
+// CTAs are added while fewer than two of them come to an SM and each keeps at
+// least a step of 16 keys for every warp: first within a cluster of up to 8
+// (joined in place); beyond that, as partials that a second launch joins,
+// only where a CTA would be left with more than 2048 keys (below, the second
+// launch costs more than it saves).  No CTA may have more pages than fit its
+// list.
+Spread spread_for(int64_t units, int64_t pages, int page_size) {
+  Spread s = {1, 1};
+  const int64_t keys = pages * page_size;
+  while (s.cluster < kMaxCluster && units * s.cluster < 2 * 152 &&
+         keys >= (int64_t)s.cluster * 2 * kGroup * kWarps)
+    s.cluster *= 2;
+  int64_t splits = 1;
+  while (units * s.cluster * splits < 2 * 152 && keys > s.cluster * splits * 2048) ++splits;
+  const int64_t least = (pages + (int64_t)s.cluster * kMaxPages - 1) / ((int64_t)s.cluster * kMaxPages);
+  s.splits = (int)(splits > least ? splits : least);
+  return s;
 }
 
-template <int D, int SOURCE>
-cudaError_t launch_attn(AttnParams p, int64_t ctas, cudaStream_t stream) {
+template <int D, bool SPARSE>
+cudaError_t launch_attn(AttnParams p, int64_t units, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
-  const cudaError_t e = tma::prepare(paged_attn_kernel<D, SOURCE>, kWarps * 32, Shape<D>::kSmem,
-                                     cache, &per_sm);
+  cudaError_t e = tma::prepare(paged_attn_kernel<D, SPARSE>, kWarps * 32, Shape<D>::kSmem, cache,
+                               &per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t wave = (int64_t)per_sm * device_sm_count();
-  p.trigger_from = 0;
-  if (ctas > wave) p.trigger_from = (int)(ctas - wave);
-  return launch_kernel(paged_attn_kernel<D, SOURCE>, dim3((unsigned)ctas, (unsigned)p.splits),
-                       dim3(kWarps * 32), Shape<D>::kSmem, stream, p);
+  const int64_t ctas = units * p.cluster, wave = (int64_t)per_sm * device_sm_count();
+  p.trigger_from = ctas > wave ? (int)(ctas - wave) : 0;
+  return launch_clusters(paged_attn_kernel<D, SPARSE>,
+                         dim3((unsigned)ctas, (unsigned)p.splits), dim3(kWarps * 32),
+                         Shape<D>::kSmem, p.cluster, stream, p);
 }
 
-template <int SOURCE>
-cudaError_t launch_attn_dim(const AttnParams& p, int head_dim, int64_t ctas,
+template <bool SPARSE>
+cudaError_t launch_attn_dim(const AttnParams& p, int head_dim, int64_t units,
                             cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_attn<64, SOURCE>(p, ctas, stream);
-    case 128: return launch_attn<128, SOURCE>(p, ctas, stream);
-    case 256: return launch_attn<256, SOURCE>(p, ctas, stream);
+    case 64: return launch_attn<64, SPARSE>(p, units, stream);
+    case 128: return launch_attn<128, SPARSE>(p, units, stream);
+    case 256: return launch_attn<256, SPARSE>(p, units, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -494,7 +617,6 @@ AttnParams common(const PagedQuery& x, const void* kv_cache, float scale) {
   p.num_q = x.num_heads_q;
   p.num_kv = x.num_heads_kv;
   p.group = x.num_heads_q / x.num_heads_kv;
-  p.chunks = (p.group + kRows - 1) / kRows;
   p.num_tokens = x.num_tokens;
   p.num_pages = x.num_pages;
   p.page_size = x.page_size;
@@ -508,26 +630,26 @@ AttnParams common(const PagedQuery& x, const void* kv_cache, float scale) {
   return p;
 }
 
-int64_t own_ctas(int64_t num_tokens, int num_q, int num_kv) {
-  const int group = num_q / num_kv;
-  return num_tokens * num_kv * ((group + kRows - 1) / kRows);
-}
+// Row tiles: block-sparse, of a token and kv head; shared prefix, of a kv head.
+int sparse_tiles(int num_q, int num_kv) { return (num_q / num_kv + kRows - 1) / kRows; }
 
-int64_t prefix_tiles(int64_t num_tokens, int num_q, int num_kv) {
+int64_t shared_tiles(int64_t num_tokens, int num_q, int num_kv) {
   return (num_tokens * (num_q / num_kv) + kRows - 1) / kRows;
 }
 
-// Parts of the prefix on the small matrix instruction, and of the tokens' own
-// keys (0: there are none).
-int prefix_slots(int64_t num_tokens, int num_q, int num_kv, int page_size, int64_t prefix_len) {
-  if (prefix_len == 0) return 0;
-  return splits_for(prefix_tiles(num_tokens, num_q, num_kv) * num_kv,
-                    (prefix_len + page_size - 1) / page_size, page_size);
+Spread sparse_spread(int64_t num_tokens, int num_q, int num_kv, int page_size, int topk) {
+  return spread_for(num_tokens * num_kv * sparse_tiles(num_q, num_kv), topk, page_size);
 }
 
-int own_slots(int64_t num_tokens, int num_q, int num_kv, int page_size, int table_width) {
-  if (table_width == 0) return 0;
-  return splits_for(own_ctas(num_tokens, num_q, num_kv), table_width, page_size);
+// The tokens' own keys, with the prefix's or without.  The own pages that a
+// tile can have: those of every token that has a row in it.
+Spread shared_spread(int64_t num_tokens, int num_q, int num_kv, int page_size,
+                     int64_t prefix_len, int table_width) {
+  const int group = num_q / num_kv;
+  const int64_t tokens = group >= kRows ? 2 : (kRows + group - 2) / group + 1;
+  const int64_t own = (tokens < num_tokens ? tokens : num_tokens) * table_width;
+  return spread_for(shared_tiles(num_tokens, num_q, num_kv) * num_kv,
+                    (prefix_len + page_size - 1) / page_size + own, page_size);
 }
 
 }  // namespace
@@ -549,7 +671,7 @@ cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, voi
 
 int64_t sparse_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int topk) {
-  const int s = splits_for(own_ctas(num_tokens, num_heads_q, num_heads_kv), topk, page_size);
+  const int s = sparse_spread(num_tokens, num_heads_q, num_heads_kv, page_size, topk).splits;
   return s == 1 ? 0 : partials_bytes(s, num_tokens * num_heads_q, head_dim);
 }
 
@@ -558,67 +680,74 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
   AttnParams p = common(x, a.kv_cache, a.scale);
   p.blocks = a.blocks;
   p.topk = a.topk;
-  const int64_t ctas = own_ctas(x.num_tokens, x.num_heads_q, x.num_heads_kv);
-  p.splits = splits_for(ctas, a.topk, x.page_size);
-  p.direct = p.splits == 1;
+  p.tiles = sparse_tiles(x.num_heads_q, x.num_heads_kv);
+  const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size, a.topk);
+  p.cluster = s.cluster;
+  p.splits = s.splits;
+  p.direct = s.splits == 1;
   p.out = static_cast<__nv_bfloat16*>(a.out);
-  const int64_t rows = (int64_t)x.num_tokens * x.num_heads_q;
-  if (!p.direct) p.parts = partials_at(a.workspace, p.splits, rows, x.head_dim);
-  const cudaError_t e = launch_attn_dim<kSparse>(p, x.head_dim, ctas, stream);
+  if (!p.direct)
+    p.parts = partials_at(a.workspace, s.splits, (int64_t)x.num_tokens * x.num_heads_q, x.head_dim);
+  const cudaError_t e = launch_attn_dim<true>(
+      p, x.head_dim, (int64_t)x.num_tokens * x.num_heads_kv * p.tiles, stream);
   if (e != cudaSuccess || p.direct) return e;
-  return launch_attn_join(p.parts, p.splits, x.head_dim, a.out, stream);
+  return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
 }
 
 int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int64_t prefix_len,
                               int table_width) {
-  const int64_t slots =
-      prefix_slots(num_tokens, num_heads_q, num_heads_kv, page_size, prefix_len);
-  int64_t tiles = 0;
-  if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len))
-    tiles = prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size,
-                              prefix_len).parts;
-  // either kernel may run: which one depends on where the cache lies
-  return partials_bytes((slots > tiles ? slots : tiles) +
-                            own_slots(num_tokens, num_heads_q, num_heads_kv, page_size,
-                                      table_width),
-                        num_tokens * num_heads_q, head_dim);
+  const int64_t rows = num_tokens * num_heads_q;
+  const int s = shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, prefix_len,
+                              table_width).splits;
+  int64_t slots = s == 1 ? 0 : s;
+  if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len)) {
+    // either way may be taken: which one depends on where the cache lies
+    const int64_t both = prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, head_dim,
+                                           page_size, prefix_len).parts +
+                         shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, 0,
+                                       table_width).splits;
+    if (both > slots) slots = both;
+  }
+  return partials_bytes(slots, rows, head_dim);
 }
 
 cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   const PagedQuery& x = a.x;
   AttnParams p = common(x, a.kv_cache, a.scale);
+  p.tiles = (int)shared_tiles(x.num_tokens, x.num_heads_q, x.num_heads_kv);
   p.prefix_pages = a.prefix_pages;
-  p.prefix_len = a.prefix_len;
   const int64_t rows = (int64_t)x.num_tokens * x.num_heads_q;
+  const int64_t units = (int64_t)p.tiles * x.num_heads_kv;
   CUtensorMap map;
   const bool tiles = prefix_tiles_fit(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
                                       x.page_size, a.prefix_len) &&
                      prefix_tiles_map(a, &map);
-  const int s1 = tiles ? prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv,
-                                           x.head_dim, x.page_size, a.prefix_len).parts
-                       : prefix_slots(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
-                                      a.prefix_len);
-  const int s2 = own_slots(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
-                           x.table_width);
-  p.parts = partials_at(a.workspace, s1 + s2, rows, x.head_dim);
-  cudaError_t e = cudaSuccess;
-  if (tiles) {
-    e = launch_prefix_tiles(a, map, p.parts, stream);
-  } else if (s1) {
-    p.row_tiles = (int)prefix_tiles(x.num_tokens, x.num_heads_q, x.num_heads_kv);
-    p.splits = s1;
-    p.first_slot = 0;
-    e = launch_attn_dim<kPrefix>(p, x.head_dim, (int64_t)p.row_tiles * x.num_heads_kv, stream);
+  p.prefix_len = tiles ? 0 : (int)a.prefix_len;
+  const Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
+                                 p.prefix_len, x.table_width);
+  p.cluster = s.cluster;
+  p.splits = s.splits;
+  if (!tiles) {
+    p.direct = s.splits == 1;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    if (!p.direct) p.parts = partials_at(a.workspace, s.splits, rows, x.head_dim);
+    const cudaError_t e = launch_attn_dim<false>(p, x.head_dim, units, stream);
+    if (e != cudaSuccess || p.direct) return e;
+    return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
   }
-  if (e == cudaSuccess && s2) {
-    p.splits = s2;
-    p.first_slot = s1;
-    e = launch_attn_dim<kOwn>(p, x.head_dim, own_ctas(x.num_tokens, x.num_heads_q, x.num_heads_kv),
-                              stream);
+  const int pre = prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
+                                    x.page_size, a.prefix_len).parts;
+  const int own = x.table_width > 0 ? s.splits : 0;
+  p.parts = partials_at(a.workspace, pre + own, rows, x.head_dim);
+  cudaError_t e = launch_prefix_tiles(a, map, p.parts, stream);
+  if (e == cudaSuccess && own) {
+    p.direct = false;
+    p.first_slot = pre;
+    e = launch_attn_dim<false>(p, x.head_dim, units, stream);
   }
   if (e != cudaSuccess) return e;
-  return launch_attn_join(p.parts, s1 + s2, x.head_dim, a.out, stream);
+  return launch_attn_join(p.parts, pre + own, x.head_dim, a.out, stream);
 }
 
 }  // namespace kvq

@@ -408,7 +408,7 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
   // one opt-in for the largest size that the validation lets through
-  cudaError_t e = tma::prepare(block_select_kernel<D>, kThreads, smem_bytes<D>(kMaxSelectBlocks),
+  const cudaError_t e = tma::prepare(block_select_kernel<D>, kThreads, smem_bytes<D>(kMaxSelectBlocks),
                                cache, &per_sm);
   if (e != cudaSuccess) return e;
   SelectParams p;
@@ -431,21 +431,8 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   p.errors = x.errors;
   const int64_t items = (int64_t)x.num_tokens * x.num_heads_kv;
   p.cluster = cluster_for(items, x.table_width);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * p.cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<D>(x.table_width);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)p.cluster, 1, 1};
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = programmatic_launch() ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, block_select_kernel<D>, p);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
+  return launch_clusters(block_select_kernel<D>, dim3((unsigned)(items * p.cluster)),
+                         dim3(kThreads), smem_bytes<D>(x.table_width), p.cluster, stream, p);
 }
 
 }  // namespace

@@ -412,6 +412,34 @@ def test_prefix_attention_large_scores_and_nonfinite_values(cuda_device):
     ref.check(got[ok], want[ok], tol[ok])
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,page,q_len,prefix", [
+    (9, 4, 4, 16, 1, 40), (6, 8, 2, 64, 2, 0), (16, 1, 1, 1, 1, 5), (12, 6, 2, 5, 3, 33),
+    (40, 8, 1, 16, 1, 300), (50, 3, 1, 8, 2, 129)])
+def test_nonfinite_values_stay_with_their_request(cuda_device, T, Hq, Hkv, page, q_len, prefix):
+    """Requests share a CTA's rows; NaN and infinite keys and values of one
+    reach no row of another."""
+    g = gen(T + page)
+    D, width, R, P = 64, -(-40 // page), -(-T // q_len), -(-prefix // page)
+    q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, R, width, extra=P + 1)
+    requests = (torch.arange(T) // q_len).int()
+    lens = ints(g, 1, width * page, T)
+    args = (spare[:P].int().cuda(), prefix, table.cuda(), lens.cuda())
+    bad = R // 2
+    spoiled = cache.clone()
+    spoiled[table[bad].long(), 0, :, :, 3] = NAN
+    spoiled[table[bad].long(), 1, :, :, 5] = math.inf
+    spoiled[table[bad].long(), 1, :, :, 6] = NAN
+    a = kvq.paged_shared_prefix_attention(q.cuda(), cache.cuda(), *args,
+                                          requests=requests.cuda()).cpu()
+    b = kvq.paged_shared_prefix_attention(q.cuda(), spoiled.cuda(), *args,
+                                          requests=requests.cuda()).cpu()
+    ok = requests != bad
+    assert torch.equal(bits(a[ok]), bits(b[ok]))
+    assert bool(b[~ok].isnan().all())  # NaN scores: every output of these rows
+    want, tol = ref.prefix_attention(q, cache, spare[:P], prefix, table, lens, D ** -0.5, requests)
+    ref.check(a, want, tol)
+
+
 def test_attention_of_a_strided_query_and_given_buffers(cuda_device):
     g = gen(43)
     T, Hq, Hkv, D, page, width, prefix = 5, 8, 2, 128, 16, 20, 100
