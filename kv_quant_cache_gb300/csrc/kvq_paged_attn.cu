@@ -59,6 +59,7 @@ struct AttnParams {
   int num_tokens;
   int64_t num_pages;
   int page_size;
+  int page_shift;            // log2 of page_size, -1: not a power of two
   const int* table;
   int num_requests, table_width;
   const int* requests;
@@ -122,9 +123,12 @@ __device__ __forceinline__ void keep_keys(uint32_t b[4], uint32_t keep, int lane
   b[1] &= hi, b[3] &= hi;
 }
 
+// How many 16-key groups or rows fit, and where they lie.
 template <int D>
 struct Shape {
   static constexpr int kStages = D == 256 ? 2 : 3;
+  static constexpr int kPad = D + 8;                  // fp32 values of an output row: rows
+                                                      // 32 bytes apart in the banks
   static constexpr int kTile = kGroup * D * 2;        // bytes of 16 K (or V) rows
   static constexpr int kStage = 2 * kTile;            // K, then V
   static constexpr int kRing = kStages * kStage;      // of one warp
@@ -132,12 +136,13 @@ struct Shape {
   static constexpr int kState = kWarps * kRows * 8;   // {m, l} per warp and row
   static constexpr int kLse = kRows * 4;              // of the CTA's part, per row
   static constexpr int kSmem = kWarps * kRing + kList + kState + kLse;
-  static_assert(kRing >= kRows * D * 4, "a warp's output fits in its ring");
+  static_assert(kRing >= kRows * kPad * 4, "a warp's output fits in its ring");
 };
 
 // SPARSE: the rows of one token's group and the blocks selected for them;
 // otherwise a tile of (token, head) pairs, the prefix and their own keys.
-template <int D, bool SPARSE>
+// WHOLE: page_size is a multiple of 16, so a group of keys lies in one page.
+template <int D, bool SPARSE, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParams p) {
   using S = Shape<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -152,33 +157,43 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
 
   // ---- which rows -----------------------------------------------------------------
   // row r is row flat0 + r of the kv head's (token, head of the group) pairs
-  const int tile = unit % p.tiles;
-  const int per = unit / p.tiles;
+  const uint32_t group = p.group;
+  const int tile = unit % p.tiles, per = unit / p.tiles;
   const int kv_head = SPARSE ? per % p.num_kv : per;
-  const int64_t flat0 = SPARSE ? (int64_t)(per / p.num_kv) * p.group + tile * kRows
-                               : (int64_t)tile * kRows;
-  const int64_t flat_end = SPARSE ? (int64_t)(per / p.num_kv + 1) * p.group
-                                  : (int64_t)p.num_tokens * p.group;
-  const int rows = (int)min((int64_t)kRows, flat_end - flat0);
-  const int t0 = (int)(flat0 / p.group);  // the first row's token
-  auto row_of = [&](int r) {              // token * num_q + head
-    const int64_t t = (flat0 + r) / p.group;
-    return t * p.num_q + kv_head * p.group + (flat0 + r - t * p.group);
+  const uint32_t flat0 = SPARSE ? (uint32_t)(per / p.num_kv) * group + tile * kRows
+                                : (uint32_t)tile * kRows;
+  const uint32_t flat_end = SPARSE ? (uint32_t)(per / p.num_kv + 1) * group
+                                   : (uint32_t)p.num_tokens * group;
+  const int rows = (int)min((uint32_t)kRows, flat_end - flat0);
+  const int t0 = SPARSE ? per / p.num_kv : (int)(flat0 / group);  // the first row's token
+  const int in0 = (int)(flat0 - (uint32_t)t0 * group);            // and its place in the group
+  // row r's token, less t0 (block-sparse: one token), and its output row
+  auto token_of = [&](int r) { return SPARSE ? 0 : (int)((uint32_t)(in0 + r) / group); };
+  auto row_of = [&](int r) {  // token * num_q + head
+    const int u = token_of(r);
+    return (int64_t)(t0 + u) * p.num_q + kv_head * (int)group + (in0 + r - u * (int)group);
   };
+
+  // ---- whose pages: lane i has token t0 + i of the tile --------------------------------
+  const int tokens = token_of(rows - 1) + 1;
+  int req = 0, len = 0;
+  if (lane < tokens) {
+    req = p.requests ? __ldg(p.requests + t0 + lane) : t0 + lane;
+    len = __ldg(p.lens + t0 + lane);
+  }
 
   // ---- Q fragments ---------------------------------------------------------------
   // a lane holds rows lane/4 and lane/4 + 8, dims 16k + 2(lane%4) + {0, 1, 8, 9}
   uint32_t qf[D / 16][4];
-  int64_t out_row[2];  // -1: no row
-  int mine[2];         // the row's token, less t0
+  int mine[2];  // the row's token, less t0; -1: no row
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = (lane >> 2) + 8 * i;
-    out_row[i] = r < rows ? row_of(r) : -1;
-    const int64_t tok = r < rows ? (flat0 + r) / p.group : t0;
-    mine[i] = r < rows ? (int)(tok - t0) : -1;
+    const int u = token_of(r);
+    mine[i] = r < rows ? u : -1;
     const __nv_bfloat16* src =
-        p.q + tok * p.q_stride + (out_row[i] - tok * p.num_q) * D + 2 * (lane & 3);
+        p.q + (int64_t)(t0 + u) * p.q_stride +
+        (int64_t)(kv_head * (int)group + in0 + r - u * (int)group) * D + 2 * (lane & 3);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       qf[k][i] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k)) : 0u;
@@ -187,15 +202,17 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
   }
 
   // ---- which pages -----------------------------------------------------------------
-  // every warp: lane i has token t0 + i of the tile (block-sparse: lane 0 alone)
-  const int tokens = (int)((flat0 + rows - 1) / p.group) - t0 + 1;
+  // a page index and a place in it (the quotient fits 32 bits: checked at launch)
+  const uint32_t page_size = p.page_size;
+  const int shift = p.page_shift;
+  auto pages_of = [&](uint32_t keys) {  // pages that hold `keys` keys
+    const uint32_t up = keys + page_size - 1;
+    return (int)(shift >= 0 ? up >> shift : up / page_size);
+  };
   bool rejected = false;
-  int req = 0, len = 0;
-  if (lane < tokens) {
-    req = p.requests ? __ldg(p.requests + t0 + lane) : t0 + lane;
-    len = __ldg(p.lens + t0 + lane);
+  {
     const int64_t room = (int64_t)p.table_width * p.page_size;
-    if (req < 0 || req >= p.num_requests || len < 0) {
+    if (lane < tokens && (req < 0 || req >= p.num_requests || len < 0)) {
       rejected = true;
       req = len = 0;
     } else if (len > room) {
@@ -204,35 +221,36 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
     }
   }
   // pages of the lane's token, and where they end in the tile's list
-  const int own = SPARSE ? (lane == 0 && len > 0 ? p.topk : 0)
-                   : (int)(((int64_t)len + p.page_size - 1) / p.page_size);
-  int64_t end = own;
+  int end = SPARSE ? (lane == 0 && len > 0 ? p.topk : 0) : pages_of(len);
+  if (!SPARSE) {
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
-    const int64_t v = __shfl_up_sync(kFullMask, end, o);
-    if (lane >= o) end += v;
+    for (int o = 1; o < 16; o <<= 1) {
+      const int v = __shfl_up_sync(kFullMask, end, o);
+      if (lane >= o) end += v;
+    }
   }
-  const int prefix = SPARSE ? 0 : (int)(((int64_t)p.prefix_len + p.page_size - 1) / p.page_size);
-  const int64_t pages = prefix + __shfl_sync(kFullMask, end, 15);
-  const int64_t parts = (int64_t)p.cluster * p.splits;
-  const int64_t share = (pages + parts - 1) / parts;
-  const int64_t page0 = share * ((int64_t)blockIdx.y * p.cluster + rank);
-  const int listed = (int)max((int64_t)0, min(share, pages - page0));
+  const int prefix = SPARSE ? 0 : pages_of(p.prefix_len);
+  const int pages = prefix + __shfl_sync(kFullMask, end, SPARSE ? 0 : 15);
+  const int parts = p.cluster * p.splits;
+  const int share = parts == 1 ? pages : (int)(((uint32_t)pages + parts - 1) / (uint32_t)parts);
+  const int64_t begin = (int64_t)share * (blockIdx.y * p.cluster + rank);
+  const int page0 = (int)min(begin, (int64_t)pages);
+  const int listed = min(share, pages - page0);
   for (int i0 = 0; i0 < listed; i0 += kWarps * 32) {
     const int i = i0 + threadIdx.x;
-    const int64_t at = page0 + i - prefix;  // among the tokens' own pages
+    const int at = page0 + i - prefix;  // among the tokens' own pages
     // the token whose pages hold `at`: the number of tokens that end before
-    int tok = 0;
+    int tok = 0, skip = 0;
     if (!SPARSE) {
       for (int k = 0; k + 1 < tokens; ++k) tok += at >= __shfl_sync(kFullMask, end, k);
+      skip = __shfl_sync(kFullMask, end, max(tok - 1, 0));
+      if (tok == 0) skip = 0;
     }
-    const int64_t skip = __shfl_sync(kFullMask, end, max(tok - 1, 0));
     const int r = __shfl_sync(kFullMask, req, tok), n = __shfl_sync(kFullMask, len, tok);
     int page = 0, valid = 0, whose = kAllRows;
     if (i < listed) {
       if (SPARSE) {
-        const int b =
-            __ldg(p.blocks + ((int64_t)t0 * p.num_kv + kv_head) * p.topk + page0 + i);
+        const int b = __ldg(p.blocks + ((int64_t)t0 * p.num_kv + kv_head) * p.topk + page0 + i);
         if (b >= 0 && (int64_t)b * p.page_size < n) {
           page = __ldg(p.table + (int64_t)r * p.table_width + b);
           valid = min(p.page_size, n - b * p.page_size);
@@ -241,11 +259,11 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
         }
       } else if (at < 0) {
         page = __ldg(p.prefix_pages + page0 + i);
-        valid = (int)min((int64_t)p.page_size, p.prefix_len - (page0 + i) * p.page_size);
+        valid = (int)min((int64_t)p.page_size,
+                         p.prefix_len - (int64_t)(page0 + i) * p.page_size);
       } else {
-        const int64_t k = at - (tok > 0 ? skip : 0);
-        page = __ldg(p.table + (int64_t)r * p.table_width + k);
-        valid = (int)min((int64_t)p.page_size, n - k * p.page_size);
+        page = __ldg(p.table + (int64_t)r * p.table_width + (at - skip));
+        valid = (int)min((int64_t)p.page_size, n - (int64_t)(at - skip) * p.page_size);
         whose = tok;
       }
       if (valid > 0 && (page < 0 || page >= p.num_pages)) {
@@ -259,33 +277,60 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
   __syncthreads();
 
   // ---- the warp's groups of keys ---------------------------------------------------
-  const int total = listed * p.page_size;  // at most kMaxPages * page_size: checked at launch
-  const int steps = (total + kGroup * kWarps - 1) / (kGroup * kWarps);
+  const uint32_t total = (uint32_t)listed * page_size;  // below 2^31: checked at launch
+  const int steps = (int)((total + kGroup * kWarps - 1) / (kGroup * kWarps));
   const uint32_t ring = tma::smem_addr(smem) + warp * S::kRing;
   const int64_t head_elems = (int64_t)p.page_size * D;
+  const int64_t v_from_k = p.num_kv * head_elems;
+  auto entry_of = [&](uint32_t key, int* off) {
+    const uint32_t at = shift >= 0 ? key >> shift : key / page_size;
+    *off = (int)(key - at * page_size);
+    return list[at];
+  };
 
-  // Starts the copies of step i's 16 keys: lane r < 16 finds row r's place.
+  // Starts the copies of step i's 16 keys.
   auto issue = [&](int i) {
-    const int k0 = (i * kWarps + warp) * kGroup;
-    int64_t row = -1;
-    if (lane < kGroup && i < steps && k0 + lane < total) {
-      const int at = (k0 + lane) / p.page_size;
-      const int off = k0 + lane - at * p.page_size;
-      const int2 e = list[at];
-      if (off < (e.y & ((1 << kValidBits) - 1)))
-        row = ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)off * D;
-    }
+    const uint32_t k0 = (uint32_t)(i * kWarps + warp) * kGroup;
     const uint32_t stage = ring + (i % S::kStages) * S::kStage;
-    constexpr int FRAGS = D / 8;          // 16-byte fragments of a row
+    constexpr int FRAGS = D / 8;                          // 16-byte fragments of a row
     constexpr int RPI = 32 / FRAGS > 0 ? 32 / FRAGS : 1;  // rows of one warp-wide copy
+    const int r0 = lane / FRAGS, c = lane % FRAGS;
+    if (WHOLE) {
+      int there = 0;  // keys of the group that exist
+      const __nv_bfloat16* src = p.cache + 8 * c;
+      if (i < steps && k0 < total) {
+        int off;
+        const int2 e = entry_of(k0, &off);
+        there = (e.y & ((1 << kValidBits) - 1)) - off;
+        if (there > 0)
+          src += ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)(off + r0) * D;
+      }
 #pragma unroll
-    for (int j = 0; j < kGroup / RPI; ++j) {
-      const int r = j * RPI + lane / FRAGS, c = lane % FRAGS;
-      const int64_t from = __shfl_sync(kFullMask, row, r);
-      const __nv_bfloat16* src = p.cache + (from < 0 ? 0 : from) + 8 * c;
-      const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
-      cp_async16(dst, src, from >= 0);
-      cp_async16(dst + S::kTile, src + (from < 0 ? 0 : p.num_kv * head_elems), from >= 0);
+      for (int j = 0; j < kGroup / RPI; ++j) {
+        const int r = j * RPI + r0;
+        const bool ok = r < there;
+        const __nv_bfloat16* from = ok ? src + j * RPI * D : p.cache;
+        const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
+        cp_async16(dst, from, ok);
+        cp_async16(dst + S::kTile, ok ? from + v_from_k : from, ok);
+      }
+    } else {
+      int64_t row = -1;  // lane r < 16 finds row r's place
+      if (lane < kGroup && i < steps && k0 + lane < total) {
+        int off;
+        const int2 e = entry_of(k0 + lane, &off);
+        if (off < (e.y & ((1 << kValidBits) - 1)))
+          row = ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)off * D;
+      }
+#pragma unroll
+      for (int j = 0; j < kGroup / RPI; ++j) {
+        const int r = j * RPI + r0;
+        const int64_t from = __shfl_sync(kFullMask, row, r);
+        const __nv_bfloat16* src = p.cache + (from < 0 ? 0 : from + 8 * c);
+        const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
+        cp_async16(dst, src, from >= 0);
+        cp_async16(dst + S::kTile, from >= 0 ? src + v_from_k : src, from >= 0);
+      }
     }
     cp_commit();
   };
@@ -304,14 +349,26 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
     cp_wait<S::kStages - 1>();
     __syncwarp();
     // whose the step's keys are: lane r < 16 for key r, -2 where there is none
-    const int k0 = (i * kWarps + warp) * kGroup;
+    const uint32_t k0 = (uint32_t)(i * kWarps + warp) * kGroup;
     int whose = -2;
-    if (lane < kGroup && k0 + lane < total) {
-      const int at = (k0 + lane) / p.page_size;
-      const int e = list[at].y;
-      if (k0 + lane - at * p.page_size < (e & ((1 << kValidBits) - 1))) whose = e >> kValidBits;
+    uint32_t todo;  // the keys that exist
+    if (WHOLE) {
+      int there = 0;
+      if (k0 < total) {
+        int off;
+        const int e = entry_of(k0, &off).y;
+        there = (e & ((1 << kValidBits) - 1)) - off;
+        whose = e >> kValidBits;
+      }
+      todo = there >= kGroup ? 0xffffu : there > 0 ? (1u << there) - 1u : 0u;
+    } else {
+      if (lane < kGroup && k0 + lane < total) {
+        int off;
+        const int e = entry_of(k0 + lane, &off).y;
+        if (off < (e & ((1 << kValidBits) - 1))) whose = e >> kValidBits;
+      }
+      todo = __ballot_sync(kFullMask, whose != -2);
     }
-    uint32_t todo = __ballot_sync(kFullMask, whose != -2);
     if (todo == 0) {
       __syncwarp();
       continue;
@@ -330,11 +387,14 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
     }
     // one round for all keys that the same rows see: a single one but where
     // small pages of several tokens share the step
-    const int first_seen_by = __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
-    const bool mixed = !SPARSE && __any_sync(kFullMask, whose != -2 && whose != first_seen_by);
+    constexpr bool kMayMix = !SPARSE && !WHOLE;
+    const int first_seen_by = kMayMix ? __shfl_sync(kFullMask, whose, __ffs(todo) - 1) : 0;
+    const bool mixed =
+        kMayMix && __any_sync(kFullMask, whose != -2 && whose != first_seen_by);
     while (todo) {
-      const int seen_by = SPARSE ? kAllRows : __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
-      const uint32_t mask = SPARSE ? todo : __ballot_sync(kFullMask, whose == seen_by);
+      const int seen_by = SPARSE ? kAllRows
+                          : WHOLE ? whose : __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
+      const uint32_t mask = kMayMix ? __ballot_sync(kFullMask, whose == seen_by) : todo;
       todo &= ~mask;
       bool sees[2];
 #pragma unroll
@@ -391,7 +451,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
         for (int n = 0; n < D / 16; ++n) {
           uint32_t b[4];
           ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
-          if (!SPARSE && mixed) keep_keys(b, keep, lane);
+          if (kMayMix && mixed) keep_keys(b, keep, lane);
           mma16816(o[2 * n], pf, b[0], b[1]);
           mma16816(o[2 * n + 1], pf, b[2], b[3]);
         }
@@ -402,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
         for (int n = 0; n < D / 16; ++n) {
           uint32_t b[4];
           ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
-          if (mixed) keep_keys(b, mask, lane);
+          if (kMayMix && mixed) keep_keys(b, mask, lane);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             float x[4] = {o[2 * n + u][0], o[2 * n + u][1], o[2 * n + u][2], o[2 * n + u][3]};
@@ -437,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
     for (int w = 0; w < kWarps; ++w)
       sum += state[w * kRows + r].y * exp2f(state[w * kRows + r].x - ref);
     const float f = sum == 0.f ? 0.f : exp2f(m[h] - ref) / sum;  // 0: the row has no key
-    float* dst = reinterpret_cast<float*>(smem + warp * S::kRing) + r * D + 2 * (lane & 3);
+    float* dst = reinterpret_cast<float*>(smem + warp * S::kRing) + r * S::kPad + 2 * (lane & 3);
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
       *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
@@ -447,32 +507,43 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
   __syncthreads();
   // the CTA's part: the sum of its warps', which are scaled to one reference
   const bool joined = p.cluster > 1;
-  const int slice = joined ? (rows * (D / 4) + p.cluster - 1) / p.cluster : rows * (D / 4);
-  float4* own_o = reinterpret_cast<float4*>(smem);
-  auto warps_sum = [&](int i) {
-    float4 v = own_o[i];
+  float* own_o = reinterpret_cast<float*>(smem);
+  auto warps_sum = [&](int at) {
+    float4 v = *reinterpret_cast<const float4*>(own_o + at);
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-      const float4 u = *reinterpret_cast<const float4*>(smem + w * S::kRing + 16 * i);
+      const float4 u = *reinterpret_cast<const float4*>(smem + w * S::kRing + 4 * at);
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
     return v;
   };
+  const int all = rows * (D / 4);  // 16-byte pieces of the rows
   if (joined) {
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) own_o[i] = warps_sum(i);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < all; i += kWarps * 32) {
+      const int at = i / (D / 4) * S::kPad + 4 * (i % (D / 4));
+      *reinterpret_cast<float4*>(own_o + at) = warps_sum(at);
+    }
     cluster.sync();
   }
   // each CTA of the cluster writes a slice of the rows
-  for (int i = rank * slice + threadIdx.x; i < min((rank + 1) * slice, rows * (D / 4));
-       i += kWarps * 32) {
-    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+  const int slice = joined ? (all + p.cluster - 1) / p.cluster : all;
+  const int last = min((rank + 1) * slice, all);
+#pragma unroll 2
+  for (int i = rank * slice + threadIdx.x; i < last; i += kWarps * 32) {
+    const int r = i / (D / 4), c = 4 * (i % (D / 4)), at = r * S::kPad + c;
     float4 v;
     float lse;
     if (joined) {
       float part[kMaxCluster], top = -INFINITY, sum = 0.f;
+      float4 u[kMaxCluster];
 #pragma unroll
       for (int k = 0; k < kMaxCluster; ++k) {
-        part[k] = k < p.cluster ? cluster.map_shared_rank(part_lse, k)[r] : -INFINITY;
+        part[k] = -INFINITY;
+        if (k < p.cluster) {
+          part[k] = cluster.map_shared_rank(part_lse, k)[r];
+          u[k] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(own_o, k) + at);
+        }
         top = fmaxf(top, part[k]);
       }
       const float ref = top == -INFINITY ? 0.f : top;
@@ -481,16 +552,15 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
       for (int k = 0; k < kMaxCluster; ++k) {
         if (part[k] == -INFINITY) continue;  // a part without a key
         const float w = exp2f(part[k] - ref);
-        const float4 u = cluster.map_shared_rank(own_o, k)[i];
         sum += w;
-        v.x = fmaf(w, u.x, v.x), v.y = fmaf(w, u.y, v.y);
-        v.z = fmaf(w, u.z, v.z), v.w = fmaf(w, u.w, v.w);
+        v.x = fmaf(w, u[k].x, v.x), v.y = fmaf(w, u[k].y, v.y);
+        v.z = fmaf(w, u[k].z, v.z), v.w = fmaf(w, u[k].w, v.w);
       }
       const float f = sum == 0.f ? 0.f : 1.f / sum;
       v.x *= f, v.y *= f, v.z *= f, v.w *= f;
       lse = sum == 0.f ? -INFINITY : ref + log2f(sum);
     } else {
-      v = warps_sum(i);
+      v = warps_sum(at);
       lse = part_lse[r];
     }
     const int64_t row = row_of(r);
@@ -565,46 +635,53 @@ struct Spread {
   int cluster, splits;
 };
 
-// CTAs are added while fewer than two of them come to an SM and each keeps at
-// least a step of 16 keys for every warp: first within a cluster of up to 8
-// (joined in place); beyond that, as partials that a second launch joins,
+// CTAs are added while all of them are resident at once (two to an SM; with
+// half as many again in a second wave the same range took 20-30 % longer) and
+// each keeps at least two steps of 16 keys for every warp: first within a
+// cluster of up to 8 (joined in place); beyond that, as partials that a second launch joins,
 // only where a CTA would be left with more than 2048 keys (below, the second
 // launch costs more than it saves).  No CTA may have more pages than fit its
 // list.
 Spread spread_for(int64_t units, int64_t pages, int page_size) {
   Spread s = {1, 1};
   const int64_t keys = pages * page_size;
-  while (s.cluster < kMaxCluster && units * s.cluster < 2 * 152 &&
+  while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 2 * 152 &&
          keys >= (int64_t)s.cluster * 2 * kGroup * kWarps)
     s.cluster *= 2;
   int64_t splits = 1;
-  while (units * s.cluster * splits < 2 * 152 && keys > s.cluster * splits * 2048) ++splits;
+  while (units * s.cluster * (splits + 1) <= 2 * 152 && keys > s.cluster * splits * 2048) ++splits;
   const int64_t least = (pages + (int64_t)s.cluster * kMaxPages - 1) / ((int64_t)s.cluster * kMaxPages);
   s.splits = (int)(splits > least ? splits : least);
   return s;
 }
 
-template <int D, bool SPARSE>
+template <int D, bool SPARSE, bool WHOLE>
 cudaError_t launch_attn(AttnParams p, int64_t units, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
-  cudaError_t e = tma::prepare(paged_attn_kernel<D, SPARSE>, kWarps * 32, Shape<D>::kSmem, cache,
-                               &per_sm);
+  const cudaError_t e = tma::prepare(paged_attn_kernel<D, SPARSE, WHOLE>, kWarps * 32, Shape<D>::kSmem,
+                                     cache, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t ctas = units * p.cluster, wave = (int64_t)per_sm * device_sm_count();
   p.trigger_from = ctas > wave ? (int)(ctas - wave) : 0;
-  return launch_clusters(paged_attn_kernel<D, SPARSE>,
+  return launch_clusters(paged_attn_kernel<D, SPARSE, WHOLE>,
                          dim3((unsigned)ctas, (unsigned)p.splits), dim3(kWarps * 32),
                          Shape<D>::kSmem, p.cluster, stream, p);
+}
+
+template <int D, bool SPARSE>
+cudaError_t launch_attn_page(const AttnParams& p, int64_t units, cudaStream_t stream) {
+  return p.page_size % kGroup == 0 ? launch_attn<D, SPARSE, true>(p, units, stream)
+                                   : launch_attn<D, SPARSE, false>(p, units, stream);
 }
 
 template <bool SPARSE>
 cudaError_t launch_attn_dim(const AttnParams& p, int head_dim, int64_t units,
                             cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_attn<64, SPARSE>(p, units, stream);
-    case 128: return launch_attn<128, SPARSE>(p, units, stream);
-    case 256: return launch_attn<256, SPARSE>(p, units, stream);
+    case 64: return launch_attn_page<64, SPARSE>(p, units, stream);
+    case 128: return launch_attn_page<128, SPARSE>(p, units, stream);
+    case 256: return launch_attn_page<256, SPARSE>(p, units, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -620,6 +697,9 @@ AttnParams common(const PagedQuery& x, const void* kv_cache, float scale) {
   p.num_tokens = x.num_tokens;
   p.num_pages = x.num_pages;
   p.page_size = x.page_size;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (x.page_size == 1 << s) p.page_shift = s;
   p.table = x.page_table;
   p.num_requests = x.num_requests;
   p.table_width = x.table_width;
