@@ -10,9 +10,13 @@
 // group's sums are taken once, so a block costs 2 D products whatever the
 // group's size: bound by reading the bounds once.
 //
-// One cluster of 1..8 CTAs per (token, kv head) (more CTAs where few tokens
-// would leave SMs idle).  Every CTA scores a share of the blocks in fp32 and
-// writes the scores into the first CTA's shared memory; that CTA selects.
+// One cluster of 1..8 CTAs takes a token and one or several of its kv heads.
+// Its CTAs score a share of the blocks each, warps side by side on the heads:
+// a page's heads lie next to each other, and read together they are one
+// contiguous stretch (64 tokens x 8 heads x 1024 blocks, heads apart: 78 us,
+// 3.9 TB/s while scoring; 512-byte pieces at random do not keep the memory
+// busy).  The fp32 scores go into the shared memory of the CTA that selects
+// for their head.
 //
 // Which block is k-th must not depend on fp32 rounding: the set a token
 // attends to is an integer result.  The scoring warps carry the largest
@@ -25,6 +29,7 @@
 #include <cooperative_groups.h>
 
 #include "kvq_device.cuh"
+#include "kvq_mma.cuh"
 #include "kvq_paged.h"
 #include "kvq_tma.cuh"
 
@@ -51,7 +56,9 @@ struct SelectParams {
   int topk, keep_first, keep_last;
   int* blocks;
   int* errors;
-  int cluster;
+  int cluster;     // CTAs of a cluster
+  int heads;       // kv heads of a cluster, at most `cluster`
+  int head_groups; // clusters of a token
 };
 
 // Order-preserving keys: a larger score has a larger key; NaN (and a page
@@ -71,87 +78,208 @@ __device__ __forceinline__ uint64_t key64(double s) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
+constexpr int kBins = 2048;
+constexpr int kFew = kThreads;  // candidates that are ranked against each other directly
+
 // Shared memory of a CTA (the selecting one uses all of it).
 template <int D>
 struct Shared {
-  float up[D], down[D];
-  double up64[D], down64[D];
+  double up64[D], down64[D];  // of the head this CTA selects for
+  // of every scoring warp: its error bound, its smallest and largest key (of
+  // blocks that are not kept anyway)
   float err[kMaxCluster * kWarps];
-  unsigned hist[256];
-  unsigned warp_a[kWarps], warp_b[kWarps];
-  unsigned long long pick;
-  unsigned place;
+  uint32_t least[kMaxCluster * kWarps], most[kMaxCluster * kWarps];
+  unsigned hist[kBins];
+  int few[kFew];  // candidates by index
+  unsigned warp_sum[kWarps];
+  unsigned count;
+  unsigned pick, place, bin_count;
+  unsigned long long kth64;
 };
 
-// The `place`-th largest (1 = largest) of the keys that `get(i, &key)` gives
-// for i < n, found one byte at a time from the top; *equal becomes how many
-// of the keys equal to it belong to the `place` largest.  All threads call.
+// While scoring, the place of the fp64 keys has the query sums (down, then up,
+// as a block's bounds are lo, then hi) of the cluster's heads in three bf16
+// parts, and their sizes rounded up.
+template <int D>
+struct QueryParts {
+  __nv_bfloat16 part[kWarps][4][2 * D];
+};
+
+// Inclusive prefix sum over the CTA of one value a thread; *total: all of it.
+template <typename Sh>
+__device__ unsigned block_scan(unsigned v, Sh& sh, unsigned* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned u = __shfl_up_sync(kFullMask, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) sh.warp_sum[warp] = v;
+  __syncthreads();
+  unsigned sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) v += sum;
+    sum += sh.warp_sum[w];
+  }
+  *total = sum;
+  __syncthreads();
+  return v;
+}
+
+// Finds the bin that holds the `place`-th largest key (1 = largest) from the
+// counts in sh.hist: sh.pick the bin, sh.place its place within the bin,
+// sh.bin_count the bin's keys.  All threads call, after a barrier.
+template <typename Sh>
+__device__ void find_bin(unsigned place, Sh& sh) {
+  constexpr int PER = kBins / kThreads;
+  const int first = kBins - 1 - PER * (int)threadIdx.x;  // this thread's highest bin
+  unsigned c[PER], sum = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) c[j] = sh.hist[first - j], sum += c[j];
+  unsigned total;
+  unsigned above = block_scan(sum, sh, &total) - sum;
+  if (above < place && place <= above + sum) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (above < place && place <= above + c[j]) {
+        sh.pick = first - j;
+        sh.place = place - above;
+        sh.bin_count = c[j];
+      }
+      above += c[j];
+    }
+  }
+  __syncthreads();
+}
+
+// The `place`-th largest of the keys that `get(i, &key)` gives for i < n (all
+// keys between lo and hi); *equal becomes how many of the keys equal to it
+// belong to the `place` largest.  One linear split of [lo, hi] into bins
+// usually leaves a few candidates, which are ranked directly; otherwise the
+// bin's own range is split again (each time by 2^11).  All threads call.
 template <typename Key, typename Get, typename Sh>
-__device__ Key radix_select(int n, unsigned place, Sh& sh, const Get& get, unsigned* equal) {
-  Key prefix = 0;
+__device__ Key select_largest(int n, unsigned place, Key lo, Key hi, Sh& sh, const Get& get,
+                              unsigned* equal) {
   const int tid = threadIdx.x;
-  for (int shift = (int)sizeof(Key) * 8 - 8; shift >= 0; shift -= 8) {
-    for (int b = tid; b < 256; b += kThreads) sh.hist[b] = 0;
+  while (true) {
+    int shift = 0;
+    while (((hi - lo) >> shift) >= (Key)kBins) ++shift;
+    for (int b = tid; b < kBins; b += kThreads) sh.hist[b] = 0;
+    if (tid == 0) sh.count = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
       Key k;
-      if (!get(i, &k)) continue;
-      const bool same = shift + 8 >= (int)sizeof(Key) * 8 || (k >> (shift + 8)) == (prefix >> (shift + 8));
-      if (same) atomicAdd(&sh.hist[(unsigned)(k >> shift) & 255u], 1u);
+      if (get(i, &k) && k >= lo && k <= hi) atomicAdd(&sh.hist[(unsigned)((k - lo) >> shift)], 1u);
     }
     __syncthreads();
-    if (tid < 32) {
-      // lane l owns bins 255 - 8l .. 248 - 8l: counts from the top
-      unsigned c[8], sum = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = sh.hist[255 - 8 * tid - j], sum += c[j];
-      unsigned above = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned v = __shfl_up_sync(kFullMask, above, o);
-        if (tid >= o) above += v;
+    find_bin(place, sh);
+    place = sh.place;
+    lo += (Key)sh.pick << shift;
+    const Key last = lo + (((Key)1 << shift) - 1);
+    if (last < hi) hi = last;
+    const unsigned c = sh.bin_count;
+    if (shift == 0 || lo == hi) {  // one value is left
+      *equal = place;
+      __syncthreads();
+      return lo;
+    }
+    if (c <= (unsigned)kFew) {
+      for (int i = tid; i < n; i += kThreads) {
+        Key k;
+        if (get(i, &k) && k >= lo && k <= hi) sh.few[atomicAdd(&sh.count, 1u)] = i;
       }
-      above -= sum;  // keys in higher bins than this lane's
-      if (above < place && place <= above + sum) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (above < place && place <= above + c[j]) {
-            sh.pick = 255 - 8 * tid - j;
-            sh.place = place - above;
-          }
-          above += c[j];
+      __syncthreads();
+      if (tid < (int)c) {
+        Key mine, other;
+        get(sh.few[tid], &mine);
+        unsigned larger = 0, same = 0;
+        for (unsigned j = 0; j < c; ++j) {
+          get(sh.few[j], &other);
+          larger += other > mine;
+          same += other == mine;
+        }
+        if (larger < place && place <= larger + same) {  // every such thread writes the same
+          sh.kth64 = (unsigned long long)mine;
+          sh.place = place - larger;
         }
       }
+      __syncthreads();
+      const Key k = (Key)sh.kth64;
+      *equal = sh.place;
+      __syncthreads();
+      return k;
     }
     __syncthreads();
-    prefix |= (Key)sh.pick << shift;
-    place = sh.place;
-    __syncthreads();
   }
-  *equal = place;
-  return prefix;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) block_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
   // scores of the first CTA: fp32 keys, then fp64 keys, one of each per block
   uint32_t* keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Shared<D>) + 15) & ~size_t(15)));
   unsigned long long* wide =
-      reinterpret_cast<unsigned long long*>(keys + ((p.table_width + 1) & ~1));
+      reinterpret_cast<unsigned long long*>(keys + ((p.table_width + 3) & ~3));
+  QueryParts<D>& queries_in = *reinterpret_cast<QueryParts<D>*>(wide);
   cg::cluster_group cluster = cg::this_cluster();
+  if (p.cluster > 1) cluster.barrier_arrive();
   grid_dependency_sync(0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = p.cluster > 1 ? (int)cluster.block_rank() : 0;
-  const int64_t tg = blockIdx.x / p.cluster;
-  const int64_t t = tg / p.num_kv;
-  const int h = (int)(tg - t * p.num_kv);
-  int* out = p.blocks + tg * p.topk;
+  const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
+  const uint32_t unit = blockIdx.x / p.cluster;
+  const int t = unit / (uint32_t)p.head_groups;
+  const int h0 = (int)(unit - (uint32_t)t * p.head_groups) * p.heads;
+  const int heads = min(p.heads, p.num_kv - h0);
+  const bool selects = rank < heads;  // for head h0 + rank
+  const int h = h0 + (selects ? rank : 0);
+  int* out = p.blocks + ((int64_t)t * p.num_kv + h) * p.topk;
 
-  // ---- the token's blocks ---------------------------------------------------------
-  int req = p.requests ? __ldg(p.requests + t) : (int)t;
+  // ---- the token's blocks, and the groups' query sums -----------------------------
+  int req = p.requests ? __ldg(p.requests + t) : t;
   int len = __ldg(p.lens + t);
+  const __nv_bfloat16* queries = p.q + t * p.q_stride + (int64_t)h0 * p.group * D;
+  bool any_weight = false;
+  for (int i = tid; i < heads * (D / 2); i += kThreads) {  // two dims of a head
+    const int head = i / (D / 2), d = 2 * (i % (D / 2));
+    const __nv_bfloat16* q = queries + (int64_t)head * p.group * D + d;
+    float sums[2][2] = {};  // down, up
+    for (int g0 = 0; g0 < p.group; g0 += 8) {  // eight loads in flight
+      uint32_t v[8];
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        v[g] = g0 + g < p.group
+                   ? __ldg(reinterpret_cast<const uint32_t*>(q + (int64_t)(g0 + g) * D))
+                   : 0u;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float f[2] = {__uint_as_float(v[g] << 16), __uint_as_float(v[g] & 0xffff0000u)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // a NaN stays one
+          sums[0][k] += f[k] < 0.f ? f[k] : f[k] == f[k] ? 0.f : f[k];
+          sums[1][k] += f[k] > 0.f ? f[k] : f[k] == f[k] ? 0.f : f[k];
+        }
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float a = sums[half][0], b = sums[half][1];
+      any_weight |= a != 0.f || b != 0.f;
+      uint32_t* to = reinterpret_cast<uint32_t*>(&queries_in.part[head][0][half * D + d]);
+      constexpr int COLUMN = D;  // 4-byte words of one part
+      const uint32_t hi = pack_bf16x2(a, b);
+      const float a1 = a - __uint_as_float(hi << 16), b1 = b - __uint_as_float(hi & 0xffff0000u);
+      const uint32_t mid = pack_bf16x2(a1, b1);
+      to[0] = hi;
+      to[COLUMN] = mid;
+      to[2 * COLUMN] =
+          pack_bf16x2(a1 - __uint_as_float(mid << 16), b1 - __uint_as_float(mid & 0xffff0000u));
+      const __nv_bfloat162 size = __halves2bfloat162(__float2bfloat16_ru(fabsf(a)),
+                                                     __float2bfloat16_ru(fabsf(b)));
+      to[3 * COLUMN] = *reinterpret_cast<const uint32_t*>(&size);
+    }
+  }
   const int64_t room = (int64_t)p.table_width * p.page_size;
   bool rejected = false;
   if (req < 0 || req >= p.num_requests || len < 0) {
@@ -163,115 +291,158 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
     len = (int)room;
   }
   if (rejected && p.errors && rank == 0 && tid == 0) atomicAdd(p.errors, 1);
-  const int n = (int)(((int64_t)len + p.page_size - 1) / p.page_size);
+  const int n = (int)(((uint32_t)len + (uint32_t)p.page_size - 1) / (uint32_t)p.page_size);
   if (n <= p.topk) {  // all of them: no score decides anything (cluster-uniform)
-    if (rank == 0)
+    if (selects)
       for (int i = tid; i < p.topk; i += kThreads) out[i] = i < n ? i : -1;
+    if (p.cluster > 1) cluster.barrier_wait();
     return;
   }
-
-  // ---- the group's query sums ------------------------------------------------------
-  for (int d = tid; d < D; d += kThreads) {
-    double up = 0., down = 0.;
-    const __nv_bfloat16* q = p.q + t * p.q_stride + (int64_t)h * p.group * D + d;
-    for (int g = 0; g < p.group; ++g) {
-      const float v = __bfloat162float(q[(int64_t)g * D]);
-      up += v > 0.f ? v : v == v ? 0.f : v;  // a NaN stays one
-      down += v < 0.f ? v : v == v ? 0.f : v;
-    }
-    sh.up64[d] = up, sh.down64[d] = down;
-    sh.up[d] = (float)up, sh.down[d] = (float)down;
-  }
-  __syncthreads();
-  // the selecting CTA's shared memory has to exist before scores go there
-  if (p.cluster > 1) cluster.sync();
+  // of any of the cluster's heads: zero queries have zero scores, exactly
+  any_weight = __syncthreads_or(any_weight);
 
   // ---- scores ------------------------------------------------------------------------
-  // A block's bounds are 2 D contiguous values (lo, then hi): lane l of a
-  // block's LPB lanes takes values 8l.. of each run of 8 LPB.
-  constexpr int LPB = D / 4 < 32 ? D / 4 : 32;
-  constexpr int VECS = 2 * D / (8 * LPB);
-  constexpr int BPW = 32 / LPB;  // blocks of one warp step
-  constexpr int UNROLL = 4;
-  uint32_t* to_keys = p.cluster > 1 ? cluster.map_shared_rank(keys, 0) : keys;
-  float* to_err = p.cluster > 1 ? cluster.map_shared_rank(sh.err, 0) : sh.err;
-  const int bl = lane % LPB;
-  float w[VECS][8];
+  // A warp takes 16 blocks at a time, as the 16 rows of the small matrix
+  // instruction: 2 D / 16 steps of bounds (row major, 8 lanes apart a row)
+  // against three columns that hold the query sums, split into three bf16
+  // parts.  Products of bf16 values are exact; four accumulators keep the
+  // running sums, and with them the rounding, small.  A second product, with
+  // the signs dropped, and a fourth column give each block's sum of
+  // |products|.  Lane l holds
+  // values 8(l%4).. of every 32 of rows l/4 and l/4 + 8: the order of the
+  // inner dimension does not matter as long as both operands have it.
+  // (As fp32 multiply-adds by 32 lanes a block this took 82 instructions a
+  // block and was bound by them and by too few loads in flight: 64 tokens x 8
+  // heads x 1024 blocks 77 us.)
+  constexpr int STEPS = 2 * D / 32;  // of 32 values: two matrix instructions
+  const int subs = kWarps / heads;              // warps of the CTA per head
+  const int mine = warp % heads, sub = warp / heads;  // this warp's head; sub == subs: idle
+  const bool scores = sub < subs;
+  uint32_t* to_keys = p.cluster > 1 ? cluster.map_shared_rank(keys, mine) : keys;
+  const int g = lane >> 2, c = lane & 3;
+  uint4 wb[STEPS];  // column g: a part of the query sums (0-2), their sizes (3), nothing
 #pragma unroll
-  for (int v = 0; v < VECS; ++v) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int at = 8 * (v * LPB + bl) + k;
-      w[v][k] = at < D ? sh.down[at] : sh.up[at - D];
-    }
-  }
+  for (int k = 0; k < STEPS; ++k)
+    wb[k] = g < 4 ? *reinterpret_cast<const uint4*>(&queries_in.part[mine][g & 3][32 * k + 8 * c])
+                  : make_uint4(0, 0, 0, 0);
   const int* row = p.table + (int64_t)req * p.table_width;
-  const int64_t head_elems = 2 * D;
-  float worst = 0.f;  // of this lane: the largest sum of |products| it saw
+  const __nv_bfloat16* bounds = p.bounds + (int64_t)(h0 + mine) * 2 * D + 8 * c;
+  const int64_t page_elems = (int64_t)p.num_kv * 2 * D;
+  float worst = 0.f;  // the largest sum of |products| seen
   bool odd = false;
-  const int per_step = BPW * UNROLL;
-  for (int j0 = (rank * kWarps + warp) * per_step; j0 < n; j0 += p.cluster * kWarps * per_step) {
-    uint4 x[UNROLL][VECS];
-    bool fine[UNROLL];
+  uint32_t least = 0xffffffffu, most = 0;
+  const int first = scores ? (rank * subs + sub) * 16 : n, stride = p.cluster * subs * 16;
+  int next[2];  // the pages of rows g and g + 8 of the coming blocks
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int j = j0 + u * BPW + lane / LPB;
-      const int page = j < n ? __ldg(row + j) : -1;
-      fine[u] = page >= 0 && page < p.num_pages;
-      if (j < n && !fine[u] && p.errors && bl == 0) atomicAdd(p.errors, 1);
-      const __nv_bfloat16* src =
-          p.bounds + ((int64_t)(fine[u] ? page : 0) * p.num_kv + h) * head_elems + 8 * bl;
+  for (int r = 0; r < 2; ++r) next[r] = first + g + 8 * r < n ? __ldg(row + first + g + 8 * r) : -1;
+  // the selecting CTA's shared memory has to exist before scores go there
+  if (p.cluster > 1) cluster.barrier_wait();
+  for (int j0 = first; j0 < n; j0 += stride) {
+    int page[2];
+    uint4 x[STEPS][2];
 #pragma unroll
-      for (int v = 0; v < VECS; ++v)
-        x[u][v] = fine[u] ? __ldg(reinterpret_cast<const uint4*>(src + 8 * LPB * v))
-                          : make_uint4(0, 0, 0, 0);
+    for (int r = 0; r < 2; ++r) {
+      const int j = j0 + g + 8 * r;
+      page[r] = next[r];
+      next[r] = j + stride < n ? __ldg(row + j + stride) : -1;
+      if (page[r] < 0 || page[r] >= p.num_pages) {
+        if (j < n && p.errors && mine == 0 && c == 0) atomicAdd(p.errors, 1);
+        page[r] = -1;
+      }
     }
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      float s = 0.f, a = 0.f;
+    for (int r = 0; r < 2; ++r) {
+      const __nv_bfloat16* src = bounds + (int64_t)max(page[r], 0) * page_elems;
 #pragma unroll
-      for (int v = 0; v < VECS; ++v) {
-        float b[8];
-        unpack_bf16x8(x[u][v], b);
+      for (int k = 0; k < STEPS; ++k)
+        x[k][r] = page[r] >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 32 * k))
+                               : make_uint4(0, 0, 0, 0);
+    }
+    float acc[4][4] = {}, size[4] = {};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s = fmaf(w[v][k], b[k], s);
-          a = fmaf(fabsf(w[v][k]), fabsf(b[k]), a);
+    for (int k = 0; k < STEPS; ++k) {
+      const uint32_t a0[4] = {x[k][0].x, x[k][1].x, x[k][0].y, x[k][1].y};
+      const uint32_t a1[4] = {x[k][0].z, x[k][1].z, x[k][0].w, x[k][1].w};
+      uint32_t b0[4], b1[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b0[i] = a0[i] & 0x7fff7fffu, b1[i] = a1[i] & 0x7fff7fffu;
+      mma16816(acc[(2 * k) & 3], a0, wb[k].x, wb[k].y);
+      mma16816(acc[(2 * k + 1) & 3], a1, wb[k].z, wb[k].w);
+      mma16816(size, b0, wb[k].x, wb[k].y);
+      mma16816(size, b1, wb[k].z, wb[k].w);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      // columns 0 and 1 are with c == 0, 2 and 3 with c == 1
+      const float left = (acc[0][2 * r] + acc[1][2 * r]) + (acc[2][2 * r] + acc[3][2 * r]);
+      const float second =
+          (acc[0][2 * r + 1] + acc[1][2 * r + 1]) + (acc[2][2 * r + 1] + acc[3][2 * r + 1]);
+      const float upper = __shfl_up_sync(kFullMask, left + second, 1);
+      const int j = j0 + g + 8 * r;
+      if (c == 1 && j < n) {
+        const float s = upper + left, total = size[2 * r + 1];
+        odd |= !(total <= 3.0e38f);  // infinite or NaN: fp32 says nothing
+        worst = fmaxf(worst, total);
+        const bool keep = j < p.keep_first || j >= n - p.keep_last;
+        const uint32_t k = keep ? kKeep32 : page[r] >= 0 ? key32(s) : key32(-INFINITY);
+        to_keys[j] = k;
+        if (!keep) {
+          least = min(least, k);
+          most = max(most, k);
         }
       }
-      odd |= !(a <= 3.0e38f);  // infinite or NaN: fp32 says nothing
-      worst = fmaxf(worst, a);
-      s = group_sum<LPB>(s);
-      const int j = j0 + u * BPW + lane / LPB;
-      if (bl == 0 && j < n) {
-        const bool keep = j < p.keep_first || j >= n - p.keep_last;
-        to_keys[j] = keep ? kKeep32 : fine[u] ? key32(s) : key32(-INFINITY);
-      }
     }
   }
-  // sum over the lanes of their largest: at least every block's sum.  The
-  // fp32 score takes at most 8 VECS + 5 additions and one rounding of the
-  // query sums on any path, so it is off by less than 32 * 2^-24 of it (and
-  // by a few steps of the smallest binary32 where products underflow).
-  worst = group_sum<LPB>(worst);
-  worst = BPW > 1 ? fmaxf(worst, __shfl_xor_sync(kFullMask, worst, 16)) : worst;
-  odd = __any_sync(kFullMask, odd || !(worst <= 3.0e38f));
-  if (lane == 0)
-    to_err[rank * kWarps + warp] =
-        odd ? INFINITY : worst > 0.f ? worst * (32.f / 16777216.f) + 1.0e-42f : 0.f;
+  // A fp32 score's error, as a share of the sum of |products| S: a matrix
+  // instruction adds 16 exact products to a sum of at most S/4 (each of four
+  // accumulators has a quarter of the steps); even if every one of them were
+  // cut off at 2^-24 of that sum, the 2 D / 16 steps (at most 32) would lose
+  // less than 32 * 16 * 2^-24 / 8 = 2^-18 S; taken twice over, and `group`
+  // roundings of the query sums and a few of the final sums besides (and
+  // products may underflow).
+  worst = group_max<32>(worst);
+  odd = __any_sync(kFullMask, odd);
+  least = __reduce_min_sync(kFullMask, least);
+  most = __reduce_max_sync(kFullMask, most);
+  if (lane == 0 && scores) {
+    Shared<D>& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, mine) : sh;
+    const int at = rank * subs + sub;
+    const float bound = 0x1p-17f + (float)(8 + p.group) * 0x1p-24f;
+    to.err[at] = odd ? INFINITY : any_weight ? worst * bound + 1.0e-35f : 0.f;
+    to.least[at] = least;
+    to.most[at] = most;
+  }
   if (p.cluster > 1) {
-    cluster.sync();  // every score has arrived; no CTA is needed any longer but the first
-    if (rank != 0) return;
+    cluster.sync();  // every score has arrived, and no CTA reads another's memory any longer
+    if (!selects) return;
   } else {
     __syncthreads();
   }
 
   // ---- the k-th largest, its doubtful neighbours ---------------------------------------
   float E = 0.f;
-  for (int i = 0; i < p.cluster * kWarps; ++i) E = fmaxf(E, sh.err[i]);
+  least = 0xffffffffu;
+  most = 0;
+  for (int i = lane; i < p.cluster * subs; i += 32) {
+    E = fmaxf(E, sh.err[i]);
+    least = min(least, sh.least[i]);
+    most = max(most, sh.most[i]);
+  }
+  E = group_max<32>(E);
+  least = __reduce_min_sync(kFullMask, least);
+  most = __reduce_max_sync(kFullMask, most);
   unsigned ties;
-  const uint32_t kth = radix_select<uint32_t>(
-      n, (unsigned)p.topk, sh, [&](int i, uint32_t* k) { *k = keys[i]; return true; }, &ties);
+  // the kept blocks are selected anyway; the others compete for what is left
+  const int kept = min(n, min(n, p.keep_first) + min(n, p.keep_last));
+  uint32_t kth;
+  if (kept >= p.topk) {
+    kth = kKeep32;
+    ties = p.topk;
+  } else {
+    kth = select_largest<uint32_t>(
+        n, (unsigned)(p.topk - kept), least, most, sh,
+        [&](int i, uint32_t* k) { *k = keys[i]; return *k != kKeep32; }, &ties);
+  }
   // keys from `in` up are selected, below `maybe` are not
   uint32_t in = kth, maybe = kth;
   if (kth != kKeep32 && E > 0.f) {
@@ -286,120 +457,150 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
       maybe = key32(down) - 2u;
     }
   }
+  // a thread's blocks from here on: `each` consecutive ones
+  const int each = (n + kThreads - 1) / kThreads;
+  const int mine0 = min(n, tid * each), mine1 = min(n, mine0 + each);
   unsigned places = ties;  // places left for the keys in [maybe, in)
   bool exact = in == maybe;
+  const bool only_ties = exact;  // equal fp32 scores are equal scores: no product was other
+                                 // than zero, or only kept blocks compete
+  unsigned long long kth64 = 0;
+  unsigned total;
   if (!exact) {
     unsigned above = 0, between = 0;
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-      const int i = i0 + tid;
-      const uint32_t k = i < n ? keys[i] : 0u;
-      above += i < n && k >= in;
-      between += i < n && k < in && k >= maybe;
+    if (tid == 0) sh.count = 0;
+    for (int i = mine0; i < mine1; ++i) {
+      above += keys[i] >= in;
+      between += keys[i] < in && keys[i] >= maybe;
     }
-    above = __reduce_add_sync(kFullMask, above);
-    between = __reduce_add_sync(kFullMask, between);
-    if (lane == 0) sh.warp_a[warp] = above, sh.warp_b[warp] = between;
-    __syncthreads();
-    above = between = 0;
-    for (int i = 0; i < kWarps; ++i) above += sh.warp_a[i], between += sh.warp_b[i];
-    __syncthreads();
-    places = (unsigned)p.topk - above;
-    if (between == places) {
+    block_scan(above | between << 16, sh, &total);  // at most 16384 each
+    places = (unsigned)p.topk - (total & 0xffffu);
+    const unsigned doubtful = total >> 16;
+    if (doubtful == places) {
       in = maybe;  // all of them
-      places = 0;
       exact = true;
-    }
-  } else {
-    // equal fp32 scores are equal scores: no product was other than zero, or
-    // only kept blocks compete; `ties` of the blocks at kth, lowest first
-  }
-  unsigned long long kth64 = 0;
-  unsigned ties64 = 0;
-  const bool only_ties = exact && places > 0;
-  if (!exact) {
-    // the doubtful ones again, one per warp, in fp64 and in one fixed order
-    for (int i = warp; i < n; i += kWarps) {
-      if (!(keys[i] < in && keys[i] >= maybe)) continue;
-      const int page = __ldg(row + i);
-      double s = 0.;
-      if (page >= 0 && page < p.num_pages) {
-        const __nv_bfloat16* b = p.bounds + ((int64_t)page * p.num_kv + h) * head_elems;
-        for (int d = lane; d < D; d += 32) {
-          s = fma(sh.down64[d], (double)__bfloat162float(b[d]), s);
-          s = fma(sh.up64[d], (double)__bfloat162float(b[D + d]), s);
+    } else {
+      // the doubtful ones again, one per warp, in fp64 and in one fixed order
+      for (int d = tid; d < D; d += kThreads) {
+        double up = 0., down = 0.;
+        const __nv_bfloat16* q = queries + (int64_t)(h - h0) * p.group * D + d;
+        for (int g = 0; g < p.group; ++g) {
+          const float v = __bfloat162float(q[(int64_t)g * D]);
+          up += v > 0.f ? v : v == v ? 0.f : v;
+          down += v < 0.f ? v : v == v ? 0.f : v;
         }
-      } else {
-        s = -(double)INFINITY;
+        sh.up64[d] = up, sh.down64[d] = down;
       }
+      const bool few = doubtful <= (unsigned)kFew;
+      if (few) {
+        for (int i = mine0; i < mine1; ++i)
+          if (keys[i] < in && keys[i] >= maybe) sh.few[atomicAdd(&sh.count, 1u)] = i;
+      }
+      __syncthreads();
+      for (int c = warp; c < (few ? (int)doubtful : n); c += kWarps) {
+        const int i = few ? sh.few[c] : c;
+        if (!few && !(keys[i] < in && keys[i] >= maybe)) continue;
+        const int page = __ldg(row + i);
+        double s = 0.;
+        if (page >= 0 && page < p.num_pages) {
+          const __nv_bfloat16* b = p.bounds + page * page_elems + (int64_t)h * 2 * D;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-      if (lane == 0) wide[i] = key64(s);
+          for (int d = 0; d < D; d += 32) {
+            s = fma(sh.down64[d + lane], (double)__bfloat162float(b[d + lane]), s);
+            s = fma(sh.up64[d + lane], (double)__bfloat162float(b[D + d + lane]), s);
+          }
+        } else {
+          s = -(double)INFINITY;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+        if (lane == 0) wide[i] = key64(s);
+      }
+      __syncthreads();
+      if (few) {
+        // each against the others: larger first, then the lower index; the
+        // places go to the first of them
+        bool sel = false;
+        int i = 0;
+        if (tid < (int)doubtful) {
+          i = sh.few[tid];
+          unsigned ahead = 0;
+          for (unsigned c = 0; c < doubtful; ++c) {
+            const int k = sh.few[c];
+            ahead += wide[k] > wide[i] || (wide[k] == wide[i] && k < i);
+          }
+          sel = ahead < places;
+        }
+        __syncthreads();
+        if (tid < (int)doubtful) keys[i] = sel ? kKeep32 : 0u;
+        __syncthreads();
+        exact = true;
+      } else {
+        kth64 = select_largest<unsigned long long>(
+            n, places, 0ull, ~0ull, sh,
+            [&](int i, unsigned long long* k) {
+              if (!(keys[i] < in && keys[i] >= maybe)) return false;
+              *k = wide[i];
+              return true;
+            },
+            &places);
+      }
     }
-    __syncthreads();
-    kth64 = radix_select<unsigned long long>(
-        n, places, sh,
-        [&](int i, unsigned long long* k) {
-          if (!(keys[i] < in && keys[i] >= maybe)) return false;
-          *k = wide[i];
-          return true;
-        },
-        &ties64);
   }
 
   // ---- the selected blocks, ascending -----------------------------------------------------
-  const unsigned ties_to_take = exact ? places : ties64;
-  unsigned taken = 0, tied = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    bool sure = false, tie = false;
-    if (i < n) {
-      const uint32_t k = keys[i];
-      if (exact) {
-        sure = only_ties ? k > kth : k >= in;
-        tie = only_ties && k == kth;
-      } else {
-        sure = k >= in;
-        if (!sure && k >= maybe) {
-          sure = wide[i] > kth64;
-          tie = wide[i] == kth64;
-        }
-      }
+  // `places` of the ties are selected, the lowest indices.  A thread keeps
+  // which of its blocks (at most 64) are in, and which are ties, in two words.
+  const uint64_t from = only_ties ? (uint64_t)kth + 1 : in;
+  uint64_t sures = 0, tied = 0;
+  for (int i = mine0; i < mine1; ++i) {
+    const uint32_t k = keys[i];
+    bool sure = k >= from, tie = only_ties && k == kth;
+    if (!exact && !sure && k >= maybe) {
+      sure = wide[i] > kth64;
+      tie = wide[i] == kth64;
     }
-    const unsigned tm = __ballot_sync(kFullMask, tie);
-    if (lane == 0) sh.warp_a[warp] = __popc(tm);
-    __syncthreads();
-    unsigned before = tied + __popc(tm & ((1u << lane) - 1u));
-    for (int j = 0; j < kWarps; ++j) {
-      const unsigned c = sh.warp_a[j];
-      if (j < warp) before += c;
-      tied += c;
+    sures |= (uint64_t)sure << (i - mine0);
+    tied |= (uint64_t)tie << (i - mine0);
+  }
+  const unsigned has = __popcll(sures) | __popcll(tied) << 16;
+  const unsigned before = block_scan(has, sh, &total) - has;
+  unsigned at = before & 0xffffu;  // places taken before this thread's blocks
+  int left = (int)places - (int)(before >> 16);  // ties that still have a place
+  at += min(before >> 16, places);
+  for (uint64_t todo = sures | tied; todo; todo &= todo - 1) {
+    const int bit = __ffsll((long long)todo) - 1;
+    if (tied >> bit & 1) {
+      if (left-- <= 0) continue;
     }
-    const bool sel = sure || (tie && before < ties_to_take);
-    const unsigned sm = __ballot_sync(kFullMask, sel);
-    if (lane == 0) sh.warp_b[warp] = __popc(sm);
-    __syncthreads();
-    unsigned at = taken + __popc(sm & ((1u << lane) - 1u));
-    for (int j = 0; j < kWarps; ++j) {
-      const unsigned c = sh.warp_b[j];
-      if (j < warp) at += c;
-      taken += c;
-    }
-    if (sel && at < (unsigned)p.topk) out[at] = i;
+    if (at < (unsigned)p.topk) out[at] = mine0 + bit;
+    ++at;
   }
 }
 
 template <int D>
 size_t smem_bytes(int width) {
-  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)((width + 1) & ~1) * 4 +
-         (size_t)width * 8;
+  const size_t wide = (size_t)width * 8;
+  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)((width + 3) & ~3) * 4 +
+         (wide > sizeof(QueryParts<D>) ? wide : sizeof(QueryParts<D>));
 }
 
-// CTAs of a cluster: more while the whole grid would leave SMs idle and a CTA
-// would still have a step of blocks for each of its warps.
-int cluster_for(int64_t items, int width) {
-  int c = 1;
-  while (c < kMaxCluster && items * c < 152 && width > c * 2 * kWarps * 8) c *= 2;
-  return c;
+// As many kv heads to a cluster (8 at most, one selecting CTA each) as leave
+// every SM a CTA, then more CTAs to a cluster (8 at most) while all of them
+// are resident at once, two to an SM, and have a tile of blocks each.
+void shape_for(SelectParams* p, int64_t num_tokens) {
+  int heads = kMaxCluster, c;
+  while (true) {
+    while (heads > 1 && heads / 2 >= p->num_kv) heads /= 2;
+    const int64_t units = num_tokens * ((p->num_kv + heads - 1) / heads);
+    c = heads;
+    while (c < kMaxCluster && units * c * 2 <= 2 * 152 && p->table_width > c * 16 * 2) c *= 2;
+    if (heads == 1 || units * c >= 152) break;
+    heads /= 2;
+  }
+  p->cluster = c;
+  p->heads = heads;
+  p->head_groups = (p->num_kv + heads - 1) / heads;
 }
 
 template <int D>
@@ -429,9 +630,9 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   p.keep_last = a.keep_last;
   p.blocks = a.blocks;
   p.errors = x.errors;
-  const int64_t items = (int64_t)x.num_tokens * x.num_heads_kv;
-  p.cluster = cluster_for(items, x.table_width);
-  return launch_clusters(block_select_kernel<D>, dim3((unsigned)(items * p.cluster)),
+  shape_for(&p, x.num_tokens);
+  const int64_t grid = (int64_t)x.num_tokens * p.head_groups * p.cluster;
+  return launch_clusters(block_select_kernel<D>, dim3((unsigned)grid),
                          dim3(kThreads), smem_bytes<D>(x.table_width), p.cluster, stream, p);
 }
 
