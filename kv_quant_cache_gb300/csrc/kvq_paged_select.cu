@@ -41,6 +41,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kSlots = 2;  // heads that one CTA selects for, at most
 
 struct SelectParams {
   const __nv_bfloat16* q;
@@ -57,7 +58,8 @@ struct SelectParams {
   int* blocks;
   int* errors;
   int cluster;     // CTAs of a cluster
-  int heads;       // kv heads of a cluster, at most `cluster`
+  int heads;       // kv heads of a cluster, at most kWarps
+  int slots;       // heads a CTA selects for
   int head_groups; // clusters of a token
 };
 
@@ -84,11 +86,11 @@ constexpr int kFew = kThreads;  // candidates that are ranked against each other
 // Shared memory of a CTA (the selecting one uses all of it).
 template <int D>
 struct Shared {
-  double up64[D], down64[D];  // of the head this CTA selects for
-  // of every scoring warp: its error bound, its smallest and largest key (of
-  // blocks that are not kept anyway)
-  float err[kMaxCluster * kWarps];
-  uint32_t least[kMaxCluster * kWarps], most[kMaxCluster * kWarps];
+  double up64[D], down64[D];  // of the head being selected for
+  // per head that this CTA selects for and scoring warp: its error bound, its
+  // smallest and largest key (of blocks that are not kept anyway)
+  float err[kSlots][kMaxCluster * kWarps];
+  uint32_t least[kSlots][kMaxCluster * kWarps], most[kSlots][kMaxCluster * kWarps];
   unsigned hist[kBins];
   int few[kFew];  // candidates by index
   unsigned warp_sum[kWarps];
@@ -214,14 +216,186 @@ __device__ Key select_largest(int n, unsigned place, Key lo, Key hi, Sh& sh, con
   }
 }
 
+// Selects the blocks of one head from its scores (all threads of the CTA):
+// `keys` of n > topk blocks, `scorers` entries of the slot's err, least and
+// most; the group's queries, the request's pages and the bounds of the head on
+// page 0 for scores that have to be taken again.
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) block_select_kernel(const SelectParams p) {
+__device__ void select_head(const SelectParams& p, Shared<D>& sh, uint32_t* keys,
+                            unsigned long long* wide, int slot, int scorers, int n,
+                            const __nv_bfloat16* queries, const int* row,
+                            const __nv_bfloat16* bounds, int* out) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t page_elems = (int64_t)p.num_kv * 2 * D;
+  // ---- the k-th largest, its doubtful neighbours ---------------------------------------
+  float E = 0.f;
+  uint32_t least = 0xffffffffu, most = 0;
+  for (int i = lane; i < scorers; i += 32) {
+    E = fmaxf(E, sh.err[slot][i]);
+    least = min(least, sh.least[slot][i]);
+    most = max(most, sh.most[slot][i]);
+  }
+  E = group_max<32>(E);
+  least = __reduce_min_sync(kFullMask, least);
+  most = __reduce_max_sync(kFullMask, most);
+  unsigned ties;
+  // the kept blocks are selected anyway; the others compete for what is left
+  const int kept = min(n, min(n, p.keep_first) + min(n, p.keep_last));
+  uint32_t kth;
+  if (kept >= p.topk) {
+    kth = kKeep32;
+    ties = p.topk;
+  } else {
+    kth = select_largest<uint32_t>(
+        n, (unsigned)(p.topk - kept), least, most, sh,
+        [&](int i, uint32_t* k) { *k = keys[i]; return *k != kKeep32; }, &ties);
+  }
+  // keys from `in` up are selected, below `maybe` are not
+  uint32_t in = kth, maybe = kth;
+  if (kth != kKeep32 && E > 0.f) {
+    const float T = value32(kth);
+    if (E == INFINITY || !(fabsf(T) <= 3.0e38f)) {
+      in = kKeep32;
+      maybe = 0;
+    } else {
+      const float up = T + 2.f * E, down = T - 2.f * E;
+      // one step outward covers the rounding of the two sums
+      in = min(key32(up) + 2u, kKeep32);
+      maybe = key32(down) - 2u;
+    }
+  }
+  // a thread's blocks from here on: `each` consecutive ones
+  const int each = (n + kThreads - 1) / kThreads;
+  const int mine0 = min(n, tid * each), mine1 = min(n, mine0 + each);
+  unsigned places = ties;  // places left for the keys in [maybe, in)
+  bool exact = in == maybe;
+  const bool only_ties = exact;  // equal fp32 scores are equal scores: no product was other
+                                 // than zero, or only kept blocks compete
+  unsigned long long kth64 = 0;
+  unsigned total;
+  if (!exact) {
+    unsigned above = 0, between = 0;
+    if (tid == 0) sh.count = 0;
+    for (int i = mine0; i < mine1; ++i) {
+      above += keys[i] >= in;
+      between += keys[i] < in && keys[i] >= maybe;
+    }
+    block_scan(above | between << 16, sh, &total);  // at most 16384 each
+    places = (unsigned)p.topk - (total & 0xffffu);
+    const unsigned doubtful = total >> 16;
+    if (doubtful == places) {
+      in = maybe;  // all of them
+      exact = true;
+    } else {
+      // the doubtful ones again, one per warp, in fp64 and in one fixed order
+      for (int d = tid; d < D; d += kThreads) {
+        double up = 0., down = 0.;
+        const __nv_bfloat16* q = queries + d;
+        for (int g = 0; g < p.group; ++g) {
+          const float v = __bfloat162float(q[(int64_t)g * D]);
+          up += v > 0.f ? v : v == v ? 0.f : v;
+          down += v < 0.f ? v : v == v ? 0.f : v;
+        }
+        sh.up64[d] = up, sh.down64[d] = down;
+      }
+      const bool few = doubtful <= (unsigned)kFew;
+      if (few) {
+        for (int i = mine0; i < mine1; ++i)
+          if (keys[i] < in && keys[i] >= maybe) sh.few[atomicAdd(&sh.count, 1u)] = i;
+      }
+      __syncthreads();
+      for (int c = warp; c < (few ? (int)doubtful : n); c += kWarps) {
+        const int i = few ? sh.few[c] : c;
+        if (!few && !(keys[i] < in && keys[i] >= maybe)) continue;
+        const int page = __ldg(row + i);
+        double s = 0.;
+        if (page >= 0 && page < p.num_pages) {
+          const __nv_bfloat16* b = bounds + page * page_elems;
+#pragma unroll
+          for (int d = 0; d < D; d += 32) {
+            s = fma(sh.down64[d + lane], (double)__bfloat162float(b[d + lane]), s);
+            s = fma(sh.up64[d + lane], (double)__bfloat162float(b[D + d + lane]), s);
+          }
+        } else {
+          s = -(double)INFINITY;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+        if (lane == 0) wide[i] = key64(s);
+      }
+      __syncthreads();
+      if (few) {
+        // each against the others: larger first, then the lower index; the
+        // places go to the first of them
+        bool sel = false;
+        int i = 0;
+        if (tid < (int)doubtful) {
+          i = sh.few[tid];
+          unsigned ahead = 0;
+          for (unsigned c = 0; c < doubtful; ++c) {
+            const int k = sh.few[c];
+            ahead += wide[k] > wide[i] || (wide[k] == wide[i] && k < i);
+          }
+          sel = ahead < places;
+        }
+        __syncthreads();
+        if (tid < (int)doubtful) keys[i] = sel ? kKeep32 : 0u;
+        __syncthreads();
+        exact = true;
+      } else {
+        kth64 = select_largest<unsigned long long>(
+            n, places, 0ull, ~0ull, sh,
+            [&](int i, unsigned long long* k) {
+              if (!(keys[i] < in && keys[i] >= maybe)) return false;
+              *k = wide[i];
+              return true;
+            },
+            &places);
+      }
+    }
+  }
+
+  // ---- the selected blocks, ascending -----------------------------------------------------
+  // `places` of the ties are selected, the lowest indices.  A thread keeps
+  // which of its blocks (at most 64) are in, and which are ties, in two words.
+  const uint64_t from = only_ties ? (uint64_t)kth + 1 : in;
+  uint64_t sures = 0, tied = 0;
+  for (int i = mine0; i < mine1; ++i) {
+    const uint32_t k = keys[i];
+    bool sure = k >= from, tie = only_ties && k == kth;
+    if (!exact && !sure && k >= maybe) {
+      sure = wide[i] > kth64;
+      tie = wide[i] == kth64;
+    }
+    sures |= (uint64_t)sure << (i - mine0);
+    tied |= (uint64_t)tie << (i - mine0);
+  }
+  const unsigned has = __popcll(sures) | __popcll(tied) << 16;
+  const unsigned before = block_scan(has, sh, &total) - has;
+  unsigned at = before & 0xffffu;  // places taken before this thread's blocks
+  int left = (int)places - (int)(before >> 16);  // ties that still have a place
+  at += min(before >> 16, places);
+  for (uint64_t todo = sures | tied; todo; todo &= todo - 1) {
+    const int bit = __ffsll((long long)todo) - 1;
+    if (tied >> bit & 1) {
+      if (left-- <= 0) continue;
+    }
+    if (at < (unsigned)p.topk) out[at] = mine0 + bit;
+    ++at;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+block_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
-  // scores of the first CTA: fp32 keys, then fp64 keys, one of each per block
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Shared<D>) + 15) & ~size_t(15)));
+  // scores of the heads this CTA selects for: fp32 keys per head and block,
+  // then fp64 keys per block (of one head at a time)
+  const int key_stride = (p.table_width + 3) & ~3;
+  uint32_t* all_keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Shared<D>) + 15) & ~size_t(15)));
   unsigned long long* wide =
-      reinterpret_cast<unsigned long long*>(keys + ((p.table_width + 3) & ~3));
+      reinterpret_cast<unsigned long long*>(all_keys + p.slots * key_stride);
   QueryParts<D>& queries_in = *reinterpret_cast<QueryParts<D>*>(wide);
   cg::cluster_group cluster = cg::this_cluster();
   if (p.cluster > 1) cluster.barrier_arrive();
@@ -232,9 +406,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) block_select_kerne
   const int t = unit / (uint32_t)p.head_groups;
   const int h0 = (int)(unit - (uint32_t)t * p.head_groups) * p.heads;
   const int heads = min(p.heads, p.num_kv - h0);
-  const bool selects = rank < heads;  // for head h0 + rank
-  const int h = h0 + (selects ? rank : 0);
-  int* out = p.blocks + ((int64_t)t * p.num_kv + h) * p.topk;
+  // CTA r selects for heads h0 + r, h0 + r + cluster, ..
+  int* outs = p.blocks + ((int64_t)t * p.num_kv + h0) * p.topk;
 
   // ---- the token's blocks, and the groups' query sums -----------------------------
   int req = p.requests ? __ldg(p.requests + t) : t;
@@ -293,8 +466,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) block_select_kerne
   if (rejected && p.errors && rank == 0 && tid == 0) atomicAdd(p.errors, 1);
   const int n = (int)(((uint32_t)len + (uint32_t)p.page_size - 1) / (uint32_t)p.page_size);
   if (n <= p.topk) {  // all of them: no score decides anything (cluster-uniform)
-    if (selects)
-      for (int i = tid; i < p.topk; i += kThreads) out[i] = i < n ? i : -1;
+    for (int head = rank; head < heads; head += p.cluster)
+      for (int i = tid; i < p.topk; i += kThreads)
+        outs[(int64_t)head * p.topk + i] = i < n ? i : -1;
     if (p.cluster > 1) cluster.barrier_wait();
     return;
   }
@@ -318,7 +492,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) block_select_kerne
   const int subs = kWarps / heads;              // warps of the CTA per head
   const int mine = warp % heads, sub = warp / heads;  // this warp's head; sub == subs: idle
   const bool scores = sub < subs;
-  uint32_t* to_keys = p.cluster > 1 ? cluster.map_shared_rank(keys, mine) : keys;
+  const int to_rank = mine % p.cluster, to_slot = mine / p.cluster;  // who selects for it
+  uint32_t* to_keys = all_keys + to_slot * key_stride;
+  if (p.cluster > 1) to_keys = cluster.map_shared_rank(to_keys, to_rank);
   const int g = lane >> 2, c = lane & 3;
   uint4 wb[STEPS];  // column g: a part of the query sums (0-2), their sizes (3), nothing
 #pragma unroll
@@ -405,201 +581,52 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) block_select_kerne
   least = __reduce_min_sync(kFullMask, least);
   most = __reduce_max_sync(kFullMask, most);
   if (lane == 0 && scores) {
-    Shared<D>& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, mine) : sh;
+    Shared<D>& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, to_rank) : sh;
     const int at = rank * subs + sub;
     const float bound = 0x1p-17f + (float)(8 + p.group) * 0x1p-24f;
-    to.err[at] = odd ? INFINITY : any_weight ? worst * bound + 1.0e-35f : 0.f;
-    to.least[at] = least;
-    to.most[at] = most;
+    to.err[to_slot][at] = odd ? INFINITY : any_weight ? worst * bound + 1.0e-35f : 0.f;
+    to.least[to_slot][at] = least;
+    to.most[to_slot][at] = most;
   }
   if (p.cluster > 1) {
     cluster.sync();  // every score has arrived, and no CTA reads another's memory any longer
-    if (!selects) return;
   } else {
     __syncthreads();
   }
 
-  // ---- the k-th largest, its doubtful neighbours ---------------------------------------
-  float E = 0.f;
-  least = 0xffffffffu;
-  most = 0;
-  for (int i = lane; i < p.cluster * subs; i += 32) {
-    E = fmaxf(E, sh.err[i]);
-    least = min(least, sh.least[i]);
-    most = max(most, sh.most[i]);
-  }
-  E = group_max<32>(E);
-  least = __reduce_min_sync(kFullMask, least);
-  most = __reduce_max_sync(kFullMask, most);
-  unsigned ties;
-  // the kept blocks are selected anyway; the others compete for what is left
-  const int kept = min(n, min(n, p.keep_first) + min(n, p.keep_last));
-  uint32_t kth;
-  if (kept >= p.topk) {
-    kth = kKeep32;
-    ties = p.topk;
-  } else {
-    kth = select_largest<uint32_t>(
-        n, (unsigned)(p.topk - kept), least, most, sh,
-        [&](int i, uint32_t* k) { *k = keys[i]; return *k != kKeep32; }, &ties);
-  }
-  // keys from `in` up are selected, below `maybe` are not
-  uint32_t in = kth, maybe = kth;
-  if (kth != kKeep32 && E > 0.f) {
-    const float T = value32(kth);
-    if (E == INFINITY || !(fabsf(T) <= 3.0e38f)) {
-      in = kKeep32;
-      maybe = 0;
-    } else {
-      const float up = T + 2.f * E, down = T - 2.f * E;
-      // one step outward covers the rounding of the two sums
-      in = min(key32(up) + 2u, kKeep32);
-      maybe = key32(down) - 2u;
-    }
-  }
-  // a thread's blocks from here on: `each` consecutive ones
-  const int each = (n + kThreads - 1) / kThreads;
-  const int mine0 = min(n, tid * each), mine1 = min(n, mine0 + each);
-  unsigned places = ties;  // places left for the keys in [maybe, in)
-  bool exact = in == maybe;
-  const bool only_ties = exact;  // equal fp32 scores are equal scores: no product was other
-                                 // than zero, or only kept blocks compete
-  unsigned long long kth64 = 0;
-  unsigned total;
-  if (!exact) {
-    unsigned above = 0, between = 0;
-    if (tid == 0) sh.count = 0;
-    for (int i = mine0; i < mine1; ++i) {
-      above += keys[i] >= in;
-      between += keys[i] < in && keys[i] >= maybe;
-    }
-    block_scan(above | between << 16, sh, &total);  // at most 16384 each
-    places = (unsigned)p.topk - (total & 0xffffu);
-    const unsigned doubtful = total >> 16;
-    if (doubtful == places) {
-      in = maybe;  // all of them
-      exact = true;
-    } else {
-      // the doubtful ones again, one per warp, in fp64 and in one fixed order
-      for (int d = tid; d < D; d += kThreads) {
-        double up = 0., down = 0.;
-        const __nv_bfloat16* q = queries + (int64_t)(h - h0) * p.group * D + d;
-        for (int g = 0; g < p.group; ++g) {
-          const float v = __bfloat162float(q[(int64_t)g * D]);
-          up += v > 0.f ? v : v == v ? 0.f : v;
-          down += v < 0.f ? v : v == v ? 0.f : v;
-        }
-        sh.up64[d] = up, sh.down64[d] = down;
-      }
-      const bool few = doubtful <= (unsigned)kFew;
-      if (few) {
-        for (int i = mine0; i < mine1; ++i)
-          if (keys[i] < in && keys[i] >= maybe) sh.few[atomicAdd(&sh.count, 1u)] = i;
-      }
-      __syncthreads();
-      for (int c = warp; c < (few ? (int)doubtful : n); c += kWarps) {
-        const int i = few ? sh.few[c] : c;
-        if (!few && !(keys[i] < in && keys[i] >= maybe)) continue;
-        const int page = __ldg(row + i);
-        double s = 0.;
-        if (page >= 0 && page < p.num_pages) {
-          const __nv_bfloat16* b = p.bounds + page * page_elems + (int64_t)h * 2 * D;
-#pragma unroll
-          for (int d = 0; d < D; d += 32) {
-            s = fma(sh.down64[d + lane], (double)__bfloat162float(b[d + lane]), s);
-            s = fma(sh.up64[d + lane], (double)__bfloat162float(b[D + d + lane]), s);
-          }
-        } else {
-          s = -(double)INFINITY;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-        if (lane == 0) wide[i] = key64(s);
-      }
-      __syncthreads();
-      if (few) {
-        // each against the others: larger first, then the lower index; the
-        // places go to the first of them
-        bool sel = false;
-        int i = 0;
-        if (tid < (int)doubtful) {
-          i = sh.few[tid];
-          unsigned ahead = 0;
-          for (unsigned c = 0; c < doubtful; ++c) {
-            const int k = sh.few[c];
-            ahead += wide[k] > wide[i] || (wide[k] == wide[i] && k < i);
-          }
-          sel = ahead < places;
-        }
-        __syncthreads();
-        if (tid < (int)doubtful) keys[i] = sel ? kKeep32 : 0u;
-        __syncthreads();
-        exact = true;
-      } else {
-        kth64 = select_largest<unsigned long long>(
-            n, places, 0ull, ~0ull, sh,
-            [&](int i, unsigned long long* k) {
-              if (!(keys[i] < in && keys[i] >= maybe)) return false;
-              *k = wide[i];
-              return true;
-            },
-            &places);
-      }
-    }
-  }
-
-  // ---- the selected blocks, ascending -----------------------------------------------------
-  // `places` of the ties are selected, the lowest indices.  A thread keeps
-  // which of its blocks (at most 64) are in, and which are ties, in two words.
-  const uint64_t from = only_ties ? (uint64_t)kth + 1 : in;
-  uint64_t sures = 0, tied = 0;
-  for (int i = mine0; i < mine1; ++i) {
-    const uint32_t k = keys[i];
-    bool sure = k >= from, tie = only_ties && k == kth;
-    if (!exact && !sure && k >= maybe) {
-      sure = wide[i] > kth64;
-      tie = wide[i] == kth64;
-    }
-    sures |= (uint64_t)sure << (i - mine0);
-    tied |= (uint64_t)tie << (i - mine0);
-  }
-  const unsigned has = __popcll(sures) | __popcll(tied) << 16;
-  const unsigned before = block_scan(has, sh, &total) - has;
-  unsigned at = before & 0xffffu;  // places taken before this thread's blocks
-  int left = (int)places - (int)(before >> 16);  // ties that still have a place
-  at += min(before >> 16, places);
-  for (uint64_t todo = sures | tied; todo; todo &= todo - 1) {
-    const int bit = __ffsll((long long)todo) - 1;
-    if (tied >> bit & 1) {
-      if (left-- <= 0) continue;
-    }
-    if (at < (unsigned)p.topk) out[at] = mine0 + bit;
-    ++at;
+  for (int head = rank, slot = 0; head < heads; head += p.cluster, ++slot) {
+    select_head<D>(p, sh, all_keys + slot * key_stride, wide, slot, p.cluster * subs, n,
+                   queries + (int64_t)head * p.group * D, row,
+                   p.bounds + (int64_t)(h0 + head) * 2 * D, outs + (int64_t)head * p.topk);
+    __syncthreads();  // before the shared arrays serve the next head
   }
 }
 
 template <int D>
-size_t smem_bytes(int width) {
+size_t smem_bytes(int width, int slots) {
   const size_t wide = (size_t)width * 8;
-  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)((width + 3) & ~3) * 4 +
+  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)slots * ((width + 3) & ~3) * 4 +
          (wide > sizeof(QueryParts<D>) ? wide : sizeof(QueryParts<D>));
 }
 
-// As many kv heads to a cluster (8 at most, one selecting CTA each) as leave
-// every SM a CTA, then more CTAs to a cluster (8 at most) while all of them
-// are resident at once, two to an SM, and have a tile of blocks each.
+// As many kv heads to a cluster (8 at most) as leave every SM a CTA, and as
+// many CTAs to a cluster (8 at most) as are all resident at once, two to an
+// SM, and have a tile of blocks each; a CTA selects for two heads at most, and
+// for one where the tables are long.
 void shape_for(SelectParams* p, int64_t num_tokens) {
-  int heads = kMaxCluster, c;
+  int heads = kWarps;
+  int64_t units;
   while (true) {
-    while (heads > 1 && heads / 2 >= p->num_kv) heads /= 2;
-    const int64_t units = num_tokens * ((p->num_kv + heads - 1) / heads);
-    c = heads;
-    while (c < kMaxCluster && units * c * 2 <= 2 * 152 && p->table_width > c * 16 * 2) c *= 2;
-    if (heads == 1 || units * c >= 152) break;
+    units = num_tokens * ((p->num_kv + heads - 1) / heads);
+    if (heads == 1 || (heads / 2 < p->num_kv && units * kMaxCluster >= 152)) break;
     heads /= 2;
   }
+  const int slots = heads > 1 && p->table_width <= 4096 ? kSlots : 1;
+  int c = heads / slots;
+  while (c < kMaxCluster && units * c * 2 <= 2 * 152 && p->table_width > c * 16 * 2) c *= 2;
   p->cluster = c;
   p->heads = heads;
+  p->slots = (heads + c - 1) / c;
   p->head_groups = (p->num_kv + heads - 1) / heads;
 }
 
@@ -609,8 +636,8 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
   // one opt-in for the largest size that the validation lets through
-  const cudaError_t e = tma::prepare(block_select_kernel<D>, kThreads, smem_bytes<D>(kMaxSelectBlocks),
-                               cache, &per_sm);
+  const cudaError_t e = tma::prepare(block_select_kernel<D>, kThreads,
+                                     smem_bytes<D>(kMaxSelectBlocks, 1), cache, &per_sm);
   if (e != cudaSuccess) return e;
   SelectParams p;
   p.q = static_cast<const __nv_bfloat16*>(x.q);
@@ -632,8 +659,8 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   p.errors = x.errors;
   shape_for(&p, x.num_tokens);
   const int64_t grid = (int64_t)x.num_tokens * p.head_groups * p.cluster;
-  return launch_clusters(block_select_kernel<D>, dim3((unsigned)grid),
-                         dim3(kThreads), smem_bytes<D>(x.table_width), p.cluster, stream, p);
+  return launch_clusters(block_select_kernel<D>, dim3((unsigned)grid), dim3(kThreads),
+                         smem_bytes<D>(x.table_width, p.slots), p.cluster, stream, p);
 }
 
 }  // namespace
