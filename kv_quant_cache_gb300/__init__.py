@@ -323,6 +323,61 @@ def dsv4_kv_cache_gather(kv_cache, slots, out=None, stream=None, errors=None):
     return out
 
 
+# ---- paged grouped-query operators ---------------------------------------------------
+# A decode step calls each of these once a layer, and for small batches the
+# call costs the host more than the kernel costs the GPU, so their argument
+# checks are written for few interpreter steps: one helper call per tensor,
+# sizes unpacked once, workspace sizes (a function of the sizes alone)
+# remembered.
+
+_BF16, _I32, _I64T, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+def _ptr(t, dtype, dev, name) -> int:
+    """Address of a contiguous ``dtype`` tensor on CUDA device ``dev`` (or of a
+    pinned host tensor, which may take part on any device)."""
+    if t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+        if dev >= 0:
+            return t.data_ptr()
+    ptr = _cuda(t, dtype, name)
+    if t.get_device() not in (dev, -1):
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, other tensors of the call on "
+                         f"cuda:{dev}: every CUDA tensor of one call must be on the same device")
+    return ptr
+
+
+def _home(t, *others) -> int:
+    """The CUDA device of a call: that of ``t``, or, where ``t`` is a pinned
+    host tensor, of the first CUDA tensor among the others (-1: there is
+    none)."""
+    dev = t.get_device()
+    return dev if dev >= 0 else _device(*others)
+
+
+def _launch(dev, stream, fn, *args) -> None:
+    """``fn(*args, stream)`` on device ``dev``; raises on an error status."""
+    if dev >= 0 and dev != _current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream, dev))
+    else:
+        st = fn(*args, _stream(stream, dev))
+    if st:
+        _check(st, fn.__name__)
+
+
+def _counted(errors, dev):
+    return None if errors is None else _ptr(errors, _I32, dev, "errors")
+
+
+def _paged_cache(kv_cache):
+    """num_pages, Hkv, page_size, head_dim of a paged cache."""
+    if kv_cache.dim() == 5:
+        pages, two, heads, page, dim = kv_cache.shape
+        if two == 2:
+            return pages, heads, page, dim
+    raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim]")
+
+
 def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox,
                          positions, slot_mapping, kv_cache, q_out=None, stream=None,
                          rotary_dim=None, errors=None) -> None:
@@ -334,97 +389,88 @@ def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache
     ``rotary_dim`` defaults to the table's width.  Tokens with a position
     outside the table are left out, slots outside the cache not written; both
     are counted in ``errors`` (int32 CUDA tensor) when given."""
+    pages, heads, page, dim = _paged_cache(kv_cache)
+    if heads != num_heads_kv or dim != head_dim:
+        raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim] of the "
+                         "call's Hkv and head_dim")
     if qkv.dim() != 2 or qkv.shape[1] != (num_heads_q + 2 * num_heads_kv) * head_dim:
         raise ValueError("qkv must be [T, (Hq+2*Hkv)*head_dim]")
     T = qkv.shape[0]
-    _paged_cache(kv_cache, num_heads_kv, head_dim)
     if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must hold one value per token")
-    if q_out is not None and q_out.shape != (T, num_heads_q, head_dim):
-        raise ValueError("q_out must be [T, Hq, head_dim]")
+    dev = _home(qkv, q_out, cos_sin_cache, slot_mapping, kv_cache, errors)
+    q_ptr = None
+    if q_out is not None:
+        if q_out.shape != (T, num_heads_q, head_dim):
+            raise ValueError("q_out must be [T, Hq, head_dim]")
+        q_ptr = _ptr(q_out, _BF16, dev, "q_out")
     if cos_sin_cache is None:
         if rotary_dim:
             raise ValueError("rotary_dim without a cos_sin_cache")
-        rotary_dim = rows = 0
+        rows = rot = 0
         cs = pos = None
-        positions = None
     else:
-        if rotary_dim is None:
-            rotary_dim = cos_sin_cache.shape[1]
-        if cos_sin_cache.dim() != 2 or cos_sin_cache.shape[1] != rotary_dim or rotary_dim == 0:
+        rows, rot = cos_sin_cache.shape if cos_sin_cache.dim() == 2 else (0, 0)
+        if rot == 0 or (rotary_dim is not None and rotary_dim != rot):
             raise ValueError("cos_sin_cache must be [max_pos, rotary_dim]")
         if positions.numel() != T:
             raise ValueError("positions must hold one value per token")
-        rows = cos_sin_cache.shape[0]
-        cs = _cuda(cos_sin_cache, torch.float32, "cos_sin_cache")
-        pos = _cuda(positions, torch.int64, "positions")
-    dev = _device(qkv, q_out, cos_sin_cache, positions, slot_mapping, kv_cache, errors)
-    st = _on(dev, lib().paged_kv_rope_append, _cuda(qkv, torch.bfloat16, "qkv"),
-             None if q_out is None else _cuda(q_out, torch.bfloat16, "q_out"), T, num_heads_q,
-             num_heads_kv, head_dim, cs, rows, int(rotary_dim), int(bool(is_neox)), pos,
-             _cuda(slot_mapping, torch.int64, "slot_mapping"),
-             _cuda(kv_cache, torch.bfloat16, "kv_cache"), kv_cache.shape[0], kv_cache.shape[3],
-             None if errors is None else _counter(errors), _stream(stream, dev))
-    _check(st, "paged_kv_rope_append")
-
-
-def _paged_cache(kv_cache, num_heads_kv=None, head_dim=None) -> None:
-    if kv_cache.dim() != 5 or kv_cache.shape[1] != 2:
-        raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim]")
-    if num_heads_kv is not None and (kv_cache.shape[2] != num_heads_kv
-                                     or kv_cache.shape[4] != head_dim):
-        raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim] of the "
-                         "call's Hkv and head_dim")
+        cs = _ptr(cos_sin_cache, _F32, dev, "cos_sin_cache")
+        pos = _ptr(positions, _I64T, dev, "positions")
+    _launch(dev, stream, (_LIB or lib()).paged_kv_rope_append, _ptr(qkv, _BF16, dev, "qkv"), q_ptr,
+            T, num_heads_q, num_heads_kv, head_dim, cs, rows, rot, 1 if is_neox else 0, pos,
+            _ptr(slot_mapping, _I64T, dev, "slot_mapping"),
+            _ptr(kv_cache, _BF16, dev, "kv_cache"), pages, page, _counted(errors, dev))
 
 
 def paged_kv_page_bounds(kv_cache, pages, lens, bounds, stream=None, errors=None):
     """Writes the smallest and largest key per dim of the first ``lens``
     (int32 [n]) tokens of each listed page (int64 [n], -1 = none) into
     ``bounds`` (bf16 [num_pages, Hkv, 2, head_dim]), and returns ``bounds``."""
-    _paged_cache(kv_cache)
-    N, _, Hkv, page, D = kv_cache.shape
+    N, Hkv, page, D = _paged_cache(kv_cache)
     if pages.dim() != 1 or lens.shape != pages.shape:
         raise ValueError("pages and lens must be 1-D, of one length")
     if bounds.shape != (N, Hkv, 2, D):
         raise ValueError("bounds must be [num_pages, Hkv, 2, head_dim]")
-    dev = _device(kv_cache, pages, lens, bounds, errors)
-    st = _on(dev, lib().paged_kv_page_bounds, _cuda(kv_cache, torch.bfloat16, "kv_cache"), N, Hkv,
-             page, D, _cuda(pages, torch.int64, "pages"), _cuda(lens, torch.int32, "lens"),
-             pages.shape[0], _cuda(bounds, torch.bfloat16, "bounds"),
-             None if errors is None else _counter(errors), _stream(stream, dev))
-    _check(st, "paged_kv_page_bounds")
+    dev = _home(kv_cache, pages, lens, bounds, errors)
+    _launch(dev, stream, (_LIB or lib()).paged_kv_page_bounds,
+            _ptr(kv_cache, _BF16, dev, "kv_cache"), N, Hkv, page, D,
+            _ptr(pages, _I64T, dev, "pages"), _ptr(lens, _I32, dev, "lens"), pages.shape[0],
+            _ptr(bounds, _BF16, dev, "bounds"), _counted(errors, dev))
     return bounds
 
 
-def _paged_q(q, head_dim, name="q"):
-    """Address and token stride of bf16 [T, Hq, D] whose heads are contiguous
-    (a token's rows may be a view into packed QKV)."""
-    if q.dim() != 3 or q.shape[2] != head_dim:
-        raise ValueError(f"{name} must be [T, Hq, {head_dim}]")
-    if q.dtype != torch.bfloat16:
-        raise ValueError(f"{name}: expected {torch.bfloat16}, got {q.dtype}")
-    if not (q.is_cuda or (q.device.type == "cpu" and q.is_pinned())):
-        raise ValueError(f"{name}: expected a CUDA tensor or a pinned host tensor")
+def _paged_q(q, head_dim, dev):
+    """Address, tokens, heads and token stride of bf16 [T, Hq, D] whose heads
+    are contiguous (a token's rows may be a view into packed QKV)."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, {head_dim}]")
     T, Hq, D = q.shape
+    if D != head_dim:
+        raise ValueError(f"q must be [T, Hq, {head_dim}]")
+    if q.dtype is not _BF16:
+        raise ValueError(f"q: expected {_BF16}, got {q.dtype}")
+    if dev < 0 or q.get_device() != dev:
+        if not (q.is_cuda or (q.device.type == "cpu" and q.is_pinned())):
+            raise ValueError("q: expected a CUDA tensor or a pinned host tensor")
     if q.is_contiguous() or T == 0:
-        return q.data_ptr(), Hq * D
-    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return q.data_ptr(), (q.stride(0) if T > 1 else Hq * D)
+        return q.data_ptr(), T, Hq, Hq * D
+    st, sh, sd = q.stride()
+    if sd != 1 or (Hq > 1 and sh != D):
+        raise ValueError("q: the heads of a token must be contiguous")
+    return q.data_ptr(), T, Hq, (st if T > 1 else Hq * D)
 
 
 def _requests(T, page_table, lens, requests):
-    """Addresses of the request arrays of a call with T tokens."""
+    """num_requests and table_width of a call with T tokens."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be [num_requests, table_width]")
+    R, width = page_table.shape
     if lens.numel() != T or (requests is not None and requests.numel() != T):
         raise ValueError("lens and requests must hold one value per token")
-    if requests is None and page_table.shape[0] < T:
+    if requests is None and R < T:
         raise ValueError("page_table must have a row per token when requests is not given")
-    return (_cuda(page_table, torch.int32, "page_table"), page_table.shape[0],
-            page_table.shape[1],
-            None if requests is None else _cuda(requests, torch.int32, "requests"),
-            _cuda(lens, torch.int32, "lens"))
+    return R, width
 
 
 def paged_kv_block_select(q, bounds, page_table, lens, page_size, topk, keep_first=0,
@@ -438,35 +484,51 @@ def paged_kv_block_select(q, bounds, page_table, lens, page_size, topk, keep_fir
     if bounds.dim() != 4 or bounds.shape[2] != 2:
         raise ValueError("bounds must be [num_pages, Hkv, 2, head_dim]")
     N, Hkv, _, D = bounds.shape
-    q_ptr, q_stride = _paged_q(q, D)
-    T, Hq = q.shape[0], q.shape[1]
-    table = _requests(T, page_table, lens, requests)
+    dev = _home(q, bounds, page_table, lens, requests, out, errors)
+    q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
+    R, width = _requests(T, page_table, lens, requests)
     if out is None:
-        out = torch.empty((T, Hkv, topk), dtype=torch.int32, device=q.device)
-    if out.shape != (T, Hkv, topk):
+        out = torch.empty((T, Hkv, topk), dtype=_I32, device=q.device)
+    elif out.shape != (T, Hkv, topk):
         raise ValueError("out must be [T, Hkv, topk]")
-    dev = _device(q, bounds, page_table, lens, requests, out, errors)
-    st = _on(dev, lib().paged_kv_block_select, q_ptr, q_stride, T, Hq, Hkv, D,
-             _cuda(bounds, torch.bfloat16, "bounds"), N, int(page_size), *table, int(topk),
-             int(keep_first), int(keep_last), _cuda(out, torch.int32, "out"),
-             None if errors is None else _counter(errors), _stream(stream, dev))
-    _check(st, "paged_kv_block_select")
+    _launch(dev, stream, (_LIB or lib()).paged_kv_block_select, q_ptr, q_stride, T, Hq, Hkv, D,
+            _ptr(bounds, _BF16, dev, "bounds"), N, page_size,
+            _ptr(page_table, _I32, dev, "page_table"), R, width,
+            None if requests is None else _ptr(requests, _I32, dev, "requests"),
+            _ptr(lens, _I32, dev, "lens"), topk, keep_first, keep_last,
+            _ptr(out, _I32, dev, "out"), _counted(errors, dev))
     return out
 
 
-def _attention_buffers(q, out, workspace, need):
-    """out and workspace of an attention call, allocated where not given; a
-    tensor of one call that must live until its kernels have run is torch's
-    to keep (its allocator reuses memory in stream order)."""
+_WORKSPACE = {}  # sizes of a call -> bytes of workspace it needs
+
+
+def _workspace_bytes(fn, *sizes) -> int:
+    need = _WORKSPACE.get((fn, sizes))
+    if need is None:
+        if len(_WORKSPACE) >= 4096:
+            _WORKSPACE.clear()
+        need = _WORKSPACE[(fn, sizes)] = getattr(lib(), fn)(*sizes)
+    return need
+
+
+def _output(q, out):
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    elif out.shape != q.shape:
+        return torch.empty(q.shape, dtype=_BF16, device=q.device)
+    if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return out
+
+
+def _workspace(q, workspace, need, dev):
+    """A workspace of ``need`` bytes (allocated if not given), its address and
+    its size.  One that is allocated here may be freed when the call returns:
+    torch's allocator reuses memory in stream order."""
     if workspace is None:
-        return out, None, None, 0
-    return (out, workspace, _cuda(workspace, workspace.dtype, "workspace"),
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return (workspace, _ptr(workspace, workspace.dtype, dev, "workspace"),
             workspace.numel() * workspace.element_size())
 
 
@@ -477,25 +539,24 @@ def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=No
     paged_kv_block_select returns them) that lie below ``lens[t]``.  ``scale``
     defaults to 1/sqrt(D).  ``workspace``: a tensor of at least
     ``paged_block_sparse_attention_workspace`` bytes, allocated per call if
-    not given."""
-    _paged_cache(kv_cache)
-    N, _, Hkv, page, D = kv_cache.shape
-    q_ptr, q_stride = _paged_q(q, D)
-    T, Hq = q.shape[0], q.shape[1]
-    if blocks.dim() != 3 or blocks.shape[0] != T or blocks.shape[1] != Hkv:
+    needed and not given."""
+    N, Hkv, page, D = _paged_cache(kv_cache)
+    dev = _home(q, kv_cache, page_table, blocks, lens, requests, out, errors)
+    q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
+    B, H, topk = blocks.shape if blocks.dim() == 3 else (-1, 0, 0)
+    if B != T or H != Hkv:
         raise ValueError("blocks must be [T, Hkv, topk]")
-    topk = blocks.shape[2]
-    table = _requests(T, page_table, lens, requests)
-    L = lib()
-    need = L.paged_block_sparse_attention_workspace(T, Hq, Hkv, D, page, topk)
-    out, workspace, ws, ws_bytes = _attention_buffers(q, out, workspace, need)
-    dev = _device(q, kv_cache, page_table, blocks, lens, requests, out, workspace, errors)
-    st = _on(dev, L.paged_block_sparse_attention, q_ptr, q_stride, T, Hq, Hkv, D,
-             _cuda(kv_cache, torch.bfloat16, "kv_cache"), N, page, *table,
-             _cuda(blocks, torch.int32, "blocks"), topk,
-             float(D ** -0.5 if scale is None else scale), _cuda(out, torch.bfloat16, "out"), ws,
-             ws_bytes, None if errors is None else _counter(errors), _stream(stream, dev))
-    _check(st, "paged_block_sparse_attention")
+    R, width = _requests(T, page_table, lens, requests)
+    out = _output(q, out)
+    workspace, ws, ws_bytes = _workspace(q, workspace, _workspace_bytes(
+        "paged_block_sparse_attention_workspace", T, Hq, Hkv, D, page, topk), dev)
+    _launch(dev, stream, (_LIB or lib()).paged_block_sparse_attention, q_ptr, q_stride, T, Hq,
+            Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
+            _ptr(page_table, _I32, dev, "page_table"), R, width,
+            None if requests is None else _ptr(requests, _I32, dev, "requests"),
+            _ptr(lens, _I32, dev, "lens"), _ptr(blocks, _I32, dev, "blocks"), topk,
+            D ** -0.5 if scale is None else scale, _ptr(out, _BF16, dev, "out"), ws, ws_bytes,
+            _counted(errors, dev))
     return out
 
 
@@ -506,25 +567,22 @@ def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_ta
     ``prefix_len`` keys of ``prefix_pages`` (int32) and the first ``lens[t]``
     keys of its own request's pages (``page_table``).  The prefix is read once
     for the whole batch.  Other arguments as paged_block_sparse_attention."""
-    _paged_cache(kv_cache)
-    N, _, Hkv, page, D = kv_cache.shape
-    q_ptr, q_stride = _paged_q(q, D)
-    T, Hq = q.shape[0], q.shape[1]
-    prefix_len = int(prefix_len)
+    N, Hkv, page, D = _paged_cache(kv_cache)
+    dev = _home(q, kv_cache, prefix_pages, page_table, lens, requests, out, errors)
+    q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
     if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page < prefix_len:
         raise ValueError("prefix_pages must be 1-D and hold prefix_len keys")
-    table = _requests(T, page_table, lens, requests)
-    L = lib()
-    need = L.paged_shared_prefix_attention_workspace(T, Hq, Hkv, D, page, prefix_len,
-                                                     page_table.shape[1])
-    out, workspace, ws, ws_bytes = _attention_buffers(q, out, workspace, need)
-    dev = _device(q, kv_cache, prefix_pages, page_table, lens, requests, out, workspace, errors)
-    st = _on(dev, L.paged_shared_prefix_attention, q_ptr, q_stride, T, Hq, Hkv, D,
-             _cuda(kv_cache, torch.bfloat16, "kv_cache"), N, page,
-             _cuda(prefix_pages, torch.int32, "prefix_pages"), prefix_len, *table,
-             float(D ** -0.5 if scale is None else scale), _cuda(out, torch.bfloat16, "out"), ws,
-             ws_bytes, None if errors is None else _counter(errors), _stream(stream, dev))
-    _check(st, "paged_shared_prefix_attention")
+    R, width = _requests(T, page_table, lens, requests)
+    out = _output(q, out)
+    workspace, ws, ws_bytes = _workspace(q, workspace, _workspace_bytes(
+        "paged_shared_prefix_attention_workspace", T, Hq, Hkv, D, page, prefix_len, width), dev)
+    _launch(dev, stream, (_LIB or lib()).paged_shared_prefix_attention, q_ptr, q_stride, T, Hq,
+            Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
+            _ptr(prefix_pages, _I32, dev, "prefix_pages"), prefix_len,
+            _ptr(page_table, _I32, dev, "page_table"), R, width,
+            None if requests is None else _ptr(requests, _I32, dev, "requests"),
+            _ptr(lens, _I32, dev, "lens"), D ** -0.5 if scale is None else scale,
+            _ptr(out, _BF16, dev, "out"), ws, ws_bytes, _counted(errors, dev))
     return out
 
 

@@ -126,11 +126,11 @@ def test_select_validation(L):
 
 @pytest.mark.parametrize("call", [sparse, prefix])
 def test_attention_validation(L, call):
-    # sizes whose call needs a workspace
-    big = dict(T=1, R=1, Hq=4, Hkv=1, stride=512, page=64, width=64)
-    big.update(topk=64) if call is sparse else big.update(length=4096)
-    need = (L.paged_block_sparse_attention_workspace(1, 4, 1, 128, 64, 64) if call is sparse else
-            L.paged_shared_prefix_attention_workspace(1, 4, 1, 128, 64, 4096, 64))
+    # sizes whose call needs a workspace: a long range that few rows see
+    big = dict(T=1, R=1, Hq=4, Hkv=1, stride=512, page=64, width=2048)
+    big.update(topk=2048) if call is sparse else big.update(length=131072)
+    need = (L.paged_block_sparse_attention_workspace(1, 4, 1, 128, 64, 2048) if call is sparse else
+            L.paged_shared_prefix_attention_workspace(1, 4, 1, 128, 64, 131072, 2048))
     assert need > 0 and need % 16 == 0
     assert rejected(call(L, ws=None, **big)) == kvq.KVQ_ERR_NULL
     assert rejected(call(L, ws=MIS, **big)) == kvq.KVQ_ERR_ALIGN
