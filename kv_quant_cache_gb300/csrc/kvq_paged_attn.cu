@@ -46,6 +46,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kRows = 16;         // query rows of a CTA
 constexpr int kGroup = 16;        // keys of one step of a warp
 constexpr int kMaxPages = 2048;   // pages a CTA can list
+constexpr int kSoloPages = 512;   // .. where it is a single warp
 
 // Whose a listed page is: of all rows, or of the rows of one token of the tile.
 constexpr int kAllRows = 31;
@@ -57,6 +58,7 @@ struct AttnParams {
   const __nv_bfloat16* cache;
   int num_q, num_kv, group;  // group = num_q / num_kv
   int tiles;                 // row tiles of a kv head (of a token and kv head: block-sparse)
+  int units;                 // row tiles in all
   int num_tokens;
   int64_t num_pages;
   int page_size;
@@ -116,24 +118,27 @@ struct Shape {
   static constexpr int kState = kWarps * kRows * 8;   // {m, l} per warp and row
   static constexpr int kLse = kRows * 4;              // of the CTA's part, per row
   static constexpr int kSmem = kWarps * kRing + kList + kState + kLse;
+  static constexpr int kSoloSmem = kRing + kSoloPages * 8;
   static_assert(kRing >= kRows * kPad * 4, "a warp's output fits in its ring");
 };
 
 // SPARSE: the rows of one token's group and the blocks selected for them;
 // otherwise a tile of (token, head) pairs, the prefix and their own keys.
 // WHOLE: page_size is a multiple of 16, so a group of keys lies in one page.
-template <int D, bool SPARSE, bool WHOLE>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParams p) {
+// SOLO: every warp has a row tile to itself (no cluster, no parts).
+template <int D, bool SPARSE, bool WHOLE, bool SOLO>
+__global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(const AttnParams p) {
   using S = Shape<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   grid_dependency_sync(p.trigger_from);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int2* list = reinterpret_cast<int2*>(smem + kWarps * S::kRing);
+  constexpr int kTeam = SOLO ? 1 : kWarps;  // warps on a row tile
+  int2* list = reinterpret_cast<int2*>(smem + kTeam * S::kRing);
   float2* state = reinterpret_cast<float2*>(smem + kWarps * S::kRing + S::kList);
   float* part_lse = reinterpret_cast<float*>(smem + kWarps * S::kRing + S::kList + S::kState);
-  const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
-  const int unit = blockIdx.x / p.cluster;
+  const int rank = !SOLO && p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
+  const int unit = SOLO ? (int)blockIdx.x : (int)blockIdx.x / p.cluster;
 
   // ---- which rows -----------------------------------------------------------------
   // row r is row flat0 + r of the kv head's (token, head of the group) pairs
@@ -216,8 +221,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
   const int64_t begin = (int64_t)share * (blockIdx.y * p.cluster + rank);
   const int page0 = (int)min(begin, (int64_t)pages);
   const int listed = min(share, pages - page0);
-  for (int i0 = 0; i0 < listed; i0 += kWarps * 32) {
-    const int i = i0 + threadIdx.x;
+  for (int i0 = 0; i0 < listed; i0 += kTeam * 32) {
+    const int i = i0 + (SOLO ? lane : (int)threadIdx.x);
     const int at = page0 + i - prefix;  // among the tokens' own pages
     // the token whose pages hold `at`: the number of tokens that end before
     int tok = 0, skip = 0;
@@ -253,12 +258,14 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
       list[i] = make_int2(page, valid | whose << kValidBits);
     }
   }
-  if (rejected && p.errors && (warp == 0 || lane >= tokens || listed > 0)) atomicAdd(p.errors, 1);
-  __syncthreads();
+  if (rejected && p.errors && (SOLO || warp == 0 || lane >= tokens || listed > 0))
+    atomicAdd(p.errors, 1);
+  if (SOLO) __syncwarp(); else __syncthreads();
 
   // ---- the warp's groups of keys ---------------------------------------------------
   const uint32_t total = (uint32_t)listed * page_size;  // below 2^31: checked at launch
-  const int steps = (int)((total + kGroup * kWarps - 1) / (kGroup * kWarps));
+  const int steps = (int)((total + kGroup * kTeam - 1) / (kGroup * kTeam));
+  const int member = SOLO ? 0 : warp;  // of the team
   const uint32_t ring = tma::smem_addr(smem) + warp * S::kRing;
   const int64_t head_elems = (int64_t)p.page_size * D;
   const int64_t v_from_k = p.num_kv * head_elems;
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
 
   // Starts the copies of step i's 16 keys.
   auto issue = [&](int i) {
-    const uint32_t k0 = (uint32_t)(i * kWarps + warp) * kGroup;
+    const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
     const uint32_t stage = ring + (i % S::kStages) * S::kStage;
     constexpr int FRAGS = D / 8;                          // 16-byte fragments of a row
     constexpr int RPI = 32 / FRAGS > 0 ? 32 / FRAGS : 1;  // rows of one warp-wide copy
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
     cp_wait<S::kStages - 1>();
     __syncwarp();
     // whose the step's keys are: lane r < 16 for key r, -2 where there is none
-    const uint32_t k0 = (uint32_t)(i * kWarps + warp) * kGroup;
+    const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
     int whose = -2;
     uint32_t todo;  // the keys that exist
     if (WHOLE) {
@@ -461,7 +468,35 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnParam
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(kFullMask, l[h], 1);
     l[h] += __shfl_xor_sync(kFullMask, l[h], 2);
-    if ((lane & 3) == 0) state[warp * kRows + (lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
+    if (!SOLO && (lane & 3) == 0)
+      state[warp * kRows + (lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
+  }
+  if (SOLO) {  // the rows are this warp's: straight from its registers
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      if (r >= rows) continue;
+      const int64_t row = row_of(r);
+      const float f = l[h] == 0.f ? 0.f : 1.f / l[h];  // 0: the row has no key
+      if (p.direct) {
+        __nv_bfloat16* dst = p.out + row * D + 2 * (lane & 3);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<uint32_t*>(dst + 8 * n) =
+              pack_bf16x2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
+      } else {
+        const int64_t slot = p.first_slot + blockIdx.y;
+        float* dst = p.parts.o + (slot * p.parts.rows + row) * D + 2 * (lane & 3);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n) =
+              make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
+        if ((lane & 3) == 0)
+          p.parts.lse[slot * p.parts.rows + row] =
+              l[h] == 0.f ? -INFINITY : (m[h] == -INFINITY ? 0.f : m[h]) + log2f(l[h]);
+      }
+    }
+    return;
   }
   __syncthreads();
 
@@ -613,6 +648,7 @@ cudaError_t launch_join(const JoinParams& in, cudaStream_t stream) {
 // How a launch of `units` row tiles over up to `pages` pages each is spread.
 struct Spread {
   int cluster, splits;
+  bool solo;  // a warp per row tile
 };
 
 // CTAs are added while all of them are resident at once (two to an SM; with
@@ -623,7 +659,7 @@ struct Spread {
 // launch costs more than it saves).  No CTA may have more pages than fit its
 // list.
 Spread spread_for(int64_t units, int64_t pages, int page_size) {
-  Spread s = {1, 1};
+  Spread s = {1, 1, false};
   const int64_t keys = pages * page_size;
   while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 2 * 152 &&
          keys >= (int64_t)s.cluster * 2 * kGroup * kWarps)
@@ -632,36 +668,49 @@ Spread spread_for(int64_t units, int64_t pages, int page_size) {
   while (units * s.cluster * (splits + 1) <= 2 * 152 && keys > s.cluster * splits * 2048) ++splits;
   const int64_t least = (pages + (int64_t)s.cluster * kMaxPages - 1) / ((int64_t)s.cluster * kMaxPages);
   s.splits = (int)(splits > least ? splits : least);
+  // With many tiles of short ranges, a CTA of one warp each: no joins between
+  // warps, and four times as many tiles in flight (640 tiles of 512 keys 32 us
+  // against 38 us, of 1024 keys 58 against 66; 1024 tiles of up to 200 keys 38
+  // against 51).  Longer ranges keep the four warps: the last tiles of a wave
+  // take four times as long on one (1280 tiles of 1024 keys 127 us against
+  // 108; 1024 tiles of 2 to 1152 keys 91 against 82).
+  s.solo = units >= 4 * 152 && keys <= 512 && pages <= kSoloPages;
   return s;
 }
 
-template <int D, bool SPARSE, bool WHOLE>
-cudaError_t launch_attn(AttnParams p, int64_t units, cudaStream_t stream) {
+template <int D, bool SPARSE, bool WHOLE, bool SOLO>
+cudaError_t launch_attn(AttnParams p, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
-  const cudaError_t e = tma::prepare(paged_attn_kernel<D, SPARSE, WHOLE>, kWarps * 32, Shape<D>::kSmem,
+  constexpr int threads = SOLO ? 32 : kWarps * 32;
+  constexpr int smem = SOLO ? Shape<D>::kSoloSmem : Shape<D>::kSmem;
+  const cudaError_t e = tma::prepare(paged_attn_kernel<D, SPARSE, WHOLE, SOLO>, threads, smem,
                                      cache, &per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = units * p.cluster, wave = (int64_t)per_sm * device_sm_count();
+  const int64_t ctas = (int64_t)p.units * p.cluster, wave = (int64_t)per_sm * device_sm_count();
   p.trigger_from = ctas > wave ? (int)(ctas - wave) : 0;
-  return launch_clusters(paged_attn_kernel<D, SPARSE, WHOLE>,
-                         dim3((unsigned)ctas, (unsigned)p.splits), dim3(kWarps * 32),
-                         Shape<D>::kSmem, p.cluster, stream, p);
+  return launch_clusters(paged_attn_kernel<D, SPARSE, WHOLE, SOLO>,
+                         dim3((unsigned)ctas, (unsigned)p.splits), dim3(threads), smem, p.cluster,
+                         stream, p);
 }
 
 template <int D, bool SPARSE>
-cudaError_t launch_attn_page(const AttnParams& p, int64_t units, cudaStream_t stream) {
-  return p.page_size % kGroup == 0 ? launch_attn<D, SPARSE, true>(p, units, stream)
-                                   : launch_attn<D, SPARSE, false>(p, units, stream);
+cudaError_t launch_attn_page(const AttnParams& p, bool solo, cudaStream_t stream) {
+  if (p.page_size % kGroup != 0) return launch_attn<D, SPARSE, false, false>(p, stream);
+  return solo ? launch_attn<D, SPARSE, true, true>(p, stream)
+              : launch_attn<D, SPARSE, true, false>(p, stream);
 }
 
 template <bool SPARSE>
-cudaError_t launch_attn_dim(const AttnParams& p, int head_dim, int64_t units,
+cudaError_t launch_attn_dim(AttnParams p, int head_dim, int64_t units, const Spread& s,
                             cudaStream_t stream) {
+  p.units = (int)units;
+  p.cluster = s.cluster;
+  p.splits = s.splits;
   switch (head_dim) {
-    case 64: return launch_attn_page<64, SPARSE>(p, units, stream);
-    case 128: return launch_attn_page<128, SPARSE>(p, units, stream);
-    case 256: return launch_attn_page<256, SPARSE>(p, units, stream);
+    case 64: return launch_attn_page<64, SPARSE>(p, s.solo, stream);
+    case 128: return launch_attn_page<128, SPARSE>(p, s.solo, stream);
+    case 256: return launch_attn_page<256, SPARSE>(p, s.solo, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -742,14 +791,12 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
   p.topk = a.topk;
   p.tiles = sparse_tiles(x.num_heads_q, x.num_heads_kv);
   const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size, a.topk);
-  p.cluster = s.cluster;
-  p.splits = s.splits;
   p.direct = s.splits == 1;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   if (!p.direct)
     p.parts = partials_at(a.workspace, s.splits, (int64_t)x.num_tokens * x.num_heads_q, x.head_dim);
   const cudaError_t e = launch_attn_dim<true>(
-      p, x.head_dim, (int64_t)x.num_tokens * x.num_heads_kv * p.tiles, stream);
+      p, x.head_dim, (int64_t)x.num_tokens * x.num_heads_kv * p.tiles, s, stream);
   if (e != cudaSuccess || p.direct) return e;
   return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
 }
@@ -786,13 +833,11 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   p.prefix_len = tiles ? 0 : (int)a.prefix_len;
   const Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
                                  p.prefix_len, x.table_width);
-  p.cluster = s.cluster;
-  p.splits = s.splits;
   if (!tiles) {
     p.direct = s.splits == 1;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     if (!p.direct) p.parts = partials_at(a.workspace, s.splits, rows, x.head_dim);
-    const cudaError_t e = launch_attn_dim<false>(p, x.head_dim, units, stream);
+    const cudaError_t e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);
     if (e != cudaSuccess || p.direct) return e;
     return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
   }
@@ -804,7 +849,7 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess && own) {
     p.direct = false;
     p.first_slot = pre;
-    e = launch_attn_dim<false>(p, x.head_dim, units, stream);
+    e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);
   }
   if (e != cudaSuccess) return e;
   return launch_attn_join(p.parts, pre + own, x.head_dim, a.out, stream);
