@@ -600,7 +600,8 @@ struct JoinParams {
   int trigger_from;
 };
 
-// One warp per row; the row's weights are found by the lanes together.
+// One warp per row.  The lanes fetch the parts' sums together, 32 parts at a
+// time, and then the outputs, eight parts in flight.
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) attn_join_kernel(const JoinParams p) {
   grid_dependency_sync(p.trigger_from);
@@ -614,17 +615,37 @@ __global__ void __launch_bounds__(kWarps * 32) attn_join_kernel(const JoinParams
   const float ref = top == -INFINITY ? 0.f : top;
   float acc[V] = {};
   float sum = 0.f;
-  for (int s = 0; s < p.slots; ++s) {
-    const float lse = p.parts.lse[s * p.parts.rows + row];
-    if (lse == -INFINITY) continue;  // a part without a key
-    const float w = exp2f(lse - ref);  // may be 0; a NaN output still counts
-    sum += w;
-    const float* o = p.parts.o + (s * p.parts.rows + row) * D + V * lane;
+  for (int s0 = 0; s0 < p.slots; s0 += 32) {
+    const float lse =
+        s0 + lane < p.slots ? p.parts.lse[(s0 + lane) * p.parts.rows + row] : -INFINITY;
+    // a part without a key (its output may be unwritten) stays out; a weight of
+    // 0 does not: a NaN output still counts
+    const uint32_t full = __ballot_sync(kFullMask, lse != -INFINITY);
+    const float weight = exp2f(lse - ref);
+    const float* from = p.parts.o + (s0 * p.parts.rows + row) * D + V * lane;
+    const int count = min(32, p.slots - s0);
+    for (int s = 0; s < count; s += 8) {
+      float v[8][V];
 #pragma unroll
-    for (int k = 0; k < V; k += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(o + k);
-      acc[k] = fmaf(w, v.x, acc[k]);
-      acc[k + 1] = fmaf(w, v.y, acc[k + 1]);
+      for (int u = 0; u < 8; ++u) {
+        const bool there = s + u < count && (full >> (s + u) & 1);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float2 x = there ? *reinterpret_cast<const float2*>(
+                                       from + (int64_t)(s + u) * p.parts.rows * D + k)
+                                 : make_float2(0.f, 0.f);
+          v[u][k] = x.x, v[u][k + 1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = __shfl_sync(kFullMask, weight, (s + u) & 31);
+        if (s + u < count && (full >> (s + u) & 1)) {
+          sum += w;
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[k] = fmaf(w, v[u][k], acc[k]);
+        }
+      }
     }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
@@ -810,8 +831,7 @@ int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads
   int64_t slots = s == 1 ? 0 : s;
   if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len)) {
     // either way may be taken: which one depends on where the cache lies
-    const int64_t both = prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, head_dim,
-                                           page_size, prefix_len).parts +
+    const int64_t both = prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, prefix_len).parts +
                          shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, 0,
                                        table_width).splits;
     if (both > slots) slots = both;
@@ -841,16 +861,17 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess || p.direct) return e;
     return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
   }
-  const int pre = prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
-                                    x.page_size, a.prefix_len).parts;
+  const int pre =
+      prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, a.prefix_len).parts;
   const int own = x.table_width > 0 ? s.splits : 0;
   p.parts = partials_at(a.workspace, pre + own, rows, x.head_dim);
-  cudaError_t e = launch_prefix_tiles(a, map, p.parts, stream);
-  if (e == cudaSuccess && own) {
+  cudaError_t e = cudaSuccess;
+  if (own) {  // first: as its last CTAs run out, the prefix's start
     p.direct = false;
     p.first_slot = pre;
     e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);
   }
+  if (e == cudaSuccess) e = launch_prefix_tiles(a, map, p.parts, own == 0, stream);
   if (e != cudaSuccess) return e;
   return launch_attn_join(p.parts, pre + own, x.head_dim, a.out, stream);
 }

@@ -2,8 +2,13 @@
 // query rows of a kv head (every token, every head of its group) against the
 // prefix's keys and values.
 //
-// One CTA takes up to 256 query rows (two tiles of 128) and one part of the
-// prefix, 128 keys at a time.  Per tile and key block
+// The work is items of up to 256 query rows of one kv head (two tiles of 128)
+// times the prefix in blocks of 128 keys.  One CTA to an SM takes an equal
+// share of the blocks; the part of an item that falls to it is a segment.  The
+// CTAs that have the same blocks of a head, for different rows, keep in step,
+// so that keys and values come from memory once (each CTA on its own way
+// through 134 MB of them: 3300 cycles a block instead of 2500).  Per tile and
+// key block
 //   S = Q K^T   [128 x 128], fp32 in tensor memory,
 //   P = 2^(S scale log2(e) - m), rounded once to bf16, over S's columns,
 //   O += P V    [128 x D], fp32 in tensor memory, P read from there.
@@ -21,8 +26,8 @@
 //     ends past the prefix, or that lists a page outside the cache, is copied
 //     by the warp's own loads instead, with zeros in V where there is no key;
 //     the softmax gives those places weight 0.
-// The result is a partial (normalised O and log2 of the weight sum) for the
-// join with the other parts and with each token's own keys.
+// A segment's result is a partial (normalised O and log2 of the weight sum)
+// for the join with the item's other segments and each token's own keys.
 //
 // Bound by the tensor cores: 4 * 256 * 128 * D operations per 2 * 128 * D * 2
 // bytes of keys and values, which the L2 serves to the CTAs that share them.
@@ -41,7 +46,6 @@ constexpr int kMmaWarp = 16, kLoadWarp = 17;  // 17: K, 18: V
 // Registers of a thread: 640 x 96 at launch; the softmax groups take 104, the
 // last group keeps 56 (512 x 104 + 128 x 56 = 60416 of 61440).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
-constexpr int kMaxPages = 2048;       // pages of a part
 constexpr float kRescaleAt = 8.f;     // log2 by which a score may exceed m
 
 struct PrefixParams {
@@ -57,11 +61,15 @@ struct PrefixParams {
   int prefix_len;
   float scale_log2;  // >= 0
   uint32_t q_flip;   // sign bits flipped in Q where the scale is negative
-  int row_tiles;     // CTAs over the rows of one kv head
-  int share;         // blocks of a part
-  int first_slot;
+  int row_tiles;     // items of one kv head
+  int lanes;         // CTAs in step: the row tiles of a head, or 1
+  int teams;         // .. and how many times so many there are
+  int64_t items;     // of a lane
+  int blocks;        // of 128 keys, of an item
+  int slots;         // partials of an item, at most
   Partials parts;
   int* errors;
+  bool alone;        // no other kernel of this call runs before this one
 };
 
 template <int D>
@@ -71,17 +79,16 @@ struct Layout {
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kTile;
   static constexpr int kV = kK + 2 * kTile;
-  static constexpr int kList = kV + 2 * kTile;
-  static constexpr int kTops = kList + kMaxPages * 4;  // [2 blocks][2 halves][256 rows]
-  static constexpr int kBars = kTops + 4096;
+  static constexpr int kTops = kV + 2 * kTile;  // [2 blocks, and the sums][2 halves][256 rows]
+  static constexpr int kBars = kTops + 3 * 2048;
   static constexpr int kEnd = kBars + 24 * 8 + 32;
   static constexpr int kSmem = kEnd + 1024;          // room to align the base
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
 // mbarriers, by index
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 9, kPFull = 11,
-       kPvDone = 15, kDrain = 17, kBarriers = 18 };  // kPFull + 2 tile + part
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12,
+       kPvDone = 16, kDrain = 18, kBarriers = 19 };  // kPFull + 2 tile + part
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -139,6 +146,49 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+// The share of a CTA, walked segment by segment: of the blocks of its lane's
+// items, one item after the other, an equal part for each team.
+struct Segments {
+  int64_t at, stop;
+  int64_t item;
+  int first, n;       // the segment: blocks first .. first + n - 1 of the item
+  int kv_head;
+  int64_t row0;       // the item's first row
+  int64_t rows_left;  // rows of the kv head from there on
+  int tiles;
+  int lane, team;
+
+  __device__ __forceinline__ Segments(const PrefixParams& p) {
+    team = (int)blockIdx.x / p.lanes;
+    lane = (int)blockIdx.x - team * p.lanes;
+    const int64_t all = p.items * p.blocks;
+    at = team * all / p.teams;
+    stop = (team + 1) * all / p.teams;
+    n = 0;
+  }
+  __device__ __forceinline__ bool next(const PrefixParams& p) {
+    at += n;
+    if (at >= stop) return false;
+    item = at / p.blocks;
+    first = (int)(at - item * p.blocks);
+    n = (int)min((int64_t)(p.blocks - first), stop - at);
+    int tile = lane;
+    kv_head = (int)item;
+    if (p.lanes != p.row_tiles) {  // one lane: a head's row tiles one after the other
+      kv_head = (int)(item / p.row_tiles);
+      tile = (int)(item - (int64_t)kv_head * p.row_tiles);
+    }
+    row0 = (int64_t)tile * (2 * kTileRows);
+    rows_left = p.rows - row0;
+    tiles = rows_left > kTileRows ? 2 : 1;
+    return true;
+  }
+  // The item's segments are numbered from the team that has its first block.
+  __device__ __forceinline__ int slot(const PrefixParams& p) const {
+    return team - (int)(((item * p.blocks + 1) * p.teams - 1) / (p.items * p.blocks));
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
@@ -146,97 +196,95 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (base - tma::smem_addr(raw));
-  int* list = reinterpret_cast<int*>(smem + L::kList);
   volatile float* tops = reinterpret_cast<float*>(smem + L::kTops);
   const uint32_t bars = base + L::kBars;
   int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 24 * 8);
-  volatile int* dead = shared_state;      // a wait ran out
-  int* any_bad = shared_state + 1;        // a listed page lies outside the cache
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_state + 2);
+  volatile int* dead = shared_state;  // a wait ran out
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_state + 1);
   auto bar = [&](int i) { return bars + 8u * i; };
 
   const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int kv_head = blockIdx.x / p.row_tiles;
-  const int64_t row0 = (int64_t)(blockIdx.x % p.row_tiles) * (2 * kTileRows);
-  const int64_t rows_left = p.rows - row0;
-  const int tiles = rows_left > kTileRows ? 2 : 1;
-  const int key0 = (int)blockIdx.y * p.share * kKeys;
-  const int key1 = (int)min((int64_t)p.prefix_len, (int64_t)key0 + (int64_t)p.share * kKeys);
-  const int n = (key1 - key0 + kKeys - 1) / kKeys;  // at least 1
-  const int page0 = key0 >> p.page_shift;
-  const int listed = ((key1 - 1) >> p.page_shift) - page0 + 1;
+  // a block comes in pieces: a page, or 128 keys of one; lane i has piece i
+  const int piece_shift = min(p.page_shift, 7), pieces = kKeys >> piece_shift;
+  const int page_mask = (1 << p.page_shift) - 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBarriers; ++i) {
-      tma::mbar_init(bar(i), i == kQFull ? 16 : i >= kPFull && i < kPFull + 4 ? 8 : 1);
+      const bool by_warps = (i >= kQFull && i < kQFull + 2) || (i >= kPFull && i < kPFull + 4);
+      tma::mbar_init(bar(i), by_warps ? 8 : 1);
     }
     tma::mbar_init_fence();
     *dead = 0;
-    *any_bad = 0;
   }
   if (warp == kMmaWarp) tc::alloc512(tma::smem_addr(tmem_slot));
-  __syncthreads();
-  grid_dependency_wait();
-  for (int i = threadIdx.x; i < listed; i += kThreads) {
-    int page = __ldg(p.prefix_pages + page0 + i);
-    if (page < 0 || page >= p.num_pages) {
-      page = -1;
-      *any_bad = 1;
-      if (p.errors) atomicAdd(p.errors, 1);
-    }
-    list[i] = page;
-  }
+  // The kernel of the tokens' own keys, launched just before, reads and writes
+  // nothing that this one writes, and lets it be scheduled only after its own
+  // wait: what came before both is done.  Its end is waited for at this one's.
+  if (p.alone) grid_dependency_wait();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
+  Segments seg(p);
 
   if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ---------------------------------------------------------------------
-    // all 512 threads bring in Q, tile after tile
-    constexpr int FRAGS = D / 8;
-    for (int i = threadIdx.x; i < tiles * kTileRows * FRAGS; i += 512) {
-      const int r = i / FRAGS, c = i % FRAGS;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows_left) {
-        const int64_t t = (row0 + r) / p.group;
-        const int h = kv_head * p.group + (int)(row0 + r - t * p.group);
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (int64_t)h * D + 8 * c));
-        v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
-      }
-      st_shared16(base + L::kQ + (r >> 7) * L::kTile + tile_offset(r & 127, c), v);
-    }
-    tma::fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bar(kQFull));
-
     const int tile = warp >> 3, half = (warp >> 2) & 1;
     const int r = tile * kTileRows + (warp & 3) * 32 + lane;  // the thread's row
     const int pair_bar = 1 + tile * 4 + (warp & 3);           // its two warps' barrier
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
     const uint32_t s_at = at + 128 * tile + 64 * half, p_at = at + 128 * tile + 32 * half;
     const uint32_t o_at = at + 256 + 128 * tile + (D / 2) * half;
-    const bool ragged_end = ((key1 - key0) & (kKeys - 1)) != 0;
-    const bool bad = *any_bad != 0;
-    float m = -INFINITY, l = 0.f;
+    uint32_t done = 0;  // blocks of this tile so far: the phase of its barriers
     bool ok = true;
-    if (tile < tiles) {
-      for (int j = 0; j < n; ++j) {
-        ok = tc::wait_warp(bar(kSFull + tile), j & 1, dead);
+    while (ok && seg.next(p)) {
+      if (tile >= seg.tiles) continue;
+      // the tile's 256 threads bring in Q; the products that read the previous
+      // segment's have all been seen to be done
+      constexpr int FRAGS = D / 8, PASS = 256 / FRAGS;  // rows of one pass
+#pragma unroll 4
+      for (int i = 0; i < kTileRows / PASS; ++i) {
+        const int qr = i * PASS + (threadIdx.x & 255) / FRAGS, c = threadIdx.x % FRAGS;
+        const int64_t from = tile * kTileRows + qr;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (from < seg.rows_left) {
+          const uint32_t t = (uint32_t)(seg.row0 + from) / (uint32_t)p.group;
+          const int h = seg.kv_head * p.group + (int)((uint32_t)(seg.row0 + from) - t * p.group);
+          v = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (int64_t)h * D + 8 * c));
+          v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
+        }
+        st_shared16(base + L::kQ + tile * L::kTile + tile_offset(qr, c), v);
+      }
+      tma::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kQFull + tile));
+
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < seg.n; ++j, ++done) {
+        // pages of the block outside the cache: their keys are not there
+        const int key0 = (seg.first + j) * kKeys;
+        bool outside = false;
+        if (lane < pieces && key0 + (lane << piece_shift) < p.prefix_len) {
+          const int page =
+              __ldg(p.prefix_pages + ((key0 + (lane << piece_shift)) >> p.page_shift));
+          outside = page < 0 || page >= p.num_pages;
+        }
+        const uint32_t bad = __ballot_sync(kFullMask, outside);
+        ok = tc::wait_warp(bar(kSFull + tile), done & 1, dead);
         if (!ok) break;
         tc::fence_after();
         uint32_t s[2][32];
         tc::ld32(s[0], s_at);
         tc::ld32(s[1], s_at + 32);
         tc::wait_ld();
-        if (bad || (ragged_end && j == n - 1)) {
+        if (bad != 0 || p.prefix_len - key0 < kKeys) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const int key = key0 + j * kKeys + 64 * half + 32 * c + k;
-              if (key >= key1 || list[(key >> p.page_shift) - page0] < 0)
+              const int key = 64 * half + 32 * c + k;
+              if (key0 + key >= p.prefix_len || (bad >> (key >> piece_shift) & 1))
                 s[c][k] = 0xff800000u;  // -inf
             }
         }
@@ -253,16 +301,16 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         top = max3(top, __uint_as_float(s[0][31]),
                    fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31])));
         // the row's maximum over both halves; from here on both have read S
-        tops[(j & 1) * 512 + half * 256 + r] = top;
+        tops[(done & 1) * 512 + half * 256 + r] = top;
         pair_sync(pair_bar);
-        top = fmaxf(m, fmaxf(top, tops[(j & 1) * 512 + (half ^ 1) * 256 + r]));
+        top = fmaxf(m, fmaxf(top, tops[(done & 1) * 512 + (half ^ 1) * 256 + r]));
         if (__any_sync(kFullMask, (top - m) * p.scale_log2 > kRescaleAt)) {
           const float f = top == m ? 1.f : ex2((m - top) * p.scale_log2);
           l *= f;
           m = top;
           if (j > 0) {
             // O is at rest once the previous block's product is done
-            ok = tc::wait_warp(bar(kPvDone + tile), (j - 1) & 1, dead);
+            ok = tc::wait_warp(bar(kPvDone + tile), (done - 1) & 1, dead);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll 1
@@ -306,20 +354,20 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         l += sum0.f[0] + sum0.f[1];
       }
       // ---- the partial -----------------------------------------------------------------
-      if (ok) ok = tc::wait_warp(bar(kPvDone + tile), (n - 1) & 1, dead);
+      if (ok) ok = tc::wait_warp(bar(kPvDone + tile), (done - 1) & 1, dead);
       tc::fence_after();
-      // the halves' sums; not the slots of the last block's maxima
       if (ok) {
-        tops[(n & 1) * 512 + half * 256 + r] = l;
+        tops[1024 + half * 256 + r] = l;
         pair_sync(pair_bar);
-        l += tops[(n & 1) * 512 + (half ^ 1) * 256 + r];
+        l += tops[1024 + (half ^ 1) * 256 + r];
         ok = *dead == 0;
       } else {
         pair_leave(pair_bar);
       }
-      const int64_t t = (row0 + r) / p.group;
-      const int64_t row = t * p.num_q + kv_head * p.group + (row0 + r - t * p.group);
-      const int64_t slot = p.first_slot + blockIdx.y;
+      const uint32_t t = (uint32_t)(seg.row0 + r) / (uint32_t)p.group;
+      const int64_t row = (int64_t)t * p.num_q + seg.kv_head * p.group +
+                          (int)((uint32_t)(seg.row0 + r) - t * p.group);
+      const int slot = seg.slot(p);
       const float f = l == 0.f ? 0.f : 1.f / l;
       float* out = p.parts.o + (slot * p.parts.rows + row) * D + (D / 2) * half;
 #pragma unroll 1
@@ -327,7 +375,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         uint32_t o[32];
         tc::ld32(o, o_at + 32 * c);
         tc::wait_ld();
-        if (r < rows_left) {
+        if (r < seg.rows_left) {
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
             *reinterpret_cast<float4*>(out + 32 * c + k) =
@@ -335,11 +383,16 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
                             __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
         }
       }
-      if (half == 0 && r < rows_left)
+      if (half == 0 && r < seg.rows_left) {
         p.parts.lse[slot * p.parts.rows + row] =
             !ok ? NAN : l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m * p.scale_log2);
+        // an item has fewer segments than others: the slots left over are empty
+        if (seg.first + seg.n == p.blocks)
+          for (int k = slot + 1; k < p.slots; ++k)
+            p.parts.lse[k * p.parts.rows + row] = -INFINITY;
+      }
+      tc::fence_before();
     }
-    tc::fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
@@ -359,39 +412,47 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       }
       tc::commit(bar(kSFull + tile));
     };
-    bool ok = tc::wait_warp(bar(kQFull), 0, dead) && tc::wait_warp(bar(kKFull), 0, dead);
-    if (ok) {
-      tc::fence_after();
-      for (int t = 0; t < tiles; ++t) scores(t, 0);
-      tc::commit(bar(kKEmpty));
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      const int stage = j & 1, next = (j + 1) & 1;
-      const bool more = j + 1 < n;
-      ok = tc::wait_warp(bar(kVFull + stage), (j >> 1) & 1, dead) &&
-           (!more || tc::wait_warp(bar(kKFull + next), ((j + 1) >> 1) & 1, dead));
-      for (int t = 0; ok && t < tiles; ++t) {
-        const uint64_t v = v_desc + (uint32_t)(stage * (L::kTile >> 4));
-        for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
-          ok = tc::wait_warp(bar(kPFull + 2 * t + c), j & 1, dead);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = 4 * (i >> 1) + 2 * c + (i & 1);
-            tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4), pv,
-                       j > 0 || c > 0 || i > 0);
-          }
-        }
+    uint32_t block = 0, done[2] = {0, 0}, segs[2] = {0, 0};  // phases of the barriers
+    bool ok = true;
+    while (ok && seg.next(p)) {
+      ok = tc::wait_warp(bar(kKFull + (block & 1)), (block >> 1) & 1, dead);
+      for (int t = 0; ok && t < seg.tiles; ++t) {
+        ok = tc::wait_warp(bar(kQFull + t), segs[t]++ & 1, dead);
         if (!ok) break;
-        tc::commit(bar(kPvDone + t));
-        // the next scores go over P, which the products above read first:
-        // matrix instructions of one thread run in order
-        if (more) scores(t, next);
+        tc::fence_after();
+        scores(t, block & 1);
       }
       if (!ok) break;
-      tc::commit(bar(kVEmpty + stage));
-      if (more) tc::commit(bar(kKEmpty + next));
+      tc::commit(bar(kKEmpty + (block & 1)));
+      for (int j = 0; ok && j < seg.n; ++j, ++block) {
+        const int stage = block & 1, next = stage ^ 1;
+        const bool more = j + 1 < seg.n;
+        ok = tc::wait_warp(bar(kVFull + stage), (block >> 1) & 1, dead) &&
+             (!more || tc::wait_warp(bar(kKFull + next), ((block + 1) >> 1) & 1, dead));
+        for (int t = 0; ok && t < seg.tiles; ++t) {
+          const uint64_t v = v_desc + (uint32_t)(stage * (L::kTile >> 4));
+          for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
+            ok = tc::wait_warp(bar(kPFull + 2 * t + c), done[t] & 1, dead);
+            if (!ok) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 4 * (i >> 1) + 2 * c + (i & 1);
+              tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4),
+                         pv, j > 0 || c > 0 || i > 0);
+            }
+          }
+          if (!ok) break;
+          ++done[t];
+          tc::commit(bar(kPvDone + t));
+          // the next scores go over P, which the products above read first:
+          // matrix instructions of one thread run in order
+          if (more) scores(t, next);
+        }
+        if (!ok) break;
+        tc::commit(bar(kVEmpty + stage));
+        if (more) tc::commit(bar(kKEmpty + next));
+      }
     }
     if (!ok) {  // nothing may be in flight when the tensor memory goes
       tc::commit(bar(kDrain));
@@ -402,53 +463,60 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     // ---- the loads: one warp for K, one for V --------------------------------------------
     const int kv = warp - kLoadWarp;
-    const int page_size = 1 << p.page_shift;
-    const int box = min(page_size, kKeys), pieces = kKeys / box;
-    const int head = kv * p.num_kv + kv_head;
-    const int64_t head_elems = (int64_t)page_size * D;
+    const int64_t head_elems = ((int64_t)D) << p.page_shift;
+    uint32_t block = 0;
     int last = -1;  // latest block whose copies were started
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int stage = j & 1, first = key0 + j * kKeys;
-      const uint32_t full = bar((kv ? kVFull : kKFull) + stage);
-      const uint32_t dst = base + (kv ? L::kV : L::kK) + stage * L::kTile;
-      // lane i has piece i of the block
-      const int key = first + lane * box;
-      const int page = lane < pieces && key < key1 ? list[(key >> p.page_shift) - page0] : -1;
-      const bool whole = first + kKeys <= key1 &&
-                         __all_sync(kFullMask, lane >= pieces || page >= 0);
-      if (j >= 2) {
-        ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + stage), ((j >> 1) - 1) & 1, dead);
-        if (!ok) break;
-      }
-      if (whole) {
-        if (lane == 0) tma::mbar_arrive_expect_tx(full, L::kTile);
-        __syncwarp();
-        if (lane < pieces) {
+    while (ok && seg.next(p)) {
+      const int head = kv * p.num_kv + seg.kv_head;
+      for (int j = 0; j < seg.n; ++j, ++block) {
+        const int stage = block & 1, first = (seg.first + j) * kKeys;
+        const uint32_t full = bar((kv ? kVFull : kKFull) + stage);
+        const uint32_t dst = base + (kv ? L::kV : L::kK) + stage * L::kTile;
+        const int key = first + (lane << piece_shift);
+        int page = -1;
+        if (lane < pieces && key < p.prefix_len) {
+          page = __ldg(p.prefix_pages + (key >> p.page_shift));
+          if (page < 0 || page >= p.num_pages) {
+            page = -1;
+            if (p.errors && kv == 0) atomicAdd(p.errors, 1);
+          }
+        }
+        const bool here = __all_sync(kFullMask, lane >= pieces || page >= 0);
+        const bool whole = here && p.prefix_len - first >= kKeys;
+        if (block >= 2) {
+          ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + stage), ((block >> 1) - 1) & 1, dead);
+          if (!ok) break;
+        }
+        if (whole) {
+          if (lane == 0) tma::mbar_arrive_expect_tx(full, L::kTile);
+          __syncwarp();
+          if (lane < pieces) {
 #pragma unroll
-          for (int b = 0; b < L::kBlocks; ++b)
-            tma::tile_load_4d(dst + b * (128 * 128) + lane * box * 128, &p.map, 64 * b,
-                              key & (page_size - 1), head, page, full);
-        }
-        last = j;
-      } else {
-        constexpr int FRAGS = D / 8, RPW = 32 / FRAGS;
+            for (int b = 0; b < L::kBlocks; ++b)
+              tma::tile_load_4d(dst + b * (128 * 128) + (lane << (piece_shift + 7)), &p.map,
+                                64 * b, key & page_mask, head, page, full);
+          }
+          last = (int)block;
+        } else {
+          constexpr int FRAGS = D / 8, RPW = 32 / FRAGS;
 #pragma unroll 4
-        for (int r = lane / FRAGS; r < kKeys; r += RPW) {
-          const int k = first + r, c = lane % FRAGS;
-          const int from = k < key1 ? list[(k >> p.page_shift) - page0] : -1;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (from >= 0)
-            v = __ldg(reinterpret_cast<const uint4*>(
-                p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
-                (int64_t)(k & (page_size - 1)) * D + 8 * c));
-          st_shared16(dst + tile_offset(r, c), v);
+          for (int i = 0; i < kKeys / RPW; ++i) {
+            const int r = i * RPW + lane / FRAGS, c = lane % FRAGS, k = first + r;
+            const int from = __shfl_sync(kFullMask, page, r >> piece_shift);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (from >= 0 && k < p.prefix_len)
+              v = __ldg(reinterpret_cast<const uint4*>(
+                  p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
+                  (int64_t)(k & page_mask) * D + 8 * c));
+            st_shared16(dst + tile_offset(r, c), v);
+          }
+          tma::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(full);
         }
-        tma::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(full);
       }
-      __syncwarp();
     }
     if (!ok && last >= 0) {  // let the copies in flight land before the CTA may end
       const uint32_t full = bar((kv ? kVFull : kKFull) + (last & 1));
@@ -461,33 +529,13 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     tc::fence_after();
     tc::dealloc512(tmem);
   }
-}
-
-// Blocks of a part.  `items` CTAs each have `blocks` blocks to share among
-// `splits` of them, one CTA to an SM: the time of a plan is its waves times
-// (blocks of a part + the start and end of a CTA, about 3 blocks' time), and
-// each part's rows go through memory once more.
-int share_for(int64_t items, int64_t blocks, int64_t out_rows, int head_dim, int page_size) {
-  const int64_t room = (int64_t)kMaxPages * page_size / kKeys;  // blocks a list can hold
-  const double per_part = (double)out_rows * head_dim * 8 / 8e12 / 1.1e-6;
-  int64_t best = 1;
-  double best_cost = 1e300;
-  for (int64_t s = 1; s <= blocks && s <= 1024; ++s) {
-    const int64_t share = (blocks + s - 1) / s;
-    if (share > room) continue;
-    const int64_t parts = (blocks + share - 1) / share;
-    const int64_t waves = (items * parts + 151) / 152;
-    const double cost = (double)waves * (share + 3) + per_part * parts;
-    if (cost < best_cost) best_cost = cost, best = share;
-    if (items * s > 152 * 16) break;
-  }
-  if (best_cost == 1e300) best = room;
-  return (int)best;
+  // before this kernel counts as done the one before it has to be
+  if (!p.alone) grid_dependency_wait();
 }
 
 template <int D>
 cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partials& parts,
-                   cudaStream_t stream) {
+                   bool alone, cudaStream_t stream) {
   const PagedQuery& x = a.x;
   using L = Layout<D>;
   static std::atomic<int> cache[kMaxDevices];
@@ -510,16 +558,19 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   p.prefix_len = (int)a.prefix_len;
   p.scale_log2 = fabsf(a.scale) * kLog2e;
   p.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
-  p.row_tiles = (int)((p.rows + 2 * kTileRows - 1) / (2 * kTileRows));
-  const PrefixTilesPlan plan = prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, D,
-                                                 x.page_size, a.prefix_len);
-  p.share = plan.share;
-  p.first_slot = 0;
+  const PrefixTilesPlan plan =
+      prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, a.prefix_len);
+  p.row_tiles = plan.row_tiles;
+  p.lanes = plan.lanes;
+  p.teams = plan.teams;
+  p.items = (int64_t)plan.row_tiles / plan.lanes * x.num_heads_kv;
+  p.blocks = plan.blocks;
+  p.slots = plan.parts;
   p.parts = parts;
   p.errors = x.errors;
-  return launch_kernel(prefix_tiles_kernel<D>,
-                             dim3((unsigned)(p.row_tiles * x.num_heads_kv), (unsigned)plan.parts),
-                             dim3(kThreads), L::kSmem, stream, p);
+  p.alone = alone;
+  return launch_kernel(prefix_tiles_kernel<D>, dim3((unsigned)(plan.lanes * plan.teams)), dim3(kThreads),
+                       L::kSmem, stream, p);
 }
 
 }  // namespace
@@ -545,20 +596,27 @@ bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map) {
 }
 
 PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_heads_kv,
-                                  int head_dim, int page_size, int64_t prefix_len) {
+                                  int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
-  const int64_t blocks = (prefix_len + kKeys - 1) / kKeys;
-  const int64_t items = (rows + 2 * kTileRows - 1) / (2 * kTileRows) * num_heads_kv;
   PrefixTilesPlan plan;
-  plan.share = share_for(items, blocks, num_tokens * num_heads_q, head_dim, page_size);
-  plan.parts = (int)((blocks + plan.share - 1) / plan.share);
+  plan.row_tiles = (int)((rows + 2 * kTileRows - 1) / (2 * kTileRows));
+  plan.blocks = (int)((prefix_len + kKeys - 1) / kKeys);
+  // In step, if that leaves at most a fifth of the SMs without a CTA (which
+  // costs as much as reading out of step); every CTA has an item or two blocks.
+  const int fit = 152 / (plan.row_tiles < 152 ? plan.row_tiles : 152);
+  plan.lanes = plan.row_tiles <= 152 && fit * plan.row_tiles * 5 >= 152 * 4 ? plan.row_tiles : 1;
+  const int64_t items = (int64_t)plan.row_tiles / plan.lanes * num_heads_kv;
+  const int64_t all = items * plan.blocks, most = all / 2 > items ? all / 2 : items;
+  plan.teams = (int)(most < 152 / plan.lanes ? most : 152 / plan.lanes);
+  // an item's blocks fall to so many teams at most
+  plan.parts = (int)((plan.blocks - 1) * (int64_t)plan.teams / all) + 2;
   return plan;
 }
 
 cudaError_t launch_prefix_tiles(const PrefixAttnArgs& a, const CUtensorMap& map,
-                                const Partials& parts, cudaStream_t stream) {
-  return a.x.head_dim == 64 ? launch<64>(a, map, parts, stream)
-                            : launch<128>(a, map, parts, stream);
+                                const Partials& parts, bool alone, cudaStream_t stream) {
+  return a.x.head_dim == 64 ? launch<64>(a, map, parts, alone, stream)
+                            : launch<128>(a, map, parts, alone, stream);
 }
 
 }  // namespace kvq
