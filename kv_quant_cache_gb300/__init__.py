@@ -95,7 +95,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.kvq_set_dsv4_dispatch_threshold.argtypes = [_I64]
     L.kvq_dsv4_dispatch_path.restype = _I
     L.kvq_dsv4_dispatch_path.argtypes = [_I64, _I]
-    for op in ("qk", "dsv4"):
+    for op in ("qk", "dsv4", "prefix"):
         getattr(L, f"kvq_{op}_num_configs").restype = _I
         getattr(L, f"kvq_{op}_num_configs").argtypes = []
         getattr(L, f"kvq_{op}_config_name").restype = ctypes.c_char_p
@@ -600,7 +600,7 @@ def dsv4_dispatch_path(num_tokens: int, num_heads: int) -> int:
 
 
 def configs(op: str) -> list:
-    """Names of the launch configurations of ``op`` ("qk" or "dsv4")."""
+    """Names of the launch configurations of ``op`` ("qk", "dsv4" or "prefix")."""
     L = lib()
     n = getattr(L, f"kvq_{op}_num_configs")()
     return [getattr(L, f"kvq_{op}_config_name")(i).decode() for i in range(n)]
@@ -612,6 +612,7 @@ def set_config(op: str, config_id: int) -> int:
     prev = getattr(lib(), f"kvq_set_{op}_config")(int(config_id))
     if prev == -2:
         raise ValueError(f"{op}: no launch configuration {config_id}")
+    _WORKSPACE.clear()  # what a call needs may depend on it
     return prev
 
 

@@ -92,8 +92,15 @@ cudaError_t launch_block_select(const BlockSelectArgs& a, cudaStream_t stream);
 cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream);
 
+// The ways the prefix can be taken (kvq_set_prefix_config).
+extern const LaunchConfig kPrefixConfigs[];
+extern const int kPrefixNumConfigs;
+int set_prefix_config(int id);  // -1: by the sizes; returns the previous one
+int prefix_config();
+
 // Bytes of workspace the two attentions need (a multiple of 16; 0: none).
-// Depends on the sizes alone, so that it can be asked for without a device.
+// Depends on the sizes (and a forced configuration) alone, so that it can be
+// asked for without a device.
 int64_t sparse_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int topk);
 int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,

@@ -305,4 +305,15 @@ kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_
   return report_launch(kvq::launch_prefix_attn(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int kvq_prefix_num_configs(void) { return kvq::kPrefixNumConfigs; }
+
+const char* kvq_prefix_config_name(int id) {
+  return (id >= 0 && id < kvq::kPrefixNumConfigs) ? kvq::kPrefixConfigs[id].name : nullptr;
+}
+
+int kvq_set_prefix_config(int id) {
+  if (id >= kvq::kPrefixNumConfigs) return -2;
+  return kvq::set_prefix_config(id < 0 ? -1 : id);
+}
+
 }  // extern "C"

@@ -575,11 +575,31 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
 
 }  // namespace
 
+namespace {
+std::atomic<int> g_prefix_config{-1};
+}  // namespace
+
+const LaunchConfig kPrefixConfigs[] = {{"rows<4w>"}, {"tiles<20w,128x128>"}};
+const int kPrefixNumConfigs = 2;
+
+int set_prefix_config(int id) { return g_prefix_config.exchange(id, std::memory_order_relaxed); }
+int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
+
+// Sizes the tiles can take, and where they pay.  Up to 16 rows of a kv head are
+// one row tile of the other kernel, which reads the prefix once.  Beyond, each
+// of its row tiles reads it again, but it is one launch without partials: by
+// the products' size, GB300, us of the rows / the tiles (32 query heads, 8 kv
+// heads of 128): 2^21 (32 tokens x 2048 keys) 16.5 / 22.4, 2^22 (16 x 8192)
+// 24.6 / 29.1, 2^23 (32 x 8192) 39.5 / 27.3, 2^24 (16 x 32768) 70 / 47; heads
+// of 64, 2^22 (32 x 4096): 23.0 / 19.8.
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len) {
-  return (head_dim == 64 || head_dim == 128) && page_size >= 8 &&
-         (page_size & (page_size - 1)) == 0 && prefix_len > 0 &&
-         num_tokens * (num_heads_q / num_heads_kv) > 16;
+  const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
+  const bool can = (head_dim == 64 || head_dim == 128) && page_size >= 8 &&
+                   (page_size & (page_size - 1)) == 0 && prefix_len > 0;
+  const int forced = prefix_config();
+  if (!can || forced >= 0) return can && forced == 1;
+  return rows > 16 && rows * num_heads_kv > ((int64_t)head_dim << 15) / prefix_len;
 }
 
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map) {

@@ -328,13 +328,23 @@ def test_sparse_attention_rows_without_keys_and_bad_indices(cuda_device):
     assert not bool(bits(got[0, :2]).any())
 
 
+@pytest.fixture(params=["auto", "rows", "tiles"])
+def prefix_way(request):
+    """Both kernels that can take a prefix, and the choice between them."""
+    ids = {"auto": -1, "rows": 0, "tiles": 1}
+    old = kvq.set_config("prefix", ids[request.param])
+    yield request.param
+    kvq.set_config("prefix", old)
+
+
 @pytest.mark.parametrize("T,Hq,Hkv,D,page,prefix,width,q_len", [
     (1, 4, 1, 128, 64, 64, 3, 1), (4, 8, 2, 128, 64, 1000, 4, 1), (6, 4, 4, 64, 16, 257, 9, 2),
     (9, 14, 2, 128, 16, 1, 2, 3), (40, 8, 1, 64, 32, 2048, 1, 1), (3, 32, 1, 128, 7, 500, 30, 1),
     (5, 6, 3, 256, 16, 333, 20, 5), (70, 16, 2, 128, 64, 4100, 2, 1), (33, 4, 1, 256, 64, 700, 1, 3),
     (130, 8, 2, 64, 64, 129, 3, 2), (64, 8, 1, 128, 128, 1024, 0, 1), (257, 8, 4, 128, 16, 2049, 1, 1),
-    (100, 5, 1, 64, 1, 600, 5, 1), (20, 16, 1, 128, 300, 1500, 2, 4)])
-def test_prefix_attention(cuda_device, T, Hq, Hkv, D, page, prefix, width, q_len):
+    (100, 5, 1, 64, 1, 600, 5, 1), (20, 16, 1, 128, 300, 1500, 2, 4), (600, 8, 2, 64, 8, 1000, 1, 1),
+    (33, 8, 1, 128, 1024, 2500, 1, 1), (150, 4, 2, 128, 64, 9000, 2, 1), (21, 64, 1, 64, 64, 130, 1, 1)])
+def test_prefix_attention(cuda_device, prefix_way, T, Hq, Hkv, D, page, prefix, width, q_len):
     g = gen(T + Hq + D + prefix)
     R, P = -(-T // q_len), -(-prefix // page)
     q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, R, width, extra=P + 2)
@@ -357,7 +367,7 @@ def test_prefix_attention(cuda_device, T, Hq, Hkv, D, page, prefix, width, q_len
     assert int(err.item()) == 0
 
 
-def test_prefix_attention_without_prefix_or_keys(cuda_device):
+def test_prefix_attention_without_prefix_or_keys(cuda_device, prefix_way):
     g = gen(40)
     T, Hq, Hkv, D, page, width = 3, 8, 2, 128, 16, 4
     q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width)
@@ -376,7 +386,7 @@ def test_prefix_attention_without_prefix_or_keys(cuda_device):
 
 
 @pytest.mark.parametrize("T", [2, 40, 300])
-def test_prefix_attention_bad_pages(cuda_device, T):
+def test_prefix_attention_bad_pages(cuda_device, prefix_way, T):
     g = gen(41)
     Hq, Hkv, D, page, width, prefix = 4, 1, 128, 64, 2, 700
     q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=11)
@@ -393,7 +403,7 @@ def test_prefix_attention_bad_pages(cuda_device, T):
     assert int(err.item()) > 0
 
 
-def test_prefix_attention_large_scores_and_nonfinite_values(cuda_device):
+def test_prefix_attention_large_scores_and_nonfinite_values(cuda_device, prefix_way):
     """Logits of a thousand and more (no exponential may overflow), a NaN
     value and an infinite one that one request each sees (the infinite one
     gives NaN where its weight is zero)."""
@@ -415,7 +425,7 @@ def test_prefix_attention_large_scores_and_nonfinite_values(cuda_device):
 @pytest.mark.parametrize("T,Hq,Hkv,page,q_len,prefix", [
     (9, 4, 4, 16, 1, 40), (6, 8, 2, 64, 2, 0), (16, 1, 1, 1, 1, 5), (12, 6, 2, 5, 3, 33),
     (40, 8, 1, 16, 1, 300), (50, 3, 1, 8, 2, 129)])
-def test_nonfinite_values_stay_with_their_request(cuda_device, T, Hq, Hkv, page, q_len, prefix):
+def test_nonfinite_values_stay_with_their_request(cuda_device, prefix_way, T, Hq, Hkv, page, q_len, prefix):
     """Requests share a CTA's rows; NaN and infinite keys and values of one
     reach no row of another."""
     g = gen(T + page)
@@ -440,7 +450,7 @@ def test_nonfinite_values_stay_with_their_request(cuda_device, T, Hq, Hkv, page,
     ref.check(a, want, tol)
 
 
-def test_attention_of_a_strided_query_and_given_buffers(cuda_device):
+def test_attention_of_a_strided_query_and_given_buffers(cuda_device, prefix_way):
     g = gen(43)
     T, Hq, Hkv, D, page, width, prefix = 5, 8, 2, 128, 16, 20, 100
     _, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=9)
@@ -460,7 +470,7 @@ def test_attention_of_a_strided_query_and_given_buffers(cuda_device):
     ref.check(out, want, tol)
 
 
-def test_cache_offsets_past_32_bits(cuda_device):
+def test_cache_offsets_past_32_bits(cuda_device, prefix_way):
     """A cache of 9 GB: element offsets past 2^32 for the append, the bounds
     and the attentions."""
     T, Hq, Hkv, D, page = 4, 8, 8, 128, 64
@@ -561,7 +571,7 @@ def test_decode_steps_together(cuda_device):
                                               s["table"], lens, scale))
 
 
-def test_decode_steps_in_a_graph(cuda_device):
+def test_decode_steps_in_a_graph(cuda_device, prefix_way):
     """The same steps captured once and replayed give the eager results, bit
     for bit, also when two captured graphs are replayed in turn."""
     s = decode_state(70)
@@ -594,7 +604,7 @@ def test_decode_steps_in_a_graph(cuda_device):
             assert torch.equal(bits(d["cache"]), bits(eager["cache"]))
 
 
-def test_same_call_twice_is_the_same(cuda_device):
+def test_same_call_twice_is_the_same(cuda_device, prefix_way):
     g = gen(80)
     T, Hq, Hkv, D, page, width, prefix = 90, 8, 2, 128, 64, 3, 2000
     q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=32)
@@ -606,7 +616,7 @@ def test_same_call_twice_is_the_same(cuda_device):
         assert torch.equal(bits(a), bits(b))
 
 
-def test_two_streams_at_once(cuda_device):
+def test_two_streams_at_once(cuda_device, prefix_way):
     """Calls on two streams, each with its own workspace, do not disturb each
     other."""
     g = gen(81)

@@ -232,6 +232,24 @@ def test_plain_forms_agree_with_torch():
     assert torch.allclose(got, direct[None], rtol=1e-12)
 
 
+def test_prefix_configurations(L):
+    assert [n.split("<")[0] for n in kvq.configs("prefix")] == ["rows", "tiles"]
+    assert L.kvq_prefix_config_name(2) is None and L.kvq_prefix_config_name(-1) is None
+    with pytest.raises(ValueError):
+        kvq.set_config("prefix", 2)
+    # few rows need no workspace; forced through the tiles they do, sizes the
+    # tiles cannot take do not
+    f = L.paged_shared_prefix_attention_workspace
+    small, odd = (40, 8, 2, 128, 64, 500, 4), (40, 8, 2, 128, 24, 500, 4)
+    assert f(*small) == 0 and f(*odd) == 0
+    assert kvq.set_config("prefix", 1) == -1
+    try:
+        assert f(*small) > 0 and f(*odd) == 0
+    finally:
+        assert kvq.set_config("prefix", -1) == 1
+    assert f(256, 64, 8, 128, 64, 32768, 8) > 0
+
+
 def test_status_of_the_new_symbols(L):
     assert ctypes.sizeof(ctypes.c_int64) == 8
     for n in ("paged_kv_rope_append", "paged_kv_page_bounds", "paged_kv_block_select",
