@@ -280,7 +280,7 @@ kvq_status dsv4_kv_cache_gather_checked(const uint8_t* kv_cache, int64_t num_blo
  *                h / (num_heads_q / num_heads_kv).
  *   page_table   int32 [num_requests, table_width]: the pages of each request
  *                in order; entries past a request's length are not read.
- *                table_width at most 2^24.
+ *                table_width at most 2^22.
  *   requests     int32 [num_tokens]: the request of each token; NULL: token t
  *                is request t (num_requests >= num_tokens).
  *   lens         int32 [num_tokens]: how many keys of its request each token
@@ -420,7 +420,7 @@ kvq_status paged_block_sparse_attention(const void* q, int64_t q_stride, int64_t
  *
  *   prefix_pages  int32 [ceil(prefix_len / page_size)]; the last one may be
  *                 partly filled.  prefix_len 0 .. 2^31 - 1 (a host value), at
- *                 most 2^24 pages.
+ *                 most 2^22 pages.
  *   scale, out, arithmetic  as paged_block_sparse_attention.  table_width 0
  *                 (no keys but the prefix's) is allowed.
  */

@@ -365,6 +365,14 @@ def _launch(dev, stream, fn, *args) -> None:
         _check(st, fn.__name__)
 
 
+def _new(shape, dtype, dev):
+    """An output or workspace on the call's device (pinned host memory where
+    every tensor of the call is)."""
+    if dev >= 0:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return torch.empty(shape, dtype=dtype, pin_memory=True)
+
+
 def _counted(errors, dev):
     return None if errors is None else _ptr(errors, _I32, dev, "errors")
 
@@ -488,7 +496,7 @@ def paged_kv_block_select(q, bounds, page_table, lens, page_size, topk, keep_fir
     q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
     R, width = _requests(T, page_table, lens, requests)
     if out is None:
-        out = torch.empty((T, Hkv, topk), dtype=_I32, device=q.device)
+        out = _new((T, Hkv, topk), _I32, dev)
     elif out.shape != (T, Hkv, topk):
         raise ValueError("out must be [T, Hkv, topk]")
     _launch(dev, stream, (_LIB or lib()).paged_kv_block_select, q_ptr, q_stride, T, Hq, Hkv, D,
@@ -512,22 +520,22 @@ def _workspace_bytes(fn, *sizes) -> int:
     return need
 
 
-def _output(q, out):
+def _output(q, out, dev):
     if out is None:
-        return torch.empty(q.shape, dtype=_BF16, device=q.device)
+        return _new(q.shape, _BF16, dev)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     return out
 
 
-def _workspace(q, workspace, need, dev):
+def _workspace(workspace, need, dev):
     """A workspace of ``need`` bytes (allocated if not given), its address and
     its size.  One that is allocated here may be freed when the call returns:
     torch's allocator reuses memory in stream order."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(need, torch.uint8, dev)
     return (workspace, _ptr(workspace, workspace.dtype, dev, "workspace"),
             workspace.numel() * workspace.element_size())
 
@@ -547,8 +555,8 @@ def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=No
     if B != T or H != Hkv:
         raise ValueError("blocks must be [T, Hkv, topk]")
     R, width = _requests(T, page_table, lens, requests)
-    out = _output(q, out)
-    workspace, ws, ws_bytes = _workspace(q, workspace, _workspace_bytes(
+    out = _output(q, out, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, _workspace_bytes(
         "paged_block_sparse_attention_workspace", T, Hq, Hkv, D, page, topk), dev)
     _launch(dev, stream, (_LIB or lib()).paged_block_sparse_attention, q_ptr, q_stride, T, Hq,
             Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
@@ -573,8 +581,8 @@ def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_ta
     if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page < prefix_len:
         raise ValueError("prefix_pages must be 1-D and hold prefix_len keys")
     R, width = _requests(T, page_table, lens, requests)
-    out = _output(q, out)
-    workspace, ws, ws_bytes = _workspace(q, workspace, _workspace_bytes(
+    out = _output(q, out, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, _workspace_bytes(
         "paged_shared_prefix_attention_workspace", T, Hq, Hkv, D, page, prefix_len, width), dev)
     _launch(dev, stream, (_LIB or lib()).paged_shared_prefix_attention, q_ptr, q_stride, T, Hq,
             Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,

@@ -15,7 +15,7 @@ using kvq::report_launch;
 constexpr int64_t kIndexLimit = (int64_t)1 << 31;
 constexpr int kMaxPageSize = 1 << 16;
 constexpr int kMaxHeads = 1 << 16;
-constexpr int64_t kMaxListed = 1 << 24;  // pages of a request, a prefix or a selection
+constexpr int64_t kMaxListed = 1 << 22;  // pages of a request, a prefix or a selection
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

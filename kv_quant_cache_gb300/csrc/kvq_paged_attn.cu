@@ -45,7 +45,7 @@ constexpr int kWarps = 4;
 constexpr int kMaxCluster = 8;
 constexpr int kRows = 16;         // query rows of a CTA
 constexpr int kGroup = 16;        // keys of one step of a warp
-constexpr int kMaxPages = 2048;   // pages a CTA can list
+constexpr int kMaxPages = 2048;   // pages a CTA lists at a time
 constexpr int kSoloPages = 512;   // .. where it is a single warp
 
 // Whose a listed page is: of all rows, or of the rows of one token of the tile.
@@ -220,107 +220,7 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
   const int share = parts == 1 ? pages : (int)(((uint32_t)pages + parts - 1) / (uint32_t)parts);
   const int64_t begin = (int64_t)share * (blockIdx.y * p.cluster + rank);
   const int page0 = (int)min(begin, (int64_t)pages);
-  const int listed = min(share, pages - page0);
-  for (int i0 = 0; i0 < listed; i0 += kTeam * 32) {
-    const int i = i0 + (SOLO ? lane : (int)threadIdx.x);
-    const int at = page0 + i - prefix;  // among the tokens' own pages
-    // the token whose pages hold `at`: the number of tokens that end before
-    int tok = 0, skip = 0;
-    if (!SPARSE) {
-      for (int k = 0; k + 1 < tokens; ++k) tok += at >= __shfl_sync(kFullMask, end, k);
-      skip = __shfl_sync(kFullMask, end, max(tok - 1, 0));
-      if (tok == 0) skip = 0;
-    }
-    const int r = __shfl_sync(kFullMask, req, tok), n = __shfl_sync(kFullMask, len, tok);
-    int page = 0, valid = 0, whose = kAllRows;
-    if (i < listed) {
-      if (SPARSE) {
-        const int b = __ldg(p.blocks + ((int64_t)t0 * p.num_kv + kv_head) * p.topk + page0 + i);
-        if (b >= 0 && (int64_t)b * p.page_size < n) {
-          page = __ldg(p.table + (int64_t)r * p.table_width + b);
-          valid = min(p.page_size, n - b * p.page_size);
-        } else if (b != -1) {
-          rejected = true;
-        }
-      } else if (at < 0) {
-        page = __ldg(p.prefix_pages + page0 + i);
-        valid = (int)min((int64_t)p.page_size,
-                         p.prefix_len - (int64_t)(page0 + i) * p.page_size);
-      } else {
-        page = __ldg(p.table + (int64_t)r * p.table_width + (at - skip));
-        valid = (int)min((int64_t)p.page_size, n - (int64_t)(at - skip) * p.page_size);
-        whose = tok;
-      }
-      if (valid > 0 && (page < 0 || page >= p.num_pages)) {
-        rejected = true;
-        valid = 0;
-      }
-      list[i] = make_int2(page, valid | whose << kValidBits);
-    }
-  }
-  if (rejected && p.errors && (SOLO || warp == 0 || lane >= tokens || listed > 0))
-    atomicAdd(p.errors, 1);
-  if (SOLO) __syncwarp(); else __syncthreads();
-
-  // ---- the warp's groups of keys ---------------------------------------------------
-  const uint32_t total = (uint32_t)listed * page_size;  // below 2^31: checked at launch
-  const int steps = (int)((total + kGroup * kTeam - 1) / (kGroup * kTeam));
-  const int member = SOLO ? 0 : warp;  // of the team
-  const uint32_t ring = tma::smem_addr(smem) + warp * S::kRing;
-  const int64_t head_elems = (int64_t)p.page_size * D;
-  const int64_t v_from_k = p.num_kv * head_elems;
-  auto entry_of = [&](uint32_t key, int* off) {
-    const uint32_t at = shift >= 0 ? key >> shift : key / page_size;
-    *off = (int)(key - at * page_size);
-    return list[at];
-  };
-
-  // Starts the copies of step i's 16 keys.
-  auto issue = [&](int i) {
-    const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
-    const uint32_t stage = ring + (i % S::kStages) * S::kStage;
-    constexpr int FRAGS = D / 8;                          // 16-byte fragments of a row
-    constexpr int RPI = 32 / FRAGS > 0 ? 32 / FRAGS : 1;  // rows of one warp-wide copy
-    const int r0 = lane / FRAGS, c = lane % FRAGS;
-    if (WHOLE) {
-      int there = 0;  // keys of the group that exist
-      const __nv_bfloat16* src = p.cache + 8 * c;
-      if (i < steps && k0 < total) {
-        int off;
-        const int2 e = entry_of(k0, &off);
-        there = (e.y & ((1 << kValidBits) - 1)) - off;
-        if (there > 0)
-          src += ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)(off + r0) * D;
-      }
-#pragma unroll
-      for (int j = 0; j < kGroup / RPI; ++j) {
-        const int r = j * RPI + r0;
-        const bool ok = r < there;
-        const __nv_bfloat16* from = ok ? src + j * RPI * D : p.cache;
-        const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
-        cp_async16(dst, from, ok);
-        cp_async16(dst + S::kTile, ok ? from + v_from_k : from, ok);
-      }
-    } else {
-      int64_t row = -1;  // lane r < 16 finds row r's place
-      if (lane < kGroup && i < steps && k0 + lane < total) {
-        int off;
-        const int2 e = entry_of(k0 + lane, &off);
-        if (off < (e.y & ((1 << kValidBits) - 1)))
-          row = ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)off * D;
-      }
-#pragma unroll
-      for (int j = 0; j < kGroup / RPI; ++j) {
-        const int r = j * RPI + r0;
-        const int64_t from = __shfl_sync(kFullMask, row, r);
-        const __nv_bfloat16* src = p.cache + (from < 0 ? 0 : from + 8 * c);
-        const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
-        cp_async16(dst, src, from >= 0);
-        cp_async16(dst + S::kTile, from >= 0 ? src + v_from_k : src, from >= 0);
-      }
-    }
-    cp_commit();
-  };
+  const int page_end = page0 + min(share, pages - page0);
 
   float o[D / 8][4];
 #pragma unroll
@@ -329,141 +229,249 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
     for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-#pragma unroll
-  for (int i = 0; i < S::kStages - 1; ++i) issue(i);
-  for (int i = 0; i < steps; ++i) {
-    issue(i + S::kStages - 1);
-    cp_wait<S::kStages - 1>();
-    __syncwarp();
-    // whose the step's keys are: lane r < 16 for key r, -2 where there is none
-    const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
-    int whose = -2;
-    uint32_t todo;  // the keys that exist
-    if (WHOLE) {
-      int there = 0;
-      if (k0 < total) {
-        int off;
-        const int e = entry_of(k0, &off).y;
-        there = (e & ((1 << kValidBits) - 1)) - off;
-        whose = e >> kValidBits;
-      }
-      todo = there >= kGroup ? 0xffffu : there > 0 ? (1u << there) - 1u : 0u;
-    } else {
-      if (lane < kGroup && k0 + lane < total) {
-        int off;
-        const int e = entry_of(k0 + lane, &off).y;
-        if (off < (e & ((1 << kValidBits) - 1))) whose = e >> kValidBits;
-      }
-      todo = __ballot_sync(kFullMask, whose != -2);
+  // as many pages at a time as the list holds: usually all of them
+  constexpr int kCapacity = SOLO ? kSoloPages : kMaxPages;
+  for (int page_lo = page0; page_lo < page_end; page_lo += kCapacity) {
+    const int listed = min(kCapacity, page_end - page_lo);
+    if (page_lo != page0) {  // the list is no longer read
+      if (SOLO) __syncwarp(); else __syncthreads();
     }
-    if (todo == 0) {
-      __syncwarp();
-      continue;
+    for (int i0 = 0; i0 < listed; i0 += kTeam * 32) {
+      const int i = i0 + (SOLO ? lane : (int)threadIdx.x);
+      const int at = page_lo + i - prefix;  // among the tokens' own pages
+      // the token whose pages hold `at`: the number of tokens that end before
+      int tok = 0, skip = 0;
+      if (!SPARSE) {
+        for (int k = 0; k + 1 < tokens; ++k) tok += at >= __shfl_sync(kFullMask, end, k);
+        skip = __shfl_sync(kFullMask, end, max(tok - 1, 0));
+        if (tok == 0) skip = 0;
+      }
+      const int r = __shfl_sync(kFullMask, req, tok), n = __shfl_sync(kFullMask, len, tok);
+      int page = 0, valid = 0, whose = kAllRows;
+      if (i < listed) {
+        if (SPARSE) {
+          const int b = __ldg(p.blocks + ((int64_t)t0 * p.num_kv + kv_head) * p.topk + page_lo + i);
+          if (b >= 0 && (int64_t)b * p.page_size < n) {
+            page = __ldg(p.table + (int64_t)r * p.table_width + b);
+            valid = min(p.page_size, n - b * p.page_size);
+          } else if (b != -1) {
+            rejected = true;
+          }
+        } else if (at < 0) {
+          page = __ldg(p.prefix_pages + page_lo + i);
+          valid = (int)min((int64_t)p.page_size,
+                           p.prefix_len - (int64_t)(page_lo + i) * p.page_size);
+        } else {
+          page = __ldg(p.table + (int64_t)r * p.table_width + (at - skip));
+          valid = (int)min((int64_t)p.page_size, n - (int64_t)(at - skip) * p.page_size);
+          whose = tok;
+        }
+        if (valid > 0 && (page < 0 || page >= p.num_pages)) {
+          rejected = true;
+          valid = 0;
+        }
+        list[i] = make_int2(page, valid | whose << kValidBits);
+      }
     }
-    const uint32_t kt = ring + (i % S::kStages) * S::kStage, vt = kt + S::kTile;
-    float raw[2][4] = {};
-    {
-      const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t b[4];
-        ldmatrix4(b, kt + r * (2 * D) + (((2 * k + half) ^ (r & 7)) << 4));
-        mma16816(raw[0], qf[k], b[0], b[1]);
-        mma16816(raw[1], qf[k], b[2], b[3]);
-      }
-    }
-    // one round for all keys that the same rows see: a single one but where
-    // small pages of several tokens share the step
-    constexpr bool kMayMix = !SPARSE && !WHOLE;
-    const int first_seen_by = kMayMix ? __shfl_sync(kFullMask, whose, __ffs(todo) - 1) : 0;
-    const bool mixed =
-        kMayMix && __any_sync(kFullMask, whose != -2 && whose != first_seen_by);
-    while (todo) {
-      const int seen_by = SPARSE ? kAllRows
-                          : WHOLE ? whose : __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
-      const uint32_t mask = kMayMix ? __ballot_sync(kFullMask, whose == seen_by) : todo;
-      todo &= ~mask;
-      bool sees[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) sees[h] = SPARSE || seen_by == kAllRows || seen_by == mine[h];
-      // scores in units of log2: s * scale * log2(e); keys not seen -inf
-      float s[2][4];
-      float top[2] = {m[0], m[1]};
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = 8 * n + 2 * (lane & 3) + (k & 1);
-          s[n][k] = sees[k >> 1] && ((mask >> key) & 1) ? raw[n][k] * p.scale_log2 : -INFINITY;
-          top[k >> 1] = fmaxf(top[k >> 1], s[n][k]);
+    if (SOLO) __syncwarp(); else __syncthreads();
+
+    // ---- the warp's groups of keys ---------------------------------------------------
+    const uint32_t total = (uint32_t)listed * page_size;  // below 2^31
+    const int steps = (int)((total + kGroup * kTeam - 1) / (kGroup * kTeam));
+    const int member = SOLO ? 0 : warp;  // of the team
+    const uint32_t ring = tma::smem_addr(smem) + warp * S::kRing;
+    const int64_t head_elems = (int64_t)p.page_size * D;
+    const int64_t v_from_k = p.num_kv * head_elems;
+    auto entry_of = [&](uint32_t key, int* off) {
+      const uint32_t at = shift >= 0 ? key >> shift : key / page_size;
+      *off = (int)(key - at * page_size);
+      return list[at];
+    };
+
+    // Starts the copies of step i's 16 keys.
+    auto issue = [&](int i) {
+      const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
+      const uint32_t stage = ring + (i % S::kStages) * S::kStage;
+      constexpr int FRAGS = D / 8;                          // 16-byte fragments of a row
+      constexpr int RPI = 32 / FRAGS > 0 ? 32 / FRAGS : 1;  // rows of one warp-wide copy
+      const int r0 = lane / FRAGS, c = lane % FRAGS;
+      if (WHOLE) {
+        int there = 0;  // keys of the group that exist
+        const __nv_bfloat16* src = p.cache + 8 * c;
+        if (i < steps && k0 < total) {
+          int off;
+          const int2 e = entry_of(k0, &off);
+          there = (e.y & ((1 << kValidBits) - 1)) - off;
+          if (there > 0)
+            src += ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)(off + r0) * D;
         }
-      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 2));
-      }
-      if (__any_sync(kFullMask, top[0] != m[0] || top[1] != m[1])) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
-          const float f = top[h] == m[h] ? 1.f : exp2f(m[h] - top[h]);
-          l[h] *= f;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
-          m[h] = top[h];
-        }
-      }
-      uint32_t pf[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        float e[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float ref = m[k >> 1] == -INFINITY ? 0.f : m[k >> 1];
-          e[k] = exp2f(s[n][k] - ref);
-        }
-        l[0] += e[0] + e[1];
-        l[1] += e[2] + e[3];
-        pf[2 * n] = pack_bf16x2(e[0], e[1]);
-        pf[2 * n + 1] = pack_bf16x2(e[2], e[3]);
-      }
-      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
-      if (SPARSE || seen_by == kAllRows) {
-        // zeros in V where there is no key, and every row sees the others
-        // (in a mixed step the others' keys have weight 0 here, but a NaN
-        // value of theirs would not stay out: they are cleared)
-        const uint32_t keep = mixed ? mask : 0xffffu;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t b[4];
-          ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
-          if (kMayMix && mixed) keep_keys(b, keep, lane);
-          mma16816(o[2 * n], pf, b[0], b[1]);
-          mma16816(o[2 * n + 1], pf, b[2], b[3]);
+        for (int j = 0; j < kGroup / RPI; ++j) {
+          const int r = j * RPI + r0;
+          const bool ok = r < there;
+          const __nv_bfloat16* from = ok ? src + j * RPI * D : p.cache;
+          const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
+          cp_async16(dst, from, ok);
+          cp_async16(dst + S::kTile, ok ? from + v_from_k : from, ok);
         }
       } else {
-        // other tokens' rows keep their sums whatever these values are (a
-        // zero weight times an infinite or NaN value would reach them)
+        int64_t row = -1;  // lane r < 16 finds row r's place
+        if (lane < kGroup && i < steps && k0 + lane < total) {
+          int off;
+          const int2 e = entry_of(k0 + lane, &off);
+          if (off < (e.y & ((1 << kValidBits) - 1)))
+            row = ((int64_t)e.x * 2 * p.num_kv + kv_head) * head_elems + (int64_t)off * D;
+        }
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
+        for (int j = 0; j < kGroup / RPI; ++j) {
+          const int r = j * RPI + r0;
+          const int64_t from = __shfl_sync(kFullMask, row, r);
+          const __nv_bfloat16* src = p.cache + (from < 0 ? 0 : from + 8 * c);
+          const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
+          cp_async16(dst, src, from >= 0);
+          cp_async16(dst + S::kTile, from >= 0 ? src + v_from_k : src, from >= 0);
+        }
+      }
+      cp_commit();
+    };
+
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < steps; ++i) {
+      issue(i + S::kStages - 1);
+      cp_wait<S::kStages - 1>();
+      __syncwarp();
+      // whose the step's keys are: lane r < 16 for key r, -2 where there is none
+      const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
+      int whose = -2;
+      uint32_t todo;  // the keys that exist
+      if (WHOLE) {
+        int there = 0;
+        if (k0 < total) {
+          int off;
+          const int e = entry_of(k0, &off).y;
+          there = (e & ((1 << kValidBits) - 1)) - off;
+          whose = e >> kValidBits;
+        }
+        todo = there >= kGroup ? 0xffffu : there > 0 ? (1u << there) - 1u : 0u;
+      } else {
+        if (lane < kGroup && k0 + lane < total) {
+          int off;
+          const int e = entry_of(k0 + lane, &off).y;
+          if (off < (e & ((1 << kValidBits) - 1))) whose = e >> kValidBits;
+        }
+        todo = __ballot_sync(kFullMask, whose != -2);
+      }
+      if (todo == 0) {
+        __syncwarp();
+        continue;
+      }
+      const uint32_t kt = ring + (i % S::kStages) * S::kStage, vt = kt + S::kTile;
+      float raw[2][4] = {};
+      {
+        const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
           uint32_t b[4];
-          ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
-          if (kMayMix && mixed) keep_keys(b, mask, lane);
+          ldmatrix4(b, kt + r * (2 * D) + (((2 * k + half) ^ (r & 7)) << 4));
+          mma16816(raw[0], qf[k], b[0], b[1]);
+          mma16816(raw[1], qf[k], b[2], b[3]);
+        }
+      }
+      // one round for all keys that the same rows see: a single one but where
+      // small pages of several tokens share the step
+      constexpr bool kMayMix = !SPARSE && !WHOLE;
+      const int first_seen_by = kMayMix ? __shfl_sync(kFullMask, whose, __ffs(todo) - 1) : 0;
+      const bool mixed =
+          kMayMix && __any_sync(kFullMask, whose != -2 && whose != first_seen_by);
+      while (todo) {
+        const int seen_by = SPARSE ? kAllRows
+                            : WHOLE ? whose : __shfl_sync(kFullMask, whose, __ffs(todo) - 1);
+        const uint32_t mask = kMayMix ? __ballot_sync(kFullMask, whose == seen_by) : todo;
+        todo &= ~mask;
+        bool sees[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float x[4] = {o[2 * n + u][0], o[2 * n + u][1], o[2 * n + u][2], o[2 * n + u][3]};
-            mma16816(x, pf, b[2 * u], b[2 * u + 1]);
+        for (int h = 0; h < 2; ++h) sees[h] = SPARSE || seen_by == kAllRows || seen_by == mine[h];
+        // scores in units of log2: s * scale * log2(e); keys not seen -inf
+        float s[2][4];
+        float top[2] = {m[0], m[1]};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (sees[k >> 1]) o[2 * n + u][k] = x[k];
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = 8 * n + 2 * (lane & 3) + (k & 1);
+            s[n][k] = sees[k >> 1] && ((mask >> key) & 1) ? raw[n][k] * p.scale_log2 : -INFINITY;
+            top[k >> 1] = fmaxf(top[k >> 1], s[n][k]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 1));
+          top[h] = fmaxf(top[h], __shfl_xor_sync(kFullMask, top[h], 2));
+        }
+        if (__any_sync(kFullMask, top[0] != m[0] || top[1] != m[1])) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
+            const float f = top[h] == m[h] ? 1.f : exp2f(m[h] - top[h]);
+            l[h] *= f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+            m[h] = top[h];
+          }
+        }
+        uint32_t pf[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float ref = m[k >> 1] == -INFINITY ? 0.f : m[k >> 1];
+            e[k] = exp2f(s[n][k] - ref);
+          }
+          l[0] += e[0] + e[1];
+          l[1] += e[2] + e[3];
+          pf[2 * n] = pack_bf16x2(e[0], e[1]);
+          pf[2 * n + 1] = pack_bf16x2(e[2], e[3]);
+        }
+        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+        if (SPARSE || seen_by == kAllRows) {
+          // zeros in V where there is no key, and every row sees the others
+          // (in a mixed step the others' keys have weight 0 here, but a NaN
+          // value of theirs would not stay out: they are cleared)
+          const uint32_t keep = mixed ? mask : 0xffffu;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
+            if (kMayMix && mixed) keep_keys(b, keep, lane);
+            mma16816(o[2 * n], pf, b[0], b[1]);
+            mma16816(o[2 * n + 1], pf, b[2], b[3]);
+          }
+        } else {
+          // other tokens' rows keep their sums whatever these values are (a
+          // zero weight times an infinite or NaN value would reach them)
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, vt + r * (2 * D) + (((2 * n + half) ^ (r & 7)) << 4));
+            if (kMayMix && mixed) keep_keys(b, mask, lane);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float x[4] = {o[2 * n + u][0], o[2 * n + u][1], o[2 * n + u][2], o[2 * n + u][3]};
+              mma16816(x, pf, b[2 * u], b[2 * u + 1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (sees[k >> 1]) o[2 * n + u][k] = x[k];
+            }
           }
         }
       }
+      __syncwarp();  // the stage is read before its next copies start
     }
-    __syncwarp();  // the stage is read before its next copies start
+    cp_wait<0>();
   }
-  cp_wait<0>();
+  if (rejected && p.errors) atomicAdd(p.errors, 1);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(kFullMask, l[h], 1);
@@ -677,8 +685,7 @@ struct Spread {
 // each keeps at least two steps of 16 keys for every warp: first within a
 // cluster of up to 8 (joined in place); beyond that, as partials that a second launch joins,
 // only where a CTA would be left with more than 2048 keys (below, the second
-// launch costs more than it saves).  No CTA may have more pages than fit its
-// list.
+// launch costs more than it saves).
 Spread spread_for(int64_t units, int64_t pages, int page_size) {
   Spread s = {1, 1, false};
   const int64_t keys = pages * page_size;
@@ -687,15 +694,14 @@ Spread spread_for(int64_t units, int64_t pages, int page_size) {
     s.cluster *= 2;
   int64_t splits = 1;
   while (units * s.cluster * (splits + 1) <= 2 * 152 && keys > s.cluster * splits * 2048) ++splits;
-  const int64_t least = (pages + (int64_t)s.cluster * kMaxPages - 1) / ((int64_t)s.cluster * kMaxPages);
-  s.splits = (int)(splits > least ? splits : least);
+  s.splits = (int)splits;
   // With many tiles of short ranges, a CTA of one warp each: no joins between
   // warps, and four times as many tiles in flight (640 tiles of 512 keys 32 us
   // against 38 us, of 1024 keys 58 against 66; 1024 tiles of up to 200 keys 38
   // against 51).  Longer ranges keep the four warps: the last tiles of a wave
   // take four times as long on one (1280 tiles of 1024 keys 127 us against
   // 108; 1024 tiles of 2 to 1152 keys 91 against 82).
-  s.solo = units >= 4 * 152 && keys <= 512 && pages <= kSoloPages;
+  s.solo = units >= 4 * 152 && keys <= 512;
   return s;
 }
 

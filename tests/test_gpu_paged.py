@@ -636,3 +636,94 @@ def test_two_streams_at_once(cuda_device, prefix_way):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(bits(a), bits(b))
+
+
+def test_long_lists_of_small_pages(cuda_device, prefix_way):
+    """More pages than a CTA lists at a time, in the prefix, in a request and
+    in a selection."""
+    g = gen(90)
+    T, Hq, Hkv, D, page, width, prefix = 3, 4, 1, 64, 1, 5000, 20000
+    N = 6000
+    q, cache = normal(g, T, Hq, D), normal(g, N, 2, Hkv, page, D)
+    table = ints(g, 0, N - 1, T, width)   # pages listed several times
+    pages = ints(g, 0, N - 1, prefix)
+    lens = torch.tensor([width, 4500, 3], dtype=torch.int32)
+    got = kvq.paged_shared_prefix_attention(q.cuda(), cache.cuda(), pages.cuda(), prefix,
+                                            table.cuda(), lens.cuda())
+    ref.check(got, *ref.prefix_attention(q, cache, pages, prefix, table, lens, D ** -0.5))
+    blocks = torch.arange(width, dtype=torch.int32).expand(T, Hkv, width).contiguous()
+    blocks[2, 0, 3:] = -1
+    got = kvq.paged_block_sparse_attention(q.cuda(), cache.cuda(), table.cuda(), blocks.cuda(),
+                                           lens.cuda())
+    blocks[1, 0, 4500:] = -1
+    ref.check(got, *ref.sparse_attention(q, cache, table, blocks, lens, D ** -0.5))
+
+
+def test_many_rows_with_long_small_pages(cuda_device):
+    """Many row tiles, so that a CTA has a whole long list to itself."""
+    g = gen(91)
+    T, Hq, Hkv, D, page, width = 700, 1, 1, 64, 16, 300
+    N = 400
+    q, cache = normal(g, T, Hq, D), normal(g, N, 2, Hkv, page, D)
+    table = ints(g, 0, N - 1, T, width)
+    lens = ints(g, 0, 40, T)
+    lens[5], lens[699] = width * page, 3000
+    none = torch.zeros(0, dtype=torch.int32)
+    got = kvq.paged_shared_prefix_attention(q.cuda(), cache.cuda(), none.cuda(), 0, table.cuda(),
+                                            lens.cuda())
+    ref.check(got, *ref.prefix_attention(q, cache, none, 0, table, lens, D ** -0.5))
+
+
+def test_many_tokens_with_few_blocks(cuda_device):
+    """Row tiles in their hundreds with a short selection each: a warp a tile."""
+    g = gen(92)
+    for T, Hq, Hkv, D, page in ((330, 8, 2, 128, 16), (90, 14, 7, 64, 64), (40, 32, 16, 256, 32)):
+        width = 12
+        q, cache, table, _ = paged_inputs(g, T, Hq, Hkv, D, page, T, width)
+        lens = ints(g, 0, width * page, T)
+        blocks = random_blocks(g, T, Hkv, 512 // page if page < 64 else 5, width, lens, page)
+        got = kvq.paged_block_sparse_attention(q.cuda(), cache.cuda(), table.cuda(), blocks.cuda(),
+                                               lens.cuda())
+        ref.check(got, *ref.sparse_attention(q, cache, table, blocks, lens, D ** -0.5))
+
+
+def test_no_tokens(cuda_device):
+    cache = torch.zeros(4, 2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    bounds = torch.zeros(4, 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    i64 = torch.zeros(0, dtype=torch.int64, device="cuda")
+    kvq.paged_kv_rope_append(torch.zeros(0, 512, dtype=torch.bfloat16, device="cuda"), 4, 2, 64,
+                             None, True, None, i64, cache)
+    kvq.paged_kv_page_bounds(cache, i64, i32(0), bounds)
+    assert kvq.paged_kv_block_select(q, bounds, i32(3, 5), i32(0), 16, 2).shape == (0, 2, 2)
+    assert kvq.paged_block_sparse_attention(q, cache, i32(3, 5), i32(0, 2, 2),
+                                            i32(0)).shape == (0, 4, 64)
+    assert kvq.paged_shared_prefix_attention(q, cache, i32(2), 20, i32(3, 5),
+                                             i32(0)).shape == (0, 4, 64)
+
+
+def test_pinned_host_tensors(cuda_device, prefix_way):
+    """The cache and the inputs in pinned host memory: the same results, bit
+    for bit, as from device memory (the tiles take device memory alone)."""
+    g = gen(93)
+    T, Hq, Hkv, D, page, width, prefix, topk = 20, 8, 2, 64, 16, 8, 90, 3
+    q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=6)
+    bounds = bounds_of(g, cache.shape[0], Hkv, D)
+    lens = ints(g, 1, width * page, T)
+    pages = spare.int()
+    old = kvq.set_config("prefix", 0) if prefix_way == "tiles" else None
+
+    def run(where):
+        x = [where(t) for t in (q, cache, table, bounds, lens, pages)]
+        blocks = kvq.paged_kv_block_select(x[0], x[3], x[2], x[4], page, topk)
+        a = kvq.paged_block_sparse_attention(x[0], x[1], x[2], blocks, x[4])
+        b = kvq.paged_shared_prefix_attention(x[0], x[1], x[5], prefix, x[2], x[4])
+        torch.cuda.synchronize()
+        return blocks.cpu(), bits(a), bits(b)
+
+    want = run(lambda t: t.cuda())
+    if old is not None:
+        kvq.set_config("prefix", old)
+    for a, b in zip(run(lambda t: t.pin_memory()), want):
+        assert torch.equal(a, b)

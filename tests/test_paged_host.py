@@ -75,7 +75,7 @@ BAD_QUERY = [
     (dict(q=None), 1), (dict(cache=None), 1), (dict(table=None), 1), (dict(lens=None), 1),
     (dict(T=-1), 2), (dict(T=2 ** 31), 2), (dict(T=2 ** 62), 2), (dict(Hq=3), 2), (dict(Hq=0), 2),
     (dict(Hkv=0), 2), (dict(page=0), 2), (dict(pages=-1), 2), (dict(R=-1), 2), (dict(width=-1), 2),
-    (dict(width=2 ** 24 + 1), 2), (dict(R=3), 2), (dict(stride=511), 2), (dict(stride=2 ** 40), 2),
+    (dict(width=2 ** 22 + 1), 2), (dict(R=3), 2), (dict(stride=511), 2), (dict(stride=2 ** 40), 2),
     (dict(D=96), 3), (dict(q=A + 8), 4), (dict(stride=516), 4), (dict(cache=A + 8), 4),
     (dict(table=MIS), 4), (dict(req=MIS), 4), (dict(lens=MIS), 4), (dict(err=MIS), 4)]
 
@@ -109,7 +109,7 @@ def prefix(L, ids=A, length=50, scale=0.1, out=0x900000, ws=0x800000, ws_bytes=1
 @pytest.mark.parametrize("call", [select, sparse, prefix])
 def test_query_validation(L, call):
     for k, want in BAD_QUERY:
-        if call is select and k == dict(width=2 ** 24 + 1):
+        if call is select and k == dict(width=2 ** 22 + 1):
             continue
         assert rejected(call(L, **k)) == want, k
     assert call(L, T=0, q=None, cache=None, table=None, lens=None) == kvq.KVQ_OK
@@ -117,7 +117,7 @@ def test_query_validation(L, call):
 
 def test_select_validation(L):
     for k in (dict(topk=0), dict(topk=-1), dict(first=-1), dict(last=-1), dict(T=2 ** 28),
-              dict(width=2 ** 24 + 1)):
+              dict(width=2 ** 22 + 1)):
         assert rejected(select(L, **k)) == kvq.KVQ_ERR_SHAPE, k
     assert rejected(select(L, width=16385)) == kvq.KVQ_ERR_UNSUPPORTED
     assert rejected(select(L, blocks=None)) == kvq.KVQ_ERR_NULL
@@ -147,10 +147,10 @@ def test_key_list_validation(L):
     assert rejected(sparse(L, blocks=None)) == kvq.KVQ_ERR_NULL
     assert rejected(sparse(L, blocks=MIS)) == kvq.KVQ_ERR_ALIGN
     assert rejected(sparse(L, topk=0)) == kvq.KVQ_ERR_SHAPE
-    assert rejected(sparse(L, topk=2 ** 24 + 1)) == kvq.KVQ_ERR_SHAPE
+    assert rejected(sparse(L, topk=2 ** 22 + 1)) == kvq.KVQ_ERR_SHAPE
     assert rejected(prefix(L, ids=None)) == kvq.KVQ_ERR_NULL
     assert rejected(prefix(L, ids=MIS)) == kvq.KVQ_ERR_ALIGN
-    for length in (-1, 2 ** 31, 2 ** 24 * 16 + 1, 2 ** 62):
+    for length in (-1, 2 ** 31, 2 ** 22 * 16 + 1, 2 ** 62):
         assert rejected(prefix(L, length=length)) == kvq.KVQ_ERR_SHAPE
 
 
