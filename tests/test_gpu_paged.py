@@ -727,3 +727,31 @@ def test_pinned_host_tensors(cuda_device, prefix_way):
         kvq.set_config("prefix", old)
     for a, b in zip(run(lambda t: t.pin_memory()), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("page,q_len,Hq,Hkv,D", [(16, 4, 4, 1, 64), (64, 3, 8, 2, 128), (5, 4, 2, 1, 64),
+                                                 (16, 2, 16, 1, 256), (128, 16, 1, 1, 64)])
+def test_causal_chunk_of_a_request(cuda_device, prefix_way, page, q_len, Hq, Hkv, D):
+    """Tokens of one request that see different lengths of it share its pages
+    in a CTA; what only a later one sees (here NaN) stays with that one."""
+    g = gen(page + q_len)
+    R, width, prefix = 7, -(-90 // page), 40
+    T = R * q_len
+    q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, R, width,
+                                          extra=-(-prefix // page))
+    requests = (torch.arange(T) // q_len).int()
+    lens = ints(g, 1, 60, R).repeat_interleave(q_len) + (torch.arange(T) % q_len).int()
+    lens[q_len:2 * q_len] = lens[q_len:2 * q_len].flip(0)  # any order of the lengths
+    last = int(lens[2 * q_len - 1 + q_len])                # request 2's longest length
+    spoiled = cache.clone()
+    at = last - 1
+    spoiled[table[2, at // page].long(), :, :, at % page] = NAN
+    args = (spare.int().cuda(), prefix, table.cuda(), lens.cuda())
+    got = [kvq.paged_shared_prefix_attention(q.cuda(), c.cuda(), *args,
+                                             requests=requests.cuda()).cpu()
+           for c in (cache, spoiled)]
+    want, tol = ref.prefix_attention(q, cache, spare, prefix, table, lens, D ** -0.5, requests)
+    ref.check(got[0], want, tol)
+    sees = (requests == 2) & (lens >= last)
+    assert int(sees.sum()) == 1 and bool(got[1][sees].isnan().all())
+    assert torch.equal(bits(got[0][~sees]), bits(got[1][~sees]))
