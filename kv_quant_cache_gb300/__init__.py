@@ -365,11 +365,17 @@ def _launch(dev, stream, fn, *args) -> None:
         _check(st, fn.__name__)
 
 
+_DEVICES = {}
+
+
 def _new(shape, dtype, dev):
     """An output or workspace on the call's device (pinned host memory where
     every tensor of the call is)."""
     if dev >= 0:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        where = _DEVICES.get(dev)
+        if where is None:  # building a device object costs more than the look-up
+            where = _DEVICES[dev] = torch.device("cuda", dev)
+        return torch.empty(shape, dtype=dtype, device=where)
     return torch.empty(shape, dtype=dtype, pin_memory=True)
 
 

@@ -10,13 +10,9 @@
 // group's sums are taken once, so a block costs 2 D products whatever the
 // group's size: bound by reading the bounds once.
 //
-// One cluster of 1..8 CTAs takes a token and one or several of its kv heads.
-// Its CTAs score a share of the blocks each, warps side by side on the heads:
-// a page's heads lie next to each other, and read together they are one
-// contiguous stretch (64 tokens x 8 heads x 1024 blocks, heads apart: 78 us,
-// 3.9 TB/s while scoring; 512-byte pieces at random do not keep the memory
-// busy).  The fp32 scores go into the shared memory of the CTA that selects
-// for their head.
+// One cluster of 1..8 CTAs takes a token and kv head.  Its CTAs score a share
+// of the blocks each, their fp32 scores go into the first CTA's shared memory,
+// and that CTA selects.
 //
 // Which block is k-th must not depend on fp32 rounding: the set a token
 // attends to is an integer result.  The scoring warps carry the largest
@@ -41,7 +37,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kSlots = 2;  // heads that one CTA selects for, at most
 
 struct SelectParams {
   const __nv_bfloat16* q;
@@ -57,10 +52,7 @@ struct SelectParams {
   int topk, keep_first, keep_last;
   int* blocks;
   int* errors;
-  int cluster;     // CTAs of a cluster
-  int heads;       // kv heads of a cluster, at most kWarps
-  int slots;       // heads a CTA selects for
-  int head_groups; // clusters of a token
+  int cluster;  // CTAs of a cluster
 };
 
 // Order-preserving keys: a larger score has a larger key; NaN (and a page
@@ -86,11 +78,11 @@ constexpr int kFew = kThreads;  // candidates that are ranked against each other
 // Shared memory of a CTA (the selecting one uses all of it).
 template <int D>
 struct Shared {
-  double up64[D], down64[D];  // of the head being selected for
-  // per head that this CTA selects for and scoring warp: its error bound, its
-  // smallest and largest key (of blocks that are not kept anyway)
-  float err[kSlots][kMaxCluster * kWarps];
-  uint32_t least[kSlots][kMaxCluster * kWarps], most[kSlots][kMaxCluster * kWarps];
+  double up64[D], down64[D];
+  // of every scoring warp: its error bound, its smallest and largest key (of
+  // blocks that are not kept anyway)
+  float err[kMaxCluster * kWarps];
+  uint32_t least[kMaxCluster * kWarps], most[kMaxCluster * kWarps];
   unsigned hist[kBins];
   int few[kFew];  // candidates by index
   unsigned warp_sum[kWarps];
@@ -100,11 +92,11 @@ struct Shared {
 };
 
 // While scoring, the place of the fp64 keys has the query sums (down, then up,
-// as a block's bounds are lo, then hi) of the cluster's heads in three bf16
-// parts, and their sizes rounded up.
+// as a block's bounds are lo, then hi) in three bf16 parts, and their sizes
+// rounded up.
 template <int D>
 struct QueryParts {
-  __nv_bfloat16 part[kWarps][4][2 * D];
+  __nv_bfloat16 part[4][2 * D];
 };
 
 // Inclusive prefix sum over the CTA of one value a thread; *total: all of it.
@@ -216,24 +208,24 @@ __device__ Key select_largest(int n, unsigned place, Key lo, Key hi, Sh& sh, con
   }
 }
 
-// Selects the blocks of one head from its scores (all threads of the CTA):
-// `keys` of n > topk blocks, `scorers` entries of the slot's err, least and
-// most; the group's queries, the request's pages and the bounds of the head on
-// page 0 for scores that have to be taken again.
+// Selects from the scores (all threads of the CTA): `keys` of n > topk blocks,
+// `scorers` entries of err, least and most; the group's queries, the request's
+// pages and the bounds of the head on page 0 for scores that have to be taken
+// again.
 template <int D>
-__device__ void select_head(const SelectParams& p, Shared<D>& sh, uint32_t* keys,
-                            unsigned long long* wide, int slot, int scorers, int n,
-                            const __nv_bfloat16* queries, const int* row,
-                            const __nv_bfloat16* bounds, int* out) {
+__device__ void select_blocks(const SelectParams& p, Shared<D>& sh, uint32_t* keys,
+                              unsigned long long* wide, int scorers, int n,
+                              const __nv_bfloat16* queries, const int* row,
+                              const __nv_bfloat16* bounds, int* out) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t page_elems = (int64_t)p.num_kv * 2 * D;
   // ---- the k-th largest, its doubtful neighbours ---------------------------------------
   float E = 0.f;
   uint32_t least = 0xffffffffu, most = 0;
   for (int i = lane; i < scorers; i += 32) {
-    E = fmaxf(E, sh.err[slot][i]);
-    least = min(least, sh.least[slot][i]);
-    most = max(most, sh.most[slot][i]);
+    E = fmaxf(E, sh.err[i]);
+    least = min(least, sh.least[i]);
+    most = max(most, sh.most[i]);
   }
   E = group_max<32>(E);
   least = __reduce_min_sync(kFullMask, least);
@@ -390,12 +382,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
 block_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
-  // scores of the heads this CTA selects for: fp32 keys per head and block,
-  // then fp64 keys per block (of one head at a time)
-  const int key_stride = (p.table_width + 3) & ~3;
-  uint32_t* all_keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Shared<D>) + 15) & ~size_t(15)));
+  // scores of the first CTA: fp32 keys, then fp64 keys, one of each per block
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Shared<D>) + 15) & ~size_t(15)));
   unsigned long long* wide =
-      reinterpret_cast<unsigned long long*>(all_keys + p.slots * key_stride);
+      reinterpret_cast<unsigned long long*>(keys + ((p.table_width + 3) & ~3));
   QueryParts<D>& queries_in = *reinterpret_cast<QueryParts<D>*>(wide);
   cg::cluster_group cluster = cg::this_cluster();
   if (p.cluster > 1) cluster.barrier_arrive();
@@ -403,20 +393,18 @@ block_select_kernel(const SelectParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
   const uint32_t unit = blockIdx.x / p.cluster;
-  const int t = unit / (uint32_t)p.head_groups;
-  const int h0 = (int)(unit - (uint32_t)t * p.head_groups) * p.heads;
-  const int heads = min(p.heads, p.num_kv - h0);
-  // CTA r selects for heads h0 + r, h0 + r + cluster, ..
-  int* outs = p.blocks + ((int64_t)t * p.num_kv + h0) * p.topk;
+  const int t = unit / (uint32_t)p.num_kv;
+  const int h = (int)(unit - (uint32_t)t * p.num_kv);
+  int* out = p.blocks + (int64_t)unit * p.topk;
 
   // ---- the token's blocks, and the groups' query sums -----------------------------
   int req = p.requests ? __ldg(p.requests + t) : t;
   int len = __ldg(p.lens + t);
-  const __nv_bfloat16* queries = p.q + t * p.q_stride + (int64_t)h0 * p.group * D;
+  const __nv_bfloat16* queries = p.q + t * p.q_stride + (int64_t)h * p.group * D;
   bool any_weight = false;
-  for (int i = tid; i < heads * (D / 2); i += kThreads) {  // two dims of a head
-    const int head = i / (D / 2), d = 2 * (i % (D / 2));
-    const __nv_bfloat16* q = queries + (int64_t)head * p.group * D + d;
+  if (tid < D / 2) {  // two dims a thread
+    const int d = 2 * tid;
+    const __nv_bfloat16* q = queries + d;
     float sums[2][2] = {};  // down, up
     for (int g0 = 0; g0 < p.group; g0 += 8) {  // eight loads in flight
       uint32_t v[8];
@@ -439,7 +427,7 @@ block_select_kernel(const SelectParams p) {
     for (int half = 0; half < 2; ++half) {
       const float a = sums[half][0], b = sums[half][1];
       any_weight |= a != 0.f || b != 0.f;
-      uint32_t* to = reinterpret_cast<uint32_t*>(&queries_in.part[head][0][half * D + d]);
+      uint32_t* to = reinterpret_cast<uint32_t*>(&queries_in.part[0][half * D + d]);
       constexpr int COLUMN = D;  // 4-byte words of one part
       const uint32_t hi = pack_bf16x2(a, b);
       const float a1 = a - __uint_as_float(hi << 16), b1 = b - __uint_as_float(hi & 0xffff0000u);
@@ -466,13 +454,12 @@ block_select_kernel(const SelectParams p) {
   if (rejected && p.errors && rank == 0 && tid == 0) atomicAdd(p.errors, 1);
   const int n = (int)(((uint32_t)len + (uint32_t)p.page_size - 1) / (uint32_t)p.page_size);
   if (n <= p.topk) {  // all of them: no score decides anything (cluster-uniform)
-    for (int head = rank; head < heads; head += p.cluster)
-      for (int i = tid; i < p.topk; i += kThreads)
-        outs[(int64_t)head * p.topk + i] = i < n ? i : -1;
+    if (rank == 0)
+      for (int i = tid; i < p.topk; i += kThreads) out[i] = i < n ? i : -1;
     if (p.cluster > 1) cluster.barrier_wait();
     return;
   }
-  // of any of the cluster's heads: zero queries have zero scores, exactly
+  // zero queries have zero scores, exactly
   any_weight = __syncthreads_or(any_weight);
 
   // ---- scores ------------------------------------------------------------------------
@@ -486,28 +473,24 @@ block_select_kernel(const SelectParams p) {
   // values 8(l%4).. of every 32 of rows l/4 and l/4 + 8: the order of the
   // inner dimension does not matter as long as both operands have it.
   // (As fp32 multiply-adds by 32 lanes a block this took 82 instructions a
-  // block and was bound by them and by too few loads in flight: 64 tokens x 8
-  // heads x 1024 blocks 77 us.)
+  // block, with too few loads in flight: 64 tokens x 8 heads of up to 1024
+  // blocks 77 us, now 51 us, 202 MB at 4.0 TB/s; one token of 1563 blocks
+  // 16 us, now 10 us.)
   constexpr int STEPS = 2 * D / 32;  // of 32 values: two matrix instructions
-  const int subs = kWarps / heads;              // warps of the CTA per head
-  const int mine = warp % heads, sub = warp / heads;  // this warp's head; sub == subs: idle
-  const bool scores = sub < subs;
-  const int to_rank = mine % p.cluster, to_slot = mine / p.cluster;  // who selects for it
-  uint32_t* to_keys = all_keys + to_slot * key_stride;
-  if (p.cluster > 1) to_keys = cluster.map_shared_rank(to_keys, to_rank);
+  uint32_t* to_keys = p.cluster > 1 ? cluster.map_shared_rank(keys, 0) : keys;
   const int g = lane >> 2, c = lane & 3;
   uint4 wb[STEPS];  // column g: a part of the query sums (0-2), their sizes (3), nothing
 #pragma unroll
   for (int k = 0; k < STEPS; ++k)
-    wb[k] = g < 4 ? *reinterpret_cast<const uint4*>(&queries_in.part[mine][g & 3][32 * k + 8 * c])
+    wb[k] = g < 4 ? *reinterpret_cast<const uint4*>(&queries_in.part[g & 3][32 * k + 8 * c])
                   : make_uint4(0, 0, 0, 0);
   const int* row = p.table + (int64_t)req * p.table_width;
-  const __nv_bfloat16* bounds = p.bounds + (int64_t)(h0 + mine) * 2 * D + 8 * c;
+  const __nv_bfloat16* bounds = p.bounds + (int64_t)h * 2 * D + 8 * c;
   const int64_t page_elems = (int64_t)p.num_kv * 2 * D;
   float worst = 0.f;  // the largest sum of |products| seen
   bool odd = false;
   uint32_t least = 0xffffffffu, most = 0;
-  const int first = scores ? (rank * subs + sub) * 16 : n, stride = p.cluster * subs * 16;
+  const int first = (rank * kWarps + warp) * 16, stride = p.cluster * kWarps * 16;
   int next[2];  // the pages of rows g and g + 8 of the coming blocks
 #pragma unroll
   for (int r = 0; r < 2; ++r) next[r] = first + g + 8 * r < n ? __ldg(row + first + g + 8 * r) : -1;
@@ -522,7 +505,7 @@ block_select_kernel(const SelectParams p) {
       page[r] = next[r];
       next[r] = j + stride < n ? __ldg(row + j + stride) : -1;
       if (page[r] < 0 || page[r] >= p.num_pages) {
-        if (j < n && p.errors && mine == 0 && c == 0) atomicAdd(p.errors, 1);
+        if (j < n && p.errors && c == 0) atomicAdd(p.errors, 1);
         page[r] = -1;
       }
     }
@@ -580,54 +563,39 @@ block_select_kernel(const SelectParams p) {
   odd = __any_sync(kFullMask, odd);
   least = __reduce_min_sync(kFullMask, least);
   most = __reduce_max_sync(kFullMask, most);
-  if (lane == 0 && scores) {
-    Shared<D>& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, to_rank) : sh;
-    const int at = rank * subs + sub;
+  if (lane == 0) {
+    Shared<D>& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, 0) : sh;
+    const int at = rank * kWarps + warp;
     const float bound = 0x1p-17f + (float)(8 + p.group) * 0x1p-24f;
-    to.err[to_slot][at] = odd ? INFINITY : any_weight ? worst * bound + 1.0e-35f : 0.f;
-    to.least[to_slot][at] = least;
-    to.most[to_slot][at] = most;
+    to.err[at] = odd ? INFINITY : any_weight ? worst * bound + 1.0e-35f : 0.f;
+    to.least[at] = least;
+    to.most[at] = most;
   }
   if (p.cluster > 1) {
-    cluster.sync();  // every score has arrived, and no CTA reads another's memory any longer
+    cluster.sync();  // every score has arrived; no CTA is needed any longer but the first
+    if (rank != 0) return;
   } else {
     __syncthreads();
   }
-
-  for (int head = rank, slot = 0; head < heads; head += p.cluster, ++slot) {
-    select_head<D>(p, sh, all_keys + slot * key_stride, wide, slot, p.cluster * subs, n,
-                   queries + (int64_t)head * p.group * D, row,
-                   p.bounds + (int64_t)(h0 + head) * 2 * D, outs + (int64_t)head * p.topk);
-    __syncthreads();  // before the shared arrays serve the next head
-  }
+  select_blocks<D>(p, sh, keys, wide, p.cluster * kWarps, n, queries, row,
+                   p.bounds + (int64_t)h * 2 * D, out);
 }
 
 template <int D>
-size_t smem_bytes(int width, int slots) {
+size_t smem_bytes(int width) {
   const size_t wide = (size_t)width * 8;
-  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)slots * ((width + 3) & ~3) * 4 +
+  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)((width + 3) & ~3) * 4 +
          (wide > sizeof(QueryParts<D>) ? wide : sizeof(QueryParts<D>));
 }
 
-// As many kv heads to a cluster (8 at most) as leave every SM a CTA, and as
-// many CTAs to a cluster (8 at most) as are all resident at once, two to an
-// SM, and have a tile of blocks each; a CTA selects for two heads at most, and
-// for one where the tables are long.
-void shape_for(SelectParams* p, int64_t num_tokens) {
-  int heads = kWarps;
-  int64_t units;
-  while (true) {
-    units = num_tokens * ((p->num_kv + heads - 1) / heads);
-    if (heads == 1 || (heads / 2 < p->num_kv && units * kMaxCluster >= 152)) break;
-    heads /= 2;
-  }
-  const int slots = heads > 1 && p->table_width <= 4096 ? kSlots : 1;
-  int c = heads / slots;
-  while (c < kMaxCluster && units * c * 2 <= 2 * 152 && p->table_width > c * 16 * 2) c *= 2;
-  p->cluster = c;
-  p->heads = heads;
-  p->slots = (heads + c - 1) / c;
-  p->head_groups = (p->num_kv + heads - 1) / heads;
+// CTAs of a cluster: more while all of them are resident at once, two to an
+// SM, and have more than a tile of blocks for each warp.  (Several heads to a
+// cluster, warps side by side on a page's neighbouring heads, was not faster:
+// of 256 dims and 64 tokens 116 us against 99 us, of 128 as fast.)
+int cluster_for(int64_t items, int width) {
+  int c = 1;
+  while (c < kMaxCluster && items * c * 2 <= 2 * 152 && width > c * 16 * 2) c *= 2;
+  return c;
 }
 
 template <int D>
@@ -637,7 +605,7 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   int per_sm = 0;
   // one opt-in for the largest size that the validation lets through
   const cudaError_t e = tma::prepare(block_select_kernel<D>, kThreads,
-                                     smem_bytes<D>(kMaxSelectBlocks, 1), cache, &per_sm);
+                                     smem_bytes<D>(kMaxSelectBlocks), cache, &per_sm);
   if (e != cudaSuccess) return e;
   SelectParams p;
   p.q = static_cast<const __nv_bfloat16*>(x.q);
@@ -657,10 +625,10 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   p.keep_last = a.keep_last;
   p.blocks = a.blocks;
   p.errors = x.errors;
-  shape_for(&p, x.num_tokens);
-  const int64_t grid = (int64_t)x.num_tokens * p.head_groups * p.cluster;
-  return launch_clusters(block_select_kernel<D>, dim3((unsigned)grid), dim3(kThreads),
-                         smem_bytes<D>(x.table_width, p.slots), p.cluster, stream, p);
+  const int64_t items = (int64_t)x.num_tokens * x.num_heads_kv;
+  p.cluster = cluster_for(items, x.table_width);
+  return launch_clusters(block_select_kernel<D>, dim3((unsigned)(items * p.cluster)),
+                         dim3(kThreads), smem_bytes<D>(x.table_width), p.cluster, stream, p);
 }
 
 }  // namespace
