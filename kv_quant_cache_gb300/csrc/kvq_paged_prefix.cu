@@ -15,10 +15,10 @@
 // Warps have one role each:
 //   * warps 0-7 and 8-15: the softmax of tile 0 and tile 1.  Two threads own
 //     a row (its tensor-memory lane), 64 keys each, and exchange only their
-//     maxima.  (One thread a row: 1500 cycles a block instead of about half,
-//     and the tensor cores waited.)  The reference m of a row only moves when
-//     a score exceeds it by more than 2^8; until then weights above 1 are as
-//     exact as those below, and O is seldom rescaled;
+//     maxima (1250 cycles from scores to weights; one thread a row: 1500).
+//     The reference m of a row only moves when a score exceeds it by more than
+//     2^8; until then weights above 1 are as exact as those below, and O is
+//     seldom rescaled;
 //   * warp 16, one lane: issues the matrix instructions.  While one tile's
 //     softmax runs, the other tile's products do;
 //   * warps 17 and 18: load K and V, two blocks ahead, by tensor-map copies (a
@@ -29,8 +29,12 @@
 // A segment's result is a partial (normalised O and log2 of the weight sum)
 // for the join with the item's other segments and each token's own keys.
 //
-// Bound by the tensor cores: 4 * 256 * 128 * D operations per 2 * 128 * D * 2
-// bytes of keys and values, which the L2 serves to the CTAs that share them.
+// Bound by the tensor cores, and by the power they may draw: 2048 rows x 8 kv
+// heads x 32768 keys of 128 dims, 275 GFLOP, take 176 us (1560 TFLOP/s, tensor
+// pipe active 72 % of the time, 141 MB read for 134 MB of keys and values);
+// run back to back the clock settles at 1.65 of 2.07 GHz at the power limit.
+// With heads of 64 the softmax bounds it: half the products for the same
+// exponentials (860 TFLOP/s).
 #include <string.h>
 
 #include "kvq_paged_attn.cuh"
