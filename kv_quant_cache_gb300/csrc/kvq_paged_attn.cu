@@ -80,10 +80,11 @@ struct AttnParams {
   int prefix_len;
   float scale_log2;
   int cluster, splits;
-  int first_slot;      // partials slot of split 0
-  Partials parts;      // used unless direct
-  __nv_bfloat16* out;  // direct
-  bool direct;
+  // The result goes to `out`, joined with `prefix_parts` partials of the
+  // prefix (0: none); with several splits it goes to partials itself.
+  __nv_bfloat16* out;
+  int prefix_parts;
+  Partials parts;
   int* errors;
   int trigger_from;
 };
@@ -127,6 +128,56 @@ struct Shape {
   static_assert(kRing >= kRows * kPad * 4, "a warp's output fits in its ring");
 };
 
+// The reference of a row's join with the prefix's parts, and the sum of all
+// weights; `lse` is the row's own part.
+__device__ __forceinline__ float parts_top(const AttnParams& p, int64_t row, float lse,
+                                           float* sum) {
+  float top = lse;
+  for (int s = 0; s < p.prefix_parts; ++s) top = fmaxf(top, p.parts.lse[s * p.parts.rows + row]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  *sum = exp2f(lse - ref);
+  for (int s = 0; s < p.prefix_parts; ++s)
+    *sum += exp2f(p.parts.lse[s * p.parts.rows + row] - ref);
+  return ref;
+}
+
+// Joins four dims of a row (its own part's, normalised, in *v) with the
+// prefix's parts; they lie at p.parts.o[at + s * part_stride].  A part without
+// a key (its output may be unwritten) stays out.  One sweep with a running
+// reference, so that the sums and outputs of four parts are in flight together.
+__device__ __forceinline__ void add_parts(const AttnParams& p, int64_t row, int64_t at,
+                                          int64_t part_stride, float lse, float4* v) {
+  float top = lse, sum = lse == -INFINITY ? 0.f : 1.f;
+  float4 a = *v;  // zeros where there is no own key
+  for (int s0 = 0; s0 < p.prefix_parts; s0 += 4) {
+    float w[4];
+    float4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = min(s0 + u, p.prefix_parts - 1);
+      w[u] = p.parts.lse[s * p.parts.rows + row];
+      x[u] = *reinterpret_cast<const float4*>(p.parts.o + at + s * part_stride);
+      if (s0 + u >= p.prefix_parts) w[u] = -INFINITY;
+    }
+    const float old = top;
+    top = fmaxf(fmaxf(top, fmaxf(w[0], w[1])), fmaxf(w[2], w[3]));
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = old == top ? 1.f : exp2f(old - ref);
+    sum *= f;
+    a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (w[u] == -INFINITY) continue;
+      const float g = exp2f(w[u] - ref);
+      sum += g;
+      a.x = fmaf(g, x[u].x, a.x), a.y = fmaf(g, x[u].y, a.y);
+      a.z = fmaf(g, x[u].z, a.z), a.w = fmaf(g, x[u].w, a.w);
+    }
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  *v = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+}
+
 // SPARSE: the rows of one token's group and the blocks selected for them;
 // otherwise a tile of (token, head) pairs, the prefix and their own keys.
 // WHOLE: page_size is a multiple of 16, so a group of keys lies in one page.
@@ -136,7 +187,10 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
   using S = Shape<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
-  grid_dependency_sync(p.trigger_from);
+  // After the prefix's tiles: they let this kernel be scheduled only when what
+  // came before both is done, and it needs their partials at its end alone.
+  const bool late = p.prefix_parts > 0;
+  if (!late) grid_dependency_sync(p.trigger_from);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kTeam = SOLO ? 1 : kWarps;  // warps on a row tile
   int2* list = reinterpret_cast<int2*>(smem + kTeam * S::kRing);
@@ -484,30 +538,44 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
     if (!SOLO && (lane & 3) == 0)
       state[warp * kRows + (lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
   }
+  if (late) {
+    grid_dependency_wait();
+    if ((int)blockIdx.x >= p.trigger_from) launch_dependents();
+  }
   if (SOLO) {  // the rows are this warp's: straight from its registers
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = (lane >> 2) + 8 * h;
       if (r >= rows) continue;
       const int64_t row = row_of(r);
-      const float f = l[h] == 0.f ? 0.f : 1.f / l[h];  // 0: the row has no key
-      if (p.direct) {
-        __nv_bfloat16* dst = p.out + row * D + 2 * (lane & 3);
+      float f = l[h] == 0.f ? 0.f : 1.f / l[h];  // 0: the row has no key
+      if (late) {
+        const float lse =
+            l[h] == 0.f ? -INFINITY : (m[h] == -INFINITY ? 0.f : m[h]) + log2f(l[h]);
+        float sum;
+        const float ref = parts_top(p, row, lse, &sum);
+        f = lse == -INFINITY ? 0.f : f * exp2f(lse - ref);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<uint32_t*>(dst + 8 * n) =
-              pack_bf16x2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
-      } else {
-        const int64_t slot = p.first_slot + blockIdx.y;
-        float* dst = p.parts.o + (slot * p.parts.rows + row) * D + 2 * (lane & 3);
+        for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+        for (int s = 0; s < p.prefix_parts; ++s) {
+          const float part = p.parts.lse[s * p.parts.rows + row];
+          if (part == -INFINITY) continue;
+          const float w = exp2f(part - ref);
+          const float* from = p.parts.o + (s * p.parts.rows + row) * D + 2 * (lane & 3);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<float2*>(dst + 8 * n) =
-              make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
-        if ((lane & 3) == 0)
-          p.parts.lse[slot * p.parts.rows + row] =
-              l[h] == 0.f ? -INFINITY : (m[h] == -INFINITY ? 0.f : m[h]) + log2f(l[h]);
+          for (int n = 0; n < D / 8; ++n) {
+            const float2 x = *reinterpret_cast<const float2*>(from + 8 * n);
+            o[n][2 * h] = fmaf(w, x.x, o[n][2 * h]);
+            o[n][2 * h + 1] = fmaf(w, x.y, o[n][2 * h + 1]);
+          }
+        }
+        f = sum == 0.f ? 0.f : 1.f / sum;
       }
+      __nv_bfloat16* dst = p.out + row * D + 2 * (lane & 3);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<uint32_t*>(dst + 8 * n) =
+            pack_bf16x2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
     }
     return;
   }
@@ -592,11 +660,12 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
       lse = part_lse[r];
     }
     const int64_t row = row_of(r);
-    if (p.direct) {
+    if (p.splits == 1) {
+      if (late) add_parts(p, row, row * D + c, (int64_t)D * p.parts.rows, lse, &v);
       *reinterpret_cast<uint2*>(p.out + row * D + c) =
           make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     } else {
-      const int64_t slot = p.first_slot + blockIdx.y;
+      const int64_t slot = blockIdx.y;
       *reinterpret_cast<float4*>(p.parts.o + (slot * p.parts.rows + row) * D + c) = v;
       if (c == 0) p.parts.lse[slot * p.parts.rows + row] = lse;
     }
@@ -823,13 +892,12 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
   p.topk = a.topk;
   p.tiles = sparse_tiles(x.num_heads_q, x.num_heads_kv);
   const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size, a.topk);
-  p.direct = s.splits == 1;
   p.out = static_cast<__nv_bfloat16*>(a.out);
-  if (!p.direct)
+  if (s.splits > 1)
     p.parts = partials_at(a.workspace, s.splits, (int64_t)x.num_tokens * x.num_heads_q, x.head_dim);
   const cudaError_t e = launch_attn_dim<true>(
       p, x.head_dim, (int64_t)x.num_tokens * x.num_heads_kv * p.tiles, s, stream);
-  if (e != cudaSuccess || p.direct) return e;
+  if (e != cudaSuccess || s.splits == 1) return e;
   return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
 }
 
@@ -842,10 +910,9 @@ int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads
   int64_t slots = s == 1 ? 0 : s;
   if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len)) {
     // either way may be taken: which one depends on where the cache lies
-    const int64_t both = prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, prefix_len).parts +
-                         shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, 0,
-                                       table_width).splits;
-    if (both > slots) slots = both;
+    const int64_t parts =
+        prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, prefix_len).parts;
+    if (parts > slots) slots = parts;
   }
   return partials_bytes(slots, rows, head_dim);
 }
@@ -861,30 +928,25 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   const bool tiles = prefix_tiles_fit(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
                                       x.page_size, a.prefix_len) &&
                      prefix_tiles_map(a, &map);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
   p.prefix_len = tiles ? 0 : (int)a.prefix_len;
-  const Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
-                                 p.prefix_len, x.table_width);
+  Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
+                           p.prefix_len, x.table_width);
   if (!tiles) {
-    p.direct = s.splits == 1;
-    p.out = static_cast<__nv_bfloat16*>(a.out);
-    if (!p.direct) p.parts = partials_at(a.workspace, s.splits, rows, x.head_dim);
+    if (s.splits > 1) p.parts = partials_at(a.workspace, s.splits, rows, x.head_dim);
     const cudaError_t e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);
-    if (e != cudaSuccess || p.direct) return e;
+    if (e != cudaSuccess || s.splits == 1) return e;
     return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
   }
-  const int pre =
+  // The tiles, and then the tokens' own keys, whose kernel joins both: its CTAs
+  // start as the tiles' run out, and need their partials at the end alone.
+  s.splits = 1;
+  p.prefix_parts =
       prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, a.prefix_len).parts;
-  const int own = x.table_width > 0 ? s.splits : 0;
-  p.parts = partials_at(a.workspace, pre + own, rows, x.head_dim);
-  cudaError_t e = cudaSuccess;
-  if (own) {  // first: as its last CTAs run out, the prefix's start
-    p.direct = false;
-    p.first_slot = pre;
-    e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);
-  }
-  if (e == cudaSuccess) e = launch_prefix_tiles(a, map, p.parts, own == 0, stream);
+  p.parts = partials_at(a.workspace, p.prefix_parts, rows, x.head_dim);
+  const cudaError_t e = launch_prefix_tiles(a, map, p.parts, stream);
   if (e != cudaSuccess) return e;
-  return launch_attn_join(p.parts, pre + own, x.head_dim, a.out, stream);
+  return launch_attn_dim<false>(p, x.head_dim, units, s, stream);
 }
 
 }  // namespace kvq

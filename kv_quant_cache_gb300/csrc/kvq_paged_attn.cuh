@@ -44,8 +44,7 @@ cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, voi
 // The prefix on the tensor cores (kvq_paged_prefix.cu): sizes it takes, the
 // parts it makes of the prefix, the tensor map of the cache (false where it
 // cannot be copied that way: not memory of the current device, no pages), and
-// the launch (partials slots 0 .. parts - 1).  `alone`: it is not preceded by
-// the kernel of the tokens' own keys, and has to wait for what came before.
+// the launch (partials slots 0 .. parts - 1).
 struct PrefixTilesPlan {
   int row_tiles;  // items of 256 query rows of a kv head
   int blocks;     // of 128 keys, of the prefix
@@ -58,6 +57,6 @@ PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_h
                                   int64_t prefix_len);
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map);
 cudaError_t launch_prefix_tiles(const PrefixAttnArgs& a, const CUtensorMap& map,
-                                const Partials& parts, bool alone, cudaStream_t stream);
+                                const Partials& parts, cudaStream_t stream);
 
 }  // namespace kvq

@@ -73,7 +73,6 @@ struct PrefixParams {
   int slots;         // partials of an item, at most
   Partials parts;
   int* errors;
-  bool alone;        // no other kernel of this call runs before this one
 };
 
 template <int D>
@@ -221,10 +220,10 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     *dead = 0;
   }
   if (warp == kMmaWarp) tc::alloc512(tma::smem_addr(tmem_slot));
-  // The kernel of the tokens' own keys, launched just before, reads and writes
-  // nothing that this one writes, and lets it be scheduled only after its own
-  // wait: what came before both is done.  Its end is waited for at this one's.
-  if (p.alone) grid_dependency_wait();
+  // All CTAs are resident at once: the kernel of the tokens' own keys may take
+  // up the SMs that have none, or are done.
+  grid_dependency_wait();
+  launch_dependents();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -533,13 +532,11 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     tc::fence_after();
     tc::dealloc512(tmem);
   }
-  // before this kernel counts as done the one before it has to be
-  if (!p.alone) grid_dependency_wait();
 }
 
 template <int D>
 cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partials& parts,
-                   bool alone, cudaStream_t stream) {
+                   cudaStream_t stream) {
   const PagedQuery& x = a.x;
   using L = Layout<D>;
   static std::atomic<int> cache[kMaxDevices];
@@ -572,7 +569,6 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   p.slots = plan.parts;
   p.parts = parts;
   p.errors = x.errors;
-  p.alone = alone;
   return launch_kernel(prefix_tiles_kernel<D>, dim3((unsigned)(plan.lanes * plan.teams)), dim3(kThreads),
                        L::kSmem, stream, p);
 }
@@ -638,9 +634,9 @@ PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_h
 }
 
 cudaError_t launch_prefix_tiles(const PrefixAttnArgs& a, const CUtensorMap& map,
-                                const Partials& parts, bool alone, cudaStream_t stream) {
-  return a.x.head_dim == 64 ? launch<64>(a, map, parts, alone, stream)
-                            : launch<128>(a, map, parts, alone, stream);
+                                const Partials& parts, cudaStream_t stream) {
+  return a.x.head_dim == 64 ? launch<64>(a, map, parts, stream)
+                            : launch<128>(a, map, parts, stream);
 }
 
 }  // namespace kvq

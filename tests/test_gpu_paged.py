@@ -755,3 +755,22 @@ def test_causal_chunk_of_a_request(cuda_device, prefix_way, page, q_len, Hq, Hkv
     sees = (requests == 2) & (lens >= last)
     assert int(sees.sum()) == 1 and bool(got[1][sees].isnan().all())
     assert torch.equal(bits(got[0][~sees]), bits(got[1][~sees]))
+
+
+def test_without_programmatic_launches(cuda_device, prefix_way):
+    """Ordinary launches give the same results, bit for bit."""
+    s = decode_state(95, B=40)
+    qkv = normal(gen(96), s["B"], (s["Hq"] + 2 * s["Hkv"]) * s["D"]).cuda()
+    results = []
+    for programmatic in (True, False):
+        d = on_gpu(s)
+        fill_bounds(d)
+        old = kvq.set_programmatic_launch(programmatic)
+        try:
+            outs = [step(d, qkv) for _ in range(3)]
+        finally:
+            kvq.set_programmatic_launch(old)
+        torch.cuda.synchronize()
+        results.append([bits(t.view(torch.int16)) for out in outs for t in out] + [bits(d["cache"])])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
