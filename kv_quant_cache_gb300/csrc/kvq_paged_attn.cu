@@ -754,20 +754,30 @@ struct Spread {
   bool solo;  // a warp per row tile
 };
 
-// CTAs are added while all of them are resident at once (two to an SM; with
-// half as many again in a second wave the same range took 20-30 % longer) and
-// each keeps at least two steps of 16 keys for every warp: first within a
-// cluster of up to 8 (joined in place); beyond that, as partials that a second launch joins,
-// only where a CTA would be left with more than 2048 keys (below, the second
-// launch costs more than it saves).
-Spread spread_for(int64_t units, int64_t pages, int page_size) {
+// CTAs are added while all of them are resident at once (two to an SM, one
+// with heads of 256; with half as many again in a second wave the same range
+// took 20-30 % longer, with twice as many, 32 tiles of 256 dims, 24 us against
+// 10.4) and each keeps at least two steps of 16 keys for every warp: first
+// within a cluster of up to 8 (joined in place); beyond that, as partials that
+// a second launch joins, only where a CTA would be left with more than 2048
+// keys (below, the second launch costs more than it saves).  Behind the
+// prefix's tiles (`late`) the SMs come free one by one, and eight seats of a
+// cluster late: there four serve up to 8192 keys (16 tokens of 32 heads of 128
+// after 2048 keys, own keys 64: 14.2 us against 19.4; 640: 17.2 / 22.4; 2048,
+// more than that: 34.8 / 29.2).
+Spread spread_for(int64_t units, int64_t pages, int page_size, int head_dim, bool late) {
   Spread s = {1, 1, false};
-  const int64_t keys = pages * page_size;
-  while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 2 * 152 &&
+  const int64_t keys = pages * page_size, seats = head_dim == 256 ? 152 : 2 * 152;
+  const int most = late && keys < 8192 ? kMaxCluster / 2 : kMaxCluster;
+  auto fit = [&](int cluster) {  // clusters resident at once: they do not fill a GPC evenly
+    return cluster < 8 ? seats / cluster - (cluster == 4 ? 2 : 0) : head_dim == 256 ? 15 : 36;
+  };
+  while (s.cluster < most && units <= fit(s.cluster * 2) &&
          keys >= (int64_t)s.cluster * 2 * kGroup * kWarps)
     s.cluster *= 2;
   int64_t splits = 1;
-  while (units * s.cluster * (splits + 1) <= 2 * 152 && keys > s.cluster * splits * 2048) ++splits;
+  while (!late && units * s.cluster * (splits + 1) <= seats && keys > s.cluster * splits * 2048)
+    ++splits;
   s.splits = (int)splits;
   // With many tiles of short ranges, a CTA of one warp each: no joins between
   // warps, and four times as many tiles in flight (640 tiles of 512 keys 32 us
@@ -847,19 +857,21 @@ int64_t shared_tiles(int64_t num_tokens, int num_q, int num_kv) {
   return (num_tokens * (num_q / num_kv) + kRows - 1) / kRows;
 }
 
-Spread sparse_spread(int64_t num_tokens, int num_q, int num_kv, int page_size, int topk) {
-  return spread_for(num_tokens * num_kv * sparse_tiles(num_q, num_kv), topk, page_size);
+Spread sparse_spread(int64_t num_tokens, int num_q, int num_kv, int head_dim, int page_size,
+                     int topk) {
+  return spread_for(num_tokens * num_kv * sparse_tiles(num_q, num_kv), topk, page_size, head_dim,
+                    false);
 }
 
-// The tokens' own keys, with the prefix's or without.  The own pages that a
-// tile can have: those of every token that has a row in it.
-Spread shared_spread(int64_t num_tokens, int num_q, int num_kv, int page_size,
-                     int64_t prefix_len, int table_width) {
+// The tokens' own keys, with the prefix's or behind its tiles (`late`).  The
+// own pages that a tile can have: those of every token that has a row in it.
+Spread shared_spread(int64_t num_tokens, int num_q, int num_kv, int head_dim, int page_size,
+                     int64_t prefix_len, int table_width, bool late) {
   const int group = num_q / num_kv;
   const int64_t tokens = group >= kRows ? 2 : (kRows + group - 2) / group + 1;
   const int64_t own = (tokens < num_tokens ? tokens : num_tokens) * table_width;
   return spread_for(shared_tiles(num_tokens, num_q, num_kv) * num_kv,
-                    (prefix_len + page_size - 1) / page_size + own, page_size);
+                    (prefix_len + page_size - 1) / page_size + own, page_size, head_dim, late);
 }
 
 }  // namespace
@@ -881,7 +893,8 @@ cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, voi
 
 int64_t sparse_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int topk) {
-  const int s = sparse_spread(num_tokens, num_heads_q, num_heads_kv, page_size, topk).splits;
+  const int s =
+      sparse_spread(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, topk).splits;
   return s == 1 ? 0 : partials_bytes(s, num_tokens * num_heads_q, head_dim);
 }
 
@@ -891,7 +904,8 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
   p.blocks = a.blocks;
   p.topk = a.topk;
   p.tiles = sparse_tiles(x.num_heads_q, x.num_heads_kv);
-  const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size, a.topk);
+  const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
+                                 x.page_size, a.topk);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   if (s.splits > 1)
     p.parts = partials_at(a.workspace, s.splits, (int64_t)x.num_tokens * x.num_heads_q, x.head_dim);
@@ -905,13 +919,13 @@ int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads
                               int head_dim, int page_size, int64_t prefix_len,
                               int table_width) {
   const int64_t rows = num_tokens * num_heads_q;
-  const int s = shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, prefix_len,
-                              table_width).splits;
+  const int s = shared_spread(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size,
+                              prefix_len, table_width, false).splits;
   int64_t slots = s == 1 ? 0 : s;
   if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len)) {
     // either way may be taken: which one depends on where the cache lies
     const int64_t parts =
-        prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, prefix_len).parts;
+        prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, head_dim, prefix_len).parts;
     if (parts > slots) slots = parts;
   }
   return partials_bytes(slots, rows, head_dim);
@@ -930,8 +944,8 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
                      prefix_tiles_map(a, &map);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.prefix_len = tiles ? 0 : (int)a.prefix_len;
-  Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
-                           p.prefix_len, x.table_width);
+  const Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
+                                 x.page_size, p.prefix_len, x.table_width, tiles);
   if (!tiles) {
     if (s.splits > 1) p.parts = partials_at(a.workspace, s.splits, rows, x.head_dim);
     const cudaError_t e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);
@@ -940,9 +954,8 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   }
   // The tiles, and then the tokens' own keys, whose kernel joins both: its CTAs
   // start as the tiles' run out, and need their partials at the end alone.
-  s.splits = 1;
-  p.prefix_parts =
-      prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, a.prefix_len).parts;
+  p.prefix_parts = prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
+                                     a.prefix_len).parts;
   p.parts = partials_at(a.workspace, p.prefix_parts, rows, x.head_dim);
   const cudaError_t e = launch_prefix_tiles(a, map, p.parts, stream);
   if (e != cudaSuccess) return e;

@@ -46,7 +46,7 @@ cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, voi
 // cannot be copied that way: not memory of the current device, no pages), and
 // the launch (partials slots 0 .. parts - 1).
 struct PrefixTilesPlan {
-  int row_tiles;  // items of 256 query rows of a kv head
+  int row_tiles;  // items of 256 query rows of a kv head (128: heads of 256)
   int blocks;     // of 128 keys, of the prefix
   int lanes, teams;  // CTAs that keep in step, and how many times so many
   int parts;      // partials of an item, at most
@@ -54,7 +54,7 @@ struct PrefixTilesPlan {
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len);
 PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_heads_kv,
-                                  int64_t prefix_len);
+                                  int head_dim, int64_t prefix_len);
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map);
 cudaError_t launch_prefix_tiles(const PrefixAttnArgs& a, const CUtensorMap& map,
                                 const Partials& parts, cudaStream_t stream);

@@ -45,10 +45,8 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;            // keys of a block
-constexpr int kThreads = 640;         // five groups of four warps
-constexpr int kMmaWarp = 16, kLoadWarp = 17;  // 17: K, 18: V
-// Registers of a thread: 640 x 96 at launch; the softmax groups take 104, the
-// last group keeps 56 (512 x 104 + 128 x 56 = 60416 of 61440).
+// Registers of a thread where there are 640: 96 at launch; the softmax groups
+// take 104, the last group keeps 56 (512 x 104 + 128 x 56 = 60416 of 61440).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 56;
 constexpr float kRescaleAt = 8.f;     // log2 by which a score may exceed m
 
@@ -75,14 +73,25 @@ struct PrefixParams {
   int* errors;
 };
 
+// Row tiles of an item: two, or one of heads of 256, whose O takes half of the
+// tensor memory.
+constexpr int row_tiles_of(int head_dim) { return head_dim == 256 ? 1 : 2; }
+
 template <int D>
 struct Layout {
-  static constexpr int kBlocks = D / 64;             // 128-byte wide column blocks
-  static constexpr int kTile = kKeys * D * 2;        // bytes of 128 rows
+  static constexpr int kTiles = row_tiles_of(D);
+  static constexpr int kMmaWarp = 8 * kTiles, kLoadWarp = kMmaWarp + 1;  // .. K, and V the next
+  static constexpr int kThreads = 32 * kMmaWarp + 128;
+  // K and V have two slots each, for two blocks, or for the two halves of a
+  // block's dims.
+  static constexpr int kSplit = D == 256 ? 2 : 1;
+  static constexpr int kWidth = D / kSplit;          // dims of a slot
+  static constexpr int kTile = kTileRows * D * 2;    // bytes of a tile of Q
+  static constexpr int kSlot = kKeys * kWidth * 2;
   static constexpr int kQ = 0;
-  static constexpr int kK = 2 * kTile;
-  static constexpr int kV = kK + 2 * kTile;
-  static constexpr int kTops = kV + 2 * kTile;  // [2 blocks, and the sums][2 halves][256 rows]
+  static constexpr int kK = kTiles * kTile;
+  static constexpr int kV = kK + 2 * kSlot;
+  static constexpr int kTops = kV + 2 * kSlot;  // [2 blocks, and the sums][2 halves][256 rows]
   static constexpr int kBars = kTops + 3 * 2048;
   static constexpr int kEnd = kBars + 24 * 8 + 32;
   static constexpr int kSmem = kEnd + 1024;          // room to align the base
@@ -91,7 +100,7 @@ struct Layout {
 
 // mbarriers, by index
 enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12,
-       kPvDone = 16, kDrain = 18, kBarriers = 19 };  // kPFull + 2 tile + part
+       kPvDone = 16, kDrain = 18, kBarriers = 19 };  // kPFull + 2 buffer + part
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -158,10 +167,10 @@ struct Segments {
   int kv_head;
   int64_t row0;       // the item's first row
   int64_t rows_left;  // rows of the kv head from there on
-  int tiles;
+  int tiles, rows;    // row tiles of the segment, rows of a whole item
   int lane, team;
 
-  __device__ __forceinline__ Segments(const PrefixParams& p) {
+  __device__ __forceinline__ Segments(const PrefixParams& p, int rows) : rows(rows) {
     team = (int)blockIdx.x / p.lanes;
     lane = (int)blockIdx.x - team * p.lanes;
     const int64_t all = p.items * p.blocks;
@@ -181,9 +190,9 @@ struct Segments {
       kv_head = (int)(item / p.row_tiles);
       tile = (int)(item - (int64_t)kv_head * p.row_tiles);
     }
-    row0 = (int64_t)tile * (2 * kTileRows);
+    row0 = (int64_t)tile * rows;
     rows_left = p.rows - row0;
-    tiles = rows_left > kTileRows ? 2 : 1;
+    tiles = rows > kTileRows && rows_left > kTileRows ? 2 : 1;
     return true;
   }
   // The item's segments are numbered from the team that has its first block.
@@ -193,9 +202,10 @@ struct Segments {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Layout<D>::kThreads, 1)
 prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
+  constexpr int kMmaWarp = L::kMmaWarp, kLoadWarp = L::kLoadWarp;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (tma::smem_addr(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (base - tma::smem_addr(raw));
@@ -228,19 +238,23 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
-  Segments seg(p);
+  Segments seg(p, L::kTiles * kTileRows);
 
   if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if constexpr (L::kTiles == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ---------------------------------------------------------------------
     const int tile = warp >> 3, half = (warp >> 2) & 1;
     const int r = tile * kTileRows + (warp & 3) * 32 + lane;  // the thread's row
     const int pair_bar = 1 + tile * 4 + (warp & 3);           // its two warps' barrier
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
-    const uint32_t s_at = at + 128 * tile + 64 * half, p_at = at + 128 * tile + 32 * half;
     const uint32_t o_at = at + 256 + 128 * tile + (D / 2) * half;
     uint32_t done = 0;  // blocks of this tile so far: the phase of its barriers
     bool ok = true;
+    auto pv_done = [&](uint32_t block) {
+      return L::kTiles == 2 ? tc::wait_warp(bar(kPvDone + tile), block & 1, dead)
+                            : tc::wait_warp(bar(kPvDone + (block & 1)), (block >> 1) & 1, dead);
+    };
     while (ok && seg.next(p)) {
       if (tile >= seg.tiles) continue;
       // the tile's 256 threads bring in Q; the products that read the previous
@@ -274,7 +288,11 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           outside = page < 0 || page >= p.num_pages;
         }
         const uint32_t bad = __ballot_sync(kFullMask, outside);
-        ok = tc::wait_warp(bar(kSFull + tile), done & 1, dead);
+        // S has two buffers: one a tile, or the blocks of one tile in turn
+        const int buf = L::kTiles == 2 ? tile : done & 1;
+        const uint32_t phase = L::kTiles == 2 ? done & 1 : (done >> 1) & 1;
+        const uint32_t s_at = at + 128 * buf + 64 * half, p_at = at + 128 * buf + 32 * half;
+        ok = tc::wait_warp(bar(kSFull + buf), phase, dead);
         if (!ok) break;
         tc::fence_after();
         uint32_t s[2][32];
@@ -313,7 +331,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           m = top;
           if (j > 0) {
             // O is at rest once the previous block's product is done
-            ok = tc::wait_warp(bar(kPvDone + tile), (done - 1) & 1, dead);
+            ok = pv_done(done - 1);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll 1
@@ -351,13 +369,13 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           tc::wait_st();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar(kPFull + 2 * tile + c));
+          if (lane == 0) tc::mbar_arrive(bar(kPFull + 2 * buf + c));
         }
         sum0 = add2(sum0, sum1);
         l += sum0.f[0] + sum0.f[1];
       }
       // ---- the partial -----------------------------------------------------------------
-      if (ok) ok = tc::wait_warp(bar(kPvDone + tile), (done - 1) & 1, dead);
+      if (ok) ok = pv_done(done - 1);
       tc::fence_after();
       if (ok) {
         tops[1024 + half * 256 + r] = l;
@@ -396,65 +414,116 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       }
       tc::fence_before();
     }
-  } else {
+  } else if constexpr (L::kTiles == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
   if (warp == kMmaWarp) {
     // ---- the matrix instructions -------------------------------------------------------
-    constexpr uint32_t qk = tc::instr_desc(kKeys, false), pv = tc::instr_desc(D, true);
+    constexpr uint32_t qk = tc::instr_desc(kKeys, false), pv = tc::instr_desc(L::kWidth, true);
     const uint64_t q_desc = tc::smem_desc(base + L::kQ, 16);
     const uint64_t k_desc = tc::smem_desc(base + L::kK, 16);
     const uint64_t v_desc = tc::smem_desc(base + L::kV, 128 * 128);
-    auto scores = [&](int tile, int stage) {
-      const uint64_t a = q_desc + (uint32_t)(tile * (L::kTile >> 4));
-      const uint64_t b = k_desc + (uint32_t)(stage * (L::kTile >> 4));
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-        tc::mma_ss(tmem + 128 * tile, a + off, b + off, qk, k > 0);
-      }
-      tc::commit(bar(kSFull + tile));
-    };
-    uint32_t block = 0, done[2] = {0, 0}, segs[2] = {0, 0};  // phases of the barriers
+    uint32_t block = 0;
     bool ok = true;
-    while (ok && seg.next(p)) {
-      ok = tc::wait_warp(bar(kKFull + (block & 1)), (block >> 1) & 1, dead);
-      for (int t = 0; ok && t < seg.tiles; ++t) {
-        ok = tc::wait_warp(bar(kQFull + t), segs[t]++ & 1, dead);
-        if (!ok) break;
-        tc::fence_after();
-        scores(t, block & 1);
-      }
-      if (!ok) break;
-      tc::commit(bar(kKEmpty + (block & 1)));
-      for (int j = 0; ok && j < seg.n; ++j, ++block) {
-        const int stage = block & 1, next = stage ^ 1;
-        const bool more = j + 1 < seg.n;
-        ok = tc::wait_warp(bar(kVFull + stage), (block >> 1) & 1, dead) &&
-             (!more || tc::wait_warp(bar(kKFull + next), ((block + 1) >> 1) & 1, dead));
+    if constexpr (L::kTiles == 2) {
+      auto scores = [&](int tile, int stage) {
+        const uint64_t a = q_desc + (uint32_t)(tile * (L::kTile >> 4));
+        const uint64_t b = k_desc + (uint32_t)(stage * (L::kSlot >> 4));
+  #pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+          tc::mma_ss(tmem + 128 * tile, a + off, b + off, qk, k > 0);
+        }
+        tc::commit(bar(kSFull + tile));
+      };
+      uint32_t done[2] = {0, 0}, segs[2] = {0, 0};  // phases of the barriers
+      while (ok && seg.next(p)) {
+        ok = tc::wait_warp(bar(kKFull + (block & 1)), (block >> 1) & 1, dead);
         for (int t = 0; ok && t < seg.tiles; ++t) {
-          const uint64_t v = v_desc + (uint32_t)(stage * (L::kTile >> 4));
-          for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
-            ok = tc::wait_warp(bar(kPFull + 2 * t + c), done[t] & 1, dead);
-            if (!ok) break;
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 4 * (i >> 1) + 2 * c + (i & 1);
-              tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4),
-                         pv, j > 0 || c > 0 || i > 0);
-            }
-          }
+          ok = tc::wait_warp(bar(kQFull + t), segs[t]++ & 1, dead);
           if (!ok) break;
-          ++done[t];
-          tc::commit(bar(kPvDone + t));
-          // the next scores go over P, which the products above read first:
-          // matrix instructions of one thread run in order
-          if (more) scores(t, next);
+          tc::fence_after();
+          scores(t, block & 1);
         }
         if (!ok) break;
-        tc::commit(bar(kVEmpty + stage));
-        if (more) tc::commit(bar(kKEmpty + next));
+        tc::commit(bar(kKEmpty + (block & 1)));
+        for (int j = 0; ok && j < seg.n; ++j, ++block) {
+          const int stage = block & 1, next = stage ^ 1;
+          const bool more = j + 1 < seg.n;
+          ok = tc::wait_warp(bar(kVFull + stage), (block >> 1) & 1, dead) &&
+               (!more || tc::wait_warp(bar(kKFull + next), ((block + 1) >> 1) & 1, dead));
+          for (int t = 0; ok && t < seg.tiles; ++t) {
+            const uint64_t v = v_desc + (uint32_t)(stage * (L::kSlot >> 4));
+            for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
+              ok = tc::wait_warp(bar(kPFull + 2 * t + c), done[t] & 1, dead);
+              if (!ok) break;
+              tc::fence_after();
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 4 * (i >> 1) + 2 * c + (i & 1);
+                tc::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v + k * (16 * 128 >> 4),
+                           pv, j > 0 || c > 0 || i > 0);
+              }
+            }
+            if (!ok) break;
+            ++done[t];
+            tc::commit(bar(kPvDone + t));
+            // the next scores go over P, which the products above read first:
+            // matrix instructions of one thread run in order
+            if (more) scores(t, next);
+          }
+          if (!ok) break;
+          tc::commit(bar(kVEmpty + stage));
+          if (more) tc::commit(bar(kKEmpty + next));
+        }
+      }
+    } else {
+      // One tile: the scores of a block go before the products with the values of
+      // the one before it, into S's other buffer (its weights have been read
+      // then), and its softmax runs meanwhile.
+      uint32_t segs = 0;
+      auto scores = [&](uint32_t block) {
+        for (int h = 0; ok && h < 2; ++h) {
+          ok = tc::wait_warp(bar(kKFull + h), block & 1, dead);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll
+          for (int k = 0; k < L::kWidth / 16; ++k) {
+            const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+            tc::mma_ss(tmem + 128 * (block & 1),
+                       q_desc + off + (uint32_t)(h * ((L::kWidth / 64) * (128 * 128) >> 4)),
+                       k_desc + off + (uint32_t)(h * (L::kSlot >> 4)), qk, h > 0 || k > 0);
+          }
+          tc::commit(bar(kKEmpty + h));
+        }
+        if (ok) tc::commit(bar(kSFull + (block & 1)));
+      };
+      while (ok && seg.next(p)) {
+        ok = tc::wait_warp(bar(kQFull), segs++ & 1, dead);
+        if (!ok) break;
+        tc::fence_after();
+        scores(block);
+        for (int j = 0; ok && j < seg.n; ++j, ++block) {
+          if (j + 1 < seg.n) scores(block + 1);
+          const int buf = block & 1;
+          for (int h = 0; ok && h < 2; ++h) {
+            ok = tc::wait_warp(bar(kVFull + h), block & 1, dead);
+            const uint64_t v = v_desc + (uint32_t)(h * (L::kSlot >> 4));
+            for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
+              if (h == 0) ok = tc::wait_warp(bar(kPFull + 2 * buf + c), (block >> 1) & 1, dead);
+              if (!ok) break;
+              tc::fence_after();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 4 * (i >> 1) + 2 * c + (i & 1);
+                tc::mma_ts(tmem + 256 + L::kWidth * h, tmem + 128 * buf + 8 * k,
+                           v + k * (16 * 128 >> 4), pv, j > 0 || c > 0 || i > 0);
+              }
+            }
+            if (ok) tc::commit(bar(kVEmpty + h));
+          }
+          if (ok) tc::commit(bar(kPvDone + buf));
+        }
       }
     }
     if (!ok) {  // nothing may be in flight when the tensor memory goes
@@ -467,15 +536,13 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     // ---- the loads: one warp for K, one for V --------------------------------------------
     const int kv = warp - kLoadWarp;
     const int64_t head_elems = ((int64_t)D) << p.page_shift;
-    uint32_t block = 0;
-    int last = -1;  // latest block whose copies were started
+    uint32_t turn = 0;  // slots filled so far
+    int last[2] = {-1, -1};  // the latest of each slot that copies were started for
     bool ok = true;
     while (ok && seg.next(p)) {
       const int head = kv * p.num_kv + seg.kv_head;
-      for (int j = 0; j < seg.n; ++j, ++block) {
-        const int stage = block & 1, first = (seg.first + j) * kKeys;
-        const uint32_t full = bar((kv ? kVFull : kKFull) + stage);
-        const uint32_t dst = base + (kv ? L::kV : L::kK) + stage * L::kTile;
+      for (int j = 0; ok && j < seg.n; ++j) {
+        const int first = (seg.first + j) * kKeys;
         const int key = first + (lane << piece_shift);
         int page = -1;
         if (lane < pieces && key < p.prefix_len) {
@@ -487,43 +554,51 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         }
         const bool here = __all_sync(kFullMask, lane >= pieces || page >= 0);
         const bool whole = here && p.prefix_len - first >= kKeys;
-        if (block >= 2) {
-          ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + stage), ((block >> 1) - 1) & 1, dead);
-          if (!ok) break;
-        }
-        if (whole) {
-          if (lane == 0) tma::mbar_arrive_expect_tx(full, L::kTile);
-          __syncwarp();
-          if (lane < pieces) {
+        for (int h = 0; h < L::kSplit; ++h, ++turn) {
+          const int slot = turn & 1;
+          const uint32_t full = bar((kv ? kVFull : kKFull) + slot);
+          const uint32_t dst = base + (kv ? L::kV : L::kK) + slot * L::kSlot;
+          if (turn >= 2) {
+            ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + slot), ((turn >> 1) - 1) & 1, dead);
+            if (!ok) break;
+          }
+          if (whole) {
+            if (lane == 0) tma::mbar_arrive_expect_tx(full, L::kSlot);
+            __syncwarp();
+            if (lane < pieces) {
 #pragma unroll
-            for (int b = 0; b < L::kBlocks; ++b)
-              tma::tile_load_4d(dst + b * (128 * 128) + (lane << (piece_shift + 7)), &p.map,
-                                64 * b, key & page_mask, head, page, full);
-          }
-          last = (int)block;
-        } else {
-          constexpr int FRAGS = D / 8, RPW = 32 / FRAGS;
+              for (int b = 0; b < L::kWidth / 64; ++b)
+                tma::tile_load_4d(dst + b * (128 * 128) + (lane << (piece_shift + 7)), &p.map,
+                                  L::kWidth * h + 64 * b, key & page_mask, head, page, full);
+            }
+            (slot ? last[1] : last[0]) = (int)turn;
+          } else {
+            constexpr int FRAGS = L::kWidth / 8, RPW = 32 / FRAGS;
 #pragma unroll 4
-          for (int i = 0; i < kKeys / RPW; ++i) {
-            const int r = i * RPW + lane / FRAGS, c = lane % FRAGS, k = first + r;
-            const int from = __shfl_sync(kFullMask, page, r >> piece_shift);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (from >= 0 && k < p.prefix_len)
-              v = __ldg(reinterpret_cast<const uint4*>(
-                  p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
-                  (int64_t)(k & page_mask) * D + 8 * c));
-            st_shared16(dst + tile_offset(r, c), v);
+            for (int i = 0; i < kKeys / RPW; ++i) {
+              const int r = i * RPW + lane / FRAGS, c = lane % FRAGS, k = first + r;
+              const int from = __shfl_sync(kFullMask, page, r >> piece_shift);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (from >= 0 && k < p.prefix_len)
+                v = __ldg(reinterpret_cast<const uint4*>(
+                    p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
+                    (int64_t)(k & page_mask) * D + L::kWidth * h + 8 * c));
+              st_shared16(dst + tile_offset(r, c), v);
+            }
+            tma::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(full);
           }
-          tma::fence_proxy_async();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(full);
         }
-        __syncwarp();
       }
     }
-    if (!ok && last >= 0) {  // let the copies in flight land before the CTA may end
-      const uint32_t full = bar((kv ? kVFull : kKFull) + (last & 1));
-      for (uint32_t i = 0; i < (1u << 22) && !tma::mbar_test(full, (last >> 1) & 1); ++i) {
+    if (!ok) {  // let the copies in flight land before the CTA may end
+      for (int slot = 0; slot < 2; ++slot) {
+        const uint32_t full = bar((kv ? kVFull : kKFull) + slot);
+        const int turn = slot ? last[1] : last[0];
+        for (uint32_t i = 0; turn >= 0 && i < (1u << 22); ++i)
+          if (tma::mbar_test(full, (turn >> 1) & 1)) break;
       }
     }
   }
@@ -541,7 +616,7 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   using L = Layout<D>;
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
-  const cudaError_t e = tma::prepare(prefix_tiles_kernel<D>, kThreads, L::kSmem, cache, &per_sm);
+  const cudaError_t e = tma::prepare(prefix_tiles_kernel<D>, L::kThreads, L::kSmem, cache, &per_sm);
   if (e != cudaSuccess) return e;
   PrefixParams p;
   memset(&p, 0, sizeof p);
@@ -560,7 +635,7 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   p.scale_log2 = fabsf(a.scale) * kLog2e;
   p.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
   const PrefixTilesPlan plan =
-      prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, a.prefix_len);
+      prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, D, a.prefix_len);
   p.row_tiles = plan.row_tiles;
   p.lanes = plan.lanes;
   p.teams = plan.teams;
@@ -569,8 +644,8 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   p.slots = plan.parts;
   p.parts = parts;
   p.errors = x.errors;
-  return launch_kernel(prefix_tiles_kernel<D>, dim3((unsigned)(plan.lanes * plan.teams)), dim3(kThreads),
-                       L::kSmem, stream, p);
+  return launch_kernel(prefix_tiles_kernel<D>, dim3((unsigned)(plan.lanes * plan.teams)),
+                       dim3(L::kThreads), L::kSmem, stream, p);
 }
 
 }  // namespace
@@ -589,17 +664,18 @@ int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 // one row tile of the other kernel, which reads the prefix once.  Beyond, each
 // of its row tiles reads it again, but it is one launch without partials: by
 // the products' size, GB300, us of the rows / the tiles (32 query heads, 8 kv
-// heads of 128): 2^21 (32 tokens x 2048 keys) 16.5 / 22.4, 2^22 (16 x 8192)
-// 24.6 / 29.1, 2^23 (32 x 8192) 39.5 / 27.3, 2^24 (16 x 32768) 70 / 47; heads
-// of 64, 2^22 (32 x 4096): 23.0 / 19.8.
+// heads of 128, own keys up to 64): 2^21 (32 tokens x 2048 keys) 16.3 / 19.8,
+// 2^22 (16 x 8192) 24.2 / 21.8, (64 x 2048) 25.6 / 26.1, 2^23 (16 x 16384)
+// 40 / 26; heads of 64, 2^21 (32 x 2048) 14.2 / 12.3, (16 x 4096) 14.3 / 15.6,
+// 2^22 (32 x 4096) 21.6 / 17.2; heads of 256, 2^21 (32 x 2048) 29.9 / 32.5,
+// 2^22 (32 x 4096) 48 / 39.
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
-  const bool can = (head_dim == 64 || head_dim == 128) && page_size >= 8 &&
-                   (page_size & (page_size - 1)) == 0 && prefix_len > 0;
+  const bool can = page_size >= 8 && (page_size & (page_size - 1)) == 0 && prefix_len > 0;
   const int forced = prefix_config();
   if (!can || forced >= 0) return can && forced == 1;
-  return rows > 16 && rows * num_heads_kv > ((int64_t)head_dim << 15) / prefix_len;
+  return rows > 16 && rows * num_heads_kv > (1 << (head_dim == 128 ? 22 : 21)) / prefix_len;
 }
 
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map) {
@@ -616,10 +692,11 @@ bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map) {
 }
 
 PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_heads_kv,
-                                  int64_t prefix_len) {
+                                  int head_dim, int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
   PrefixTilesPlan plan;
-  plan.row_tiles = (int)((rows + 2 * kTileRows - 1) / (2 * kTileRows));
+  const int of_item = row_tiles_of(head_dim) * kTileRows;
+  plan.row_tiles = (int)((rows + of_item - 1) / of_item);
   plan.blocks = (int)((prefix_len + kKeys - 1) / kKeys);
   // In step, if that leaves at most a fifth of the SMs without a CTA (which
   // costs as much as reading out of step); every CTA has an item or two blocks.
@@ -635,8 +712,12 @@ PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_h
 
 cudaError_t launch_prefix_tiles(const PrefixAttnArgs& a, const CUtensorMap& map,
                                 const Partials& parts, cudaStream_t stream) {
-  return a.x.head_dim == 64 ? launch<64>(a, map, parts, stream)
-                            : launch<128>(a, map, parts, stream);
+  switch (a.x.head_dim) {
+    case 64: return launch<64>(a, map, parts, stream);
+    case 128: return launch<128>(a, map, parts, stream);
+    case 256: return launch<256>(a, map, parts, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace kvq

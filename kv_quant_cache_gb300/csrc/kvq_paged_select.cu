@@ -588,13 +588,19 @@ size_t smem_bytes(int width) {
          (wide > sizeof(QueryParts<D>) ? wide : sizeof(QueryParts<D>));
 }
 
-// CTAs of a cluster: more while all of them are resident at once, two to an
-// SM, and have more than a tile of blocks for each warp.  (Several heads to a
-// cluster, warps side by side on a page's neighbouring heads, was not faster:
-// of 256 dims and 64 tokens 116 us against 99 us, of 128 as fast.)
-int cluster_for(int64_t items, int width) {
+// CTAs of a cluster: more while all of them are resident at once, two to an SM
+// (one with heads of 256, and for clusters of eight, which find room later),
+// and have more than a tile of blocks for each warp.  4 tokens x 8 kv heads x
+// 1024 blocks of 128 dims take 8.7 us in clusters of four, 10.7 in eights; 16
+// tokens, 17.2 us in one CTA each, 16.0 in pairs; 8 tokens of 256 dims 16.9 us in
+// pairs, 23.3 in fours.  (Several heads to a cluster, warps side by side on a
+// page's neighbouring heads, was not faster: of 256 dims and 64 tokens 116 us
+// against 99 us, of 128 as fast.)
+int cluster_for(int64_t items, int width, int head_dim) {
   int c = 1;
-  while (c < kMaxCluster && items * c * 2 <= 2 * 152 && width > c * 16 * 2) c *= 2;
+  while (c < kMaxCluster && width > c * 16 * 2 &&
+         items * c * 2 <= (head_dim == 256 || c * 2 == 8 ? 152 : 2 * 152))
+    c *= 2;
   return c;
 }
 
@@ -626,7 +632,7 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   p.blocks = a.blocks;
   p.errors = x.errors;
   const int64_t items = (int64_t)x.num_tokens * x.num_heads_kv;
-  p.cluster = cluster_for(items, x.table_width);
+  p.cluster = cluster_for(items, x.table_width, D);
   return launch_clusters(block_select_kernel<D>, dim3((unsigned)(items * p.cluster)),
                          dim3(kThreads), smem_bytes<D>(x.table_width), p.cluster, stream, p);
 }

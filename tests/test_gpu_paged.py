@@ -774,3 +774,28 @@ def test_without_programmatic_launches(cuda_device, prefix_way):
         results.append([bits(t.view(torch.int16)) for out in outs for t in out] + [bits(d["cache"])])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,page,prefix", [
+    (70, 16, 2, 64, 3000), (300, 4, 2, 8, 1290), (17, 1, 1, 16, 128), (129, 2, 2, 32, 129),
+    (64, 2, 1, 128, 20000), (257, 5, 1, 1024, 1500), (700, 2, 1, 64, 640), (40, 32, 8, 256, 77)])
+@pytest.mark.parametrize("std", [1.0, 100.0])
+def test_prefix_attention_of_heads_of_256(cuda_device, prefix_way, T, Hq, Hkv, page, prefix, std):
+    """A row tile, several, and a row more; a block of the prefix, a key more,
+    and many; with large scores, whose maxima keep moving, as well."""
+    g = gen(97 + T + prefix)
+    D, width, P = 256, 2 if page < 64 else 1, -(-prefix // page)
+    q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=P + 1, std=std)
+    lens = ints(g, 0, min(width * page, 40), T)
+    pages = spare[:P].int()
+    outside = P > 4
+    if outside:
+        pages[2] = cache.shape[0] + 1
+    err = counter()
+    args = (q.cuda(), cache.cuda(), pages.cuda(), prefix, table.cuda(), lens.cuda())
+    got = kvq.paged_shared_prefix_attention(*args, scale=-0.05, errors=err)
+    again = kvq.paged_shared_prefix_attention(*args, scale=-0.05)
+    want, tol = ref.prefix_attention(q, cache, pages, prefix, table, lens, -0.05)
+    ref.check(got, want, tol)
+    assert torch.equal(bits(got), bits(again))
+    assert (int(err.item()) > 0) == outside
