@@ -12,11 +12,11 @@
 // no table lookup stands between a page and its loads.  Then each of its warps
 // works alone, on every kWarps-th group of 16 keys, with an online softmax of
 // its own:
-//   * K and V rows of the group come in by 16-byte asynchronous copies,
-//     kStages groups deep, into a shared-memory ring that only this warp
-//     uses, so there is no CTA barrier in the loop; a 16-byte fragment c of
-//     row r is stored at c ^ (r & 7), which keeps the matrix loads free of
-//     bank conflicts;
+//   * K and V rows of the group come in by 16-byte asynchronous copies, three
+//     groups deep (heads of 256: one and a half), into a shared-memory ring
+//     that only this warp uses, so there is no CTA barrier in the loop; a
+//     16-byte fragment c of row r is stored at c ^ (r & 7), which keeps the
+//     matrix loads free of bank conflicts;
 //   * S = Q K^T and O += P V are 16x8x16 matrix instructions, fp32
 //     accumulators; the P fragments are the S fragments, rounded once to
 //     bf16 (the row sum adds the unrounded fp32 values);
@@ -25,12 +25,16 @@
 // The warps' states are joined in shared memory, the CTAs' through the
 // cluster's shared memory (one launch, no workspace).  Only where a cluster
 // per 16 rows would leave most of the GPU idle on a long range is the range
-// split further, into partials for the join kernel.
+// split further, into partials for the join kernel.  Where the prefix was
+// taken by the tensor-core tiles, this kernel runs behind theirs for the own
+// keys and joins their partials to its rows as it writes them.
 //
 // Bound by the reading of K and V: 16 rows of products per key row keep the
 // tensor pipes a fifth busy, which is why the small matrix instruction is
 // enough here and one tile of 16 rows is as cheap as one row.  64 sequences x 8
-// kv heads x 4096 selected keys of 128 dims, 1.07 GB: 158-163 us, 6.6-6.8 TB/s.
+// kv heads x 4096 selected keys of 128 dims, 1.07 GB: 158-163 us, 6.6-6.8 TB/s;
+// of 256 dims, 2.15 GB: 300 us (one CTA an SM with two whole groups a warp, 347
+// us; three CTAs of two warps, 399 us).
 // Short ranges are bound by latency instead: about 5 us from a CTA's start to
 // its end (length, page table, keys: three dependent reads; two joins).  Two
 // warps a CTA, two or four stages, three CTAs to an SM and an L2 prefetch of
@@ -51,6 +55,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kRows = 16;         // query rows of a CTA
 constexpr int kGroup = 16;        // keys of one step of a warp
 constexpr int kMaxPages = 2048;   // pages a CTA lists at a time
+constexpr int kFlight = 8;        // parts of the prefix that a thread loads together
 constexpr int kSoloPages = 512;   // .. where it is a single warp
 
 // Whose a listed page is: of all rows, or of the rows of one token of the tile.
@@ -114,18 +119,23 @@ __device__ __forceinline__ void keep_keys(uint32_t b[4], uint32_t keep, int lane
 // How many 16-key groups or rows fit, and where they lie.
 template <int D>
 struct Shape {
-  static constexpr int kStages = D == 256 ? 2 : 3;
+  // A warp's ring holds K and V of three steps; with heads of 256 a step and a
+  // half, three tiles that keys and values take in turn, so that two CTAs fit
+  // an SM here too.
+  static constexpr bool kHalf = D == 256;
+  static constexpr int kStages = 3;
   static constexpr int kPad = D + 8;                  // fp32 values of an output row: rows
                                                       // 32 bytes apart in the banks
   static constexpr int kTile = kGroup * D * 2;        // bytes of 16 K (or V) rows
   static constexpr int kStage = 2 * kTile;            // K, then V
-  static constexpr int kRing = kStages * kStage;      // of one warp
+  static constexpr int kRing = kStages * (kHalf ? kTile : kStage);
   static constexpr int kList = kMaxPages * 8;         // {page, valid keys}
   static constexpr int kState = kWarps * kRows * 8;   // {m, l} per warp and row
   static constexpr int kLse = kRows * 4;              // of the CTA's part, per row
   static constexpr int kSmem = kWarps * kRing + kList + kState + kLse;
   static constexpr int kSoloSmem = kRing + kSoloPages * 8;
   static_assert(kRing >= kRows * kPad * 4, "a warp's output fits in its ring");
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
 // The reference of a row's join with the prefix's parts, and the sum of all
@@ -144,29 +154,32 @@ __device__ __forceinline__ float parts_top(const AttnParams& p, int64_t row, flo
 // Joins four dims of a row (its own part's, normalised, in *v) with the
 // prefix's parts; they lie at p.parts.o[at + s * part_stride].  A part without
 // a key (its output may be unwritten) stays out.  One sweep with a running
-// reference, so that the sums and outputs of four parts are in flight together.
+// reference, so that the sums and outputs of several parts are in flight
+// together (with four instead of eight, 20 to 40 parts take 2-4 us longer).
 __device__ __forceinline__ void add_parts(const AttnParams& p, int64_t row, int64_t at,
                                           int64_t part_stride, float lse, float4* v) {
   float top = lse, sum = lse == -INFINITY ? 0.f : 1.f;
   float4 a = *v;  // zeros where there is no own key
-  for (int s0 = 0; s0 < p.prefix_parts; s0 += 4) {
-    float w[4];
-    float4 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int s = min(s0 + u, p.prefix_parts - 1);
-      w[u] = p.parts.lse[s * p.parts.rows + row];
-      x[u] = *reinterpret_cast<const float4*>(p.parts.o + at + s * part_stride);
-      if (s0 + u >= p.prefix_parts) w[u] = -INFINITY;
-    }
+  for (int s0 = 0; s0 < p.prefix_parts; s0 += kFlight) {
+    float w[kFlight];
+    float4 x[kFlight];
     const float old = top;
-    top = fmaxf(fmaxf(top, fmaxf(w[0], w[1])), fmaxf(w[2], w[3]));
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      w[u] = -INFINITY;
+      if (s0 + u < p.prefix_parts) {
+        w[u] = p.parts.lse[(s0 + u) * p.parts.rows + row];
+        x[u] = *reinterpret_cast<const float4*>(p.parts.o + at + (s0 + u) * part_stride);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) top = fmaxf(top, w[u]);
     const float ref = top == -INFINITY ? 0.f : top;
     const float f = old == top ? 1.f : exp2f(old - ref);
     sum *= f;
     a.x *= f, a.y *= f, a.z *= f, a.w *= f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kFlight; ++u) {
       if (w[u] == -INFINITY) continue;
       const float g = exp2f(w[u] - ref);
       sum += g;
@@ -347,10 +360,17 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
       return list[at];
     };
 
-    // Starts the copies of step i's 16 keys.
-    auto issue = [&](int i) {
+    // Where step i's keys and values lie.
+    auto k_tile = [&](int i) {
+      return ring + (S::kHalf ? 2 * i % S::kStages * S::kTile : i % S::kStages * S::kStage);
+    };
+    auto v_tile = [&](int i) {
+      return S::kHalf ? ring + (2 * i + 1) % S::kStages * S::kTile : k_tile(i) + S::kTile;
+    };
+    // Starts the copies of step i's 16 keys, their values, or both.
+    auto issue = [&](int i, bool keys, bool values) {
       const uint32_t k0 = (uint32_t)(i * kTeam + member) * kGroup;
-      const uint32_t stage = ring + (i % S::kStages) * S::kStage;
+      const uint32_t kt = k_tile(i), vt = v_tile(i);
       constexpr int FRAGS = D / 8;                          // 16-byte fragments of a row
       constexpr int RPI = 32 / FRAGS > 0 ? 32 / FRAGS : 1;  // rows of one warp-wide copy
       const int r0 = lane / FRAGS, c = lane % FRAGS;
@@ -369,9 +389,9 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
           const int r = j * RPI + r0;
           const bool ok = r < there;
           const __nv_bfloat16* from = ok ? src + j * RPI * D : p.cache;
-          const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
-          cp_async16(dst, from, ok);
-          cp_async16(dst + S::kTile, ok ? from + v_from_k : from, ok);
+          const uint32_t at = r * (2 * D) + ((c ^ (r & 7)) << 4);
+          if (keys) cp_async16(kt + at, from, ok);
+          if (values) cp_async16(vt + at, ok ? from + v_from_k : from, ok);
         }
       } else {
         int64_t row = -1;  // lane r < 16 finds row r's place
@@ -386,18 +406,29 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
           const int r = j * RPI + r0;
           const int64_t from = __shfl_sync(kFullMask, row, r);
           const __nv_bfloat16* src = p.cache + (from < 0 ? 0 : from + 8 * c);
-          const uint32_t dst = stage + r * (2 * D) + ((c ^ (r & 7)) << 4);
-          cp_async16(dst, src, from >= 0);
-          cp_async16(dst + S::kTile, from >= 0 ? src + v_from_k : src, from >= 0);
+          const uint32_t at = r * (2 * D) + ((c ^ (r & 7)) << 4);
+          if (keys) cp_async16(kt + at, src, from >= 0);
+          if (values) cp_async16(vt + at, from >= 0 ? src + v_from_k : src, from >= 0);
         }
       }
       cp_commit();
     };
 
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      if (S::kHalf) issue(0, i == 0, i == 1);
+      else issue(i, true, true);
+    }
+    // heads of 256: the next step's values take the place of the keys
+    auto next_values = [&](int i) {
+      __syncwarp();
+      issue(i + 1, false, true);
+      cp_wait<S::kStages - 1>();
+      __syncwarp();
+    };
     for (int i = 0; i < steps; ++i) {
-      issue(i + S::kStages - 1);
+      if (S::kHalf) issue(i + 1, true, false);
+      else issue(i + S::kStages - 1, true, true);
       cp_wait<S::kStages - 1>();
       __syncwarp();
       // whose the step's keys are: lane r < 16 for key r, -2 where there is none
@@ -422,10 +453,11 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
         todo = __ballot_sync(kFullMask, whose != -2);
       }
       if (todo == 0) {
-        __syncwarp();
+        if (S::kHalf) next_values(i);
+        else __syncwarp();
         continue;
       }
-      const uint32_t kt = ring + (i % S::kStages) * S::kStage, vt = kt + S::kTile;
+      const uint32_t kt = k_tile(i), vt = v_tile(i);
       float raw[2][4] = {};
       {
         const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
@@ -437,6 +469,7 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
           mma16816(raw[1], qf[k], b[2], b[3]);
         }
       }
+      if (S::kHalf) next_values(i);
       // one round for all keys that the same rows see: a single one but where
       // small pages of several tokens share the step
       constexpr bool kMayMix = !SPARSE && !WHOLE;
@@ -754,29 +787,28 @@ struct Spread {
   bool solo;  // a warp per row tile
 };
 
-// CTAs are added while all of them are resident at once (two to an SM, one
-// with heads of 256; with half as many again in a second wave the same range
-// took 20-30 % longer, with twice as many, 32 tiles of 256 dims, 24 us against
-// 10.4) and each keeps at least two steps of 16 keys for every warp: first
-// within a cluster of up to 8 (joined in place); beyond that, as partials that
-// a second launch joins, only where a CTA would be left with more than 2048
-// keys (below, the second launch costs more than it saves).  Behind the
-// prefix's tiles (`late`) the SMs come free one by one, and eight seats of a
-// cluster late: there four serve up to 8192 keys (16 tokens of 32 heads of 128
-// after 2048 keys, own keys 64: 14.2 us against 19.4; 640: 17.2 / 22.4; 2048,
-// more than that: 34.8 / 29.2).
-Spread spread_for(int64_t units, int64_t pages, int page_size, int head_dim, bool late) {
+// CTAs are added while all of them are resident at once (two to an SM; with
+// half as many again in a second wave the same range took 20-30 % longer, with
+// twice as many, 24 us against 10.4) and each keeps at least two steps of 16
+// keys for every warp: first within a cluster of up to 8 (joined in place);
+// beyond that, as partials that a second launch joins, only where a CTA would
+// be left with more than 2048 keys (below, the second launch costs more than it
+// saves).  Behind the prefix's tiles (`late`) the SMs come free one by one, and
+// eight seats of a cluster late: there four serve up to 8192 keys (16 tokens of
+// 32 heads of 128 after 2048 keys, own keys 64: 14.2 us against 19.4; 640: 17.2
+// / 22.4; 2048, more than that: 34.8 / 29.2).
+Spread spread_for(int64_t units, int64_t pages, int page_size, bool late) {
   Spread s = {1, 1, false};
-  const int64_t keys = pages * page_size, seats = head_dim == 256 ? 152 : 2 * 152;
+  const int64_t keys = pages * page_size;
   const int most = late && keys < 8192 ? kMaxCluster / 2 : kMaxCluster;
-  auto fit = [&](int cluster) {  // clusters resident at once: they do not fill a GPC evenly
-    return cluster < 8 ? seats / cluster - (cluster == 4 ? 2 : 0) : head_dim == 256 ? 15 : 36;
-  };
+  // clusters resident at once: larger ones do not fill the SMs evenly
+  auto fit = [](int cluster) { return cluster == 8 ? 36 : cluster == 4 ? 74 : 2 * 152 / cluster; };
   while (s.cluster < most && units <= fit(s.cluster * 2) &&
          keys >= (int64_t)s.cluster * 2 * kGroup * kWarps)
     s.cluster *= 2;
   int64_t splits = 1;
-  while (!late && units * s.cluster * (splits + 1) <= seats && keys > s.cluster * splits * 2048)
+  while (!late && units * s.cluster * (splits + 1) <= 2 * 152 &&
+         keys > s.cluster * splits * 2048)
     ++splits;
   s.splits = (int)splits;
   // With many tiles of short ranges, a CTA of one warp each: no joins between
@@ -857,21 +889,19 @@ int64_t shared_tiles(int64_t num_tokens, int num_q, int num_kv) {
   return (num_tokens * (num_q / num_kv) + kRows - 1) / kRows;
 }
 
-Spread sparse_spread(int64_t num_tokens, int num_q, int num_kv, int head_dim, int page_size,
-                     int topk) {
-  return spread_for(num_tokens * num_kv * sparse_tiles(num_q, num_kv), topk, page_size, head_dim,
-                    false);
+Spread sparse_spread(int64_t num_tokens, int num_q, int num_kv, int page_size, int topk) {
+  return spread_for(num_tokens * num_kv * sparse_tiles(num_q, num_kv), topk, page_size, false);
 }
 
 // The tokens' own keys, with the prefix's or behind its tiles (`late`).  The
 // own pages that a tile can have: those of every token that has a row in it.
-Spread shared_spread(int64_t num_tokens, int num_q, int num_kv, int head_dim, int page_size,
+Spread shared_spread(int64_t num_tokens, int num_q, int num_kv, int page_size,
                      int64_t prefix_len, int table_width, bool late) {
   const int group = num_q / num_kv;
   const int64_t tokens = group >= kRows ? 2 : (kRows + group - 2) / group + 1;
   const int64_t own = (tokens < num_tokens ? tokens : num_tokens) * table_width;
   return spread_for(shared_tiles(num_tokens, num_q, num_kv) * num_kv,
-                    (prefix_len + page_size - 1) / page_size + own, page_size, head_dim, late);
+                    (prefix_len + page_size - 1) / page_size + own, page_size, late);
 }
 
 }  // namespace
@@ -893,8 +923,7 @@ cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, voi
 
 int64_t sparse_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int topk) {
-  const int s =
-      sparse_spread(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, topk).splits;
+  const int s = sparse_spread(num_tokens, num_heads_q, num_heads_kv, page_size, topk).splits;
   return s == 1 ? 0 : partials_bytes(s, num_tokens * num_heads_q, head_dim);
 }
 
@@ -904,8 +933,7 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
   p.blocks = a.blocks;
   p.topk = a.topk;
   p.tiles = sparse_tiles(x.num_heads_q, x.num_heads_kv);
-  const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
-                                 x.page_size, a.topk);
+  const Spread s = sparse_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size, a.topk);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   if (s.splits > 1)
     p.parts = partials_at(a.workspace, s.splits, (int64_t)x.num_tokens * x.num_heads_q, x.head_dim);
@@ -919,8 +947,8 @@ int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads
                               int head_dim, int page_size, int64_t prefix_len,
                               int table_width) {
   const int64_t rows = num_tokens * num_heads_q;
-  const int s = shared_spread(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size,
-                              prefix_len, table_width, false).splits;
+  const int s = shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, prefix_len,
+                              table_width, false).splits;
   int64_t slots = s == 1 ? 0 : s;
   if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len)) {
     // either way may be taken: which one depends on where the cache lies
@@ -944,8 +972,8 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
                      prefix_tiles_map(a, &map);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.prefix_len = tiles ? 0 : (int)a.prefix_len;
-  const Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
-                                 x.page_size, p.prefix_len, x.table_width, tiles);
+  const Spread s = shared_spread(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.page_size,
+                                 p.prefix_len, x.table_width, tiles);
   if (!tiles) {
     if (s.splits > 1) p.parts = partials_at(a.workspace, s.splits, rows, x.head_dim);
     const cudaError_t e = launch_attn_dim<false>(p, x.head_dim, units, s, stream);

@@ -12,29 +12,35 @@
 //   S = Q K^T   [128 x 128], fp32 in tensor memory,
 //   P = 2^(S scale log2(e) - m), rounded once to bf16, over S's columns,
 //   O += P V    [128 x D], fp32 in tensor memory, P read from there.
+// With heads of 256, O of one tile takes half of the tensor memory: an item is
+// one tile, and its blocks take S's two places in turn instead.
 // Warps have one role each:
-//   * warps 0-7 and 8-15: the softmax of tile 0 and tile 1.  Two threads own
+//   * warps 0-7 and 8-15: the softmax of tile 0 and of tile 1 (the warps
+//     behind these are 8 lower where there is no tile 1).  Two threads own
 //     a row (its tensor-memory lane), 64 keys each, and exchange only their
 //     maxima (1250 cycles from scores to weights; one thread a row: 1500).
 //     The reference m of a row only moves when a score exceeds it by more than
 //     2^8; until then weights above 1 are as exact as those below, and O is
 //     seldom rescaled;
 //   * warp 16, one lane: issues the matrix instructions.  While one tile's
-//     softmax runs, the other tile's products do;
-//   * warps 17 and 18: load K and V, two blocks ahead, by tensor-map copies (a
-//     page, or 128 keys of one, at a time; 128-byte swizzle).  A block that
+//     (or block's) softmax runs, the other's products do;
+//   * warps 17 and 18: load K and V, two blocks ahead (heads of 256: the two
+//     halves of a block's dims), by tensor-map copies (a page, or 128 keys of
+//     one, at a time; 128-byte swizzle).  A block that
 //     ends past the prefix, or that lists a page outside the cache, is copied
 //     by the warp's own loads instead, with zeros in V where there is no key;
 //     the softmax gives those places weight 0.
-// A segment's result is a partial (normalised O and log2 of the weight sum)
-// for the join with the item's other segments and each token's own keys.
+// A segment's result is a partial (normalised O and log2 of the weight sum).
+// The kernel of the tokens' own keys, launched behind this one, joins them.
 //
 // Bound by the tensor cores, and by the power they may draw: 2048 rows x 8 kv
 // heads x 32768 keys of 128 dims, 275 GFLOP, take 176 us (1560 TFLOP/s, tensor
 // pipe active 72 % of the time, 141 MB read for 134 MB of keys and values);
 // run back to back the clock settles at 1.65 of 2.07 GHz at the power limit.
 // With heads of 64 the softmax bounds it: half the products for the same
-// exponentials (860 TFLOP/s).
+// exponentials (939 TFLOP/s); of 256, 1580 TFLOP/s (348 us, 16-token pages 408
+// us; a prefetch of the next block into the L2 gained 3 % there and lost 20 %
+// with small pages).
 #include <string.h>
 
 #include "kvq_paged_attn.cuh"
@@ -667,8 +673,9 @@ int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 // heads of 128, own keys up to 64): 2^21 (32 tokens x 2048 keys) 16.3 / 19.8,
 // 2^22 (16 x 8192) 24.2 / 21.8, (64 x 2048) 25.6 / 26.1, 2^23 (16 x 16384)
 // 40 / 26; heads of 64, 2^21 (32 x 2048) 14.2 / 12.3, (16 x 4096) 14.3 / 15.6,
-// 2^22 (32 x 4096) 21.6 / 17.2; heads of 256, 2^21 (32 x 2048) 29.9 / 32.5,
-// 2^22 (32 x 4096) 48 / 39.
+// 2^22 (32 x 4096) 21.6 / 17.2; heads of 256, 2^21 (32 x 2048) 28 / 30, (16 x
+// 4096) 27.7 / 28.1, 2^22 (32 x 4096) 43 / 34, 2^25 (256 tokens x 64 heads x
+// 16384) 1700 / 200.
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
