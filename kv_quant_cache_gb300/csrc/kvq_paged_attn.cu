@@ -54,7 +54,6 @@ constexpr int kWarps = 4;
 constexpr int kMaxCluster = 8;
 constexpr int kRows = 16;         // query rows of a CTA
 constexpr int kGroup = 16;        // keys of one step of a warp
-constexpr int kMaxPages = 2048;   // pages a CTA lists at a time
 constexpr int kFlight = 8;        // parts of the prefix that a thread loads together
 constexpr int kSoloPages = 512;   // .. where it is a single warp
 
@@ -89,6 +88,7 @@ struct AttnParams {
   // prefix (0: none); with several splits it goes to partials itself.
   __nv_bfloat16* out;
   int prefix_parts;
+  int prefix_ctas;  // .. from so many CTAs
   Partials parts;
   int* errors;
   int trigger_from;
@@ -119,9 +119,12 @@ __device__ __forceinline__ void keep_keys(uint32_t b[4], uint32_t keep, int lane
 // How many 16-key groups or rows fit, and where they lie.
 template <int D>
 struct Shape {
+  // CTAs of an SM: four of 64 dims (a shorter list; three with one of 2048 pages:
+  // 64 sequences x 8 kv heads x 4096 keys 114 us against 89)
+  static constexpr int kCtas = D == 64 ? 4 : 2;
+  static constexpr int kMaxPages = D == 64 ? 512 : 2048;  // pages a CTA lists at a time
   // A warp's ring holds K and V of three steps; with heads of 256 a step and a
-  // half, three tiles that keys and values take in turn, so that two CTAs fit
-  // an SM here too.
+  // half, three tiles that keys and values take in turn, so that two CTAs fit.
   static constexpr bool kHalf = D == 256;
   static constexpr int kStages = 3;
   static constexpr int kPad = D + 8;                  // fp32 values of an output row: rows
@@ -135,7 +138,7 @@ struct Shape {
   static constexpr int kSmem = kWarps * kRing + kList + kState + kLse;
   static constexpr int kSoloSmem = kRing + kSoloPages * 8;
   static_assert(kRing >= kRows * kPad * 4, "a warp's output fits in its ring");
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // The reference of a row's join with the prefix's parts, and the sum of all
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
   cg::cluster_group cluster = cg::this_cluster();
   // After the prefix's tiles: they let this kernel be scheduled only when what
   // came before both is done, and it needs their partials at its end alone.
-  const bool late = p.prefix_parts > 0;
+  const bool late = !SPARSE && p.prefix_parts > 0;
   if (!late) grid_dependency_sync(p.trigger_from);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kTeam = SOLO ? 1 : kWarps;  // warps on a row tile
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__((SOLO ? 1 : kWarps) * 32) paged_attn_kernel(co
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
   // as many pages at a time as the list holds: usually all of them
-  constexpr int kCapacity = SOLO ? kSoloPages : kMaxPages;
+  constexpr int kCapacity = SOLO ? kSoloPages : S::kMaxPages;
   for (int page_lo = page0; page_lo < page_end; page_lo += kCapacity) {
     const int listed = min(kCapacity, page_end - page_lo);
     if (page_lo != page0) {  // the list is no longer read
@@ -826,12 +829,18 @@ cudaError_t launch_attn(AttnParams p, cudaStream_t stream) {
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
   constexpr int threads = SOLO ? 32 : kWarps * 32;
-  constexpr int smem = SOLO ? Shape<D>::kSoloSmem : Shape<D>::kSmem;
+  constexpr int most = 110 * 1024;
+  int smem = SOLO ? Shape<D>::kSoloSmem : Shape<D>::kSmem;
   const cudaError_t e = tma::prepare(paged_attn_kernel<D, SPARSE, WHOLE, SOLO>, threads, smem,
-                                     cache, &per_sm);
+                                     cache, &per_sm, most);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)p.units * p.cluster, wave = (int64_t)per_sm * device_sm_count();
   p.trigger_from = ctas > wave ? (int)(ctas - wave) : 0;
+  // Behind the prefix's tiles, where these have most SMs, the SMs come free one
+  // by one: the first shall not take four CTAs if two on each are enough (33 x 3
+  // tokens of 64 dims 27.6 us against 32.3; where the tiles leave SMs free, 64
+  // tokens of 32 heads after 2048 keys, 17.7 us against 14.2).
+  if (p.prefix_ctas > 76 && ctas <= 2 * 152 && smem < most) smem = most;
   return launch_clusters(paged_attn_kernel<D, SPARSE, WHOLE, SOLO>,
                          dim3((unsigned)ctas, (unsigned)p.splits), dim3(threads), smem, p.cluster,
                          stream, p);
@@ -982,8 +991,10 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   }
   // The tiles, and then the tokens' own keys, whose kernel joins both: its CTAs
   // start as the tiles' run out, and need their partials at the end alone.
-  p.prefix_parts = prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
-                                     a.prefix_len).parts;
+  const PrefixTilesPlan plan = prefix_tiles_plan(x.num_tokens, x.num_heads_q, x.num_heads_kv,
+                                                 x.head_dim, a.prefix_len);
+  p.prefix_parts = plan.parts;
+  p.prefix_ctas = plan.lanes * plan.teams;
   p.parts = partials_at(a.workspace, p.prefix_parts, rows, x.head_dim);
   const cudaError_t e = launch_prefix_tiles(a, map, p.parts, stream);
   if (e != cudaSuccess) return e;

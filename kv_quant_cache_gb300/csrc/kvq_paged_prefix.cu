@@ -672,10 +672,10 @@ int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 // the products' size, GB300, us of the rows / the tiles (32 query heads, 8 kv
 // heads of 128, own keys up to 64): 2^21 (32 tokens x 2048 keys) 16.3 / 19.8,
 // 2^22 (16 x 8192) 24.2 / 21.8, (64 x 2048) 25.6 / 26.1, 2^23 (16 x 16384)
-// 40 / 26; heads of 64, 2^21 (32 x 2048) 14.2 / 12.3, (16 x 4096) 14.3 / 15.6,
-// 2^22 (32 x 4096) 21.6 / 17.2; heads of 256, 2^21 (32 x 2048) 28 / 30, (16 x
-// 4096) 27.7 / 28.1, 2^22 (32 x 4096) 43 / 34, 2^25 (256 tokens x 64 heads x
-// 16384) 1700 / 200.
+// 40 / 25; heads of 64, 2^21 (32 x 2048) 12.6 / 11.9, (16 x 4096) 12.6 / 14.4,
+// 2^22 (32 x 4096) 18.2 / 16.1; heads of 256, 2^21 (32 x 2048) 28 / 29, (16 x
+// 4096) 27.4 / 26.2, 2^22 (32 x 4096) 43 / 32, 2^28 (256 tokens x 64 heads x
+// 16384) 1760 / 205.
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);

@@ -198,11 +198,12 @@ inline bool encode_bf16_4d_swizzled(CUtensorMap* map, const void* base, const cu
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Opts `kernel` in to `smem` bytes of dynamic shared memory and counts its
-// resident CTAs per SM, once per device (cached).
+// Opts `kernel` in to `smem` bytes of dynamic shared memory (to `most`, where a
+// launch may ask for more) and counts its resident CTAs per SM at `smem`, once
+// per device (cached).
 template <typename Kernel>
 cudaError_t prepare(Kernel kernel, int threads, size_t smem, std::atomic<int>* cache,
-                    int* per_sm) {
+                    int* per_sm, size_t most = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -214,7 +215,8 @@ cudaError_t prepare(Kernel kernel, int threads, size_t smem, std::atomic<int>* c
       return cudaSuccess;
     }
   }
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(most > smem ? most : smem));
   if (e != cudaSuccess) return e;
   int n = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
