@@ -34,8 +34,6 @@ namespace cg = cooperative_groups;
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
 struct SelectParams {
@@ -73,11 +71,12 @@ __device__ __forceinline__ uint64_t key64(double s) {
 }
 
 constexpr int kBins = 2048;
-constexpr int kFew = kThreads;  // candidates that are ranked against each other directly
 
-// Shared memory of a CTA (the selecting one uses all of it).
-template <int D>
+// Shared memory of a CTA of T threads (the selecting one uses all of it).
+template <int D, int T>
 struct Shared {
+  static constexpr int kThreads = T, kWarps = T / 32;
+  static constexpr int kFew = T;  // candidates that are ranked against each other directly
   double up64[D], down64[D];
   // of every scoring warp: its error bound, its smallest and largest key (of
   // blocks that are not kept anyway)
@@ -102,6 +101,7 @@ struct QueryParts {
 // Inclusive prefix sum over the CTA of one value a thread; *total: all of it.
 template <typename Sh>
 __device__ unsigned block_scan(unsigned v, Sh& sh, unsigned* total) {
+  constexpr int kWarps = Sh::kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -126,7 +126,7 @@ __device__ unsigned block_scan(unsigned v, Sh& sh, unsigned* total) {
 // sh.bin_count the bin's keys.  All threads call, after a barrier.
 template <typename Sh>
 __device__ void find_bin(unsigned place, Sh& sh) {
-  constexpr int PER = kBins / kThreads;
+  constexpr int PER = kBins / Sh::kThreads;
   const int first = kBins - 1 - PER * (int)threadIdx.x;  // this thread's highest bin
   unsigned c[PER], sum = 0;
 #pragma unroll
@@ -155,6 +155,7 @@ __device__ void find_bin(unsigned place, Sh& sh) {
 template <typename Key, typename Get, typename Sh>
 __device__ Key select_largest(int n, unsigned place, Key lo, Key hi, Sh& sh, const Get& get,
                               unsigned* equal) {
+  constexpr int kThreads = Sh::kThreads, kFew = Sh::kFew;
   const int tid = threadIdx.x;
   while (true) {
     int shift = 0;
@@ -212,11 +213,12 @@ __device__ Key select_largest(int n, unsigned place, Key lo, Key hi, Sh& sh, con
 // `scorers` entries of err, least and most; the group's queries, the request's
 // pages and the bounds of the head on page 0 for scores that have to be taken
 // again.
-template <int D>
-__device__ void select_blocks(const SelectParams& p, Shared<D>& sh, uint32_t* keys,
+template <int D, typename Sh>
+__device__ void select_blocks(const SelectParams& p, Sh& sh, uint32_t* keys,
                               unsigned long long* wide, int scorers, int n,
                               const __nv_bfloat16* queries, const int* row,
                               const __nv_bfloat16* bounds, int* out) {
+  constexpr int kThreads = Sh::kThreads, kWarps = Sh::kWarps, kFew = Sh::kFew;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t page_elems = (int64_t)p.num_kv * 2 * D;
   // ---- the k-th largest, its doubtful neighbours ---------------------------------------
@@ -377,13 +379,15 @@ __device__ void select_blocks(const SelectParams& p, Shared<D>& sh, uint32_t* ke
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2)
+template <int D, int kThreads>
+__global__ void __launch_bounds__(kThreads, (D == 256 ? 1 : 2) * 256 / kThreads)
 block_select_kernel(const SelectParams p) {
+  using Sh = Shared<D, kThreads>;
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint8_t smem[];
-  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
+  Sh& sh = *reinterpret_cast<Sh*>(smem);
   // scores of the first CTA: fp32 keys, then fp64 keys, one of each per block
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Shared<D>) + 15) & ~size_t(15)));
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + ((sizeof(Sh) + 15) & ~size_t(15)));
   unsigned long long* wide =
       reinterpret_cast<unsigned long long*>(keys + ((p.table_width + 3) & ~3));
   QueryParts<D>& queries_in = *reinterpret_cast<QueryParts<D>*>(wide);
@@ -402,8 +406,7 @@ block_select_kernel(const SelectParams p) {
   int len = __ldg(p.lens + t);
   const __nv_bfloat16* queries = p.q + t * p.q_stride + (int64_t)h * p.group * D;
   bool any_weight = false;
-  if (tid < D / 2) {  // two dims a thread
-    const int d = 2 * tid;
+  for (int d = 2 * tid; d < D; d += 2 * kThreads) {  // two dims a thread
     const __nv_bfloat16* q = queries + d;
     float sums[2][2] = {};  // down, up
     for (int g0 = 0; g0 < p.group; g0 += 8) {  // eight loads in flight
@@ -474,7 +477,7 @@ block_select_kernel(const SelectParams p) {
   // inner dimension does not matter as long as both operands have it.
   // (As fp32 multiply-adds by 32 lanes a block this took 82 instructions a
   // block, with too few loads in flight: 64 tokens x 8 heads of up to 1024
-  // blocks 77 us, now 51 us, 202 MB at 4.0 TB/s; one token of 1563 blocks
+  // blocks 77 us, now 50 us, 202 MB at 4.0 TB/s; one token of 1563 blocks
   // 16 us, now 10 us.)
   constexpr int STEPS = 2 * D / 32;  // of 32 values: two matrix instructions
   uint32_t* to_keys = p.cluster > 1 ? cluster.map_shared_rank(keys, 0) : keys;
@@ -564,7 +567,7 @@ block_select_kernel(const SelectParams p) {
   least = __reduce_min_sync(kFullMask, least);
   most = __reduce_max_sync(kFullMask, most);
   if (lane == 0) {
-    Shared<D>& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, 0) : sh;
+    Sh& to = p.cluster > 1 ? *cluster.map_shared_rank(&sh, 0) : sh;
     const int at = rank * kWarps + warp;
     const float bound = 0x1p-17f + (float)(8 + p.group) * 0x1p-24f;
     to.err[at] = odd ? INFINITY : any_weight ? worst * bound + 1.0e-35f : 0.f;
@@ -581,10 +584,10 @@ block_select_kernel(const SelectParams p) {
                    p.bounds + (int64_t)h * 2 * D, out);
 }
 
-template <int D>
+template <int D, int kThreads>
 size_t smem_bytes(int width) {
   const size_t wide = (size_t)width * 8;
-  return ((sizeof(Shared<D>) + 15) & ~size_t(15)) + (size_t)((width + 3) & ~3) * 4 +
+  return ((sizeof(Shared<D, kThreads>) + 15) & ~size_t(15)) + (size_t)((width + 3) & ~3) * 4 +
          (wide > sizeof(QueryParts<D>) ? wide : sizeof(QueryParts<D>));
 }
 
@@ -604,14 +607,15 @@ int cluster_for(int64_t items, int width, int head_dim) {
   return c;
 }
 
-template <int D>
-cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
+template <int D, int kThreads>
+cudaError_t launch_select(const BlockSelectArgs& a, int cluster, cudaStream_t stream) {
   const PagedQuery& x = a.x;
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
   // one opt-in for the largest size that the validation lets through
-  const cudaError_t e = tma::prepare(block_select_kernel<D>, kThreads,
-                                     smem_bytes<D>(kMaxSelectBlocks), cache, &per_sm);
+  const cudaError_t e =
+      tma::prepare(block_select_kernel<D, kThreads>, kThreads,
+                   smem_bytes<D, kThreads>(kMaxSelectBlocks), cache, &per_sm);
   if (e != cudaSuccess) return e;
   SelectParams p;
   p.q = static_cast<const __nv_bfloat16*>(x.q);
@@ -632,9 +636,23 @@ cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
   p.blocks = a.blocks;
   p.errors = x.errors;
   const int64_t items = (int64_t)x.num_tokens * x.num_heads_kv;
-  p.cluster = cluster_for(items, x.table_width, D);
-  return launch_clusters(block_select_kernel<D>, dim3((unsigned)(items * p.cluster)),
-                         dim3(kThreads), smem_bytes<D>(x.table_width), p.cluster, stream, p);
+  p.cluster = cluster;
+  return launch_clusters(block_select_kernel<D, kThreads>, dim3((unsigned)(items * cluster)),
+                         dim3(kThreads), smem_bytes<D, kThreads>(x.table_width), cluster, stream,
+                         p);
+}
+
+// More items than CTAs that are resident at once: CTAs of half the threads, of
+// which twice as many are, so that some select while others score.  256 tokens
+// x 8 heads of 128 dims, 64 blocks 30 us against 46, 256 blocks 60 against 76;
+// 64 tokens, 1024 blocks 49.8 / 51.3 (of 64 dims 27.5 / 30.0, of 256 91 / 99),
+// 2048 blocks, which therefore keep the larger, 128 / 99.
+template <int D>
+cudaError_t launch_select(const BlockSelectArgs& a, cudaStream_t stream) {
+  const int64_t items = (int64_t)a.x.num_tokens * a.x.num_heads_kv;
+  if (items > (D == 256 ? 152 : 2 * 152) && a.x.table_width <= 1024)
+    return launch_select<D, 128>(a, 1, stream);
+  return launch_select<D, 256>(a, cluster_for(items, a.x.table_width, D), stream);
 }
 
 }  // namespace

@@ -799,3 +799,31 @@ def test_prefix_attention_of_heads_of_256(cuda_device, prefix_way, T, Hq, Hkv, p
     ref.check(got, want, tol)
     assert torch.equal(bits(got), bits(again))
     assert (int(err.item()) > 0) == outside
+
+
+@pytest.mark.parametrize("T,Hkv,D,width,topk", [
+    (40, 8, 128, 1024, 32), (160, 1, 256, 130, 16), (62, 5, 64, 600, 300), (310, 1, 128, 300, 200),
+    (77, 4, 64, 1025, 7), (153, 1, 256, 16, 15)])
+def test_block_select_of_many_tokens(cuda_device, T, Hkv, D, width, topk):
+    """More tokens and heads than CTAs that run at once, for some of them with
+    equal blocks, with scores that fp32 cannot order, and with zero queries."""
+    g = gen(98 + T + width)
+    page = 16
+    bounds = bounds_of(g, width + 40, Hkv, D)
+    few = width // 3
+    bounds[:few] = bounds[0]  # equal
+    bounds[few:2 * few] = bounds[few]  # these differ where the query is tiny
+    bounds[few:2 * few, :, 1, 5] = (1 + torch.arange(few)[:, None] / 1024).bfloat16()
+    q = normal(g, T, 2 * Hkv, D)
+    q[:, :, 5] = 2.0 ** -22
+    q[1::7] = 0
+    rows = torch.stack([torch.randperm(width, generator=g) for _ in range(3)]).int()
+    spread = torch.randperm(width + 40, generator=g)[:width].int()
+    table = torch.cat([rows, spread[None]])
+    requests = ints(g, 0, 3, T)
+    lens = ints(g, 0, width * page, T)
+    lens[:T // 2] = width * page
+    err = counter()
+    got = run_select(q, bounds, table, lens, page, topk, 1, 1, requests=requests, errors=err)
+    assert torch.equal(got, ref.select(q, bounds, table, lens, page, topk, 1, 1, requests))
+    assert int(err.item()) == 0
