@@ -976,7 +976,9 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   const int64_t rows = (int64_t)x.num_tokens * x.num_heads_q;
   const int64_t units = (int64_t)p.tiles * x.num_heads_kv;
   CUtensorMap map;
-  const bool tiles = prefix_tiles_fit(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
+  // (the tiles scale their masked scores, -inf, too: a scale of zero is not theirs)
+  const bool tiles = a.scale != 0.f &&
+                     prefix_tiles_fit(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
                                       x.page_size, a.prefix_len) &&
                      prefix_tiles_map(a, &map);
   p.out = static_cast<__nv_bfloat16*>(a.out);

@@ -827,3 +827,40 @@ def test_block_select_of_many_tokens(cuda_device, T, Hkv, D, width, topk):
     got = run_select(q, bounds, table, lens, page, topk, 1, 1, requests=requests, errors=err)
     assert torch.equal(got, ref.select(q, bounds, table, lens, page, topk, 1, 1, requests))
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-42, -1e-42])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefix_attention_with_no_or_hardly_any_scale(cuda_device, prefix_way, D, scale):
+    """A scale of zero: the mean of the values that exist, in a partly filled
+    block and beside a page outside the cache as well."""
+    g = gen(99 + D)
+    T, Hq, Hkv, page, width, prefix = 40, 4, 1, 16, 2, 300
+    q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=19)
+    pages = spare.int()
+    pages[5] = -2
+    lens = ints(g, 0, width * page, T)
+    got = kvq.paged_shared_prefix_attention(q.cuda(), cache.cuda(), pages.cuda(), prefix,
+                                            table.cuda(), lens.cuda(), scale=scale)
+    ref.check(got, *ref.prefix_attention(q, cache, pages, prefix, table, lens, scale))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_lists_longer_than_a_cta_keeps(cuda_device, D):
+    """More row tiles than CTAs that are resident, and of a few tokens more
+    pages than a CTA lists at a time."""
+    g = gen(100 + D)
+    T, Hq, Hkv, page, topk = 165, 4, 2, 16, 2600
+    N = 500
+    q, cache = normal(g, T, Hq, D), normal(g, N, 2, Hkv, page, D)
+    table = ints(g, 0, N - 1, T, topk)
+    lens = ints(g, 0, 40, T)
+    lens[3], lens[100], lens[164] = topk * page, 513 * page, 2048 * page + 1
+    blocks = torch.full((T, Hkv, topk), -1, dtype=torch.int32)
+    for t in range(T):
+        n = -(-int(lens[t]) // page)
+        for h in range(Hkv):
+            blocks[t, h, topk - n:] = torch.randperm(n, generator=g).int()
+    got = kvq.paged_block_sparse_attention(q.cuda(), cache.cuda(), table.cuda(), blocks.cuda(),
+                                           lens.cuda())
+    ref.check(got, *ref.sparse_attention(q, cache, table, blocks, lens, D ** -0.5))
