@@ -158,6 +158,14 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  const int bytes = there ? 16 : 0;  // 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
@@ -255,6 +263,10 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     const int pair_bar = 1 + tile * 4 + (warp & 3);           // its two warps' barrier
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
     const uint32_t o_at = at + 256 + 128 * tile + (D / 2) * half;
+    // The warp's slice of its tile of Q, which it fills, and, when the products
+    // that read Q are done, passes the results through.
+    constexpr int kSlice = L::kTile / 8;
+    uint8_t* slice = smem + L::kQ + tile * L::kTile + (warp & 7) * kSlice;
     uint32_t done = 0;  // blocks of this tile so far: the phase of its barriers
     bool ok = true;
     auto pv_done = [&](uint32_t block) {
@@ -263,21 +275,28 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     };
     while (ok && seg.next(p)) {
       if (tile >= seg.tiles) continue;
-      // the tile's 256 threads bring in Q; the products that read the previous
-      // segment's have all been seen to be done
-      constexpr int FRAGS = D / 8, PASS = 256 / FRAGS;  // rows of one pass
-#pragma unroll 4
-      for (int i = 0; i < kTileRows / PASS; ++i) {
-        const int qr = i * PASS + (threadIdx.x & 255) / FRAGS, c = threadIdx.x % FRAGS;
+      // Q comes in, to each warp's slice of the tile; the products that read the
+      // previous segment's have all been seen to be done
+#pragma unroll
+      for (int i = 0; i < kSlice / 512; ++i) {
+        const int at = (warp & 7) * kSlice + i * 512 + lane * 16;
+        const int qr = (at & (128 * 128 - 1)) >> 7;
+        const int d = (at >> 14) * 64 + ((((at >> 4) ^ qr) & 7) << 3);
         const int64_t from = tile * kTileRows + qr;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (from < seg.rows_left) {
-          const uint32_t t = (uint32_t)(seg.row0 + from) / (uint32_t)p.group;
-          const int h = seg.kv_head * p.group + (int)((uint32_t)(seg.row0 + from) - t * p.group);
-          v = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (int64_t)h * D + 8 * c));
-          v.x ^= p.q_flip, v.y ^= p.q_flip, v.z ^= p.q_flip, v.w ^= p.q_flip;
+        const bool here = from < seg.rows_left;
+        const uint32_t flat = (uint32_t)(seg.row0 + (here ? from : 0));
+        const uint32_t t = flat / (uint32_t)p.group;
+        const int h = seg.kv_head * p.group + (int)(flat - t * p.group);
+        cp_async16(base + L::kQ + tile * L::kTile + at,
+                   p.q + (int64_t)t * p.q_stride + (int64_t)h * D + d, here);
+      }
+      cp_wait_all();
+      if (p.q_flip) {
+        for (int i = 0; i < kSlice / 512; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(slice + i * 512 + lane * 16);
+          const uint4 v = *at;
+          *at = make_uint4(v.x ^ p.q_flip, v.y ^ p.q_flip, v.z ^ p.q_flip, v.w ^ p.q_flip);
         }
-        st_shared16(base + L::kQ + tile * L::kTile + tile_offset(qr, c), v);
       }
       tma::fence_proxy_async();
       __syncwarp();
@@ -396,18 +415,38 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
                           (int)((uint32_t)(seg.row0 + r) - t * p.group);
       const int slot = seg.slot(p);
       const float f = l == 0.f ? 0.f : 1.f / l;
-      float* out = p.parts.o + (slot * p.parts.rows + row) * D + (D / 2) * half;
+      // Through shared memory, so that lanes side by side write a row's values
+      // side by side: 32 rows x kWide values at a time, fragments of four
+      // exchanged by row against bank conflicts.
+      constexpr int kWide = D == 64 ? 16 : 32, kFrags = kWide / 4;
+      auto place = [&](int of, int frag) {
+        return reinterpret_cast<float4*>(
+            slice + (of * kFrags + (frag ^ ((kFrags == 8 ? of : of >> 1) & (kFrags - 1)))) * 16);
+      };
+      float* out = p.parts.o + slot * p.parts.rows * D + (D / 2) * half;
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];
         tc::ld32(o, o_at + 32 * c);
         tc::wait_ld();
-        if (r < seg.rows_left) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(out + 32 * c + k) =
-                make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
-                            __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+        for (int k0 = 0; k0 < 32; k0 += kWide) {
+#pragma unroll
+          for (int k = 0; k < kFrags; ++k) {
+            const uint32_t* x = o + k0 + 4 * k;
+            *place(lane, k) =
+                make_float4(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f,
+                            __uint_as_float(x[2]) * f, __uint_as_float(x[3]) * f);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kFrags; ++i) {
+            const int of = i * (32 / kFrags) + lane / kFrags, k = lane % kFrags;
+            const int64_t to = __shfl_sync(kFullMask, (int)row, of);
+            if (r - lane + of < seg.rows_left)
+              *reinterpret_cast<float4*>(out + to * D + 32 * c + k0 + 4 * k) = *place(of, k);
+          }
+          __syncwarp();
         }
       }
       if (half == 0 && r < seg.rows_left) {
@@ -670,19 +709,19 @@ int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 // one row tile of the other kernel, which reads the prefix once.  Beyond, each
 // of its row tiles reads it again, but it is one launch without partials: by
 // the products' size, GB300, us of the rows / the tiles (32 query heads, 8 kv
-// heads of 128, own keys up to 64): 2^21 (32 tokens x 2048 keys) 16.3 / 19.8,
-// 2^22 (16 x 8192) 24.2 / 21.8, (64 x 2048) 25.6 / 26.1, 2^23 (16 x 16384)
-// 40 / 25; heads of 64, 2^21 (32 x 2048) 12.6 / 11.9, (16 x 4096) 12.6 / 14.4,
-// 2^22 (32 x 4096) 18.2 / 16.1; heads of 256, 2^21 (32 x 2048) 28 / 29, (16 x
-// 4096) 27.4 / 26.2, 2^22 (32 x 4096) 43 / 32, 2^28 (256 tokens x 64 heads x
-// 16384) 1760 / 205.
+// heads of 128, own keys up to 64): 2^20 (16 tokens x 2048 keys) 13.0 / 12.6,
+// (64 x 512) 14.1 / 15.8, 2^21 (32 x 2048) 16.8 / 17.2, (64 x 1024) 18.2 / 19.9,
+// 2^22 (16 x 8192) 25 / 20, (64 x 2048) 26 / 22, 2^23 (16 x 16384) 41 / 25; heads
+// of 64, 2^21 (32 x 2048) 12.6 / 11.3, (16 x 4096) 12.6 / 14.5, 2^22 (32 x 4096)
+// 18 / 15; heads of 256, 2^20 (64 x 512) 23 / 26, 2^21 (32 x 2048) 28 / 24, 2^22
+// (32 x 4096) 43 / 27, 2^28 (256 tokens x 64 heads x 16384) 1760 / 190.
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
   const bool can = page_size >= 8 && (page_size & (page_size - 1)) == 0 && prefix_len > 0;
   const int forced = prefix_config();
   if (!can || forced >= 0) return can && forced == 1;
-  return rows > 16 && rows * num_heads_kv > (1 << (head_dim == 128 ? 22 : 21)) / prefix_len;
+  return rows > 16 && rows * num_heads_kv > (head_dim == 256 ? 3 << 19 : 1 << 21) / prefix_len;
 }
 
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map) {
