@@ -368,14 +368,20 @@ def _launch(dev, stream, fn, *args) -> None:
 _DEVICES = {}
 
 
-def _new(shape, dtype, dev):
+def _new(shape, dtype, dev, stream):
     """An output or workspace on the call's device (pinned host memory where
-    every tensor of the call is)."""
+    every tensor of the call is), allocated for the stream of the call: memory
+    that other streams still use is not given to it, nor its memory to them
+    when it is freed."""
     if dev >= 0:
         where = _DEVICES.get(dev)
         if where is None:  # building a device object costs more than the look-up
             where = _DEVICES[dev] = torch.device("cuda", dev)
-        return torch.empty(shape, dtype=dtype, device=where)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=where)
+        handle = _stream(stream, dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=where)):
+            return torch.empty(shape, dtype=dtype, device=where)
     return torch.empty(shape, dtype=dtype, pin_memory=True)
 
 
@@ -502,7 +508,7 @@ def paged_kv_block_select(q, bounds, page_table, lens, page_size, topk, keep_fir
     q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
     R, width = _requests(T, page_table, lens, requests)
     if out is None:
-        out = _new((T, Hkv, topk), _I32, dev)
+        out = _new((T, Hkv, topk), _I32, dev, stream)
     elif out.shape != (T, Hkv, topk):
         raise ValueError("out must be [T, Hkv, topk]")
     _launch(dev, stream, (_LIB or lib()).paged_kv_block_select, q_ptr, q_stride, T, Hq, Hkv, D,
@@ -526,22 +532,22 @@ def _workspace_bytes(fn, *sizes) -> int:
     return need
 
 
-def _output(q, out, dev):
+def _output(q, out, dev, stream):
     if out is None:
-        return _new(q.shape, _BF16, dev)
+        return _new(q.shape, _BF16, dev, stream)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     return out
 
 
-def _workspace(workspace, need, dev):
+def _workspace(workspace, need, dev, stream):
     """A workspace of ``need`` bytes (allocated if not given), its address and
     its size.  One that is allocated here may be freed when the call returns:
-    torch's allocator reuses memory in stream order."""
+    torch's allocator reuses memory in the order of the call's stream."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = _new(need, torch.uint8, dev)
+        workspace = _new(need, torch.uint8, dev, stream)
     return (workspace, _ptr(workspace, workspace.dtype, dev, "workspace"),
             workspace.numel() * workspace.element_size())
 
@@ -561,9 +567,9 @@ def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=No
     if B != T or H != Hkv:
         raise ValueError("blocks must be [T, Hkv, topk]")
     R, width = _requests(T, page_table, lens, requests)
-    out = _output(q, out, dev)
+    out = _output(q, out, dev, stream)
     workspace, ws, ws_bytes = _workspace(workspace, _workspace_bytes(
-        "paged_block_sparse_attention_workspace", T, Hq, Hkv, D, page, topk), dev)
+        "paged_block_sparse_attention_workspace", T, Hq, Hkv, D, page, topk), dev, stream)
     _launch(dev, stream, (_LIB or lib()).paged_block_sparse_attention, q_ptr, q_stride, T, Hq,
             Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
             _ptr(page_table, _I32, dev, "page_table"), R, width,
@@ -587,9 +593,10 @@ def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_ta
     if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page < prefix_len:
         raise ValueError("prefix_pages must be 1-D and hold prefix_len keys")
     R, width = _requests(T, page_table, lens, requests)
-    out = _output(q, out, dev)
+    out = _output(q, out, dev, stream)
     workspace, ws, ws_bytes = _workspace(workspace, _workspace_bytes(
-        "paged_shared_prefix_attention_workspace", T, Hq, Hkv, D, page, prefix_len, width), dev)
+        "paged_shared_prefix_attention_workspace", T, Hq, Hkv, D, page, prefix_len, width),
+        dev, stream)
     _launch(dev, stream, (_LIB or lib()).paged_shared_prefix_attention, q_ptr, q_stride, T, Hq,
             Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
             _ptr(prefix_pages, _I32, dev, "prefix_pages"), prefix_len,

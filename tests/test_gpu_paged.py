@@ -864,3 +864,37 @@ def test_lists_longer_than_a_cta_keeps(cuda_device, D):
     got = kvq.paged_block_sparse_attention(q.cuda(), cache.cuda(), table.cuda(), blocks.cuda(),
                                            lens.cuda())
     ref.check(got, *ref.sparse_attention(q, cache, table, blocks, lens, D ** -0.5))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_of_a_call_on_a_given_stream(cuda_device, prefix_way, raw):
+    """What a call on a stream of its own allocates is not memory that work of
+    the current stream, which is behind, still writes."""
+    g = gen(101)
+    T, Hq, Hkv, D, page, width, prefix = 70, 8, 1, 128, 64, 1, 3000
+    q, cache, table, spare = paged_inputs(g, T, Hq, Hkv, D, page, T, width, extra=47)
+    lens = ints(g, 0, page, T)
+    want, tol = ref.prefix_attention(q, cache, spare, prefix, table, lens, D ** -0.5)
+    args = [t.cuda() for t in (q, cache, spare.int())] + [prefix] + [t.cuda() for t in (table, lens)]
+    blocks = torch.zeros(T, Hkv, 1, dtype=torch.int32, device="cuda")
+    bounds = torch.zeros(cache.shape[0], Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+    need = kvq.lib().paged_shared_prefix_attention_workspace(T, Hq, Hkv, D, page, prefix, width)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    for _ in range(3):
+        torch.cuda.synchronize()
+        junk = [torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+                for n in (need, T * Hq * D * 2, T * Hkv * 4) for _ in range(2)]
+        torch.cuda._sleep(10000000)  # about five milliseconds, in front of the filling
+        for x in junk:
+            x.fill_(255)
+        del x, junk  # back to the current stream's memory, the filling still to come
+        out = kvq.paged_shared_prefix_attention(*args, stream=stream)
+        sparse = kvq.paged_block_sparse_attention(args[0], args[1], args[4], blocks, args[5],
+                                                  stream=stream)
+        picked = kvq.paged_kv_block_select(args[0], bounds, args[4], args[5], page, 1,
+                                           stream=stream)
+        torch.cuda.synchronize()
+        ref.check(out, want, tol)
+        ref.check(sparse, *ref.sparse_attention(q, cache, table, blocks.cpu(), lens, D ** -0.5))
+        assert bool((picked.cpu().view(T) == torch.where(lens > 0, 0, -1)).all())
