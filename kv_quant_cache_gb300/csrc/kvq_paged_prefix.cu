@@ -34,13 +34,16 @@
 // The kernel of the tokens' own keys, launched behind this one, joins them.
 //
 // Bound by the tensor cores, and by the power they may draw: 2048 rows x 8 kv
-// heads x 32768 keys of 128 dims, 275 GFLOP, take 176 us (1560 TFLOP/s, tensor
-// pipe active 72 % of the time, 141 MB read for 134 MB of keys and values);
+// heads x 32768 keys of 128 dims, 275 GFLOP, take 160 us (1720 TFLOP/s, tensor
+// pipe active 77 % of the time, 141 MB read for 134 MB of keys and values);
 // run back to back the clock settles at 1.65 of 2.07 GHz at the power limit.
 // With heads of 64 the softmax bounds it: half the products for the same
-// exponentials (939 TFLOP/s); of 256, 1580 TFLOP/s (348 us, 16-token pages 408
-// us; a prefetch of the next block into the L2 gained 3 % there and lost 20 %
-// with small pages).
+// exponentials (949 TFLOP/s with the own keys' kernel); of 256, 1690 TFLOP/s (a
+// prefetch of the next block into the L2 gained 3 % there and lost 20 % with
+// 16-token pages).  On a short prefix half of the time is a CTA's start and
+// end, 5 us: Q comes in by asynchronous copies, all at once, and the partials
+// leave line by line through shared memory (with loads of four at a time and a
+// row's pieces stored by one lane, 9 us; of 256 dims 7 instead of 13).
 #include <string.h>
 
 #include "kvq_paged_attn.cuh"
