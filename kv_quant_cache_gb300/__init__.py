@@ -380,7 +380,9 @@ def _new(shape, dtype, dev, stream):
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=where)
         handle = _stream(stream, dev)
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=where)):
+        of_call = (torch.cuda.ExternalStream(handle, device=where) if handle
+                   else torch.cuda.default_stream(where))
+        with torch.cuda.stream(of_call):
             return torch.empty(shape, dtype=dtype, device=where)
     return torch.empty(shape, dtype=dtype, pin_memory=True)
 

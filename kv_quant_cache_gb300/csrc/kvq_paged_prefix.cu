@@ -36,7 +36,7 @@
 // Bound by the tensor cores, and by the power they may draw: 2048 rows x 8 kv
 // heads x 32768 keys of 128 dims, 275 GFLOP, take 160 us (1720 TFLOP/s, tensor
 // pipe active 77 % of the time, 141 MB read for 134 MB of keys and values);
-// run back to back the clock settles at 1.65 of 2.07 GHz at the power limit.
+// run back to back the clock settles at 1.75 of 2.07 GHz at the power limit.
 // With heads of 64 the softmax bounds it: half the products for the same
 // exponentials (949 TFLOP/s with the own keys' kernel); of 256, 1690 TFLOP/s (a
 // prefetch of the next block into the L2 gained 3 % there and lost 20 % with

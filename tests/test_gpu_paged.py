@@ -898,3 +898,8 @@ def test_memory_of_a_call_on_a_given_stream(cuda_device, prefix_way, raw):
         ref.check(out, want, tol)
         ref.check(sparse, *ref.sparse_attention(q, cache, table, blocks.cpu(), lens, D ** -0.5))
         assert bool((picked.cpu().view(T) == torch.where(lens > 0, 0, -1)).all())
+    with torch.cuda.stream(side):  # the default stream, asked for by its handle
+        blocks = kvq.paged_kv_block_select(args[0], bounds, args[4], args[5], page, 1, stream=0)
+        again = kvq.paged_shared_prefix_attention(*args, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(blocks.cpu(), picked.cpu()) and torch.equal(bits(again), bits(out))
