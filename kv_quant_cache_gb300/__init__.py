@@ -542,16 +542,34 @@ def _output(q, out, dev, stream):
     return out
 
 
-def _workspace(workspace, need, dev, stream):
-    """A workspace of ``need`` bytes (allocated if not given), its address and
-    its size.  One that is allocated here may be freed when the call returns:
-    torch's allocator reuses memory in the order of the call's stream."""
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
+# Memory of torch's allocator without a tensor around it, on the current device
+# for a stream (after a launch a tensor costs 4 us to make, this 1 us).
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _launch_attention(dev, stream, fn, args, workspace, need, errors) -> None:
+    """``fn(*args, workspace, its bytes, errors, stream)``.  A workspace of
+    ``need`` bytes that is not given is allocated for the call alone: torch's
+    allocator hands it on in the order of the call's stream."""
+    errors = _counted(errors, dev)
+    if workspace is None and need and dev >= 0 and _raw_free and dev == _current_device():
+        handle = _stream(stream, dev)
+        ws = _raw_alloc(need, handle)
+        try:
+            st = fn(*args, ws, need, errors, handle)
+        finally:
+            _raw_free(ws)
+        if st:
+            _check(st, fn.__name__)
+        return
+    if workspace is None and need:
         workspace = _new(need, torch.uint8, dev, stream)
-    return (workspace, _ptr(workspace, workspace.dtype, dev, "workspace"),
-            workspace.numel() * workspace.element_size())
+    if workspace is None:
+        _launch(dev, stream, fn, *args, None, 0, errors)
+    else:
+        _launch(dev, stream, fn, *args, _ptr(workspace, workspace.dtype, dev, "workspace"),
+                workspace.numel() * workspace.element_size(), errors)
 
 
 def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=None, out=None,
@@ -570,15 +588,15 @@ def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=No
         raise ValueError("blocks must be [T, Hkv, topk]")
     R, width = _requests(T, page_table, lens, requests)
     out = _output(q, out, dev, stream)
-    workspace, ws, ws_bytes = _workspace(workspace, _workspace_bytes(
-        "paged_block_sparse_attention_workspace", T, Hq, Hkv, D, page, topk), dev, stream)
-    _launch(dev, stream, (_LIB or lib()).paged_block_sparse_attention, q_ptr, q_stride, T, Hq,
-            Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
-            _ptr(page_table, _I32, dev, "page_table"), R, width,
-            None if requests is None else _ptr(requests, _I32, dev, "requests"),
-            _ptr(lens, _I32, dev, "lens"), _ptr(blocks, _I32, dev, "blocks"), topk,
-            D ** -0.5 if scale is None else scale, _ptr(out, _BF16, dev, "out"), ws, ws_bytes,
-            _counted(errors, dev))
+    need = _workspace_bytes("paged_block_sparse_attention_workspace", T, Hq, Hkv, D, page, topk)
+    _launch_attention(
+        dev, stream, (_LIB or lib()).paged_block_sparse_attention,
+        (q_ptr, q_stride, T, Hq, Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
+         _ptr(page_table, _I32, dev, "page_table"), R, width,
+         None if requests is None else _ptr(requests, _I32, dev, "requests"),
+         _ptr(lens, _I32, dev, "lens"), _ptr(blocks, _I32, dev, "blocks"), topk,
+         D ** -0.5 if scale is None else scale, _ptr(out, _BF16, dev, "out")),
+        workspace, need, errors)
     return out
 
 
@@ -596,16 +614,16 @@ def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_ta
         raise ValueError("prefix_pages must be 1-D and hold prefix_len keys")
     R, width = _requests(T, page_table, lens, requests)
     out = _output(q, out, dev, stream)
-    workspace, ws, ws_bytes = _workspace(workspace, _workspace_bytes(
-        "paged_shared_prefix_attention_workspace", T, Hq, Hkv, D, page, prefix_len, width),
-        dev, stream)
-    _launch(dev, stream, (_LIB or lib()).paged_shared_prefix_attention, q_ptr, q_stride, T, Hq,
-            Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
-            _ptr(prefix_pages, _I32, dev, "prefix_pages"), prefix_len,
-            _ptr(page_table, _I32, dev, "page_table"), R, width,
-            None if requests is None else _ptr(requests, _I32, dev, "requests"),
-            _ptr(lens, _I32, dev, "lens"), D ** -0.5 if scale is None else scale,
-            _ptr(out, _BF16, dev, "out"), ws, ws_bytes, _counted(errors, dev))
+    need = _workspace_bytes("paged_shared_prefix_attention_workspace", T, Hq, Hkv, D, page,
+                            prefix_len, width)
+    _launch_attention(
+        dev, stream, (_LIB or lib()).paged_shared_prefix_attention,
+        (q_ptr, q_stride, T, Hq, Hkv, D, _ptr(kv_cache, _BF16, dev, "kv_cache"), N, page,
+         _ptr(prefix_pages, _I32, dev, "prefix_pages"), prefix_len,
+         _ptr(page_table, _I32, dev, "page_table"), R, width,
+         None if requests is None else _ptr(requests, _I32, dev, "requests"),
+         _ptr(lens, _I32, dev, "lens"), D ** -0.5 if scale is None else scale,
+         _ptr(out, _BF16, dev, "out")), workspace, need, errors)
     return out
 
 
