@@ -28,8 +28,9 @@
 //     halves of a block's dims), by tensor-map copies (a page, or 128 keys of
 //     one, at a time; 128-byte swizzle).  A block that
 //     ends past the prefix, or that lists a page outside the cache, is copied
-//     by the warp's own loads instead, with zeros in V where there is no key;
-//     the softmax gives those places weight 0.
+//     by the warp's own copies instead, all in flight at once, with zeros in V
+//     where there is no key (3000 keys of 256 dims: 40 us with loads of four at
+//     a time, 29); the softmax gives those places weight 0.
 // A segment's result is a partial (normalised O and log2 of the weight sum).
 // The kernel of the tokens' own keys, launched behind this one, joins them.
 //
@@ -168,12 +169,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
                : "memory");
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
-}
 
 // The share of a CTA, walked segment by segment: of the blocks of its lane's
 // items, one item after the other, an equal part for each team.
@@ -622,17 +617,17 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
             (slot ? last[1] : last[0]) = (int)turn;
           } else {
             constexpr int FRAGS = L::kWidth / 8, RPW = 32 / FRAGS;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < kKeys / RPW; ++i) {
               const int r = i * RPW + lane / FRAGS, c = lane % FRAGS, k = first + r;
               const int from = __shfl_sync(kFullMask, page, r >> piece_shift);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (from >= 0 && k < p.prefix_len)
-                v = __ldg(reinterpret_cast<const uint4*>(
-                    p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
-                    (int64_t)(k & page_mask) * D + L::kWidth * h + 8 * c));
-              st_shared16(dst + tile_offset(r, c), v);
+              const bool there = from >= 0 && k < p.prefix_len;
+              const __nv_bfloat16* src =
+                  p.cache + ((int64_t)from * 2 * p.num_kv + head) * head_elems +
+                  (int64_t)(k & page_mask) * D + L::kWidth * h + 8 * c;
+              cp_async16(dst + tile_offset(r, c), there ? src : p.cache, there);
             }
+            cp_wait_all();
             tma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full);
@@ -717,14 +712,17 @@ int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 // 2^22 (16 x 8192) 25 / 20, (64 x 2048) 26 / 22, 2^23 (16 x 16384) 41 / 25; heads
 // of 64, 2^21 (32 x 2048) 12.6 / 11.3, (16 x 4096) 12.6 / 14.5, 2^22 (32 x 4096)
 // 18 / 15; heads of 256, 2^20 (64 x 512) 23 / 26, 2^21 (32 x 2048) 28 / 24, 2^22
-// (32 x 4096) 43 / 27, 2^28 (256 tokens x 64 heads x 16384) 1760 / 190.
+// (32 x 4096) 43 / 27, 2^28 (256 tokens x 64 heads x 16384) 1760 / 190.  (In a
+// graph; outside one the second launch costs the host 5 us, which is why heads
+// of 64 stay with one at 2^21.)
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
                       int page_size, int64_t prefix_len) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
   const bool can = page_size >= 8 && (page_size & (page_size - 1)) == 0 && prefix_len > 0;
   const int forced = prefix_config();
   if (!can || forced >= 0) return can && forced == 1;
-  return rows > 16 && rows * num_heads_kv > (head_dim == 256 ? 3 << 19 : 1 << 21) / prefix_len;
+  const int64_t least = (head_dim == 64 ? 6 : head_dim == 128 ? 4 : 3) << 19;
+  return rows > 16 && rows * num_heads_kv > least / prefix_len;
 }
 
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map) {
