@@ -106,6 +106,8 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.kvq_qk_config_for.argtypes = [_I64, _I, _I]
     L.kvq_set_stage_wait_limit.restype = ctypes.c_uint32
     L.kvq_set_stage_wait_limit.argtypes = [ctypes.c_uint32]
+    L.kvq_set_tile_wait_limit.restype = ctypes.c_uint32
+    L.kvq_set_tile_wait_limit.argtypes = [ctypes.c_uint32]
     L.kvq_stage_events.restype = _I
     L.kvq_stage_events.argtypes = [_P, _P, _I]
     L.kvq_set_programmatic_launch.restype = _I
@@ -661,6 +663,13 @@ def set_stage_wait_limit(polls: int) -> int:
     """Polls of a stage barrier before a warp of a staged QK launch shape
     finishes from global memory (0: always); returns the previous limit."""
     return lib().kvq_set_stage_wait_limit(int(polls))
+
+
+def set_tile_wait_limit(polls: int) -> int:
+    """Polls of a barrier before a CTA of the shared prefix's tensor-core tiles
+    gives up, and its rows become NaN (0: without a poll); returns the previous
+    limit."""
+    return lib().kvq_set_tile_wait_limit(int(polls))
 
 
 def stage_events(reset: bool = False) -> tuple:

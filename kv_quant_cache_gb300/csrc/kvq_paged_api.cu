@@ -316,4 +316,6 @@ int kvq_set_prefix_config(int id) {
   return kvq::set_prefix_config(id < 0 ? -1 : id);
 }
 
+uint32_t kvq_set_tile_wait_limit(uint32_t polls) { return kvq::set_tile_wait_limit(polls); }
+
 }  // extern "C"

@@ -81,6 +81,7 @@ struct PrefixParams {
   int slots;         // partials of an item, at most
   Partials parts;
   int* errors;
+  uint32_t wait_polls;  // of a barrier, before the waiter gives up
 };
 
 // Row tiles of an item: two, or one of heads of 256, whose O takes half of the
@@ -227,6 +228,9 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   volatile int* dead = shared_state;  // a wait ran out
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_state + 1);
   auto bar = [&](int i) { return bars + 8u * i; };
+  auto await = [&](int i, uint32_t parity) {
+    return tc::wait_warp(bar(i), parity, dead, p.wait_polls);
+  };
 
   const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // a block comes in pieces: a page, or 128 keys of one; lane i has piece i
@@ -268,8 +272,8 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     uint32_t done = 0;  // blocks of this tile so far: the phase of its barriers
     bool ok = true;
     auto pv_done = [&](uint32_t block) {
-      return L::kTiles == 2 ? tc::wait_warp(bar(kPvDone + tile), block & 1, dead)
-                            : tc::wait_warp(bar(kPvDone + (block & 1)), (block >> 1) & 1, dead);
+      return L::kTiles == 2 ? await(kPvDone + tile, block & 1)
+                            : await(kPvDone + (block & 1), (block >> 1) & 1);
     };
     while (ok && seg.next(p)) {
       if (tile >= seg.tiles) continue;
@@ -299,6 +303,11 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       tma::fence_proxy_async();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(kQFull + tile));
+      if (p.wait_polls == 0) {  // (not looked at in every wait: heads of 256 3 % slower)
+        *dead = 1;
+        ok = false;
+        break;
+      }
 
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < seg.n; ++j, ++done) {
@@ -315,7 +324,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         const int buf = L::kTiles == 2 ? tile : done & 1;
         const uint32_t phase = L::kTiles == 2 ? done & 1 : (done >> 1) & 1;
         const uint32_t s_at = at + 128 * buf + 64 * half, p_at = at + 128 * buf + 32 * half;
-        ok = tc::wait_warp(bar(kSFull + buf), phase, dead);
+        ok = await(kSFull + buf, phase);
         if (!ok) break;
         tc::fence_after();
         uint32_t s[2][32];
@@ -481,9 +490,9 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       };
       uint32_t done[2] = {0, 0}, segs[2] = {0, 0};  // phases of the barriers
       while (ok && seg.next(p)) {
-        ok = tc::wait_warp(bar(kKFull + (block & 1)), (block >> 1) & 1, dead);
+        ok = await(kKFull + (block & 1), (block >> 1) & 1);
         for (int t = 0; ok && t < seg.tiles; ++t) {
-          ok = tc::wait_warp(bar(kQFull + t), segs[t]++ & 1, dead);
+          ok = await(kQFull + t, segs[t]++ & 1);
           if (!ok) break;
           tc::fence_after();
           scores(t, block & 1);
@@ -493,12 +502,12 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         for (int j = 0; ok && j < seg.n; ++j, ++block) {
           const int stage = block & 1, next = stage ^ 1;
           const bool more = j + 1 < seg.n;
-          ok = tc::wait_warp(bar(kVFull + stage), (block >> 1) & 1, dead) &&
-               (!more || tc::wait_warp(bar(kKFull + next), ((block + 1) >> 1) & 1, dead));
+          ok = await(kVFull + stage, (block >> 1) & 1) &&
+               (!more || await(kKFull + next, ((block + 1) >> 1) & 1));
           for (int t = 0; ok && t < seg.tiles; ++t) {
             const uint64_t v = v_desc + (uint32_t)(stage * (L::kSlot >> 4));
             for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
-              ok = tc::wait_warp(bar(kPFull + 2 * t + c), done[t] & 1, dead);
+              ok = await(kPFull + 2 * t + c, done[t] & 1);
               if (!ok) break;
               tc::fence_after();
   #pragma unroll
@@ -527,7 +536,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       uint32_t segs = 0;
       auto scores = [&](uint32_t block) {
         for (int h = 0; ok && h < 2; ++h) {
-          ok = tc::wait_warp(bar(kKFull + h), block & 1, dead);
+          ok = await(kKFull + h, block & 1);
           if (!ok) break;
           tc::fence_after();
 #pragma unroll
@@ -542,7 +551,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         if (ok) tc::commit(bar(kSFull + (block & 1)));
       };
       while (ok && seg.next(p)) {
-        ok = tc::wait_warp(bar(kQFull), segs++ & 1, dead);
+        ok = await(kQFull, segs++ & 1);
         if (!ok) break;
         tc::fence_after();
         scores(block);
@@ -550,10 +559,10 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           if (j + 1 < seg.n) scores(block + 1);
           const int buf = block & 1;
           for (int h = 0; ok && h < 2; ++h) {
-            ok = tc::wait_warp(bar(kVFull + h), block & 1, dead);
+            ok = await(kVFull + h, block & 1);
             const uint64_t v = v_desc + (uint32_t)(h * (L::kSlot >> 4));
             for (int c = 0; ok && c < 2; ++c) {  // keys 0-31 and 64-95, then the others
-              if (h == 0) ok = tc::wait_warp(bar(kPFull + 2 * buf + c), (block >> 1) & 1, dead);
+              if (h == 0) ok = await(kPFull + 2 * buf + c, (block >> 1) & 1);
               if (!ok) break;
               tc::fence_after();
 #pragma unroll
@@ -571,8 +580,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     }
     if (!ok) {  // nothing may be in flight when the tensor memory goes
       tc::commit(bar(kDrain));
-      for (uint32_t i = 0; i < (1u << 22) && !tma::mbar_test(bar(kDrain), 0); ++i) {
-      }
+      tc::drain(bar(kDrain), 0);
       __syncwarp();
     }
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
@@ -580,7 +588,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     const int kv = warp - kLoadWarp;
     const int64_t head_elems = ((int64_t)D) << p.page_shift;
     uint32_t turn = 0;  // slots filled so far
-    int last[2] = {-1, -1};  // the latest of each slot that copies were started for
+    int last[2] = {-1, -1};  // of each slot: its latest turn, if that is the copy engine's
     bool ok = true;
     while (ok && seg.next(p)) {
       const int head = kv * p.num_kv + seg.kv_head;
@@ -602,7 +610,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           const uint32_t full = bar((kv ? kVFull : kKFull) + slot);
           const uint32_t dst = base + (kv ? L::kV : L::kK) + slot * L::kSlot;
           if (turn >= 2) {
-            ok = tc::wait_warp(bar((kv ? kVEmpty : kKEmpty) + slot), ((turn >> 1) - 1) & 1, dead);
+            ok = await((kv ? kVEmpty : kKEmpty) + slot, ((turn >> 1) - 1) & 1);
             if (!ok) break;
           }
           if (whole) {
@@ -631,6 +639,8 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
             tma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full);
+            // the copies of the slot's turn before have been read: none is in flight
+            (slot ? last[1] : last[0]) = -1;
           }
           __syncwarp();
         }
@@ -638,10 +648,8 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     }
     if (!ok) {  // let the copies in flight land before the CTA may end
       for (int slot = 0; slot < 2; ++slot) {
-        const uint32_t full = bar((kv ? kVFull : kKFull) + slot);
         const int turn = slot ? last[1] : last[0];
-        for (uint32_t i = 0; turn >= 0 && i < (1u << 22); ++i)
-          if (tma::mbar_test(full, (turn >> 1) & 1)) break;
+        if (turn >= 0) tc::drain(bar((kv ? kVFull : kKFull) + slot), (turn >> 1) & 1);
       }
     }
   }
@@ -651,6 +659,8 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     tc::dealloc512(tmem);
   }
 }
+
+std::atomic<uint32_t> g_tile_wait_limit{tc::kPolls};
 
 template <int D>
 cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partials& parts,
@@ -687,6 +697,7 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   p.slots = plan.parts;
   p.parts = parts;
   p.errors = x.errors;
+  p.wait_polls = g_tile_wait_limit.load(std::memory_order_relaxed);
   return launch_kernel(prefix_tiles_kernel<D>, dim3((unsigned)(plan.lanes * plan.teams)),
                        dim3(L::kThreads), L::kSmem, stream, p);
 }
@@ -701,6 +712,9 @@ const LaunchConfig kPrefixConfigs[] = {{"rows<4w>"}, {"tiles<20w,128x128>"}};
 const int kPrefixNumConfigs = 2;
 
 int set_prefix_config(int id) { return g_prefix_config.exchange(id, std::memory_order_relaxed); }
+uint32_t set_tile_wait_limit(uint32_t polls) {
+  return g_tile_wait_limit.exchange(polls, std::memory_order_relaxed);
+}
 int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 
 // Sizes the tiles can take, and where they pay.  Up to 16 rows of a kv head are

@@ -13,17 +13,18 @@ namespace kvq {
 namespace tc {
 
 // ---- waits -------------------------------------------------------------------
-// No wait is endless: after kPolls polls or kClocks cycles the waiter raises
-// the CTA's `dead` flag and returns false, and every other waiter of the CTA
-// that polls sees the flag.  (The cycle counter, not the nanosecond timer: a
-// read of that one takes longer than most waits.)
-constexpr uint32_t kPolls = 1u << 24;
+// No wait is endless: after `polls` polls (of the launch; one at least) or
+// kClocks cycles the waiter raises the CTA's `dead` flag and returns false, and
+// every other waiter of the CTA that polls sees the flag.  (The cycle counter, not
+// the nanosecond timer: a read of that one takes longer than most waits.)
+constexpr uint32_t kPolls = 1u << 24;      // unless kvq_set_tile_wait_limit says otherwise
 constexpr long long kClocks = 2000000000;  // about 1 s
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* dead,
+                                     uint32_t polls) {
   if (tma::mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  for (uint32_t i = 1; i < kPolls; ++i) {
+  for (uint32_t i = 1; i < polls; ++i) {
     if (tma::mbar_test(bar, parity)) return true;
     if ((i & 63u) == 0 && (*dead || clock64() - t0 > kClocks)) break;
   }
@@ -32,8 +33,18 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 }
 
 // The same by a whole warp, which stays converged.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* dead) {
-  return __all_sync(kFullMask, wait(bar, parity, dead));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* dead,
+                                          uint32_t polls) {
+  return __all_sync(kFullMask, wait(bar, parity, dead, polls));
+}
+
+// What a role that gives up still has in flight: waits until it has landed,
+// bounded by the same clock whatever the launch's limit.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1; i < kPolls && !tma::mbar_test(bar, parity); ++i) {
+    if ((i & 63u) == 0 && clock64() - t0 > kClocks) break;
+  }
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {

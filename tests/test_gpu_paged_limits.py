@@ -1,0 +1,58 @@
+"""The tensor-core tiles of the shared prefix when a wait on one of their
+barriers runs out: the launch's limit is set so low that waits which would end
+well are given up.  Nothing is broken to get there."""
+import time
+
+import pytest
+import torch
+
+import kv_quant_cache_gb300 as kvq
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+LIMITS = [0, 1, 2, 3, 5, 8, 16, 40, 100, 300]
+
+
+@pytest.fixture
+def tiles():
+    old = kvq.set_config("prefix", 1)
+    yield
+    kvq.set_config("prefix", old)
+
+
+def many_items(D, seed=1):
+    """200 kv heads behind 200 keys: the blocks of each CTA are those of two or
+    three heads, every second one partly filled.  -> (arguments, the outputs'
+    exact values, their bounds)"""
+    g = torch.Generator().manual_seed(seed + D)
+    T, H, page, prefix = 20, 200, 64, 200
+    q = torch.randn(T, H, D, generator=g).bfloat16()
+    cache = torch.randn(4 + T, 2, H, page, D, generator=g).bfloat16()
+    ids = torch.randperm(4 + T, generator=g).int()
+    lens = torch.randint(0, 9, (T,), generator=g, dtype=torch.int32)
+    pages, table = ids[:4], ids[4:].view(T, 1)
+    want = ref.prefix_attention(q, cache, pages, prefix, table, lens, D ** -0.5)
+    return [q.cuda(), cache.cuda(), pages.cuda(), prefix, table.cuda(), lens.cuda()], *want
+
+
+def run_out(args, limit):
+    """(outputs, errors) of a call under ``limit``, which has to end in time."""
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    old = kvq.set_tile_wait_limit(limit)
+    try:
+        start = time.monotonic()
+        out = kvq.paged_shared_prefix_attention(*args, errors=err)
+        torch.cuda.synchronize()
+        assert time.monotonic() - start < 20
+    finally:
+        assert kvq.set_tile_wait_limit(old) == limit
+    return out.cpu(), int(err.item())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_wait_that_runs_out_ends_the_call(cuda_device, tiles, D):
+    args, want, tol = many_items(D)
+    for limit in LIMITS:
+        run_out(args, limit)
+        ref.check(kvq.paged_shared_prefix_attention(*args), want, tol)  # and none after it

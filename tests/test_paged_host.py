@@ -255,3 +255,14 @@ def test_status_of_the_new_symbols(L):
     for n in ("paged_kv_rope_append", "paged_kv_page_bounds", "paged_kv_block_select",
               "paged_block_sparse_attention", "paged_shared_prefix_attention"):
         assert hasattr(L, n) and callable(getattr(kvq, n))
+
+
+def test_tile_wait_limit_round_trip(L):
+    """The limit of the tiles' waits: returns the one before, 2^24 to start with."""
+    old = kvq.set_tile_wait_limit(17)
+    try:
+        assert old == 1 << 24
+        assert kvq.set_tile_wait_limit(0) == 17
+        assert kvq.set_tile_wait_limit(2 ** 32 - 1) == 0
+    finally:
+        assert kvq.set_tile_wait_limit(old) == 2 ** 32 - 1
