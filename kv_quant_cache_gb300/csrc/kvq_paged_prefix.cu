@@ -151,12 +151,12 @@ __device__ __forceinline__ void pair_sync(int id) {
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
 
-// Its arrival alone, by a warp that gives up (`dead` is set): the other one's
-// next pair_sync, its last before it fails in a wait of its own, passes.
-__device__ __forceinline__ void pair_leave(int id) {
-  __threadfence_block();
-  asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
-}
+// What a warp that gives up hands its partner in place of a maximum or a sum (a
+// NaN that no instruction makes).  It does so at the pair's next barrier, which
+// the partner reaches as well, and both leave there: a barrier is always met by
+// both, and no warp waits at one alone.
+constexpr uint32_t kGaveUp = 0x7fc0deadu;
+__device__ __forceinline__ bool gave_up(float x) { return __float_as_uint(x) == kGaveUp; }
 
 // Where 16-byte fragment c of row r lies in a swizzled 128-row tile.
 __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
@@ -272,8 +272,14 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     uint32_t done = 0;  // blocks of this tile so far: the phase of its barriers
     bool ok = true;
     auto pv_done = [&](uint32_t block) {
-      return L::kTiles == 2 ? await(kPvDone + tile, block & 1)
-                            : await(kPvDone + (block & 1), (block >> 1) & 1);
+      const int buf = L::kTiles == 2 ? tile : block & 1;
+      const uint32_t phase = L::kTiles == 2 ? block & 1 : (block >> 1) & 1;
+      return await(kPvDone + buf, phase);
+    };
+    // Meets the partner at the pair's next barrier, whose values lie at `slot`.
+    auto give_up = [&](int slot) {
+      tops[slot + half * 256 + r] = __uint_as_float(kGaveUp);
+      pair_sync(pair_bar);
     };
     while (ok && seg.next(p)) {
       if (tile >= seg.tiles) continue;
@@ -324,8 +330,11 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         const int buf = L::kTiles == 2 ? tile : done & 1;
         const uint32_t phase = L::kTiles == 2 ? done & 1 : (done >> 1) & 1;
         const uint32_t s_at = at + 128 * buf + 64 * half, p_at = at + 128 * buf + 32 * half;
-        ok = await(kSFull + buf, phase);
-        if (!ok) break;
+        if (!await(kSFull + buf, phase)) {
+          give_up((done & 1) * 512);
+          ok = false;
+          break;
+        }
         tc::fence_after();
         uint32_t s[2][32];
         tc::ld32(s[0], s_at);
@@ -356,15 +365,26 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         // the row's maximum over both halves; from here on both have read S
         tops[(done & 1) * 512 + half * 256 + r] = top;
         pair_sync(pair_bar);
-        top = fmaxf(m, fmaxf(top, tops[(done & 1) * 512 + (half ^ 1) * 256 + r]));
-        if (__any_sync(kFullMask, (top - m) * p.scale_log2 > kRescaleAt)) {
+        const float other = tops[(done & 1) * 512 + (half ^ 1) * 256 + r];
+        top = fmaxf(m, fmaxf(top, other));
+        // one vote for both that are rare (32768 keys x 2048 rows x 8 heads: 171.6 us
+        // with the own keys' kernel; a vote each: 173.4)
+        if (__any_sync(kFullMask,
+                       (top - m) * p.scale_log2 > kRescaleAt || gave_up(other))) {
+          if (__any_sync(kFullMask, gave_up(other))) {
+            ok = false;
+            break;
+          }
           const float f = top == m ? 1.f : ex2((m - top) * p.scale_log2);
           l *= f;
           m = top;
           if (j > 0) {
             // O is at rest once the previous block's product is done
-            ok = pv_done(done - 1);
-            if (!ok) break;
+            if (!pv_done(done - 1)) {
+              give_up(j + 1 < seg.n ? ((done + 1) & 1) * 512 : 1024);
+              ok = false;
+              break;
+            }
             tc::fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
@@ -407,16 +427,15 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         l += sum0.f[0] + sum0.f[1];
       }
       // ---- the partial -----------------------------------------------------------------
-      if (ok) ok = pv_done(done - 1);
-      tc::fence_after();
       if (ok) {
-        tops[1024 + half * 256 + r] = l;
+        const bool last = pv_done(done - 1);
+        tops[1024 + half * 256 + r] = last ? l : __uint_as_float(kGaveUp);
         pair_sync(pair_bar);
-        l += tops[1024 + (half ^ 1) * 256 + r];
-        ok = *dead == 0;
-      } else {
-        pair_leave(pair_bar);
+        const float other = tops[1024 + (half ^ 1) * 256 + r];
+        l += other;
+        ok = last && !__any_sync(kFullMask, gave_up(other));
       }
+      tc::fence_after();
       const uint32_t t = (uint32_t)(seg.row0 + r) / (uint32_t)p.group;
       const int64_t row = (int64_t)t * p.num_q + seg.kv_head * p.group +
                           (int)((uint32_t)(seg.row0 + r) - t * p.group);

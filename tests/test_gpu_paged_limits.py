@@ -56,3 +56,12 @@ def test_a_wait_that_runs_out_ends_the_call(cuda_device, tiles, D):
     for limit in LIMITS:
         run_out(args, limit)
         ref.check(kvq.paged_shared_prefix_attention(*args), want, tol)  # and none after it
+
+
+def test_a_wait_that_runs_out_ends_the_call_with_heads_of_256(cuda_device, tiles):
+    """Two blocks' scores are under way at once there: a warp whose partner has
+    given up on the first finds the second's ready, and must not wait for it."""
+    args, want, tol = many_items(256)
+    for limit in LIMITS + [600, 1000, 2000]:
+        run_out(args, limit)
+        ref.check(kvq.paged_shared_prefix_attention(*args), want, tol)
