@@ -276,12 +276,23 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
       const uint32_t phase = L::kTiles == 2 ? block & 1 : (block >> 1) & 1;
       return await(kPvDone + buf, phase);
     };
+    auto row_of = [&](const Segments& seg) {  // of the thread's row: token * num_q + head
+      const uint32_t flat = (uint32_t)(seg.row0 + r), t = flat / (uint32_t)p.group;
+      return (int64_t)t * p.num_q + seg.kv_head * p.group + (int)(flat - t * p.group);
+    };
+    auto put_sum = [&](const Segments& seg, int64_t row, int slot, float lse) {
+      if (half != 0 || r >= seg.rows_left) return;
+      p.parts.lse[slot * p.parts.rows + row] = lse;
+      // an item has fewer segments than others: the slots left over are empty
+      if (seg.first + seg.n == p.blocks)
+        for (int k = slot + 1; k < p.slots; ++k) p.parts.lse[k * p.parts.rows + row] = -INFINITY;
+    };
     // Meets the partner at the pair's next barrier, whose values lie at `slot`.
     auto give_up = [&](int slot) {
       tops[slot + half * 256 + r] = __uint_as_float(kGaveUp);
       pair_sync(pair_bar);
     };
-    while (ok && seg.next(p)) {
+    while (seg.next(p)) {
       if (tile >= seg.tiles) continue;
       // Q comes in, to each warp's slice of the tile; the products that read the
       // previous segment's have all been seen to be done
@@ -435,10 +446,9 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         l += other;
         ok = last && !__any_sync(kFullMask, gave_up(other));
       }
+      if (!ok) break;
       tc::fence_after();
-      const uint32_t t = (uint32_t)(seg.row0 + r) / (uint32_t)p.group;
-      const int64_t row = (int64_t)t * p.num_q + seg.kv_head * p.group +
-                          (int)((uint32_t)(seg.row0 + r) - t * p.group);
+      const int64_t row = row_of(seg);
       const int slot = seg.slot(p);
       const float f = l == 0.f ? 0.f : 1.f / l;
       // Through shared memory, so that lanes side by side write a row's values
@@ -475,15 +485,16 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
           __syncwarp();
         }
       }
-      if (half == 0 && r < seg.rows_left) {
-        p.parts.lse[slot * p.parts.rows + row] =
-            !ok ? NAN : l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m * p.scale_log2);
-        // an item has fewer segments than others: the slots left over are empty
-        if (seg.first + seg.n == p.blocks)
-          for (int k = slot + 1; k < p.slots; ++k)
-            p.parts.lse[k * p.parts.rows + row] = -INFINITY;
-      }
+      put_sum(seg, row, slot,
+              l == 0.f ? -INFINITY : log2f(l) + (m == -INFINITY ? 0.f : m * p.scale_log2));
       tc::fence_before();
+    }
+    // The warp has given up: what this segment and those still to come should
+    // have held is marked, whatever the workspace had there before.
+    if (!ok) {
+      do {
+        if (tile < seg.tiles) put_sum(seg, row_of(seg), seg.slot(p), NAN);
+      } while (seg.next(p));
     }
   } else if constexpr (L::kTiles == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -673,6 +684,7 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
     }
   }
   __syncthreads();
+  if (threadIdx.x == 0 && p.errors && *dead) atomicAdd(p.errors, 1);
   if (warp == kMmaWarp) {
     tc::fence_after();
     tc::dealloc512(tmem);

@@ -65,3 +65,28 @@ def test_a_wait_that_runs_out_ends_the_call_with_heads_of_256(cuda_device, tiles
     for limit in LIMITS + [600, 1000, 2000]:
         run_out(args, limit)
         ref.check(kvq.paged_shared_prefix_attention(*args), want, tol)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_a_wait_that_ran_out_are_marked(cuda_device, tiles, D):
+    """What a CTA that gave up has not computed becomes NaN and is counted, in
+    its later heads as well; nothing that the workspace held before gets out."""
+    args, want, tol = many_items(D, seed=2)
+    T, H, _ = args[0].shape
+    need = kvq.lib().paged_shared_prefix_attention_workspace(T, H, H, D, 64, args[3], 1)
+    marked = set()
+    for limit in LIMITS + [600, 1000, 2000, 1 << 24]:
+        workspace = torch.full((need // 4,), 3.0, device="cuda")  # sums and outputs alike
+        old = kvq.set_tile_wait_limit(limit)
+        try:
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = kvq.paged_shared_prefix_attention(*args, workspace=workspace, errors=err).cpu()
+        finally:
+            kvq.set_tile_wait_limit(old)
+        lost = got.isnan().all(-1)
+        ref.check(got[~lost], want[~lost], tol[~lost])
+        assert (int(err.item()) > 0) == bool(lost.any())
+        marked.add(int(lost.sum()))
+        if limit == 0:
+            assert bool(lost.all())
+    assert 0 in marked  # the default limit
