@@ -554,8 +554,9 @@ int kvq_dsv4_config_for(int64_t num_tokens, int num_heads);
 /* The prefix of paged_shared_prefix_attention: 0 the kernel for few rows
  * ("rows"), 1 the tensor-core tiles ("tiles"; sizes they cannot take -- a
  * page_size below 8 or no power of two, a cache outside the current device's
- * memory -- take the other).  Ask for the workspace after changing it.  The
- * two round differently, each within the stated bounds. */
+ * memory -- take the other).  Ask for the workspace after changing it; a call
+ * that another thread's change overtakes is refused if its workspace does not
+ * do.  The two round differently, each within the stated bounds. */
 int kvq_prefix_num_configs(void);
 const char* kvq_prefix_config_name(int id);
 int kvq_set_prefix_config(int id);

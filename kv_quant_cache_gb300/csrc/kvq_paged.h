@@ -78,6 +78,7 @@ struct PrefixAttnArgs {
   const void* kv_cache;
   const int* prefix_pages;
   int64_t prefix_len;
+  int config;  // prefix_config() as it was when the workspace was checked
   float scale;
   void* out;
   void* workspace;
@@ -101,10 +102,12 @@ uint32_t set_tile_wait_limit(uint32_t polls);  // kvq_set_tile_wait_limit
 
 // Bytes of workspace the two attentions need (a multiple of 16; 0: none).
 // Depends on the sizes (and a forced configuration) alone, so that it can be
-// asked for without a device.
+// asked for without a device.  A call reads prefix_config() once and hands it
+// on: one that changes meanwhile may not change what the workspace is for.
 int64_t sparse_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int topk);
 int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
-                              int head_dim, int page_size, int64_t prefix_len, int table_width);
+                              int head_dim, int page_size, int64_t prefix_len, int table_width,
+                              int config);
 
 }  // namespace kvq

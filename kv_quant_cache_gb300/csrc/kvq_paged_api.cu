@@ -261,7 +261,7 @@ int64_t paged_shared_prefix_attention_workspace(int64_t num_tokens, int num_head
       num_tokens * num_heads_q >= kIndexLimit)
     return 0;
   return kvq::prefix_attn_workspace(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size,
-                                    prefix_len, (int)table_width);
+                                    prefix_len, (int)table_width, kvq::prefix_config());
 }
 
 kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_t num_tokens,
@@ -284,8 +284,9 @@ kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_
   c = check_requests(q, kv_cache, page_table, num_requests, table_width, requests, lens,
                      num_tokens, error_count);
   if (c != KVQ_OK) return c;
+  const int config = kvq::prefix_config();
   const int64_t need = kvq::prefix_attn_workspace(num_tokens, num_heads_q, num_heads_kv, head_dim,
-                                                  page_size, prefix_len, (int)table_width);
+                                                  page_size, prefix_len, (int)table_width, config);
   if (!out || (prefix_len > 0 && !prefix_pages) || (need > 0 && !workspace)) return KVQ_ERR_NULL;
   if (!aligned(prefix_pages, 4) || !aligned(out, 16) || (need > 0 && !aligned(workspace, 16)))
     return KVQ_ERR_ALIGN;
@@ -299,6 +300,7 @@ kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_
   a.kv_cache = kv_cache;
   a.prefix_pages = prefix_pages;
   a.prefix_len = prefix_len;
+  a.config = config;
   a.scale = scale;
   a.out = out;
   a.workspace = workspace;

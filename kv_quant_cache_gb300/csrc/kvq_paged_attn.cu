@@ -954,12 +954,13 @@ cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream) {
 
 int64_t prefix_attn_workspace(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                               int head_dim, int page_size, int64_t prefix_len,
-                              int table_width) {
+                              int table_width, int config) {
   const int64_t rows = num_tokens * num_heads_q;
   const int s = shared_spread(num_tokens, num_heads_q, num_heads_kv, page_size, prefix_len,
                               table_width, false).splits;
   int64_t slots = s == 1 ? 0 : s;
-  if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len)) {
+  if (prefix_tiles_fit(num_tokens, num_heads_q, num_heads_kv, head_dim, page_size, prefix_len,
+                       config)) {
     // either way may be taken: which one depends on where the cache lies
     const int64_t parts =
         prefix_tiles_plan(num_tokens, num_heads_q, num_heads_kv, head_dim, prefix_len).parts;
@@ -979,7 +980,7 @@ cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream) {
   // (the tiles scale their masked scores, -inf, too: a scale of zero is not theirs)
   const bool tiles = a.scale != 0.f &&
                      prefix_tiles_fit(x.num_tokens, x.num_heads_q, x.num_heads_kv, x.head_dim,
-                                      x.page_size, a.prefix_len) &&
+                                      x.page_size, a.prefix_len, a.config) &&
                      prefix_tiles_map(a, &map);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.prefix_len = tiles ? 0 : (int)a.prefix_len;

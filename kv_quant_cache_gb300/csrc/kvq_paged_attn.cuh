@@ -52,7 +52,7 @@ struct PrefixTilesPlan {
   int parts;      // partials of an item, at most
 };
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
-                      int page_size, int64_t prefix_len);
+                      int page_size, int64_t prefix_len, int config);
 PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_heads_kv,
                                   int head_dim, int64_t prefix_len);
 bool prefix_tiles_map(const PrefixAttnArgs& a, CUtensorMap* map);

@@ -761,11 +761,10 @@ int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 // graph; outside one the second launch costs the host 5 us, which is why heads
 // of 64 stay with one at 2^21.)
 bool prefix_tiles_fit(int64_t num_tokens, int num_heads_q, int num_heads_kv, int head_dim,
-                      int page_size, int64_t prefix_len) {
+                      int page_size, int64_t prefix_len, int config) {
   const int64_t rows = num_tokens * (num_heads_q / num_heads_kv);
   const bool can = page_size >= 8 && (page_size & (page_size - 1)) == 0 && prefix_len > 0;
-  const int forced = prefix_config();
-  if (!can || forced >= 0) return can && forced == 1;
+  if (!can || config >= 0) return can && config == 1;
   const int64_t least = (head_dim == 64 ? 6 : head_dim == 128 ? 4 : 3) << 19;
   return rows > 16 && rows * num_heads_kv > least / prefix_len;
 }
