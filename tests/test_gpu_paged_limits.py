@@ -74,7 +74,6 @@ def test_rows_of_a_wait_that_ran_out_are_marked(cuda_device, tiles, D):
     args, want, tol = many_items(D, seed=2)
     T, H, _ = args[0].shape
     need = kvq.lib().paged_shared_prefix_attention_workspace(T, H, H, D, 64, args[3], 1)
-    marked = set()
     for limit in LIMITS + [600, 1000, 2000, 1 << 24]:
         workspace = torch.full((need // 4,), 3.0, device="cuda")  # sums and outputs alike
         old = kvq.set_tile_wait_limit(limit)
@@ -85,8 +84,8 @@ def test_rows_of_a_wait_that_ran_out_are_marked(cuda_device, tiles, D):
             kvq.set_tile_wait_limit(old)
         lost = got.isnan().all(-1)
         ref.check(got[~lost], want[~lost], tol[~lost])
-        assert (int(err.item()) > 0) == bool(lost.any())
-        marked.add(int(lost.sum()))
+        # (warps that have none of the 20 rows may be those that give up)
+        assert int(err.item()) > 0 or not bool(lost.any())
         if limit == 0:
             assert bool(lost.all())
-    assert 0 in marked  # the default limit
+    assert int(err.item()) == 0 and not bool(lost.any())  # the default limit
