@@ -524,15 +524,19 @@ def paged_kv_block_select(q, bounds, page_table, lens, page_size, topk, keep_fir
     return out
 
 
-_WORKSPACE = {}  # sizes of a call -> bytes of workspace it needs
+# Sizes of a call -> bytes of workspace it needs.  set_config puts an empty table
+# in its place: what another thread found under the setting before goes into the
+# old one.
+_WORKSPACE = {}
 
 
 def _workspace_bytes(fn, *sizes) -> int:
-    need = _WORKSPACE.get((fn, sizes))
+    table = _WORKSPACE
+    need = table.get((fn, sizes))
     if need is None:
-        if len(_WORKSPACE) >= 4096:
-            _WORKSPACE.clear()
-        need = _WORKSPACE[(fn, sizes)] = getattr(lib(), fn)(*sizes)
+        if len(table) >= 4096:
+            table.clear()
+        need = table[(fn, sizes)] = getattr(lib(), fn)(*sizes)
     return need
 
 
@@ -655,7 +659,8 @@ def set_config(op: str, config_id: int) -> int:
     prev = getattr(lib(), f"kvq_set_{op}_config")(int(config_id))
     if prev == -2:
         raise ValueError(f"{op}: no launch configuration {config_id}")
-    _WORKSPACE.clear()  # what a call needs may depend on it
+    global _WORKSPACE
+    _WORKSPACE = {}  # what a call needs may depend on it
     return prev
 
 

@@ -266,3 +266,30 @@ def test_tile_wait_limit_round_trip(L):
         assert kvq.set_tile_wait_limit(2 ** 32 - 1) == 0
     finally:
         assert kvq.set_tile_wait_limit(old) == 2 ** 32 - 1
+
+
+def test_size_found_while_the_configuration_changes(L, monkeypatch):
+    """A workspace size that was computed under the setting before a change is
+    not what later calls are given."""
+    name, sizes = "paged_shared_prefix_attention_workspace", (40, 8, 2, 128, 64, 501, 4)
+
+    class Changing:
+        def __getattr__(self, symbol):
+            f = getattr(L, symbol)
+            if symbol != name:
+                return f
+
+            def size(*args):
+                need = f(*args)
+                kvq.set_config("prefix", 1)  # as another thread might
+                return need
+            return size
+
+    assert kvq.set_config("prefix", -1) == -1
+    try:
+        with monkeypatch.context() as m:
+            m.setattr(kvq, "lib", Changing)
+            assert kvq._workspace_bytes(name, *sizes) == 0
+        assert kvq._workspace_bytes(name, *sizes) == getattr(L, name)(*sizes) > 0
+    finally:
+        kvq.set_config("prefix", -1)
