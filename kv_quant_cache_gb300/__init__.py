@@ -371,10 +371,11 @@ _DEVICES = {}
 
 
 def _new(shape, dtype, dev, stream):
-    """An output or workspace on the call's device (pinned host memory where
-    every tensor of the call is), allocated for the stream of the call: memory
-    that other streams still use is not given to it, nor its memory to them
-    when it is freed."""
+    """An output or workspace on the call's device, allocated for the stream of
+    the call: memory that other streams still use is not given to it, nor its
+    memory to them when it is freed.  Where every tensor of the call is pinned
+    host memory so is an output; that has no order of streams, and like the
+    call's other tensors it is the caller's to keep until the call is done."""
     if dev >= 0:
         where = _DEVICES.get(dev)
         if where is None:  # building a device object costs more than the look-up
@@ -557,9 +558,12 @@ _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 def _launch_attention(dev, stream, fn, args, workspace, need, errors) -> None:
     """``fn(*args, workspace, its bytes, errors, stream)``.  A workspace of
     ``need`` bytes that is not given is allocated for the call alone: torch's
-    allocator hands it on in the order of the call's stream."""
+    allocator hands it on in the order of the call's stream.  It is device
+    memory for pinned tensors too: given back, pinned memory would be handed on
+    at once, with the call's kernels still to write it."""
     errors = _counted(errors, dev)
-    if workspace is None and need and dev >= 0 and _raw_free and dev == _current_device():
+    here = dev if dev >= 0 or not need else _current_device()
+    if workspace is None and need and _raw_free and here == _current_device():
         handle = _stream(stream, dev)
         ws = _raw_alloc(need, handle)
         try:
@@ -569,10 +573,9 @@ def _launch_attention(dev, stream, fn, args, workspace, need, errors) -> None:
         if st:
             _check(st, fn.__name__)
         return
-    if workspace is None and need:
-        workspace = _new(need, torch.uint8, dev, stream)
     if workspace is None:
-        _launch(dev, stream, fn, *args, None, 0, errors)
+        workspace = _new(need, torch.uint8, here, stream) if need else None
+        _launch(dev, stream, fn, *args, workspace.data_ptr() if need else None, need, errors)
     else:
         _launch(dev, stream, fn, *args, _ptr(workspace, workspace.dtype, dev, "workspace"),
                 workspace.numel() * workspace.element_size(), errors)
@@ -587,7 +590,7 @@ def paged_block_sparse_attention(q, kv_cache, page_table, blocks, lens, scale=No
     ``paged_block_sparse_attention_workspace`` bytes, allocated per call if
     needed and not given."""
     N, Hkv, page, D = _paged_cache(kv_cache)
-    dev = _home(q, kv_cache, page_table, blocks, lens, requests, out, errors)
+    dev = _home(q, kv_cache, page_table, blocks, lens, requests, out, errors, workspace)
     q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
     B, H, topk = blocks.shape if blocks.dim() == 3 else (-1, 0, 0)
     if B != T or H != Hkv:
@@ -614,7 +617,7 @@ def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_ta
     keys of its own request's pages (``page_table``).  The prefix is read once
     for the whole batch.  Other arguments as paged_block_sparse_attention."""
     N, Hkv, page, D = _paged_cache(kv_cache)
-    dev = _home(q, kv_cache, prefix_pages, page_table, lens, requests, out, errors)
+    dev = _home(q, kv_cache, prefix_pages, page_table, lens, requests, out, errors, workspace)
     q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
     if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page < prefix_len:
         raise ValueError("prefix_pages must be 1-D and hold prefix_len keys")

@@ -77,3 +77,47 @@ def test_configuration_that_changes_during_calls(cuda_device):
         kvq.set_config("prefix", old)
     assert seen <= {kvq.KVQ_OK, kvq.KVQ_ERR_NULL} and kvq.KVQ_OK in seen
     ref.check(out, want, tol)
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_pinned_calls_whose_range_is_split(cuda_device, monkeypatch, raw):
+    """Every tensor in pinned host memory, a range long enough for partials:
+    pinned memory that the program takes and fills as soon as the call returns,
+    with the kernels still to come, is not the call's workspace."""
+    if not raw:
+        monkeypatch.setattr(kvq, "_raw_free", None)
+    T, Hq, Hkv, D, page, prefix, topk = 1, 4, 1, 128, 64, 40000, 700
+    L = kvq.lib()
+    needs = [L.paged_shared_prefix_attention_workspace(T, Hq, Hkv, D, page, prefix, 1),
+             L.paged_block_sparse_attention_workspace(T, Hq, Hkv, D, page, topk)]
+    assert min(needs) > 0
+    host = batch(gen(2), T, Hq, Hkv, D, page, prefix, 1, page)
+    blocks = torch.arange(topk, dtype=torch.int32).expand(T, Hkv, topk).contiguous()
+    some = torch.full((T,), (topk - 1) * page + 5, dtype=torch.int32)
+    long_table = host[2].repeat(2)[:topk].view(T, topk).contiguous()
+    want, tol = exact(host)
+    sparse = ref.sparse_attention(host[0], host[1], long_table, blocks, some, D ** -0.5)
+    args = to(host, lambda t: t.pin_memory())
+    blocks, some, long_table = blocks.pin_memory(), some.pin_memory(), long_table.pin_memory()
+    old = kvq.set_config("prefix", 0)  # the tiles take device memory alone
+    try:
+        for _ in range(2):
+            torch.cuda.synchronize()
+            torch.cuda._sleep(10000000)  # about five milliseconds
+            a = kvq.paged_shared_prefix_attention(*args)
+            b = kvq.paged_block_sparse_attention(args[0], args[1], long_table, blocks, some)
+            taken = [torch.empty(n, dtype=torch.uint8, pin_memory=True) for n in needs * 2]
+            for x in taken:
+                x.fill_(7)
+            torch.cuda.synchronize()
+            assert a.is_pinned() and b.is_pinned()
+            ref.check(a, want, tol)
+            ref.check(b, *sparse)
+            assert all(bool((x == 7).all()) for x in taken)
+        # a workspace of the caller's may be device memory there
+        ws = torch.empty(needs[0], dtype=torch.uint8, device="cuda")
+        c = kvq.paged_shared_prefix_attention(*args, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(c), bits(a))
+    finally:
+        kvq.set_config("prefix", old)

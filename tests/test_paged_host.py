@@ -293,3 +293,31 @@ def test_size_found_while_the_configuration_changes(L, monkeypatch):
         assert kvq._workspace_bytes(name, *sizes) == getattr(L, name)(*sizes) > 0
     finally:
         kvq.set_config("prefix", -1)
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_workspace_of_a_call_on_pinned_tensors(monkeypatch, raw):
+    """No device among the call's tensors: the workspace is the current
+    device's, in the order of the call's stream, with torch's allocator by
+    itself (``raw``) and with tensors from it."""
+    made, calls = [], []
+
+    def fn(*args):
+        calls.append(args)
+        return 0
+
+    def new(shape, dtype, dev, stream):
+        made.append((shape, dev, stream))
+        return torch.zeros(shape, dtype=dtype)
+
+    monkeypatch.setattr(kvq, "_current_device", lambda: 3)
+    monkeypatch.setattr(kvq, "_stream", lambda stream, dev: 77)
+    monkeypatch.setattr(kvq, "_new", new)
+    monkeypatch.setattr(kvq, "_raw_alloc", lambda n, stream: made.append((n, stream)) or 4096)
+    monkeypatch.setattr(kvq, "_raw_free", (lambda p: made.append(p)) if raw else None)
+    kvq._launch_attention(-1, None, fn, (1, 2), None, 640, None)
+    assert made == ([(640, 77), 4096] if raw else [(640, 3, None)])
+    assert len(calls) == 1 and calls[0][:2] + calls[0][3:] == (1, 2, 640, None, 77)
+    assert not raw or calls[0][2] == 4096
+    kvq._launch_attention(-1, None, fn, (1, 2), None, 0, None)  # none needed, none made
+    assert calls[1] == (1, 2, None, 0, None, 77) and len(made) == (2 if raw else 1)
