@@ -423,7 +423,7 @@ def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache
     T = qkv.shape[0]
     if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must hold one value per token")
-    dev = _home(qkv, q_out, cos_sin_cache, slot_mapping, kv_cache, errors)
+    dev = _home(qkv, q_out, cos_sin_cache, positions, slot_mapping, kv_cache, errors)
     q_ptr = None
     if q_out is not None:
         if q_out.shape != (T, num_heads_q, head_dim):

@@ -121,3 +121,19 @@ def test_pinned_calls_whose_range_is_split(cuda_device, monkeypatch, raw):
         assert torch.equal(bits(c), bits(a))
     finally:
         kvq.set_config("prefix", old)
+
+
+def test_append_with_its_positions_alone_on_the_device(cuda_device):
+    """One device tensor among pinned ones decides the device, whichever it is."""
+    g = gen(3)
+    T, Hq, Hkv, D, page = 6, 4, 2, 64, 16
+    qkv, cache = normal(g, T, (Hq + 2 * Hkv) * D), normal(g, 3, 2, Hkv, page, D)
+    slots, pos = torch.randperm(3 * page, generator=g)[:T], torch.arange(T)
+    table = torch.randn(8, D, generator=g)
+    got = []
+    for move in (lambda t: t.cuda(), lambda t: t.pin_memory()):
+        x, kv = move(qkv.clone()), move(cache.clone())
+        kvq.paged_kv_rope_append(x, Hq, Hkv, D, move(table), True, pos.cuda(), move(slots), kv)
+        torch.cuda.synchronize()
+        got.append((bits(x), bits(kv)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
