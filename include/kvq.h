@@ -391,7 +391,8 @@ kvq_status paged_kv_block_select(const void* q, int64_t q_stride, int64_t num_to
  *            listed twice is attended to twice.  Keys at or past lens[t] are
  *            not there; an index that is negative (but for -1) or starts at
  *            or past lens[t] is rejected.
- *   scale    factor of the logits (finite), e.g. 1 / sqrt(head_dim).
+ *   scale    factor of the logits, e.g. 1 / sqrt(head_dim); finite, and
+ *            scale * log2(e) as well (|scale| up to 2.35e38).
  *   out      bf16 [num_tokens, num_heads_q, head_dim], 16-byte aligned, not
  *            overlapping q.  A token without any key gets zeros.
  * out = softmax(scale q K^T) V per query head.  Scores, softmax statistics

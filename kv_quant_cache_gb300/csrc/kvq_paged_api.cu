@@ -26,6 +26,10 @@ bool prefix_ok(int64_t prefix_len, int page_size) {
          (prefix_len + page_size - 1) / page_size <= kMaxListed;
 }
 
+// The kernels take the scale in units of log2: infinite there, it would make
+// NaN of a score of zero.
+bool scale_ok(float scale) { return std::isfinite(scale * 1.4426950408889634f); }
+
 // Sizes that every operator takes.
 kvq_status check_cache(int num_heads_kv, int head_dim, int64_t num_pages, int page_size) {
   if (num_heads_kv < 1 || num_heads_kv > kMaxHeads || num_pages < 0 ||
@@ -225,7 +229,7 @@ kvq_status paged_block_sparse_attention(const void* q, int64_t q_stride, int64_t
                     table_width);
   if (c != KVQ_OK) return c;
   if (topk < 1 || topk > kMaxListed) return KVQ_ERR_SHAPE;
-  if (!std::isfinite(scale)) return KVQ_ERR_VALUE;
+  if (!scale_ok(scale)) return KVQ_ERR_VALUE;
   if (num_tokens == 0) return KVQ_OK;
   c = check_requests(q, kv_cache, page_table, num_requests, table_width, requests, lens,
                      num_tokens, error_count);
@@ -279,7 +283,7 @@ kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_
                     table_width);
   if (c != KVQ_OK) return c;
   if (!prefix_ok(prefix_len, page_size)) return KVQ_ERR_SHAPE;
-  if (!std::isfinite(scale)) return KVQ_ERR_VALUE;
+  if (!scale_ok(scale)) return KVQ_ERR_VALUE;
   if (num_tokens == 0) return KVQ_OK;
   c = check_requests(q, kv_cache, page_table, num_requests, table_width, requests, lens,
                      num_tokens, error_count);

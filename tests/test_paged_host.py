@@ -321,3 +321,10 @@ def test_workspace_of_a_call_on_pinned_tensors(monkeypatch, raw):
     assert not raw or calls[0][2] == 4096
     kvq._launch_attention(-1, None, fn, (1, 2), None, 0, None)  # none needed, none made
     assert calls[1] == (1, 2, None, 0, None, 77) and len(made) == (2 if raw else 1)
+
+
+@pytest.mark.parametrize("call", [sparse, prefix])
+def test_scale_whose_logarithmic_form_overflows(L, call):
+    """scale * log2(e) past the largest float: a score of zero would be NaN."""
+    for scale in (2.5e38, -2.5e38, 3.4e38, math.nan, -math.inf):
+        assert rejected(call(L, scale=scale)) == kvq.KVQ_ERR_VALUE
