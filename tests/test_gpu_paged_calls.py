@@ -137,3 +137,70 @@ def test_append_with_its_positions_alone_on_the_device(cuda_device):
         torch.cuda.synchronize()
         got.append((bits(x), bits(kv)))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def against_exact(g, host, bad_page=False, **k):
+    """A call against the exact values, and repeated bit for bit."""
+    if bad_page:
+        host[2][1] = host[1].shape[0]
+    want, tol = exact(host)
+    args = to(host, lambda t: t.cuda())
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kvq.paged_shared_prefix_attention(*args, errors=err, **k)
+    ref.check(got, want, tol)
+    assert (int(err.item()) > 0) == bad_page
+    assert torch.equal(bits(got), bits(kvq.paged_shared_prefix_attention(*args, **k)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("prefix", [70, 1100])
+def test_hundreds_of_row_tiles_behind_a_prefix(cuda_device, D, prefix):
+    """640 row tiles with few keys of their own each: a warp takes a tile and
+    joins the parts of the prefix to it; tokens without own keys as well."""
+    old = kvq.set_config("prefix", 1)
+    try:
+        g = gen(4 + D)
+        against_exact(g, batch(g, 640, 16, 2, D, 16, prefix, 3, 44), bad_page=prefix > 1000)
+    finally:
+        kvq.set_config("prefix", old)
+
+
+@pytest.mark.parametrize("T,Hkv,D,prefix", [
+    (613, 2, 256, 400),    # 39 row tiles of a head
+    (1240, 2, 128, 300),   # 39
+    (1240, 1, 64, 700),    # 39
+    (980, 1, 256, 129),    # 62: these stay in step
+    (2500, 1, 128, 260),   # 79
+    (2460, 1, 256, 128),   # 154, more than there are SMs
+    (4950, 1, 64, 200)])   # 155
+def test_row_tiles_that_fill_the_sms_unevenly(cuda_device, T, Hkv, D, prefix):
+    """Where CTAs in step would leave many SMs idle, each takes its share of a
+    head's row tiles one after the other."""
+    old = kvq.set_config("prefix", 1)
+    try:
+        g = gen(5 + T)
+        against_exact(g, batch(g, T, 8 * Hkv, Hkv, D, 64, prefix, 1, 5), bad_page=prefix == 300)
+    finally:
+        kvq.set_config("prefix", old)
+
+
+def test_workspaces_without_the_allocator_by_itself(cuda_device, monkeypatch):
+    """A torch whose allocator is not reached by itself: tensors are the
+    workspaces, with the same results, on a stream of the call's own too."""
+    host = batch(gen(6), 70, 8, 1, 128, 64, 3000, 1, 64)
+    args = to(host, lambda t: t.cuda())
+    want = kvq.paged_shared_prefix_attention(*args)
+    ref.check(want, *exact(host))
+    monkeypatch.setattr(kvq, "_raw_free", None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream):
+        got = kvq.paged_shared_prefix_attention(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(got), bits(want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kvq.paged_shared_prefix_attention(*args)
+    got.zero_()
+    graph.replay()
+    assert torch.equal(bits(got), bits(want))
