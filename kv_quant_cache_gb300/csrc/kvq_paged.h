@@ -100,7 +100,7 @@ int set_prefix_config(int id);  // -1: by the sizes; returns the previous one
 int prefix_config();
 uint32_t set_tile_wait_limit(uint32_t polls);  // kvq_set_tile_wait_limit
 
-// Bytes of workspace the two attentions need (a multiple of 16; 0: none).
+// Bytes of workspace the two attentions need (0: none).
 // Depends on the sizes (and a forced configuration) alone, so that it can be
 // asked for without a device.  A call reads prefix_config() once and hands it
 // on: one that changes meanwhile may not change what the workspace is for.

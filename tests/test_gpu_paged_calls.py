@@ -204,3 +204,68 @@ def test_workspaces_without_the_allocator_by_itself(cuda_device, monkeypatch):
     got.zero_()
     graph.replay()
     assert torch.equal(bits(got), bits(want))
+
+
+@pytest.mark.parametrize("way", [-1, 0, 1])
+def test_the_largest_pages(cuda_device, way):
+    """Pages of 65536 tokens through every operator: the last slot of one, a
+    full page, a few keys of one, a prefix that ends inside its second."""
+    g = gen(7)
+    T, Hq, Hkv, D, page = 20, 4, 1, 64, 65536
+    cache = normal(g, 4, 2, Hkv, page, D)
+    qkv = normal(g, 2, (Hq + 2 * Hkv) * D)
+    slots = torch.tensor([page - 1, 4 * page - 1])
+    d = cache.cuda()
+    kvq.paged_kv_rope_append(qkv.cuda(), Hq, Hkv, D, None, True, None, slots.cuda(), d)
+    rows = qkv.view(2, Hq + 2 * Hkv, D)
+    for i, p in enumerate((0, 3)):
+        cache[p, 0, 0, -1], cache[p, 1, 0, -1] = rows[i, Hq], rows[i, Hq + 1]
+    assert torch.equal(bits(d), bits(cache))
+    fill = torch.tensor([page, 1, page - 1, page], dtype=torch.int32)
+    bounds = torch.zeros(4, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+    kvq.paged_kv_page_bounds(d, torch.arange(4, device="cuda"), fill.cuda(), bounds)
+    keys = [cache[p, 0, 0, :fill[p]] for p in range(4)]
+    want = torch.stack([torch.stack([k.amin(0), k.amax(0)]) for k in keys])[:, None]
+    assert torch.equal(bits(bounds), bits(want))
+    q = normal(g, T, Hq, D)
+    table = torch.tensor([[0, 1, 3]], dtype=torch.int32)
+    requests = torch.zeros(T, dtype=torch.int32)
+    lens = torch.full((T,), 3, dtype=torch.int32)
+    lens[0], lens[1], lens[2] = 2 * page + 7, page, 0
+    blocks = kvq.paged_kv_block_select(q.cuda(), bounds, table.cuda(), lens.cuda(), page, 2,
+                                       requests=requests.cuda())
+    assert torch.equal(blocks.cpu(), ref.select(q, want, table, lens, page, 2, 0, 0, requests))
+    got = kvq.paged_block_sparse_attention(q.cuda(), d, table.cuda(), blocks, lens.cuda(),
+                                           requests=requests.cuda())
+    ref.check(got, *ref.sparse_attention(q, cache, table, blocks.cpu(), lens, D ** -0.5, requests))
+    old = kvq.set_config("prefix", way)
+    try:
+        pages = torch.tensor([2, 3], dtype=torch.int32)
+        got = kvq.paged_shared_prefix_attention(q.cuda(), d, pages.cuda(), page + 77, table.cuda(),
+                                                lens.cuda(), requests=requests.cuda())
+    finally:
+        kvq.set_config("prefix", old)
+    ref.check(got, *ref.prefix_attention(q, cache, pages, page + 77, table, lens, D ** -0.5,
+                                         requests))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_selection_from_the_widest_table(cuda_device, D):
+    """16384 blocks, of which a third are equal and a third differ in a dim
+    whose query is tiny; half of them selected, or few, or all but one."""
+    g = gen(8 + D)
+    T, Hq, Hkv, page, width, some = 2, 4, 1, 4, 16384, 5000
+    mid, half = torch.randn(some, Hkv, 1, D, generator=g) * 0.5, torch.rand(some, Hkv, 2, D, generator=g)
+    half[:, :, 0] *= -1
+    bounds = (mid + half).bfloat16()
+    bounds[:1700] = bounds[0]
+    bounds[1700:3400] = bounds[1700]
+    bounds[1700:3400, :, 1, 5] = (1 + torch.arange(1700)[:, None] / 2048).bfloat16()
+    q = normal(g, T, Hq, D)
+    q[:, :, 5] = 2.0 ** -22
+    table = torch.randint(0, some, (T, width), generator=g, dtype=torch.int32)
+    lens = torch.tensor([width * page, width * page - page - 1], dtype=torch.int32)
+    for topk, first, last in ((8192, 0, 0), (33, 2, 2), (16383, 0, 1), (6000, 0, 0)):
+        got = kvq.paged_kv_block_select(q.cuda(), bounds.cuda(), table.cuda(), lens.cuda(), page,
+                                        topk, first, last)
+        assert torch.equal(got.cpu(), ref.select(q, bounds, table, lens, page, topk, first, last))
