@@ -348,7 +348,8 @@ kvq_status paged_kv_rope_append(void* qkv, void* q_out, int64_t num_tokens, int 
  *           minima, then the maxima.  Entries of pages not listed are left
  *           as they are.  Exact (no rounding); a NaN key gives NaN.
  * A page or length outside its range is skipped and counted.  A page may be
- * listed twice with the same length; with two lengths either may win.
+ * listed twice with the same length; with two lengths its entry may mix the
+ * two (the minima of one, the maxima of the other).
  */
 kvq_status paged_kv_page_bounds(const void* kv_cache, int64_t num_pages, int num_heads_kv,
                                 int page_size, int head_dim, const int64_t* pages,
@@ -367,9 +368,12 @@ kvq_status paged_kv_page_bounds(const void* kv_cache, int64_t num_pages, int num
  *                that are selected ahead of every score.
  *   blocks       int32 [num_tokens, num_heads_kv, topk], written: the
  *                selected block indices in ascending order, then -1.
- * The selection is that of exact arithmetic: fp32 scores too close to call
- * are computed again in fp64, and of equal scores the lower index wins.  A
- * NaN score, and a block whose page lies outside the cache, rank with -inf.
+ * The selection does not depend on fp32 rounding: scores too close to call
+ * are computed again in fp64, all in one order of their terms, and of equal
+ * ones the lower index wins.  (Where the terms' exponents span more bits than
+ * fp64 has, its rounding may order scores that are equal or closer than
+ * that.)  A NaN score, and a block whose page lies outside the cache, rank
+ * with -inf.
  * n <= topk selects all n without reading bounds.  table_width at most 16384
  * (else KVQ_ERR_UNSUPPORTED).
  */
@@ -390,7 +394,8 @@ kvq_status paged_kv_block_select(const void* q, int64_t q_stride, int64_t num_to
  *            request's pages, -1 = none (anywhere in the list).  A block
  *            listed twice is attended to twice.  Keys at or past lens[t] are
  *            not there; an index that is negative (but for -1) or starts at
- *            or past lens[t] is rejected.
+ *            or past lens[t] is rejected.  The list of a token that sees no
+ *            key (lens[t] 0, or its request or length rejected) is not read.
  *   scale    factor of the logits, e.g. 1 / sqrt(head_dim); finite, and
  *            scale * log2(e) as well (|scale| up to 2.35e38).
  *   out      bf16 [num_tokens, num_heads_q, head_dim], 16-byte aligned, not
@@ -530,15 +535,16 @@ kvq_status kvq_stage_events(uint64_t* fallbacks, uint64_t* drain_timeouts, int r
  * kernel may be scheduled while the kernel before it on the stream is still
  * finishing.  Every kernel of this library first waits until the kernels it
  * depends on have completed and their writes are visible
- * (griddepcontrol.wait); its one-shot launch shapes then let the next kernel
- * be scheduled (griddepcontrol.launch_dependents), its persistent shapes do
- * not.  Results and stream order are those of ordinary launches; only the
- * launch gaps shrink: on GB300 a 32-layer decode step captured in a CUDA
- * graph goes from 2.47 to 1.79 us per launch, a mid-size step gains 3 %, and
- * the 32768-token step is unchanged.  A kernel of the caller's that follows
- * one of ours and was itself launched with the attribute must wait
- * (griddepcontrol.wait or cudaGridDependencySynchronize) before reading our
- * outputs, as with any programmatic launch.  Returns the previous setting
+ * (griddepcontrol.wait; of a shared prefix's two launches the first waits for
+ * all that came before, the second for the first); its one-shot launch shapes
+ * then let the next kernel be scheduled (griddepcontrol.launch_dependents), its
+ * persistent shapes do not.  Results and stream order are those of ordinary
+ * launches; only the launch gaps shrink: on GB300 a 32-layer decode step
+ * captured in a CUDA graph goes from 2.47 to 1.79 us per launch, a mid-size
+ * step gains 3 %, and the 32768-token step is unchanged.  A kernel of the
+ * caller's that follows one of ours and was itself launched with the attribute
+ * must wait (griddepcontrol.wait or cudaGridDependencySynchronize) before
+ * reading our outputs, as with any programmatic launch.  Returns the previous setting
  * (0 or 1).  Not synchronised with launches on other threads.  No
  * counterpart in the source pages: a launch option of this library.
  */

@@ -50,7 +50,9 @@ __device__ __forceinline__ float group_max(float v) {
 
 // Programmatic dependent launch.  Every kernel starts by waiting until the
 // grids it depends on have completed and their writes are visible (a no-op
-// when it was launched the ordinary way).  One-shot grids then let the next
+// when it was launched the ordinary way); paged_attn_kernel behind the prefix's
+// tiles waits at its end, which is sound only because the tiles trigger after
+// their own wait: a kernel in front of a late waiter must not trigger sooner.  One-shot grids then let the next
 // grid on the stream be scheduled: it can start once their last wave runs.
 // Persistent grids do not trigger: all their CTAs are resident from the
 // start, and a dependent scheduled early would only take SM resources and

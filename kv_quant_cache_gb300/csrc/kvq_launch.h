@@ -83,7 +83,10 @@ int device_sm_count();
 // be scheduled while the previous kernel on the stream is finishing, and
 // every kernel of this library waits for that kernel's completion before its
 // first memory access (grid_dependency_sync), so results and stream order are
-// those of an ordinary launch.
+// those of an ordinary launch.  One exception: behind the prefix's tiles,
+// paged_attn_kernel reads its inputs first and waits before it reads the tiles'
+// partials and before it writes.  It may because prefix_tiles_kernel lets it be
+// scheduled only after its own wait: what came before both has completed then.
 bool programmatic_launch();
 
 // Launches `kernel` with one by-value parameter block and returns the

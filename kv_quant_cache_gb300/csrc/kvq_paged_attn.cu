@@ -790,9 +790,10 @@ struct Spread {
   bool solo;  // a warp per row tile
 };
 
-// CTAs are added while all of them are resident at once (two to an SM; with
-// half as many again in a second wave the same range took 20-30 % longer, with
-// twice as many, 24 us against 10.4) and each keeps at least two steps of 16
+// CTAs are added while all of them are resident at once, two to an SM of the
+// part's 152 (heads of 64 have four, but these numbers; with half as many again
+// in a second wave the same range took 20-30 % longer, with twice as many, 24 us
+// against 10.4) and each keeps at least two steps of 16
 // keys for every warp: first within a cluster of up to 8 (joined in place);
 // beyond that, as partials that a second launch joins, only where a CTA would
 // be left with more than 2048 keys (below, the second launch costs more than it

@@ -247,7 +247,8 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
   }
   if (warp == kMmaWarp) tc::alloc512(tma::smem_addr(tmem_slot));
   // All CTAs are resident at once: the kernel of the tokens' own keys may take
-  // up the SMs that have none, or are done.
+  // up the SMs that have none, or are done.  Not before the wait: that kernel
+  // reads its inputs without one.
   grid_dependency_wait();
   launch_dependents();
   tc::fence_before();
@@ -789,7 +790,8 @@ PrefixTilesPlan prefix_tiles_plan(int64_t num_tokens, int num_heads_q, int num_h
   const int of_item = row_tiles_of(head_dim) * kTileRows;
   plan.row_tiles = (int)((rows + of_item - 1) / of_item);
   plan.blocks = (int)((prefix_len + kKeys - 1) / kKeys);
-  // In step, if that leaves at most a fifth of the SMs without a CTA (which
+  // The part has 152 SMs (with fewer, some CTAs form a second wave).  In step, if
+  // that leaves at most a fifth of the SMs without a CTA (which
   // costs as much as reading out of step); every CTA has an item or two blocks.
   const int fit = 152 / (plan.row_tiles < 152 ? plan.row_tiles : 152);
   plan.lanes = plan.row_tiles <= 152 && fit * plan.row_tiles * 5 >= 152 * 4 ? plan.row_tiles : 1;

@@ -644,7 +644,7 @@ cudaError_t launch_select(const BlockSelectArgs& a, int cluster, cudaStream_t st
 
 // More items than CTAs that are resident at once: CTAs of half the threads, of
 // which twice as many are, so that some select while others score.  256 tokens
-// x 8 heads of 128 dims, 64 blocks 30 us against 46, 256 blocks 60 against 76;
+// x 8 heads of 128 dims, 64 blocks 28 us against 46, 256 blocks 60 against 76;
 // 64 tokens, 1024 blocks 49.8 / 51.3 (of 64 dims 27.5 / 30.0, of 256 91 / 99),
 // 2048 blocks, which therefore keep the larger, 128 / 99.
 template <int D>
