@@ -148,8 +148,10 @@ def _cuda(t: torch.Tensor, dtype, name: str) -> int:
     device's address space at the same address under unified addressing)."""
     if type(t) is torch.Tensor and t.is_cuda and t.dtype == dtype and t.is_contiguous():
         return t.data_ptr()  # the common case, checked first (per-call cost)
+    # (a host tensor without elements counts as pinned: there is nothing to pin)
     if not isinstance(t, torch.Tensor) or not (t.is_cuda or (t.device.type == "cpu"
-                                                             and t.is_pinned())):
+                                                             and (t.numel() == 0
+                                                                  or t.is_pinned()))):
         raise ValueError(f"{name}: expected a CUDA tensor or a pinned host tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -476,7 +478,7 @@ def _paged_q(q, head_dim, dev):
     if q.dtype is not _BF16:
         raise ValueError(f"q: expected {_BF16}, got {q.dtype}")
     if dev < 0 or q.get_device() != dev:
-        if not (q.is_cuda or (q.device.type == "cpu" and q.is_pinned())):
+        if not (q.is_cuda or (q.device.type == "cpu" and (q.numel() == 0 or q.is_pinned()))):
             raise ValueError("q: expected a CUDA tensor or a pinned host tensor")
     if q.is_contiguous() or T == 0:
         return q.data_ptr(), T, Hq, Hq * D

@@ -269,3 +269,20 @@ def test_selection_from_the_widest_table(cuda_device, D):
         got = kvq.paged_kv_block_select(q.cuda(), bounds.cuda(), table.cuda(), lens.cuda(), page,
                                         topk, first, last)
         assert torch.equal(got.cpu(), ref.select(q, bounds, table, lens, page, topk, first, last))
+
+
+def test_pinned_calls_with_empty_lists(cuda_device):
+    """No prefix, no pages of their own, no tokens, with everything pinned."""
+    T, Hq, Hkv, D, page = 5, 4, 2, 64, 16
+    host = batch(gen(9), T, Hq, Hkv, D, page, 0, 2, 2 * page)
+    want, tol = exact(host)
+    args = to(host, lambda t: t.pin_memory())
+    got = kvq.paged_shared_prefix_attention(*args)
+    torch.cuda.synchronize()
+    ref.check(got, want, tol)
+    args[4], args[5] = args[4][:, :0], torch.zeros(T, dtype=torch.int32).pin_memory()
+    got = kvq.paged_shared_prefix_attention(*args)
+    torch.cuda.synchronize()
+    assert not bool(bits(got).any())
+    args[0], args[5] = args[0][:0], args[5][:0]
+    assert kvq.paged_shared_prefix_attention(*args).shape == (0, Hq, D)

@@ -328,3 +328,15 @@ def test_scale_whose_logarithmic_form_overflows(L, call):
     """scale * log2(e) past the largest float: a score of zero would be NaN."""
     for scale in (2.5e38, -2.5e38, 3.4e38, math.nan, -math.inf):
         assert rejected(call(L, scale=scale)) == kvq.KVQ_ERR_VALUE
+
+
+def test_host_tensors_without_elements():
+    """torch calls no empty tensor pinned; a list without entries has to be
+    taken all the same, of the right type only."""
+    for dev in (-1, 0):
+        assert kvq._ptr(torch.empty(0, dtype=torch.int32), torch.int32, dev, "pages") == 0
+        with pytest.raises(ValueError):
+            kvq._ptr(torch.empty(0, dtype=torch.int64), torch.int32, dev, "pages")
+        with pytest.raises(ValueError):
+            kvq._ptr(torch.zeros(1, dtype=torch.int32), torch.int32, dev, "pages")
+    assert kvq._paged_q(torch.empty(0, 4, 64, dtype=torch.bfloat16), 64, -1)[1:] == (0, 4, 256)
