@@ -443,6 +443,115 @@ kvq_status paged_shared_prefix_attention(const void* q, int64_t q_stride, int64_
                                          void* workspace, int64_t workspace_bytes,
                                          int32_t* error_count, kvq_stream_t stream);
 
+/*
+ * The paged cache held in 4 bits: the grouped-query cache above in 9/32 of its
+ * bytes, with its own append, a reader and its attention.
+ *
+ *   kv_cache     uint8 [num_pages, 2, num_heads_kv, page_size, 9 head_dim / 16],
+ *                contiguous, 16-byte aligned.  Of each page the keys of every kv
+ *                head, then the values; slot s is offset s % page_size of page
+ *                s / page_size.  The block of one head and page holds the codes of
+ *                its page_size tokens, head_dim / 2 bytes each, and behind them,
+ *                per token and group of 64 dims, a bf16 scale and a bf16 zero.
+ *                Code c (0 .. 15) stands for zero + scale (c - 8).  A little-endian
+ *                32-bit word of codes holds 8 dims: its nibble i < 4 is dim 2i,
+ *                nibble i + 4 dim 2i + 1.
+ *   head_dim     64, 128 or 256; page_size a multiple of 16, up to 65536 (else
+ *                KVQ_ERR_UNSUPPORTED, above that KVQ_ERR_SHAPE).
+ * The general contract and the rules on indices and error_count of the paged
+ * operators above hold.  No counterpart in the source pages.
+ */
+
+/*
+ * paged_kv4_rope_append -- paged_kv_rope_append into such a cache.  Arguments,
+ * rejections and the rotated query rows as there.  K and V are quantised from
+ * the bf16 values x that a bf16 cache would hold (K: the rotation rounded
+ * correctly to fp32, then to bf16), per group of 64 dims with least and largest
+ * value lo and hi:
+ *   scale = bf16((hi - lo) / 15), zero = bf16(lo + 8 scale), in fp32 before bf16,
+ *   code  = (x - zero) / scale, the difference in fp32, to the nearest whole
+ *           number, ties to even, held to -8 .. 7, plus 8; 8 where the scale is 0.
+ * A group with a NaN or an infinity, or whose hi - lo overflows fp32, reads back
+ * as NaN.  No two tokens may have the same slot.
+ */
+kvq_status paged_kv4_rope_append(void* qkv, void* q_out, int64_t num_tokens, int num_heads_q,
+                                 int num_heads_kv, int head_dim, const float* cos_sin_cache,
+                                 int64_t max_pos, int rotary_dim, int is_neox,
+                                 const int64_t* positions, const int64_t* slot_mapping,
+                                 void* kv_cache, int64_t num_pages, int page_size,
+                                 int32_t* error_count, kvq_stream_t stream);
+
+/*
+ * paged_kv4_gather -- listed tokens read back as bf16.
+ *
+ *   slots   int64 [num_listed]; -1 = rows of +0.  A slot outside the cache (and
+ *           not -1) gives rows of +0 too and is counted.
+ *   k, v    bf16 [num_listed, num_heads_kv, head_dim], 16-byte aligned, written:
+ *           zero + scale (c - 8), rounded to fp32 and then to bf16.  Not
+ *           overlapping each other (KVQ_ERR_VALUE).
+ */
+kvq_status paged_kv4_gather(const void* kv_cache, int64_t num_pages, int num_heads_kv,
+                            int page_size, int head_dim, const int64_t* slots,
+                            int64_t num_listed, void* k, void* v, int32_t* error_count,
+                            kvq_stream_t stream);
+
+/*
+ * paged_kv4_attention -- attention of each token over the first lens[t] keys of its
+ * request, of its 4-bit cache.
+ *
+ *   tokens_per_request  >= 1; token t belongs to request t / tokens_per_request
+ *            (num_tokens a multiple of it).  Several tokens are draft tokens or a
+ *            causal chunk, each with its own length; one without a length (0) gets
+ *            zeros, which is how a batch of unequal chunks is padded.
+ *   page_table  int32 [num_tokens / tokens_per_request, table_width].
+ *   lens, scale, out, workspace  as in paged_block_sparse_attention.
+ * out = softmax(scale q K^T) V per query head, K and V the values that the codes
+ * stand for.  Scores, softmax statistics and sums in fp32; the product of a
+ * softmax numerator with the scale of V is rounded to bf16 for the product with
+ * V's codes, the output once at the end.
+ */
+int64_t paged_kv4_attention_workspace(int64_t num_tokens, int64_t tokens_per_request,
+                                      int num_heads_q, int num_heads_kv, int head_dim,
+                                      int page_size, int64_t table_width);
+kvq_status paged_kv4_attention(const void* q, int64_t q_stride, int64_t num_tokens,
+                               int64_t tokens_per_request, int num_heads_q, int num_heads_kv,
+                               int head_dim, const void* kv_cache, int64_t num_pages,
+                               int page_size, const int32_t* page_table, int64_t table_width,
+                               const int32_t* lens, float scale, void* out, void* workspace,
+                               int64_t workspace_bytes, int32_t* error_count,
+                               kvq_stream_t stream);
+
+/*
+ * dsv4_latent_attention -- attention of each token's heads over cache entries
+ * that dsv4_qnorm_rope_kv_rope_quant_insert wrote: the 512-dim vector of an entry
+ * is key and value of every head.
+ *
+ *   q          bf16, rows of num_heads * 512 contiguous values, q_stride elements
+ *              apart (a multiple of 8); 16-byte aligned.  num_heads >= 1.
+ *   kv_cache   uint8 [num_blocks, block_size, 584], 8-byte aligned.
+ *   slots      int32 [num_tokens, list_width]: the entries of each token, -1 =
+ *              none (anywhere in the list).  A slot listed twice is attended to
+ *              twice; a slot outside the cache (and not -1) is left out and
+ *              counted.  list_width at most 2^30.
+ *   lens       int32 [num_tokens]: how much of its list each token has, 0 allowed;
+ *              what lies behind is not read.  A negative length counts as 0, one
+ *              past list_width as that; both are counted.
+ *   scale      as in paged_block_sparse_attention, e.g. 1 / sqrt(512).
+ *   out        bf16 [num_tokens, num_heads, 512], 16-byte aligned, not overlapping
+ *              q.  A token without any entry gets zeros.
+ * An entry's values are those of dsv4_kv_cache_gather.  Scores, softmax statistics
+ * and sums in fp32; the softmax numerators are rounded to bf16 for the product
+ * with the values, the output once at the end.
+ * No counterpart in the source pages, which end where the entry is written.
+ */
+int64_t dsv4_latent_attention_workspace(int64_t num_tokens, int num_heads, int64_t list_width);
+kvq_status dsv4_latent_attention(const void* q, int64_t q_stride, int64_t num_tokens,
+                                 int num_heads, const uint8_t* kv_cache, int64_t num_blocks,
+                                 int block_size, const int32_t* slots, int64_t list_width,
+                                 const int32_t* lens, float scale, void* out, void* workspace,
+                                 int64_t workspace_bytes, int32_t* error_count,
+                                 kvq_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* kvq_status_string(kvq_status status);
 

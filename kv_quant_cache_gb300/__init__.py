@@ -85,6 +85,20 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.paged_shared_prefix_attention.restype = _I
     L.paged_shared_prefix_attention.argtypes = [_P, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I64,
                                                 _P, _I64, _I64, _P, _P, _F, _P, _P, _I64, _P, _P]
+    L.paged_kv4_rope_append.restype = _I
+    L.paged_kv4_rope_append.argtypes = L.paged_kv_rope_append.argtypes
+    L.paged_kv4_gather.restype = _I
+    L.paged_kv4_gather.argtypes = [_P, _I64, _I, _I, _I, _P, _I64, _P, _P, _P, _P]
+    L.paged_kv4_attention_workspace.restype = _I64
+    L.paged_kv4_attention_workspace.argtypes = [_I64, _I64, _I, _I, _I, _I, _I64]
+    L.paged_kv4_attention.restype = _I
+    L.paged_kv4_attention.argtypes = [_P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I64,
+                                      _P, _F, _P, _P, _I64, _P, _P]
+    L.dsv4_latent_attention_workspace.restype = _I64
+    L.dsv4_latent_attention_workspace.argtypes = [_I64, _I, _I64]
+    L.dsv4_latent_attention.restype = _I
+    L.dsv4_latent_attention.argtypes = [_P, _I64, _I64, _I, _P, _I64, _I, _P, _I64, _P, _F, _P,
+                                        _P, _I64, _P, _P]
     L.kvq_status_string.restype = ctypes.c_char_p
     L.kvq_status_string.argtypes = [_I]
     L.kvq_last_cuda_error.restype = _I
@@ -405,21 +419,12 @@ def _paged_cache(kv_cache):
     raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim]")
 
 
-def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox,
-                         positions, slot_mapping, kv_cache, q_out=None, stream=None,
-                         rotary_dim=None, errors=None) -> None:
-    """RoPE of the Q and K heads of ``qkv`` [T, (Hq+2Hkv)*head_dim] and the K
-    and V heads written to ``kv_cache`` (bf16 [num_pages, 2, Hkv, page_size,
-    head_dim]) at ``slot_mapping`` (int64 [T], -1 = none), in one pass.  The
-    rotated query rows go to ``q_out`` (bf16 [T, Hq, head_dim]) or stay in
-    place.  ``cos_sin_cache`` None: no rotation (after fused_qk_norm_rope);
-    ``rotary_dim`` defaults to the table's width.  Tokens with a position
-    outside the table are left out, slots outside the cache not written; both
-    are counted in ``errors`` (int32 CUDA tensor) when given."""
-    pages, heads, page, dim = _paged_cache(kv_cache)
+def _rope_append(fn, dtype, sizes, qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache,
+                 is_neox, positions, slot_mapping, kv_cache, q_out, stream, rotary_dim, errors):
+    """The append of either paged cache: ``sizes`` and ``dtype`` are the cache's."""
+    pages, heads, page, dim = sizes
     if heads != num_heads_kv or dim != head_dim:
-        raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, head_dim] of the "
-                         "call's Hkv and head_dim")
+        raise ValueError("kv_cache must be of the call's Hkv and head_dim")
     if qkv.dim() != 2 or qkv.shape[1] != (num_heads_q + 2 * num_heads_kv) * head_dim:
         raise ValueError("qkv must be [T, (Hq+2*Hkv)*head_dim]")
     T = qkv.shape[0]
@@ -444,10 +449,26 @@ def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache
             raise ValueError("positions must hold one value per token")
         cs = _ptr(cos_sin_cache, _F32, dev, "cos_sin_cache")
         pos = _ptr(positions, _I64T, dev, "positions")
-    _launch(dev, stream, (_LIB or lib()).paged_kv_rope_append, _ptr(qkv, _BF16, dev, "qkv"), q_ptr,
+    _launch(dev, stream, fn, _ptr(qkv, _BF16, dev, "qkv"), q_ptr,
             T, num_heads_q, num_heads_kv, head_dim, cs, rows, rot, 1 if is_neox else 0, pos,
             _ptr(slot_mapping, _I64T, dev, "slot_mapping"),
-            _ptr(kv_cache, _BF16, dev, "kv_cache"), pages, page, _counted(errors, dev))
+            _ptr(kv_cache, dtype, dev, "kv_cache"), pages, page, _counted(errors, dev))
+
+
+def paged_kv_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox,
+                         positions, slot_mapping, kv_cache, q_out=None, stream=None,
+                         rotary_dim=None, errors=None) -> None:
+    """RoPE of the Q and K heads of ``qkv`` [T, (Hq+2Hkv)*head_dim] and the K
+    and V heads written to ``kv_cache`` (bf16 [num_pages, 2, Hkv, page_size,
+    head_dim]) at ``slot_mapping`` (int64 [T], -1 = none), in one pass.  The
+    rotated query rows go to ``q_out`` (bf16 [T, Hq, head_dim]) or stay in
+    place.  ``cos_sin_cache`` None: no rotation (after fused_qk_norm_rope);
+    ``rotary_dim`` defaults to the table's width.  Tokens with a position
+    outside the table are left out, slots outside the cache not written; both
+    are counted in ``errors`` (int32 CUDA tensor) when given."""
+    _rope_append((_LIB or lib()).paged_kv_rope_append, _BF16, _paged_cache(kv_cache), qkv,
+                 num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox, positions,
+                 slot_mapping, kv_cache, q_out, stream, rotary_dim, errors)
 
 
 def paged_kv_page_bounds(kv_cache, pages, lens, bounds, stream=None, errors=None):
@@ -634,6 +655,108 @@ def paged_shared_prefix_attention(q, kv_cache, prefix_pages, prefix_len, page_ta
          _ptr(page_table, _I32, dev, "page_table"), R, width,
          None if requests is None else _ptr(requests, _I32, dev, "requests"),
          _ptr(lens, _I32, dev, "lens"), D ** -0.5 if scale is None else scale,
+         _ptr(out, _BF16, dev, "out")), workspace, need, errors)
+    return out
+
+
+# ---- operators on quantised caches ----------------------------------------------------
+
+_U8 = torch.uint8
+
+
+def _kv4_cache(kv_cache):
+    """num_pages, Hkv, page_size, head_dim of a paged cache held in 4 bits."""
+    if kv_cache.dim() == 5:
+        pages, two, heads, page, held = kv_cache.shape
+        if two == 2 and held % 9 == 0:
+            return pages, heads, page, held // 9 * 16
+    raise ValueError("kv_cache must be [num_pages, 2, Hkv, page_size, 9*head_dim/16]")
+
+
+def paged_kv4_rope_append(qkv, num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox,
+                          positions, slot_mapping, kv_cache, q_out=None, stream=None,
+                          rotary_dim=None, errors=None) -> None:
+    """``paged_kv_rope_append`` into a cache held in 4 bits: ``kv_cache`` uint8
+    [num_pages, 2, Hkv, page_size, 9*head_dim/16], ``page_size`` a multiple of 16.
+    Per token, head and group of 64 dims one bf16 scale and one bf16 zero; the
+    layout is described with the C entry point."""
+    _rope_append((_LIB or lib()).paged_kv4_rope_append, _U8, _kv4_cache(kv_cache), qkv,
+                 num_heads_q, num_heads_kv, head_dim, cos_sin_cache, is_neox, positions,
+                 slot_mapping, kv_cache, q_out, stream, rotary_dim, errors)
+
+
+def paged_kv4_gather(kv_cache, slots, k=None, v=None, stream=None, errors=None):
+    """(k, v) bf16 [n, Hkv, head_dim]: the tokens at ``slots`` (int64 [n], -1 =
+    rows of zeros) read back from a cache held in 4 bits; ``k`` and ``v`` are
+    allocated if not given."""
+    N, Hkv, page, D = _kv4_cache(kv_cache)
+    if slots.dim() != 1:
+        raise ValueError("slots must be a 1-D int64 tensor")
+    shape = (slots.shape[0], Hkv, D)
+    dev = _home(kv_cache, slots, k, v, errors)
+    if k is None:
+        k = _new(shape, _BF16, dev, stream)
+    if v is None:
+        v = _new(shape, _BF16, dev, stream)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("k and v must be [len(slots), Hkv, head_dim]")
+    _launch(dev, stream, (_LIB or lib()).paged_kv4_gather, _ptr(kv_cache, _U8, dev, "kv_cache"),
+            N, Hkv, page, D, _ptr(slots, _I64T, dev, "slots"), shape[0], _ptr(k, _BF16, dev, "k"),
+            _ptr(v, _BF16, dev, "v"), _counted(errors, dev))
+    return k, v
+
+
+def paged_kv4_attention(q, kv_cache, page_table, lens, scale=None, out=None,
+                        tokens_per_request=1, workspace=None, stream=None, errors=None):
+    """bf16 [T, Hq, D]: attention of each token of ``q`` over the first ``lens[t]``
+    (int32 [T]) keys of its request, of a cache held in 4 bits.  Token t belongs
+    to request t // ``tokens_per_request``, row of ``page_table`` (int32
+    [requests, width]).  ``scale`` defaults to 1/sqrt(D).  ``workspace``: a tensor
+    of at least ``paged_kv4_attention_workspace`` bytes, allocated per call if
+    needed and not given."""
+    N, Hkv, page, D = _kv4_cache(kv_cache)
+    dev = _home(q, kv_cache, page_table, lens, out, errors, workspace)
+    q_ptr, T, Hq, q_stride = _paged_q(q, D, dev)
+    R, width = page_table.shape if page_table.dim() == 2 else (-1, 0)
+    if tokens_per_request < 1 or R * tokens_per_request != T:
+        raise ValueError("page_table must be [T / tokens_per_request, table_width]")
+    if lens.numel() != T:
+        raise ValueError("lens must hold one value per token")
+    out = _output(q, out, dev, stream)
+    need = _workspace_bytes("paged_kv4_attention_workspace", T, tokens_per_request, Hq, Hkv, D,
+                            page, width)
+    _launch_attention(
+        dev, stream, (_LIB or lib()).paged_kv4_attention,
+        (q_ptr, q_stride, T, tokens_per_request, Hq, Hkv, D, _ptr(kv_cache, _U8, dev, "kv_cache"),
+         N, page, _ptr(page_table, _I32, dev, "page_table"), width,
+         _ptr(lens, _I32, dev, "lens"), D ** -0.5 if scale is None else scale,
+         _ptr(out, _BF16, dev, "out")), workspace, need, errors)
+    return out
+
+
+def dsv4_latent_attention(q, kv_cache, slots, lens, scale=None, out=None, workspace=None,
+                          stream=None, errors=None):
+    """bf16 [T, H, 512]: attention of each token's heads over the cache entries at
+    the first ``lens[t]`` (int32 [T]) of its ``slots`` (int32 [T, width], -1 =
+    none); an entry's 512-dim vector is key and value of every head.  ``kv_cache``
+    as dsv4_qnorm_rope_kv_rope_quant_insert writes it.  ``scale`` defaults to
+    1/sqrt(512).  ``workspace``: a tensor of at least
+    ``dsv4_latent_attention_workspace`` bytes, allocated per call if needed and
+    not given."""
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != ENTRY_BYTES:
+        raise ValueError("kv_cache must be [num_blocks, block_size, 584]")
+    dev = _home(q, kv_cache, slots, lens, out, errors, workspace)
+    q_ptr, T, H, q_stride = _paged_q(q, DSV4_DIM, dev)
+    if slots.dim() != 2 or slots.shape[0] != T or lens.numel() != T:
+        raise ValueError("slots must be [T, width] and lens hold one value per token")
+    out = _output(q, out, dev, stream)
+    width = slots.shape[1]
+    need = _workspace_bytes("dsv4_latent_attention_workspace", T, H, width)
+    _launch_attention(
+        dev, stream, (_LIB or lib()).dsv4_latent_attention,
+        (q_ptr, q_stride, T, H, _ptr(kv_cache, _U8, dev, "kv_cache"), kv_cache.shape[0],
+         kv_cache.shape[1], _ptr(slots, _I32, dev, "slots"), width,
+         _ptr(lens, _I32, dev, "lens"), DSV4_DIM ** -0.5 if scale is None else scale,
          _ptr(out, _BF16, dev, "out")), workspace, need, errors)
     return out
 

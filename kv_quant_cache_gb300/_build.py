@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, "libkvq.so")
 
 SOURCES = ["kvq_api.cu", "kvq_qk_norm_rope.cu", "kvq_qk_bulk.cu", "kvq_qk_general.cu",
            "kvq_dsv4.cu", "kvq_dsv4_gather.cu", "kvq_paged_api.cu", "kvq_paged_append.cu",
-           "kvq_paged_select.cu", "kvq_paged_attn.cu", "kvq_paged_prefix.cu"]
+           "kvq_paged_select.cu", "kvq_paged_attn.cu", "kvq_paged_prefix.cu",
+           "kvq_kv4_api.cu", "kvq_kv4_append.cu", "kvq_kv4_attn.cu", "kvq_latent_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      "-I", INCLUDE, "-I", CSRC]

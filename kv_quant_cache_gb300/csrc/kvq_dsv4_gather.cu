@@ -21,15 +21,19 @@
 // bf16.  Entries are 8-byte aligned, so every entry access is an 8-byte
 // load; every output row is two 16-byte stores per lane.
 #include "kvq_device.cuh"
+#include "kvq_dsv4_entry.cuh"
 #include "kvq_launch.h"
 
 namespace kvq {
 namespace {
 
-constexpr int kDim = 512;
-constexpr int kEntry = 584;
-constexpr int kRopeAt = 448;
-constexpr int kScaleAt = 576;
+using dsv4::dequant8;
+using dsv4::kDim;
+using dsv4::kEntry;
+using dsv4::kRopeAt;
+using dsv4::kScaleAt;
+using dsv4::ue8m0_scale;
+
 constexpr int kRopeLane = 24;
 constexpr int kWarps = 8;
 constexpr int kRows = 4;  // rows per warp, all loads in flight together
@@ -43,26 +47,6 @@ struct GatherParams {
   int* errors;        // bounds-checked launches: rows rejected
   int trigger_from;   // first CTA of the last wave
 };
-
-// 2^(byte - 127) as a binary32 (byte 0 gives the subnormal 2^-127).
-__device__ __forceinline__ float ue8m0_scale(uint32_t byte) {
-  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
-}
-
-// Eight e4m3 codes (element 0 in the lowest byte) times a power of two ->
-// eight bf16, packed.
-__device__ __forceinline__ uint4 dequant8(const uint2 codes, float scale) {
-  const uint32_t w[2] = {codes.x, codes.y};
-  uint32_t o[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1)));
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    o[k] = pack_bf16x2(f.x * scale, f.y * scale);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
 
 // One row's entry as held by a lane.
 struct EntryRegs {

@@ -84,6 +84,43 @@ struct PrefixAttnArgs {
   void* workspace;
 };
 
+// The paged cache held in 4 bits (kvq_kv4.cuh); its append takes AppendArgs.
+struct Kv4GatherArgs {
+  const void* kv_cache;
+  const int64_t* slots;
+  int64_t num_listed;
+  void* k;
+  void* v;
+  int num_heads_kv, head_dim, page_size;
+  int64_t num_pages;
+  int* errors;
+};
+
+struct Kv4AttnArgs {
+  PagedQuery x;  // (requests is not used)
+  const void* kv_cache;
+  int per_request;  // tokens of a request
+  float scale;
+  void* out;
+  void* workspace;
+};
+
+// Attention over listed 584-byte latent entries.
+struct LatentAttnArgs {
+  const void* q;
+  int64_t q_stride;  // elements between tokens
+  int num_tokens, num_heads;
+  const uint8_t* kv_cache;
+  int64_t num_slots;
+  const int* slots;  // [num_tokens, list_width]
+  int list_width;
+  const int* lens;
+  float scale;
+  void* out;
+  void* workspace;
+  int* errors;
+};
+
 // Pages of one request (or of the block selection) that a call may list.
 constexpr int kMaxSelectBlocks = 16384;
 
@@ -92,6 +129,18 @@ cudaError_t launch_page_bounds(const PageBoundsArgs& a, cudaStream_t stream);
 cudaError_t launch_block_select(const BlockSelectArgs& a, cudaStream_t stream);
 cudaError_t launch_sparse_attn(const SparseAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_attn(const PrefixAttnArgs& a, cudaStream_t stream);
+
+cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv4_gather(const Kv4GatherArgs& a, cudaStream_t stream);
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t stream);
+
+// Row tiles of the attention over the 4-bit cache (CTAs at least), and the bytes of
+// workspace that it and the latent attention need.
+int64_t kv4_attn_units(int64_t num_tokens, int per_request, int num_heads_q, int num_heads_kv);
+int64_t kv4_attn_workspace(int64_t num_tokens, int per_request, int num_heads_q,
+                           int num_heads_kv, int head_dim, int page_size, int table_width);
+int64_t latent_attn_workspace(int64_t num_tokens, int num_heads, int list_width);
 
 // The ways the prefix can be taken (kvq_set_prefix_config).
 extern const LaunchConfig kPrefixConfigs[];
