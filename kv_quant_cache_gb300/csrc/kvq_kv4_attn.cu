@@ -1,9 +1,9 @@
 // kvq_kv4_attn.cu -- attention over the paged cache held in 4 bits, for the few
-// query rows of a decode step.
+// query rows of a decode step or a short chunk.
 //
-// One cluster of 1..8 CTAs takes up to 16 query rows of one request and kv head
-// (tokens x heads of the group) and the request's keys, its CTAs a part each.  A
-// warp works alone on every kWarps-th group of 16 keys, with an online softmax of
+// One cluster of 1..8 CTAs takes up to 8, 16 or 32 query rows of one request and kv
+// head (tokens x heads of the group) and the request's keys, its CTAs a part each.
+// A warp works alone on every kWarps-th group of 16 keys, with an online softmax of
 // its own.  With q_j the row's dims of group j of 64, and n = c - 8 the codes:
 //   S   = scale sum_j ( s_kj (q_j n_kj) + z_kj sum(q_j) )
 //   O_j = sum_k (P_k s_kj) n_kj + sum_k P_k z_kj
@@ -11,19 +11,30 @@
 // shift, a mask and a subtraction, two at a time, and go straight into 16x8x16
 // matrix instructions; K's scales and zeros are applied to S in fp32, V's scales
 // to the weights P, whose product is rounded once to bf16 (the row sum adds the
-// unrounded P), V's zeros to P in fp32.  K's codes keep the 16 that the mask leaves
-// in them, which S takes back with the zero: (z - 24 s) sum(q).  (V's must not:
-// the sum over a long range would lose in the offset what it is to keep.)
+// unrounded P), V's zeros to P in fp32.
+//
+// The codes are the first operand of both products, S^T = K Q^T and O^T = V^T P^T:
+// 16 keys (or dims) against 8 rows, so that the 1 to 8 rows that most models have to
+// a kv head fill the instruction, and what is done per score is done on no
+// padding.  More rows are more second operands to the same codes.  The transposed
+// P takes one matrix transposition in registers.
+//
+// K's codes keep the 16 that the mask leaves in them: the accumulators start from
+// -24 sum(q_j).  V's must not: the sum over a long range would lose in the offset
+// what it is to keep.  The reference of a row's softmax
+// moves only when a score exceeds it by more than 2^8, which spares the exchange
+// of maxima: until then weights above 1 are as exact as those below.
 //
 // A group's codes come in by 16-byte asynchronous copies, three groups ahead, into
 // a ring that only this warp uses, so that there is no CTA barrier in the loop.
 // 32-byte pieces (a group of dims of one key) are exchanged so that the four
-// keys that a load touches lie in different banks.  The matrix instructions may take
-// the keys in any order: key_of() lists the one that does for the loads of K and of V.
+// keys that a load touches lie in different banks; the matrix instructions may take
+// the keys in any order, and key_of() is one that does for the loads of K and of V.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kvq_kv4.cuh"
-#include "kvq_mma.cuh"
 #include "kvq_paged_attn.cuh"
 #include "kvq_tma.cuh"
 
@@ -34,9 +45,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kRows = 16;   // query rows of a CTA
 constexpr int kStep = 16;   // keys of one step of a warp
 constexpr int kStages = 4;
+constexpr float kRescaleAt = 8.f;  // log2 by which a score may exceed the reference
 
 struct Attn4Params {
   const __nv_bfloat16* q;
@@ -53,25 +64,31 @@ struct Attn4Params {
   const int* lens;
   float scale_log2;
   int cluster, splits;
+  int part_steps;            // steps of a CTA's part; 0: an equal share
   __nv_bfloat16* out;
   Partials parts;            // with several splits
   int* errors;
   int trigger_from;
 };
 
-template <int D>
+// D dims, NT times 8 query rows.
+template <int D, int NT>
 struct Shape4 {
-  static constexpr int kCtas = D == 256 ? 2 : 3;         // of an SM, by their registers
+  static constexpr int kRows = 8 * NT;
+  // CTAs of an SM, by their registers
+  static constexpr int kCtas = D * NT <= 64 ? 5 : D * NT <= 128 ? 4 : 2;
   static constexpr int kGroups = D / kv4::kGroup;
   static constexpr int kCodes = kStep * D / 2;           // bytes of 16 keys' codes
   static constexpr int kMeta = kStep * kGroups * 4;      // .. scales and zeros
   static constexpr int kStage = 2 * (kCodes + kMeta);    // K codes, V codes, K meta, V meta
   static constexpr int kRing = kStages * kStage;
   static constexpr int kPad = D + 8;                     // fp32 values of an output row
+  static constexpr int kOut = kRows * kPad * 4;          // a warp's output takes its ring's place
+  static constexpr int kWarp = kRing > kOut ? kRing : kOut;
   static constexpr int kState = kWarps * kRows * 8;      // {m, l} per warp and row
   static constexpr int kLse = kRows * 4;
-  static constexpr int kSmem = kWarps * kRing + kState + kLse;
-  static_assert(kRing >= kRows * kPad * 4, "a warp's output fits in its ring");
+  static constexpr int kSmem = kWarps * kWarp + kState + kLse;
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -86,15 +103,13 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
-  return v;
+// (not volatile: the compiler may move these about, as loads and products of a step
+// have nothing to do with each other)
+__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The key of a step that stands at row (or column) n of half h of the matrix
@@ -110,26 +125,40 @@ __device__ __forceinline__ uint32_t piece_at(int r, int j) {
 }
 
 __device__ __forceinline__ uint32_t less24(uint32_t pair) {  // 16 + c -> c - 8, twice, exact
+  constexpr uint32_t k24 = 0x41c041c0u;
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&pair),
-                                   __floats2bfloat162_rn(24.f, 24.f));
+                                   *reinterpret_cast<const __nv_bfloat162*>(&k24));
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Transposes an 8x8 matrix of 16-bit values, two neighbours of a row to a lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, Shape4<D>::kCtas)
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Shape4<D, NT>::kCtas)
 attn4_kernel(const Attn4Params p) {
-  using S = Shape4<D>;
-  constexpr int GROUPS = S::kGroups;
+  using S = Shape4<D, NT>;
+  constexpr int GROUPS = S::kGroups, kRows = S::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   grid_dependency_sync(p.trigger_from);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;  // the lane's place in a matrix fragment
-  float2* state = reinterpret_cast<float2*>(smem + kWarps * S::kRing);
-  float* part_lse = reinterpret_cast<float*>(smem + kWarps * S::kRing + S::kState);
+  float2* state = reinterpret_cast<float2*>(smem + kWarps * S::kWarp);
+  float* part_lse = reinterpret_cast<float*>(smem + kWarps * S::kWarp + S::kState);
   const int rank = p.cluster > 1 ? (int)(blockIdx.x % p.cluster) : 0;
   const int unit = (int)blockIdx.x / p.cluster;
 
@@ -155,17 +184,86 @@ attn4_kernel(const Attn4Params p) {
   }
   const int most = __reduce_max_sync(kFullMask, len);
   const int least = __reduce_min_sync(kFullMask, lane < rows ? len : most);
-  int sees[2];  // keys that rows g and g + 8 see
-  sees[0] = __shfl_sync(kFullMask, len, g);
-  sees[1] = __shfl_sync(kFullMask, len, g + 8);
+
+  // ---- which keys: an equal share of the request's groups of 16, or a fixed part ---------
+  const int parts = p.cluster * p.splits;
+  const int all_steps = most / kStep + (most % kStep != 0);
+  const int share = p.part_steps ? p.part_steps : (all_steps + parts - 1) / parts;
+  const int64_t begin = (int64_t)share * (blockIdx.y * p.cluster + rank);
+  const int first = (int)min(begin, (int64_t)all_steps) + warp;
+  const int last = (int)min(begin + share, (int64_t)all_steps);
+  const int steps = first < last ? (last - first + kWarps - 1) / kWarps : 0;
+  const int* table = p.table + (int64_t)req * p.table_width;
+  const int64_t head_block = (int64_t)p.page_size * kv4::row_bytes(D);
+  const uint8_t* cache = p.cache + kv_head * head_block;
+  const int64_t v_from_k = p.num_kv * head_block;
+  const uint32_t ring = tma::smem_addr(smem) + warp * S::kWarp;
+
+  // The pages of 32 steps at a time, one a lane, looked up a window ahead: where the
+  // step's codes and scales lie in the cache (-1: outside it).
+  int64_t codes_at = 0, next_codes;
+  int64_t meta_at = 0, next_meta;
+  auto look_up = [&](int i, int64_t* codes, int64_t* meta) {
+    *codes = -1, *meta = 0;
+    if (i >= steps) return;
+    const uint32_t key = (uint32_t)(first + i * kWarps) * kStep;
+    const uint32_t at = p.page_shift >= 0 ? key >> p.page_shift : key / (uint32_t)p.page_size;
+    const int off = (int)(key - at * (uint32_t)p.page_size);
+    const int id = __ldg(table + at);
+    if (id >= 0 && id < p.num_pages) {
+      const int64_t page = (int64_t)id * 2 * v_from_k;
+      *codes = page + off * (D / 2);
+      *meta = page + (int64_t)p.page_size * (D / 2) + off * (GROUPS * 4);
+    } else {
+      rejected = true;
+    }
+  };
+  look_up(lane, &next_codes, &next_meta);
+  uint32_t outside = 0;  // of the last 32 steps issued: bit i % 32, the page is not there
+
+  // where the lane's fragments of a step go
+  uint32_t place[S::kCodes / 512];
+#pragma unroll
+  for (int k = 0; k < S::kCodes / 512; ++k) {
+    const int f = lane + 32 * k;
+    place[k] = piece_at<GROUPS>((f >> 1) / GROUPS, (f >> 1) % GROUPS) + ((f & 1) << 4);
+  }
+  const int meta_from = 16 * (lane & 15);
+  const bool meta_v = lane >= 16, meta_mine = (lane & 15) < S::kMeta / 16;
+  auto issue = [&](int i) {
+    if ((i & 31) == 0) {
+      codes_at = next_codes, meta_at = next_meta;
+      look_up(i + 32 + lane, &next_codes, &next_meta);
+    }
+    const int64_t codes = __shfl_sync(kFullMask, codes_at, i & 31);
+    const int64_t meta = __shfl_sync(kFullMask, meta_at, i & 31);
+    outside = (outside & ~(1u << (i & 31))) | ((codes < 0 ? 1u : 0u) << (i & 31));
+    if (codes >= 0) {
+      const uint8_t* k = cache + codes + 16 * lane;
+      const uint8_t* v = k + v_from_k;
+      const uint32_t to = ring + i % kStages * S::kStage;
+#pragma unroll
+      for (int f = 0; f < S::kCodes / 512; ++f) {
+        copy16(to + place[f], k + 512 * f);
+        copy16(to + S::kCodes + place[f], v + 512 * f);
+      }
+      if (meta_mine)
+        copy16(to + 2 * S::kCodes + (meta_v ? S::kMeta : 0) + meta_from,
+               cache + meta + (meta_v ? v_from_k : 0) + meta_from);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
 
   // ---- Q fragments --------------------------------------------------------------------
-  // step s of group j: dims 64 j + 16 t + 2 s + {0, 1} and those 8 further, rows g, g + 8
-  uint32_t qf[D / 16][4];
-  float qsum[2][GROUPS];
+  // row 8 n + g; step s of group j: dims 64 j + 16 t + 2 s + {0, 1} and those 8 further
+  uint32_t qf[NT][D / 16][2];
+  float qsum[NT][GROUPS][2];  // of rows 8 n + 2 t and the next
+  int sees[NT][2];            // .. and the keys they see
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = g + 8 * i;
+  for (int n = 0; n < NT; ++n) {
+    const int r = 8 * n + g;
     const int u = (row0 + r) / p.group;
     const __nv_bfloat16* src =
         p.q + (t0 + u) * p.q_stride + (int64_t)(kv_head * p.group + row0 + r - u * p.group) * D;
@@ -180,237 +278,233 @@ attn4_kernel(const Attn4Params p) {
       float sum = 0.f;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        qf[4 * j + s][i] = x[s];
-        qf[4 * j + s][2 + i] = y[s];
+        qf[n][4 * j + s][0] = x[s];
+        qf[n][4 * j + s][1] = y[s];
         sum += (low(x[s]) + high(x[s])) + (low(y[s]) + high(y[s]));
       }
       sum += __shfl_xor_sync(kFullMask, sum, 1);
       sum += __shfl_xor_sync(kFullMask, sum, 2);
-      qsum[i][j] = sum;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        qsum[n][j][c] = __shfl_sync(kFullMask, sum, 4 * (2 * t + c));
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) sees[n][c] = __shfl_sync(kFullMask, len, 8 * n + 2 * t + c);
+  }
+
+  const uint32_t sixteen = kv4::sixteen_pair();
+  // tile 4 j + e of O^T: its row g is dim 64 j + 8 g + 2 e, row g + 8 the next; columns 2 t
+  // and 2 t + 1 are those rows of Q
+  float o[NT][D / 16][4];
+  float zeros[NT][GROUPS][2];  // sum of P z over this lane's keys
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      m[n][c] = -INFINITY, l[n][c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < GROUPS; ++j) zeros[n][j][c] = 0.f;
     }
   }
 
-  // ---- which keys: of the request's groups of 16 an equal share ------------------------
-  const int parts = p.cluster * p.splits;
-  const int all_steps = most / kStep + (most % kStep != 0);
-  const int share = (int)(((int64_t)all_steps + parts - 1) / parts);
-  const int64_t begin = (int64_t)share * (blockIdx.y * p.cluster + rank);
-  const int first = (int)min(begin, (int64_t)all_steps) + warp;
-  const int last = (int)min(begin + share, (int64_t)all_steps);
-  const int steps = first < last ? (last - first + kWarps - 1) / kWarps : 0;
-  const int* table = p.table + (int64_t)req * p.table_width;
-  const int64_t head_block = (int64_t)p.page_size * kv4::row_bytes(D);
-  const uint32_t ring = tma::smem_addr(smem) + warp * S::kRing;
+  // A step of 16 keys; all: every row sees every one of them.
+  auto step = [&](int i, auto all_seen) {
+    constexpr bool ALL = decltype(all_seen)::value;
+    const uint8_t* kc = smem + warp * S::kWarp + i % kStages * S::kStage;
+    const uint8_t* vc = kc + S::kCodes;
+    const uint32_t* km = reinterpret_cast<const uint32_t*>(vc + S::kCodes);
+    const uint32_t* vm = km + kStep * GROUPS;
+    const int key0 = (first + i * kWarps) * kStep;
 
-  // The pages of 32 steps at a time, one a lane, looked up a window ahead: page (-1:
-  // outside the cache) and the step's first key in it.
-  int page = 0, off = 0, next_page, next_off;
-  auto look_up = [&](int i, int* page, int* off) {
-    *page = -1, *off = 0;
-    if (i >= steps) return;
-    const uint32_t key = (uint32_t)(first + i * kWarps) * kStep;
-    const uint32_t at = p.page_shift >= 0 ? key >> p.page_shift : key / (uint32_t)p.page_size;
-    *off = (int)(key - at * (uint32_t)p.page_size);
-    const int id = __ldg(table + at);
-    if (id >= 0 && id < p.num_pages) *page = id;
-    else rejected = true;
-  };
-  look_up(lane, &next_page, &next_off);
-  uint32_t outside = 0;  // of the last 32 steps issued: bit i % 32, the page is not there
-
-  auto issue = [&](int i) {
-    if ((i & 31) == 0) {
-      page = next_page, off = next_off;
-      look_up(i + 32 + lane, &next_page, &next_off);
-    }
-    const int id = __shfl_sync(kFullMask, page, i & 31);
-    const int key = __shfl_sync(kFullMask, off, i & 31);
-    outside = (outside & ~(1u << (i & 31))) | ((id < 0 ? 1u : 0u) << (i & 31));
-    if (i < steps && id >= 0) {
-      const uint8_t* k = p.cache + ((int64_t)id * 2 * p.num_kv + kv_head) * head_block;
-      const uint8_t* v = k + p.num_kv * head_block;
-      const int64_t codes = (int64_t)key * (D / 2);
-      const int64_t meta = (int64_t)p.page_size * (D / 2) + key * (GROUPS * 4);
-      const uint32_t to = ring + i % kStages * S::kStage;
+    // ---- S^T: keys g and g + 8 (of key_of), rows 2 t and 2 t + 1 ---------------------------
+    float s[NT][4];
 #pragma unroll
-      for (int f = lane; f < S::kCodes / 16; f += 32) {
-        const uint32_t at = piece_at<GROUPS>((f >> 1) / GROUPS, (f >> 1) % GROUPS) + ((f & 1) << 4);
-        copy16(to + at, k + codes + 16 * f);
-        copy16(to + S::kCodes + at, v + codes + 16 * f);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+      uint2 w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[h] = *reinterpret_cast<const uint2*>(kc + piece_at<GROUPS>(key_of(h, g), j) + 8 * t);
+      float raw[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[n][k] = -24.f * qsum[n][j][k & 1];
+      auto part = [&](auto index) {
+        constexpr int I = decltype(index)::value;
+        auto pair = [&](uint32_t w) { return kv4::pair16<I>(w, sixteen); };
+        const uint32_t a[4] = {pair(w[0].x), pair(w[1].x), pair(w[0].y), pair(w[1].y)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(raw[n], a, qf[n][4 * j + I][0], qf[n][4 * j + I][1]);
+      };
+      part(std::integral_constant<int, 0>());
+      part(std::integral_constant<int, 1>());
+      part(std::integral_constant<int, 2>());
+      part(std::integral_constant<int, 3>());
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t meta = km[key_of(h, g) * GROUPS + j];
+        const float sk = low(meta), zk = high(meta);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            s[n][2 * h + c] = fmaf(sk, raw[n][2 * h + c], fmaf(zk, qsum[n][j][c], s[n][2 * h + c]));
       }
-      const int f = lane & 15;
-      if (f < S::kMeta / 16)
-        copy16(to + 2 * S::kCodes + (lane >> 4) * S::kMeta + 16 * f,
-               (lane >> 4 ? v : k) + meta + 16 * f);
     }
-    copy_commit();
+
+    // ---- softmax, in units of log2 ----------------------------------------------------------
+    bool moved = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float& x = s[n][2 * h + c];
+          x *= p.scale_log2;
+          if (!ALL && key0 + key_of(h, g) >= sees[n][c]) x = -INFINITY;
+        }
+        // (from -inf on every score exceeds it; -inf itself does not)
+        moved |= fmaxf(s[n][c], s[n][2 + c]) > m[n][c] + kRescaleAt;
+      }
+    if (__any_sync(kFullMask, moved)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = fmaxf(m[n][c], fmaxf(s[n][c], s[n][2 + c]));
+          top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 16));
+          // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
+          const float f = top == m[n][c] ? 1.f : ex2(m[n][c] - top);
+          m[n][c] = top;
+          l[n][c] *= f;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) o[n][k][c] *= f, o[n][k][2 + c] *= f;
+#pragma unroll
+          for (int j = 0; j < GROUPS; ++j) zeros[n][j][c] *= f;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float ref = m[n][c] == -INFINITY ? 0.f : m[n][c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[n][2 * h + c] = ex2(s[n][2 * h + c] - ref);
+        l[n][c] += s[n][c] + s[n][2 + c];
+      }
+
+    // ---- O^T --------------------------------------------------------------------------------
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+      uint32_t b[NT][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t meta = vm[key_of(h, g) * GROUPS + j];
+        const float sv = low(meta), zv = high(meta);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float e[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            // (a key that a row does not see may hold anything)
+            const bool seen = ALL || key0 + key_of(h, g) < sees[n][c];
+            e[c] = seen ? s[n][2 * h + c] * sv : 0.f;
+            if (seen) zeros[n][j][c] = fmaf(s[n][2 * h + c], zv, zeros[n][j][c]);
+          }
+          b[n][h] = transposed(pack_bf16x2(e[0], e[1]));
+        }
+      }
+      uint32_t even[2], odd[2];  // codes of two keys each: dims 2 i, dims 2 i + 1 of the word
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        auto word = [&](int c) {
+          return *reinterpret_cast<const uint32_t*>(
+              vc + piece_at<GROUPS>(key_of(h, 2 * t + c), j) + 4 * g);
+        };
+        const uint32_t x = word(0), y = word(1);
+        even[h] = __byte_perm(x, y, 0x5410);
+        odd[h] = __byte_perm(x, y, 0x7632);
+      }
+      auto part = [&](auto index) {
+        constexpr int I = decltype(index)::value;
+        auto pair = [&](uint32_t w) { return kv4::pair16<I>(w, sixteen); };
+        const uint32_t a[4] = {less24(pair(even[0])), less24(pair(odd[0])),
+                               less24(pair(even[1])), less24(pair(odd[1]))};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(o[n][4 * j + I], a, b[n][0], b[n][1]);
+      };
+      part(std::integral_constant<int, 0>());
+      part(std::integral_constant<int, 1>());
+      part(std::integral_constant<int, 2>());
+      part(std::integral_constant<int, 3>());
+    }
   };
-
-  float o[D / 8][4];  // tile 8 j + e: dims 64 j + 8 n + e of its columns n
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[n][k] = 0.f;
-  float zeros[2][GROUPS] = {};  // sum of P z over this lane's keys
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
   for (int i = 0; i < steps; ++i) {
     issue(i + kStages - 1);
     copy_wait<kStages - 1>();
     __syncwarp();
     if (outside >> (i & 31) & 1) continue;  // (nothing was copied)
-    const uint32_t kc = ring + i % kStages * S::kStage, vc = kc + S::kCodes;
-    const uint32_t km = vc + S::kCodes, vm = km + S::kMeta;
-    const int key0 = (first + i * kWarps) * kStep;
-    const bool whole = key0 <= least - kStep;  // every row sees every key
-
-    // ---- S ------------------------------------------------------------------------------
-    float s[2][4] = {};
-#pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      float raw[2][4] = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 w = lds64(kc + piece_at<GROUPS>(key_of(h, g), j) + 8 * t);
-        mma16816(raw[h], qf[4 * j], kv4::pair16<0>(w.x), kv4::pair16<0>(w.y));
-        mma16816(raw[h], qf[4 * j + 1], kv4::pair16<1>(w.x), kv4::pair16<1>(w.y));
-        mma16816(raw[h], qf[4 * j + 2], kv4::pair16<2>(w.x), kv4::pair16<2>(w.y));
-        mma16816(raw[h], qf[4 * j + 3], kv4::pair16<3>(w.x), kv4::pair16<3>(w.y));
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t w = lds32(km + (key_of(h, 2 * t + c) * GROUPS + j) * 4);
-          const float sk = low(w), zk = fmaf(-24.f, sk, high(w));
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            s[h][2 * r + c] += fmaf(sk, raw[h][2 * r + c], zk * qsum[r][j]);
-        }
-    }
-
-    // ---- softmax: rows g (r = 0) and g + 8 ------------------------------------------------
-    bool seen[2][4];
-    float top[2] = {m[0], m[1]};
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        seen[h][k] = whole || key0 + key_of(h, 2 * t + (k & 1)) < sees[k >> 1];
-        s[h][k] = seen[h][k] ? s[h][k] * p.scale_log2 : -INFINITY;
-        top[k >> 1] = fmaxf(top[k >> 1], s[h][k]);
-      }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], 2));
-    }
-    if (__any_sync(kFullMask, top[0] != m[0] || top[1] != m[1])) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
-        const float f = top[r] == m[r] ? 1.f : exp2f(m[r] - top[r]);
-        l[r] *= f;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
-#pragma unroll
-        for (int j = 0; j < GROUPS; ++j) zeros[r][j] *= f;
-        m[r] = top[r];
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float ref = m[k >> 1] == -INFINITY ? 0.f : m[k >> 1];
-        s[h][k] = exp2f(s[h][k] - ref);
-        l[k >> 1] += s[h][k];
-      }
-
-    // ---- O --------------------------------------------------------------------------------
-#pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      float e[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t w = lds32(vm + (key_of(h, 2 * t + c) * GROUPS + j) * 4);
-          const float sv = low(w), zv = high(w);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int k = 2 * r + c;
-            // (a key that a row does not see may hold anything)
-            e[h][k] = seen[h][k] ? s[h][k] * sv : 0.f;
-            zeros[r][j] = seen[h][k] ? fmaf(s[h][k], zv, zeros[r][j]) : zeros[r][j];
-          }
-        }
-      const uint32_t pf[4] = {pack_bf16x2(e[0][0], e[0][1]), pack_bf16x2(e[0][2], e[0][3]),
-                              pack_bf16x2(e[1][0], e[1][1]), pack_bf16x2(e[1][2], e[1][3])};
-      uint32_t even[2], odd[2];  // codes of two keys each: dims 2 i, dims 2 i + 1 of the word
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t a = lds32(vc + piece_at<GROUPS>(key_of(h, 2 * t), j) + 4 * g);
-        const uint32_t b = lds32(vc + piece_at<GROUPS>(key_of(h, 2 * t + 1), j) + 4 * g);
-        even[h] = __byte_perm(a, b, 0x5410);
-        odd[h] = __byte_perm(a, b, 0x7632);
-      }
-      float(*to)[4] = o + 8 * j;
-      mma16816(to[0], pf, less24(kv4::pair16<0>(even[0])), less24(kv4::pair16<0>(even[1])));
-      mma16816(to[1], pf, less24(kv4::pair16<0>(odd[0])), less24(kv4::pair16<0>(odd[1])));
-      mma16816(to[2], pf, less24(kv4::pair16<1>(even[0])), less24(kv4::pair16<1>(even[1])));
-      mma16816(to[3], pf, less24(kv4::pair16<1>(odd[0])), less24(kv4::pair16<1>(odd[1])));
-      mma16816(to[4], pf, less24(kv4::pair16<2>(even[0])), less24(kv4::pair16<2>(even[1])));
-      mma16816(to[5], pf, less24(kv4::pair16<2>(odd[0])), less24(kv4::pair16<2>(odd[1])));
-      mma16816(to[6], pf, less24(kv4::pair16<3>(even[0])), less24(kv4::pair16<3>(even[1])));
-      mma16816(to[7], pf, less24(kv4::pair16<3>(odd[0])), less24(kv4::pair16<3>(odd[1])));
-    }
+    if ((first + i * kWarps) * kStep <= least - kStep) step(i, std::true_type());
+    else step(i, std::false_type());
     __syncwarp();  // the stage is read before its next copies start
   }
   copy_wait<0>();
   if (rejected && p.errors) atomicAdd(p.errors, 1);
+  auto all_keys = [](float x) {  // the sum over the lanes that hold the same rows
+    x += __shfl_xor_sync(kFullMask, x, 4);
+    x += __shfl_xor_sync(kFullMask, x, 8);
+    return x + __shfl_xor_sync(kFullMask, x, 16);
+  };
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(kFullMask, l[r], 1);
-    l[r] += __shfl_xor_sync(kFullMask, l[r], 2);
-    if (t == 0) state[warp * kRows + g + 8 * r] = make_float2(m[r], l[r]);
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      zeros[r][j] += __shfl_xor_sync(kFullMask, zeros[r][j], 1);
-      zeros[r][j] += __shfl_xor_sync(kFullMask, zeros[r][j], 2);
+    for (int c = 0; c < 2; ++c) {
+      l[n][c] = all_keys(l[n][c]);
+      if (g == 0) state[warp * kRows + 8 * n + 2 * t + c] = make_float2(m[n][c], l[n][c]);
+#pragma unroll
+      for (int j = 0; j < GROUPS; ++j) zeros[n][j][c] = all_keys(zeros[n][j][c]);
     }
-  }
   __syncthreads();
 
   // ---- join the warps ------------------------------------------------------------------
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = g + 8 * h;
-    float top = -INFINITY, sum = 0.f;
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, state[w * kRows + r].x);
-    const float ref = top == -INFINITY ? 0.f : top;
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * n + 2 * t + c;
+      float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      sum += state[w * kRows + r].y * exp2f(state[w * kRows + r].x - ref);
-    const float f = sum == 0.f ? 0.f : exp2f(m[h] - ref) / sum;  // 0: the row has no key
-    float* dst = reinterpret_cast<float*>(smem + warp * S::kRing) + r * S::kPad + 16 * t;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, state[w * kRows + r].x);
+      const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j)
+      for (int w = 0; w < kWarps; ++w)
+        sum += state[w * kRows + r].y * exp2f(state[w * kRows + r].x - ref);
+      const float f = sum == 0.f ? 0.f : exp2f(m[n][c] - ref) / sum;  // 0: the row has no key
+      float* dst = reinterpret_cast<float*>(smem + warp * S::kWarp) + r * S::kPad + 8 * g;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)  // dims 64 j + 16 t + 8 c + e
+      for (int j = 0; j < GROUPS; ++j) {
+        const float z = zeros[n][j][c];
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float z = zeros[h][j];
-          const int k = 2 * h + c;
-          *reinterpret_cast<float4*>(dst + 64 * j + 8 * c + e) = make_float4(
-              (o[8 * j + e][k] + z) * f, (o[8 * j + e + 1][k] + z) * f,
-              (o[8 * j + e + 2][k] + z) * f, (o[8 * j + e + 3][k] + z) * f);
+        for (int e = 0; e < 4; e += 2) {
+          const float *x = o[n][4 * j + e], *y = o[n][4 * j + e + 1];
+          *reinterpret_cast<float4*>(dst + 64 * j + 2 * e) = make_float4(
+              (x[c] + z) * f, (x[2 + c] + z) * f, (y[c] + z) * f, (y[2 + c] + z) * f);
         }
-    if (warp == 0 && t == 0) part_lse[r] = sum == 0.f ? -INFINITY : ref + log2f(sum);
-  }
+      }
+      if (warp == 0 && g == 0) part_lse[r] = sum == 0.f ? -INFINITY : ref + log2f(sum);
+    }
   __syncthreads();
   // the CTA's part: the sum of its warps', which are scaled to one reference
   const bool joined = p.cluster > 1;
@@ -419,7 +513,7 @@ attn4_kernel(const Attn4Params p) {
     float4 v = *reinterpret_cast<const float4*>(own_o + at);
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-      const float4 u = *reinterpret_cast<const float4*>(smem + w * S::kRing + 4 * at);
+      const float4 u = *reinterpret_cast<const float4*>(smem + w * S::kWarp + 4 * at);
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
     return v;
@@ -484,51 +578,65 @@ attn4_kernel(const Attn4Params p) {
 // ---- launch ------------------------------------------------------------------------------
 
 struct Spread4 {
+  int rows;  // of a tile: 8, 16 or 32
+  int tiles;
+  int64_t units;
   int cluster, splits;
+  int part_steps;
 };
 
 // CTAs are added while all of them are resident at once and each keeps at least
 // two steps for every warp: first within a cluster, joined in place; beyond that as
-// partials that a second launch joins.
-Spread4 spread4_for(int64_t units, int64_t keys, int head_dim) {
-  const int per_sm = head_dim == 256 ? 2 : 3;
-  Spread4 s = {1, 1};
-  while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 152 * per_sm &&
+// partials that a second launch joins.  Where there are more row tiles than that, a
+// long range is cut in parts of 2048 keys all the same: lengths differ, and the
+// last tiles of a wave would keep a few SMs busy alone.
+Spread4 spread4(int64_t num_tokens, int per_request, int num_heads_q, int num_heads_kv,
+                int head_dim, int page_size, int table_width) {
+  Spread4 s;
+  const int64_t rows = (int64_t)num_heads_q / num_heads_kv * per_request;
+  s.rows = rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
+  s.tiles = (int)((rows + s.rows - 1) / s.rows);
+  s.units = num_tokens / per_request * num_heads_kv * s.tiles;
+  const int64_t keys = (int64_t)table_width * page_size;
+  const int size = head_dim * (s.rows / 8);
+  const int64_t resident = 152 * (size <= 64 ? 5 : size <= 128 ? 4 : 2);
+  s.cluster = 1, s.part_steps = 0;
+  while (s.cluster < kMaxCluster && s.units * s.cluster * 2 <= resident &&
          keys >= (int64_t)s.cluster * 2 * 2 * kStep * kWarps)
     s.cluster *= 2;
-  while (units * s.cluster * (s.splits + 1) <= 152 * per_sm && keys > s.cluster * s.splits * 2048)
-    ++s.splits;
+  int64_t splits = 1;
+  if (s.units * s.cluster * 2 <= resident) {
+    while (s.units * s.cluster * (splits + 1) <= resident && keys > s.cluster * splits * 1024)
+      ++splits;
+  } else if (keys >= (int64_t)s.cluster * 4096) {
+    s.part_steps = 2048 / kStep;
+    splits = (keys + s.cluster * 2048 - 1) / (s.cluster * 2048);
+    if (splits > 65535) splits = 65535, s.part_steps = 0;
+  }
+  s.splits = (int)splits;
   return s;
 }
 
-int tiles4(int num_heads_q, int num_heads_kv, int per_request) {
-  return (int)(((int64_t)num_heads_q / num_heads_kv * per_request + kRows - 1) / kRows);
-}
-
-Spread4 spread4(int64_t num_tokens, int per_request, int num_heads_q, int num_heads_kv,
-                int head_dim, int page_size, int table_width) {
-  const int64_t units = num_tokens / per_request * num_heads_kv *
-                        tiles4(num_heads_q, num_heads_kv, per_request);
-  return spread4_for(units, (int64_t)table_width * page_size, head_dim);
-}
-
-template <int D>
+template <int D, int NT>
 cudaError_t launch4(Attn4Params p, int64_t units, cudaStream_t stream) {
+  using S = Shape4<D, NT>;
   static std::atomic<int> cache[kMaxDevices];
   int per_sm = 0;
   const cudaError_t e =
-      tma::prepare(attn4_kernel<D>, kWarps * 32, Shape4<D>::kSmem, cache, &per_sm);
+      tma::prepare(attn4_kernel<D, NT>, kWarps * 32, S::kSmem, cache, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t ctas = units * p.cluster, wave = (int64_t)per_sm * device_sm_count();
   p.trigger_from = ctas > wave ? (int)(ctas - wave) : 0;
-  return launch_clusters(attn4_kernel<D>, dim3((unsigned)ctas, (unsigned)p.splits),
-                         dim3(kWarps * 32), Shape4<D>::kSmem, p.cluster, stream, p);
+  return launch_clusters(attn4_kernel<D, NT>, dim3((unsigned)ctas, (unsigned)p.splits),
+                         dim3(kWarps * 32), S::kSmem, p.cluster, stream, p);
 }
 
 }  // namespace
 
 int64_t kv4_attn_units(int64_t num_tokens, int per_request, int num_heads_q, int num_heads_kv) {
-  return num_tokens / per_request * num_heads_kv * tiles4(num_heads_q, num_heads_kv, per_request);
+  // (the smallest tiles there are)
+  const int64_t rows = (int64_t)num_heads_q / num_heads_kv * per_request;
+  return num_tokens / per_request * num_heads_kv * ((rows + 7) / 8);
 }
 
 int64_t kv4_attn_workspace(int64_t num_tokens, int per_request, int num_heads_q,
@@ -540,6 +648,8 @@ int64_t kv4_attn_workspace(int64_t num_tokens, int per_request, int num_heads_q,
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
   const PagedQuery& x = a.x;
+  const Spread4 s = spread4(x.num_tokens, a.per_request, x.num_heads_q, x.num_heads_kv,
+                            x.head_dim, x.page_size, x.table_width);
   Attn4Params p = {};
   p.q = static_cast<const __nv_bfloat16*>(x.q);
   p.q_stride = x.q_stride;
@@ -548,30 +658,33 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
   p.num_kv = x.num_heads_kv;
   p.group = x.num_heads_q / x.num_heads_kv;
   p.per_request = a.per_request;
-  p.tiles = tiles4(x.num_heads_q, x.num_heads_kv, a.per_request);
+  p.tiles = s.tiles;
   p.num_pages = x.num_pages;
   p.page_size = x.page_size;
   p.page_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (x.page_size == 1 << s) p.page_shift = s;
+  for (int k = 0; k < 31; ++k)
+    if (x.page_size == 1 << k) p.page_shift = k;
   p.table = x.page_table;
   p.table_width = x.table_width;
   p.lens = x.lens;
   p.scale_log2 = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.errors = x.errors;
-  const Spread4 s = spread4(x.num_tokens, a.per_request, x.num_heads_q, x.num_heads_kv,
-                            x.head_dim, x.page_size, x.table_width);
   p.cluster = s.cluster;
   p.splits = s.splits;
+  p.part_steps = s.part_steps;
   if (s.splits > 1)
     p.parts = partials_at(a.workspace, s.splits, (int64_t)x.num_tokens * x.num_heads_q, x.head_dim);
-  const int64_t units = kv4_attn_units(x.num_tokens, a.per_request, x.num_heads_q, x.num_heads_kv);
   cudaError_t e = cudaErrorInvalidValue;
-  switch (x.head_dim) {
-    case 64: e = launch4<64>(p, units, stream); break;
-    case 128: e = launch4<128>(p, units, stream); break;
-    case 256: e = launch4<256>(p, units, stream); break;
+  switch (x.head_dim + s.rows) {
+    case 64 + 8: e = launch4<64, 1>(p, s.units, stream); break;
+    case 64 + 16: e = launch4<64, 2>(p, s.units, stream); break;
+    case 64 + 32: e = launch4<64, 4>(p, s.units, stream); break;
+    case 128 + 8: e = launch4<128, 1>(p, s.units, stream); break;
+    case 128 + 16: e = launch4<128, 2>(p, s.units, stream); break;
+    case 128 + 32: e = launch4<128, 4>(p, s.units, stream); break;
+    case 256 + 8: e = launch4<256, 1>(p, s.units, stream); break;
+    case 256 + 16: e = launch4<256, 2>(p, s.units, stream); break;
   }
   if (e != cudaSuccess || s.splits == 1) return e;
   return launch_attn_join(p.parts, s.splits, x.head_dim, a.out, stream);
