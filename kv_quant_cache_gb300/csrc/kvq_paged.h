@@ -148,6 +148,7 @@ extern const int kPrefixNumConfigs;
 int set_prefix_config(int id);  // -1: by the sizes; returns the previous one
 int prefix_config();
 uint32_t set_tile_wait_limit(uint32_t polls);  // kvq_set_tile_wait_limit
+uint32_t tile_wait_limit();
 
 // Bytes of workspace the two attentions need (0: none).
 // Depends on the sizes (and a forced configuration) alone, so that it can be

@@ -927,7 +927,6 @@ cudaError_t launch_attn_join(const Partials& parts, int slots, int head_dim, voi
     case 64: return launch_join<64>(p, stream);
     case 128: return launch_join<128>(p, stream);
     case 256: return launch_join<256>(p, stream);
-    case 512: return launch_join<512>(p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -729,7 +729,7 @@ cudaError_t launch(const PrefixAttnArgs& a, const CUtensorMap& map, const Partia
   p.slots = plan.parts;
   p.parts = parts;
   p.errors = x.errors;
-  p.wait_polls = g_tile_wait_limit.load(std::memory_order_relaxed);
+  p.wait_polls = tile_wait_limit();
   return launch_kernel(prefix_tiles_kernel<D>, dim3((unsigned)(plan.lanes * plan.teams)),
                        dim3(L::kThreads), L::kSmem, stream, p);
 }
@@ -747,6 +747,7 @@ int set_prefix_config(int id) { return g_prefix_config.exchange(id, std::memory_
 uint32_t set_tile_wait_limit(uint32_t polls) {
   return g_tile_wait_limit.exchange(polls, std::memory_order_relaxed);
 }
+uint32_t tile_wait_limit() { return g_tile_wait_limit.load(std::memory_order_relaxed); }
 int prefix_config() { return g_prefix_config.load(std::memory_order_relaxed); }
 
 // Sizes the tiles can take, and where they pay.  Up to 16 rows of a kv head are

@@ -108,6 +108,39 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&r)[16]) {
       : "memory");
 }
 
+// 32 lanes x 16 (8) columns, as ld32.
+__device__ __forceinline__ void ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void ld8(uint32_t (&r)[8], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+// By the number of columns.
+__device__ __forceinline__ void ld(uint32_t (&r)[32], uint32_t addr) { ld32(r, addr); }
+__device__ __forceinline__ void ld(uint32_t (&r)[16], uint32_t addr) { ld16(r, addr); }
+__device__ __forceinline__ void ld(uint32_t (&r)[8], uint32_t addr) { ld8(r, addr); }
+__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[32]) { st32(addr, r); }
+__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[16]) { st16(addr, r); }
+__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[8]) { st8(addr, r); }
+
 // ---- descriptors -----------------------------------------------------------------
 // Shared-memory matrix of 128-byte rows with the 128-byte swizzle, base
 // 1024-byte aligned.  Groups of 8 rows are 1024 bytes apart.  Where the rows
@@ -125,9 +158,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t block) {
 }
 
 // bf16 x bf16 -> fp32, M = 128; k_rows_b: the second operand's rows run along
-// the inner dimension.
-__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool k_rows_b) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((k_rows_b ? 1u : 0u) << 16) |
+// the inner dimension (k_rows_a: the first's).
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool k_rows_b,
+                                                         bool k_rows_a = false) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((k_rows_a ? 1u : 0u) << 15) |
+         ((k_rows_b ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
