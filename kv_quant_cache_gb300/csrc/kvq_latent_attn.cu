@@ -12,12 +12,13 @@
 // Warps have one role each:
 //   * warps 0-7: the softmax.  A thread has one entry (its tensor-memory lane) and half
 //     of the heads.  The reference of a head moves only when a score exceeds it by
-//     more than 2^8, so that the exchange of maxima between lanes, and the
+//     more than 2^30, so that the exchange of maxima between lanes, and the
 //     rescaling of O^T, are rare; weights go to shared memory as rows of heads;
-//   * warps 8-15: read entries (8 bytes a lane, a whole tile ahead in registers) and
-//     decode them, a quarter of the dims at a time: as soon as the second product of the
-//     tile before is done with a quarter, the next tile's takes its place;
-//   * warp 16: issues the matrix instructions.
+//   * warps 8-23: read entries (8 bytes a lane, a whole tile ahead in registers) and
+//     decode them, four warps to a quarter of the dims: as soon as the second product
+//     of the tile before is done with a quarter, the next tile's takes its place;
+//   * warp 24: issues the matrix instructions;
+//   * warp 25: looks the lists up, up to four tiles ahead.
 //
 // With few units a CTA to an SM takes an equal share of all tiles of all lists, from
 // the lists' actual lengths; a unit that falls to several CTAs goes to partials,
@@ -34,16 +35,16 @@ namespace {
 constexpr int kDim = dsv4::kDim;
 constexpr int kKeys = 128;          // entries of a tile
 constexpr int kQuarters = 4;        // of the dims
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // (three warps of that group have no work)
-// Registers of the softmax, loading and other warps: of the 96 each that a CTA of 20
-// warps is launched with.
-constexpr int kSoftmaxRegs = 104, kLoadRegs = 120, kOtherRegs = 32;
-static_assert(2 * kSoftmaxRegs + 2 * kLoadRegs + kOtherRegs <= 5 * 96, "registers of an SM's part");
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 16;
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps, kListWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // (two warps of that group have no work)
+constexpr int kAhead = 4;  // tiles whose slots are in shared memory
+// (28 warps of 72 registers each.  A softmax warp reads its scores twice, half of its
+// heads at a time, to make do with them.)
 constexpr int kSharedUnits = 4 * 152;  // up to so many units the tiles are shared out
 constexpr int kCtas = 152;             // .. to so many CTAs
-constexpr float kRescaleAt = 8.f;      // log2 by which a score may exceed the reference
+// log2 by which a score may exceed its reference: weights are as exact above 1 as below
+constexpr float kRescaleAt = 30.f;
 
 struct LatentParams {
   const __nv_bfloat16* q;
@@ -65,8 +66,8 @@ struct LatentParams {
 };
 
 // mbarriers, by index
-enum { kXFull = 0, kXEmpty = 4, kQFull = 8, kSFull = 9, kPFull = 10, kODone = 11, kDrain = 12,
-       kBarriers = 13 };
+enum { kXFull = 0, kXEmpty = 4, kListFull = 8, kListEmpty = 12, kQFull = 16, kSFull = 17,
+       kPFull = 18, kODone = 19, kDrain = 20, kBarriers = 21 };
 
 template <int NH>
 struct Layout {
@@ -76,10 +77,11 @@ struct Layout {
   static constexpr int kQChunk = NH * 128;              // 64 dims of Q
   static constexpr int kQ = kP + kChunk;
   static constexpr int kTops = kQ + 8 * kQChunk;        // [4 quadrants of lanes][NH]
-  static constexpr int kRef = kTops + 4 * 64 * 4;       // [NH] references
-  static constexpr int kStart = kRef + 64 * 4;          // [tokens + 1] first tiles
-  static constexpr int kBars = kStart + (kSharedUnits + 8) * 4;
-  static constexpr int kEnd = kBars + 16 * 8 + 32;
+  static constexpr int kRef = kTops + 4 * 64 * 4;       // [NH] references, [NH] factors
+  static constexpr int kStart = kRef + 2 * 64 * 4;      // [tokens + 1] first tiles
+  static constexpr int kLists = kStart + (kSharedUnits + 8) * 4;  // [kAhead][128] slots
+  static constexpr int kBars = kLists + kAhead * kKeys * 4;
+  static constexpr int kEnd = kBars + 24 * 8 + 48;
   static constexpr int kSmem = kEnd + 1024;             // room to align the base
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -128,6 +130,28 @@ __device__ __forceinline__ float columns(float (&v)[N], int lane, Op op) {
     }
   }
   return v[0];
+}
+
+// Eight e4m3 codes, none of them NaN, times 2^(byte - 127), byte up to 134, as bf16.
+// Sign and magnitude are put where a bf16 has them, with the exponent's bias short by
+// 120: one product mends that and applies the scale, subnormal codes included.
+__device__ __forceinline__ uint4 decode8(const uint2& codes, uint32_t byte) {
+  const uint32_t pair = byte * 0x00800080u + 0x3c003c00u;  // 2^(byte - 7), twice
+  const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&pair);
+  auto two = [&](uint32_t word, uint32_t which) {
+    uint32_t x;  // (code, its sign bit eight times), twice
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(word), "r"(which));
+    x = (x << 4) & 0x87f087f0u;
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), scale);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  };
+  return make_uint4(two(codes.x, 0x9180), two(codes.x, 0xb3a2), two(codes.y, 0x9180),
+                    two(codes.y, 0xb3a2));
+}
+
+__device__ __forceinline__ bool has_nan(const uint2& codes) {  // a magnitude of 127
+  const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
+  return ((((codes.x & m) + one) | ((codes.y & m) + one)) & 0x80808080u) != 0;
 }
 
 // How many entries of its list a token has; a length outside the list is cut.
@@ -207,12 +231,15 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
   uint8_t* smem = raw + (base - tma::smem_addr(raw));
   volatile float* tops = reinterpret_cast<float*>(smem + L::kTops);
   float* refs = reinterpret_cast<float*>(smem + L::kRef);
+  float* moves = refs + 64;  // factors of the heads
   int* start = reinterpret_cast<int*>(smem + L::kStart);
   const uint32_t bars = base + L::kBars;
-  int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 16 * 8);
+  volatile int* lists = reinterpret_cast<int*>(smem + L::kLists);
+  int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 24 * 8);
   volatile int* dead = shared_state;      // a wait ran out
   volatile int* quit = shared_state + 1;  // .. of a softmax warp
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shared_state + 2);
+  volatile int* place = shared_state + 4;  // [kAhead] of a tile in its segment: first 1, last 2
   auto bar = [&](int i) { return bars + 8u * i; };
   auto await = [&](int i, uint32_t parity) {
     return tc::wait_warp(bar(i), parity, dead, p.wait_polls);
@@ -221,7 +248,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBarriers; ++i)
-      tma::mbar_init(bar(i), i < kXEmpty ? kLoadWarps
+      tma::mbar_init(bar(i), i < kXEmpty ? kLoadWarps / kQuarters
+                             : i >= kListEmpty && i < kQFull ? kLoadWarps + kSoftmaxWarps + 1
                              : i == kQFull || i == kPFull ? kSoftmaxWarps : 1);
     tma::mbar_init_fence();
     *dead = *quit = 0;
@@ -260,172 +288,194 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
   const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
   const uint32_t s_tmem = tmem, o_tmem = tmem + 128;  // S^T; O^T, NH columns a quarter
   Segments seg(p, start);
+  // tiles of the CTA, and the barrier phase of the list of tile i
+  int left = (int)(seg.stop - seg.at);
+  if (!p.shared_out) left = list_tiles(list_len(p, __ldg(p.lens + blockIdx.x / p.blocks)));
+  auto list_phase = [](uint32_t i) { return i / kAhead & 1; };
 
   if (warp < kSoftmaxWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ---------------------------------------------------------------------
     const int quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;  // the thread's entry of a tile
     const uint32_t lanes = (uint32_t)quad << 21;
     const int col0 = half * COLS;  // .. and its first head
     uint32_t done = 0, segs = 0;  // phases of the barriers
-    bool ok = true, rejected = false;
+    bool ok = true;
     while (ok && seg.next(p, start)) {
       const int head0 = seg.block * NH, rows = min(NH, p.num_heads - head0);
       // Q, swizzled; the products that read the last segment's are done
-      for (int i = threadIdx.x; i < NH * 64; i += 32 * kSoftmaxWarps) {
-        const int h = i >> 6, c = i & 63;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (h < rows)
-          v = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)seg.token * p.q_stride +
-                                                   (int64_t)(head0 + h) * kDim) + c);
-        *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * L::kQChunk + h * 128 +
-                                  (((c & 7) ^ (h & 7)) << 4)) = v;
+      const __nv_bfloat16* q = p.q + (int64_t)seg.token * p.q_stride + (int64_t)head0 * kDim;
+      constexpr int FLIGHT = 8;  // loads of a thread at a time
+#pragma unroll 1
+      for (int i0 = threadIdx.x; i0 < NH * 64; i0 += FLIGHT * 32 * kSoftmaxWarps) {
+        uint4 v[FLIGHT];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+          const int i = i0 + u * 32 * kSoftmaxWarps;
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (i >> 6 < rows) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        }
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+          const int i = i0 + u * 32 * kSoftmaxWarps, h = i >> 6, c = i & 63;
+          if (h < NH)
+            *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * L::kQChunk + h * 128 +
+                                      (((c & 7) ^ (h & 7)) << 4)) = v[u];
+        }
       }
       tma::fence_proxy_async();
-      if (threadIdx.x < NH) refs[threadIdx.x] = -INFINITY;
+      if (threadIdx.x < NH) refs[threadIdx.x] = 0.f;
       softmax_sync();
       if (lane == 0) tc::mbar_arrive(bar(kQFull));
 
-      const int* list = p.slots + (int64_t)seg.token * p.list_width;
-      auto listed = [&](int tile) {  // the thread's slot of a tile, -1: none
-        const int at = tile * kKeys + r;
-        return at < seg.len ? __ldg(list + at) : -1;
-      };
-      int slot = listed(seg.first);
+      bool fresh = true;  // no entry so far: the references mean nothing
       float l[COLS];
 #pragma unroll
       for (int c = 0; c < COLS; ++c) l[c] = 0.f;
       for (int j = 0; j < seg.n; ++j, ++done) {
-        const bool there = slot >= 0 && slot < p.num_slots;
-        rejected |= !there && slot != -1;
-        if (j + 1 < seg.n) slot = listed(seg.first + j + 1);
-        const bool ready = p.wait_polls != 0 && await(kSFull, done & 1);
+        const bool ready = p.wait_polls != 0 && await(kListFull + done % kAhead, list_phase(done)) &&
+                           await(kSFull, done & 1);
         if (!ready) *dead = *quit = 1;
-        bool moved = !ready;
-        float x[COLS];
-        auto scores = [&]() {  // in units of log2
-          uint32_t s[COLS];
-          tc::ld(s, s_tmem + lanes + col0);
+        const bool there = ready && lists[done % kAhead * kKeys + r] >= 0;
+        // scores in units of log2, less their heads' references; PART heads at a time
+        constexpr int PART = COLS < 16 ? COLS : 16;
+        const float none = there ? 0.f : -INFINITY;
+        auto scores = [&](int c0, float (&x)[PART]) {
+          uint32_t s[PART];
+          tc::ld(s, s_tmem + lanes + col0 + c0);
           tc::wait_ld();
 #pragma unroll
-          for (int c = 0; c < COLS; ++c)
-            x[c] = there ? __uint_as_float(s[c]) * p.scale_log2 : -INFINITY;
+          for (int c = 0; c < PART; c += 4) {
+            const float4 ref = *reinterpret_cast<const float4*>(refs + col0 + c0 + c);
+            x[c] = fmaf(__uint_as_float(s[c]), p.scale_log2, none - ref.x);
+            x[c + 1] = fmaf(__uint_as_float(s[c + 1]), p.scale_log2, none - ref.y);
+            x[c + 2] = fmaf(__uint_as_float(s[c + 2]), p.scale_log2, none - ref.z);
+            x[c + 3] = fmaf(__uint_as_float(s[c + 3]), p.scale_log2, none - ref.w);
+          }
         };
+        bool moved = !ready || (fresh && there);
         if (ready) {
           tc::fence_after();
-          scores();
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) moved |= x[c] > refs[col0 + c] + kRescaleAt;
+          for (int c0 = 0; c0 < COLS; c0 += PART) {
+            float x[PART], top = -INFINITY;
+            scores(c0, x);
+#pragma unroll
+            for (int c = 0; c < PART; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
+            moved |= !fresh && top > kRescaleAt;
+          }
         }
         if (softmax_vote(moved)) {  // rare
           if (*quit) {
             ok = false;
             break;
           }
-          const float mine = columns(x, lane, [](float a, float b) { return fmaxf(a, b); });
-          if (lane % (32 / COLS) == 0) tops[quad * 64 + col0 + lane / (32 / COLS)] = mine;
+#pragma unroll
+          for (int c0 = 0; c0 < COLS; c0 += PART) {
+            float x[PART];
+            scores(c0, x);
+            const float mine = columns(x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (lane % (32 / PART) == 0) tops[quad * 64 + col0 + c0 + lane / (32 / PART)] = mine;
+          }
           softmax_sync();
+          if (threadIdx.x < NH) {  // how far each head's reference moves, and where to
+            float by = fresh ? -INFINITY : 0.f;
+            for (int k = 0; k < 4; ++k) by = fmaxf(by, tops[k * 64 + threadIdx.x]);
+            if (by == -INFINITY) by = 0.f;
+            moves[threadIdx.x] = fresh ? 0.f : ex2(-by);
+            refs[threadIdx.x] += by;
+          }
+          const bool rescale = !fresh;
+          fresh = false;
+          softmax_sync();
+          if (rescale) {
 #pragma unroll
-          for (int c0 = 0; c0 < COLS; c0 += 8) {
-            float f[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float old = refs[col0 + c0 + c];
-              float to = old;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) to = fmaxf(to, tops[k * 64 + col0 + c0 + c]);
-              f[c] = to == old ? 1.f : ex2(old - to);
-              l[c0 + c] *= f[c];
-            }
-            if (j == 0) continue;
+            for (int c = 0; c < COLS; ++c) l[c] *= moves[col0 + c];
             // O^T is at rest: the scores came after the products before them
 #pragma unroll 1
-            for (int k = 0; k < kQuarters; ++k) {
-              const uint32_t at = o_tmem + lanes + k * NH + col0 + c0;
+            for (int k = 0; k < kQuarters * COLS / 8; ++k) {
+              const int c0 = col0 + 8 * (k % (COLS / 8));
+              const uint32_t at = o_tmem + lanes + k / (COLS / 8) * NH + c0;
               uint32_t o[8];
               tc::ld8(o, at);
               tc::wait_ld();
 #pragma unroll
-              for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
+              for (int c = 0; c < 8; ++c)
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * moves[c0 + c]);
               tc::st8(at, o);
             }
+            tc::wait_st();
           }
-          tc::wait_st();
-          softmax_sync();
-          if (threadIdx.x < NH) {
-            float to = refs[threadIdx.x];
-            for (int k = 0; k < 4; ++k) to = fmaxf(to, tops[k * 64 + threadIdx.x]);
-            refs[threadIdx.x] = to;
-          }
-          softmax_sync();
-          scores();
         }
 #pragma unroll
-        for (int c0 = 0; c0 < COLS; c0 += 8) {
-          uint32_t w[4];
+        for (int c0 = 0; c0 < COLS; c0 += PART) {
+          float x[PART];
+          scores(c0, x);
 #pragma unroll
-          for (int c = c0; c < c0 + 8; c += 2) {
-            const float ra = refs[col0 + c], rb = refs[col0 + c + 1];
-            const float a = ex2(x[c] - (ra == -INFINITY ? 0.f : ra));
-            const float b = ex2(x[c + 1] - (rb == -INFINITY ? 0.f : rb));
-            l[c] += a, l[c + 1] += b;
-            w[(c - c0) >> 1] = pack_bf16x2(a, b);
+          for (int c1 = 0; c1 < PART; c1 += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int c = c1; c < c1 + 8; c += 2) {
+              const float a = ex2(x[c]), b = ex2(x[c + 1]);
+              l[c0 + c] += a, l[c0 + c + 1] += b;
+              w[(c - c1) >> 1] = pack_bf16x2(a, b);
+            }
+            *reinterpret_cast<uint4*>(smem + L::kP + r * 128 +
+                                      ((((col0 + c0 + c1) >> 3) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4*>(smem + L::kP + r * 128 +
-                                    ((((col0 + c0) >> 3) ^ (r & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
         }
         tma::fence_proxy_async();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(kPFull));
+        if (lane == 0) {
+          tc::mbar_arrive(bar(kPFull));
+          tc::mbar_arrive(bar(kListEmpty + done % kAhead));
+        }
       }
       // ---- the unit's output, or a partial -------------------------------------------------
+      const int slot_at = 2 * (int)blockIdx.x + (seg.count > 1);
       if (ok) {
-        const bool last = await(kODone, segs++ & 1);
-        if (!last) *dead = *quit = 1;
         const float mine = columns(l, lane, [](float a, float b) { return a + b; });
         if (lane % (32 / COLS) == 0) tops[quad * 64 + col0 + lane / (32 / COLS)] = mine;
+        if (!await(kODone, segs++ & 1)) *dead = *quit = 1;
         softmax_sync();
         ok = !*quit;
       }
       if (!ok) break;
       tc::fence_after();
-      const int slot_at = 2 * (int)blockIdx.x + (seg.count > 1);
-      float f[COLS];
-#pragma unroll
-      for (int c = 0; c < COLS; ++c) {
+      if (threadIdx.x < NH) {
         float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum += tops[k * 64 + col0 + c];
-        f[c] = sum == 0.f ? 0.f : 1.f / sum;  // 0: no entry
-        if (!seg.whole() && r == 0) {
-          const float ref = refs[col0 + c];
-          p.part_lse[slot_at * NH + col0 + c] =
-              sum == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) + log2f(sum);
-        }
+        for (int k = 0; k < 4; ++k) sum += tops[k * 64 + threadIdx.x];
+        moves[threadIdx.x] = sum == 0.f ? 0.f : 1.f / sum;  // 0: no entry
+        if (!seg.whole())
+          p.part_lse[slot_at * NH + threadIdx.x] =
+              sum == 0.f ? -INFINITY : refs[threadIdx.x] + log2f(sum);
       }
+      softmax_sync();
+      // (short loops: straight code that runs once a unit costs more to fetch than to run)
+      const bool whole = seg.whole();
+      const int64_t row0 = whole ? (int64_t)seg.token * p.num_heads + head0 : (int64_t)slot_at * NH;
 #pragma unroll 1
-      for (int k = 0; k < kQuarters; ++k) {
-        uint32_t o[COLS];
-        tc::ld(o, o_tmem + lanes + k * NH + col0);
+      for (int k = 0; k < kQuarters * COLS / 8; ++k) {
+        const int c0 = col0 + 8 * (k % (COLS / 8)), quarter = k / (COLS / 8);
+        uint32_t o[8];
+        tc::ld8(o, o_tmem + lanes + quarter * NH + c0);
         tc::wait_ld();
-        const int d = 128 * k + r;
+        const int64_t at = (row0 + c0) * kDim + 128 * quarter + r;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
-          const float v = __uint_as_float(o[c]) * f[c];
-          if (seg.whole()) {
-            if (col0 + c < rows)
-              p.out[((int64_t)seg.token * p.num_heads + head0 + col0 + c) * kDim + d] =
-                  __float2bfloat16_rn(v);
-          } else {
-            p.part_o[((int64_t)slot_at * NH + col0 + c) * kDim + d] = v;
-          }
+          for (int c = 0; c < 8; ++c)
+            if (c0 + c < rows)
+              p.out[at + c * kDim] = __float2bfloat16_rn(__uint_as_float(o[c]) * moves[c0 + c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            p.part_o[at + c * kDim] = __uint_as_float(o[c]) * moves[c0 + c];
         }
       }
       tc::fence_before();
-      softmax_sync();  // tops, refs and Q may be written again
+      softmax_sync();  // tops, moves, refs and Q may be written again
     }
     // Given up: what this segment and those still to come should have held is marked.
     if (!ok) {
@@ -442,146 +492,180 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         }
       } while (seg.next(p, start));
     }
-    if (rejected && half == 0 && p.errors) atomicAdd(p.errors, 1);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    // ---- entries: a quarter of the dims at a time -------------------------------------------
-    // The thread has fragment i (8 dims) of each quarter, of 8 entries 16 apart.
-    const int lw = warp - kSoftmaxWarps, i = lane & 15;
-    const int key0 = 2 * lw + (lane >> 4);
-    constexpr int N = kKeys / 16;
-    uint2 code[kQuarters][N], more[N];
-    uint32_t ex;  // four exponents of entry i / 2 of the thread's half warp
-    int slot[N];
-    Segments ahead = seg;
-    int ahead_j = 0;
-    bool any = ahead.next(p, start);
-    // the slots of the next tile that is to be read (-1: none)
-    auto slots_of_next = [&]() {
-#pragma unroll
-      for (int k = 0; k < N; ++k) slot[k] = -1;
-      if (!any) return;
-      const int* list = p.slots + (int64_t)ahead.token * p.list_width;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int at = (ahead.first + ahead_j) * kKeys + key0 + 16 * k;
-        if (at < ahead.len) slot[k] = __ldg(list + at);
-        if (slot[k] >= p.num_slots) slot[k] = -1;
-      }
-      if (++ahead_j == ahead.n) {
-        any = ahead.next(p, start);
-        ahead_j = 0;
-      }
+    // ---- entries: four warps to a quarter of the dims ------------------------------------
+    const int quarter = (warp - kSoftmaxWarps) >> 2;
+    // The thread has fragment i of the quarter (8 dims; of the last one four coded dims and
+    // four rotary ones) of 16 entries, 8 apart: the same place in the swizzle.
+    const int i = lane & 15, key0 = 2 * (warp & 3) + (lane >> 4);
+    constexpr int N = 16, STRIDE = kKeys / N;
+    // of entry i of the half warp's: its slot (-1: none) and the exponents of the quarter
+    int slot = -1;
+    uint32_t ex = 0;
+    auto next_slots = [&](uint32_t tile) {
+      slot = -1;
+      if (tile >= (uint32_t)left || !await(kListFull + tile % kAhead, list_phase(tile))) return;
+      slot = lists[tile % kAhead * kKeys + key0 + STRIDE * i];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kListEmpty + tile % kAhead));
     };
-    auto entry = [&](int k) { return p.cache + (int64_t)slot[k] * dsv4::kEntry; };
-    auto read = [&](int q) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        code[q][k] = make_uint2(0, 0);
-        if (q == 3) more[k] = make_uint2(0, 0);
-        if (slot[k] < 0) continue;
-        if (q < 3 || i < 8) {
-          code[q][k] = __ldg(reinterpret_cast<const uint2*>(entry(k) + 128 * q + 8 * i));
-        } else {
-          const uint2* rope =
-              reinterpret_cast<const uint2*>(entry(k) + dsv4::kRopeAt + 16 * (i - 8));
-          code[q][k] = __ldg(rope);
-          more[k] = __ldg(rope + 1);
-        }
-      }
-    };
+    auto slot_of = [&](int k) { return __shfl_sync(kFullMask, slot, (lane & 16) + k); };
     auto read_scales = [&]() {
-      int of = -1;
-#pragma unroll
-      for (int k = 0; k < N; ++k) of = i >> 1 == k ? slot[k] : of;
-      ex = of < 0 ? 0
-                  : __ldg(reinterpret_cast<const uint32_t*>(p.cache + (int64_t)of * dsv4::kEntry +
-                                                            dsv4::kScaleAt + 4 * (i & 1)));
+      ex = slot < 0 ? 0
+                    : __ldg(reinterpret_cast<const uint32_t*>(p.cache + (int64_t)slot * dsv4::kEntry +
+                                                              dsv4::kScaleAt + 4 * (quarter >> 1)));
     };
-    slots_of_next();
-#pragma unroll
-    for (int q = 0; q < kQuarters; ++q) read(q);
+    // bytes over 134, or a NaN code: the whole warp decodes the long way
+    auto large = [&]() { return (((ex & 0x7f7f7f7fu) + 0x79797979u) & ex & 0x80808080u) != 0; };
+    auto hand_over = [&]() {
+      tma::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kXFull + quarter));
+    };
+    next_slots(0);
     read_scales();
-    uint32_t tile = 0;
-    bool ok = true;
-    while (ok && seg.next(p, start)) {
-      for (int j = 0; ok && j < seg.n; ++j, ++tile) {
-        slots_of_next();
+    if (quarter < 3) {
+      uint8_t* x_at = smem + L::kX + (2 * quarter + (i >> 3)) * L::kChunk + key0 * 128 +
+                      (((i & 7) ^ (key0 & 7)) << 4);
+      const int shift = 16 * (quarter & 1) + (i & 8);  // of the fragment's exponent
+      uint2 code[N];
+      auto read = [&]() {
 #pragma unroll
-        for (int q = 0; q < kQuarters; ++q) {
-          if (tile > 0) ok = ok && await(kXEmpty + q, (tile - 1) & 1);
-          if (!ok) break;
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const int r = key0 + 16 * k;
-            const uint32_t four = __shfl_sync(kFullMask, ex, (lane & 16) + 2 * k + (q >> 1));
-            uint4 v;
-            if (q < 3 || i < 8) {
-              const uint32_t byte = four >> (16 * (q & 1) + (i & 8)) & 0xffu;
-              v = dsv4::dequant8(code[q][k], dsv4::ue8m0_scale(byte));
-            } else {
-              v = make_uint4(code[q][k].x, code[q][k].y, more[k].x, more[k].y);
-            }
-            *reinterpret_cast<uint4*>(smem + L::kX + (2 * q + (i >> 3)) * L::kChunk + r * 128 +
-                                      (((i & 7) ^ (r & 7)) << 4)) = v;
-          }
-          tma::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar(kXFull + q));
-          read(q);
+        for (int k = 0; k < N; ++k) {
+          const int of = slot_of(k);
+          const uint8_t* e = p.cache + (int64_t)of * dsv4::kEntry + 128 * quarter + 8 * i;
+          code[k] = make_uint2(0, 0);
+          if (of >= 0) code[k] = __ldg(reinterpret_cast<const uint2*>(e));
         }
+      };
+      read();
+      for (int tile = 0; tile < left; ++tile) {
+        next_slots(tile + 1);
+        bool odd = large();
+#pragma unroll
+        for (int k = 0; k < N; ++k) odd |= has_nan(code[k]);
+        odd = __any_sync(kFullMask, odd);
+        if (tile > 0 && !await(kXEmpty + quarter, (tile - 1) & 1)) break;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const uint32_t byte = __shfl_sync(kFullMask, ex, (lane & 16) + k) >> shift & 0xffu;
+          *reinterpret_cast<uint4*>(x_at + STRIDE * k * 128) =
+              odd ? dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte)) : decode8(code[k], byte);
+        }
+        hand_over();
         read_scales();
+        read();
+      }
+    } else {
+      uint8_t* x_at =
+          smem + L::kX + 6 * L::kChunk + key0 * 128 + (((i >> 1) ^ (key0 & 7)) << 4) + 8 * (i & 1);
+      uint32_t code[N];
+      uint2 rope[N];
+      auto read = [&]() {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int of = slot_of(k);
+          const uint8_t* e = p.cache + (int64_t)of * dsv4::kEntry;
+          code[k] = 0, rope[k] = make_uint2(0, 0);
+          if (of >= 0) {
+            code[k] = __ldg(reinterpret_cast<const uint32_t*>(e + 384 + 4 * i));
+            rope[k] = __ldg(reinterpret_cast<const uint2*>(e + dsv4::kRopeAt + 8 * i));
+          }
+        }
+      };
+      read();
+      for (int tile = 0; tile < left; ++tile) {
+        next_slots(tile + 1);
+        bool odd = large();
+#pragma unroll
+        for (int k = 0; k < N; ++k) odd |= has_nan(make_uint2(code[k], 0));
+        odd = __any_sync(kFullMask, odd);
+        if (tile > 0 && !await(kXEmpty + quarter, (tile - 1) & 1)) break;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const uint32_t byte = __shfl_sync(kFullMask, ex, (lane & 16) + k) >> 16 & 0xffu;
+          const uint2 codes = make_uint2(code[k], 0);
+          const uint4 v = odd ? dsv4::dequant8(codes, dsv4::ue8m0_scale(byte)) : decode8(codes, byte);
+          *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128) = make_uint2(v.x, v.y);
+          *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128 + L::kChunk) = rope[k];
+        }
+        hand_over();
+        read_scales();
+        read();
       }
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  }
-  if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp) {
     // ---- the matrix instructions -------------------------------------------------------
     constexpr uint32_t qk = tc::instr_desc(NH, false), pv = tc::instr_desc(NH, true, true);
     const uint64_t x_desc = tc::smem_desc(base + L::kX, 16);
     const uint64_t q_desc = tc::smem_desc(base + L::kQ, 16);
     const uint64_t xt_desc = tc::smem_desc(base + L::kX, L::kChunk);
     const uint64_t p_desc = tc::smem_desc(base + L::kP, L::kChunk);
-    uint32_t tile = 0, segs = 0;
+    uint32_t segs = 0;
     bool ok = true;
-    while (ok && seg.next(p, start)) {
-      ok = await(kQFull, segs & 1);
-      for (int j = 0; ok && j < seg.n; ++j, ++tile) {
-        for (int q = 0; ok && q < kQuarters; ++q) {
-          ok = await(kXFull + q, tile & 1);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t chunk = 2 * q + (k >> 2), off = (k & 3) * 32;
-            tc::mma_ss(s_tmem, x_desc + ((chunk * L::kChunk + off) >> 4),
-                       q_desc + ((chunk * L::kQChunk + off) >> 4), qk, q > 0 || k > 0);
-          }
-        }
-        if (!ok) break;
-        tc::commit(bar(kSFull));
-        ok = await(kPFull, tile & 1);
+    for (uint32_t tile = 0; ok && tile < (uint32_t)left; ++tile) {
+      ok = await(kListFull + tile % kAhead, list_phase(tile));
+      const int where = place[tile % kAhead];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kListEmpty + tile % kAhead));
+      if (where & 1) ok = ok && await(kQFull, segs++ & 1);
+#pragma unroll 1
+      for (int q = 0; ok && q < kQuarters; ++q) {
+        ok = await(kXFull + q, tile & 1);
         if (!ok) break;
         tc::fence_after();
-        for (int q = 0; q < kQuarters; ++q) {
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc::mma_ss(o_tmem + q * NH, xt_desc + ((2 * q * L::kChunk + k * 2048) >> 4),
-                       p_desc + (k * 2048 >> 4), pv, j > 0 || k > 0);
-          tc::commit(bar(kXEmpty + q));
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t chunk = 2 * q + (k >> 2), off = (k & 3) * 32;
+          tc::mma_ss(s_tmem, x_desc + ((chunk * L::kChunk + off) >> 4),
+                     q_desc + ((chunk * L::kQChunk + off) >> 4), qk, q > 0 || k > 0);
         }
       }
-      if (ok) {
-        tc::commit(bar(kODone));
-        ++segs;
+      if (!ok) break;
+      tc::commit(bar(kSFull));
+      ok = await(kPFull, tile & 1);
+      if (!ok) break;
+      tc::fence_after();
+#pragma unroll 1
+      for (int q = 0; q < kQuarters; ++q) {
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc::mma_ss(o_tmem + q * NH, xt_desc + ((2 * q * L::kChunk + k * 2048) >> 4),
+                     p_desc + (k * 2048 >> 4), pv, !(where & 1) || k > 0);
+        tc::commit(bar(kXEmpty + q));
       }
+      if (where & 2) tc::commit(bar(kODone));
     }
     if (!ok) {  // nothing may be in flight when the tensor memory goes
       tc::commit(bar(kDrain));
       tc::drain(bar(kDrain), 0);
       __syncwarp();
     }
+  } else if (warp == kListWarp) {
+    // ---- the lists ------------------------------------------------------------------------
+    bool ok = true, rejected = false;
+    uint32_t tile = 0;
+    while (ok && seg.next(p, start)) {
+      const int* list = p.slots + (int64_t)seg.token * p.list_width;
+      for (int j = 0; ok && j < seg.n; ++j, ++tile) {
+        int slot[kKeys / 32];
+#pragma unroll
+        for (int u = 0; u < kKeys / 32; ++u) {
+          const int at = (seg.first + j) * kKeys + 32 * u + lane;
+          slot[u] = at < seg.len ? __ldg(list + at) : -1;
+          if (slot[u] < -1 || slot[u] >= p.num_slots) rejected = true, slot[u] = -1;
+        }
+        if (tile >= kAhead) ok = await(kListEmpty + tile % kAhead, list_phase(tile - kAhead));
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < kKeys / 32; ++u)
+          lists[tile % kAhead * kKeys + 32 * u + lane] = slot[u];
+        if (lane == 0) place[tile % kAhead] = (j == 0 ? 1 : 0) | (j + 1 == seg.n ? 2 : 0);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(kListFull + tile % kAhead));
+      }
+    }
+    if (rejected && p.errors) atomicAdd(p.errors, 1);
   }
   tc::fence_before();
   __syncthreads();
@@ -645,17 +729,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Join
   constexpr int V = kDim / 32;  // dims of a lane, four at a time
   float acc[V] = {};
   float sum = 0.f;
-  for (int s = 0; s < parts; ++s) {
-    const float lse = p.x.part_lse[at(s)];
-    if (lse == -INFINITY) continue;  // a part without an entry
-    const float w = exp2f(lse - ref);
-    sum += w;
-    const float4* from = reinterpret_cast<const float4*>(p.x.part_o + at(s) * kDim) + lane;
+  constexpr int FLIGHT = 4;  // parts whose outputs are loaded together
+  for (int s0 = 0; s0 < parts; s0 += FLIGHT) {
+    float w[FLIGHT];
+    float4 v[FLIGHT][V / 4];
 #pragma unroll
-    for (int k = 0; k < V; k += 4) {
-      const float4 v = from[8 * k];
-      acc[k] = fmaf(w, v.x, acc[k]), acc[k + 1] = fmaf(w, v.y, acc[k + 1]);
-      acc[k + 2] = fmaf(w, v.z, acc[k + 2]), acc[k + 3] = fmaf(w, v.w, acc[k + 3]);
+    for (int u = 0; u < FLIGHT; ++u) {
+      w[u] = -INFINITY;
+      if (s0 + u >= parts) continue;
+      w[u] = p.x.part_lse[at(s0 + u)];
+      const float4* from = reinterpret_cast<const float4*>(p.x.part_o + at(s0 + u) * kDim) + lane;
+#pragma unroll
+      for (int k = 0; k < V / 4; ++k) v[u][k] = from[32 * k];
+    }
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      if (w[u] == -INFINITY) continue;  // a part without an entry
+      const float g = exp2f(w[u] - ref);
+      sum += g;
+#pragma unroll
+      for (int k = 0; k < V / 4; ++k) {
+        acc[4 * k] = fmaf(g, v[u][k].x, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(g, v[u][k].y, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(g, v[u][k].z, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(g, v[u][k].w, acc[4 * k + 3]);
+      }
     }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
