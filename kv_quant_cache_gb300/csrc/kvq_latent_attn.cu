@@ -132,16 +132,38 @@ __device__ __forceinline__ float columns(float (&v)[N], int lane, Op op) {
   return v[0];
 }
 
+// Multiplication and addition where a shift or a sum would do: those share a pipe of half
+// the rate with the logic below, this one does not.  (The factors come from registers
+// that the compiler does not know, or it would make shifts and sums of them.)
+struct Factors {
+  uint32_t one, sixteen;
+};
+__device__ __forceinline__ Factors factors() {
+  Factors f;
+  asm volatile("mov.b32 %0, 1;" : "=r"(f.one));
+  asm volatile("mov.b32 %0, 16;" : "=r"(f.sixteen));
+  return f;
+}
+__device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t which) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(a), "r"(which));
+  return d;
+}
+
 // Eight e4m3 codes, none of them NaN, times 2^(byte - 127), byte up to 134, as bf16.
 // Sign and magnitude are put where a bf16 has them, with the exponent's bias short by
 // 120: one product mends that and applies the scale, subnormal codes included.
-__device__ __forceinline__ uint4 decode8(const uint2& codes, uint32_t byte) {
-  const uint32_t pair = byte * 0x00800080u + 0x3c003c00u;  // 2^(byte - 7), twice
+__device__ __forceinline__ uint4 decode8(const uint2& codes, uint32_t byte, const Factors& f) {
+  const uint32_t pair = mad(byte, 0x00800080u, 0x3c003c00u);  // 2^(byte - 7), twice
   const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&pair);
   auto two = [&](uint32_t word, uint32_t which) {
-    uint32_t x;  // (code, its sign bit eight times), twice
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(word), "r"(which));
-    x = (x << 4) & 0x87f087f0u;
+    // (code, its sign bit eight times), twice
+    uint32_t x = mad(prmt(word, which), f.sixteen, 0) & 0x87f087f0u;
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), scale);
     return *reinterpret_cast<const uint32_t*>(&v);
   };
@@ -149,9 +171,10 @@ __device__ __forceinline__ uint4 decode8(const uint2& codes, uint32_t byte) {
                     two(codes.y, 0xb3a2));
 }
 
-__device__ __forceinline__ bool has_nan(const uint2& codes) {  // a magnitude of 127
-  const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
-  return ((((codes.x & m) + one) | ((codes.y & m) + one)) & 0x80808080u) != 0;
+// Collects in bits 7 of the bytes whether a code is NaN, a magnitude of 127: adding one
+// then changes its sign bit.  (Only behind a NaN may a carry reach the next byte.)
+__device__ __forceinline__ uint32_t nan_bits(uint32_t so_far, uint32_t codes, const Factors& f) {
+  return so_far | (mad(codes, f.one, 0x01010101u) ^ codes);
 }
 
 // How many entries of its list a token has; a length outside the list is cut.
@@ -342,6 +365,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         const float none = there ? 0.f : -INFINITY;
         auto scores = [&](int c0, float (&x)[PART]) {
           uint32_t s[PART];
+          __syncwarp();
           tc::ld(s, s_tmem + lanes + col0 + c0);
           tc::wait_ld();
 #pragma unroll
@@ -353,16 +377,36 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
             x[c + 3] = fmaf(__uint_as_float(s[c + 3]), p.scale_log2, none - ref.w);
           }
         };
+        // The weights of PART heads, added to (taken off) the sums and handed over; not
+        // those of a thread with a score far above its reference.
+        auto weigh = [&](int c0, float sign) {
+          float x[PART], top = -INFINITY;
+          scores(c0, x);
+#pragma unroll
+          for (int c = 0; c < PART; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
+          if (top > kRescaleAt) return true;
+#pragma unroll
+          for (int c1 = 0; c1 < PART; c1 += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int c = c1; c < c1 + 8; c += 2) {
+              const float a = ex2(x[c]), b = ex2(x[c + 1]);
+              l[c0 + c] = fmaf(a, sign, l[c0 + c]);
+              l[c0 + c + 1] = fmaf(b, sign, l[c0 + c + 1]);
+              w[(c - c1) >> 1] = pack_bf16x2(a, b);
+            }
+            *reinterpret_cast<uint4*>(smem + L::kP + r * 128 +
+                                      ((((col0 + c0 + c1) >> 3) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          return false;
+        };
         bool moved = !ready || (fresh && there);
         if (ready) {
           tc::fence_after();
+          if (!fresh) {
 #pragma unroll
-          for (int c0 = 0; c0 < COLS; c0 += PART) {
-            float x[PART], top = -INFINITY;
-            scores(c0, x);
-#pragma unroll
-            for (int c = 0; c < PART; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
-            moved |= !fresh && top > kRescaleAt;
+            for (int c0 = 0; c0 < COLS; c0 += PART) moved |= weigh(c0, 1.f);
           }
         }
         if (softmax_vote(moved)) {  // rare
@@ -372,6 +416,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           }
 #pragma unroll
           for (int c0 = 0; c0 < COLS; c0 += PART) {
+            // (what is lost in taking off what was added is lost against larger weights)
+            if (!fresh) weigh(c0, -1.f);
             float x[PART];
             scores(c0, x);
             const float mine = columns(x, lane, [](float a, float b) { return fmaxf(a, b); });
@@ -406,24 +452,11 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
             }
             tc::wait_st();
           }
-        }
 #pragma unroll
-        for (int c0 = 0; c0 < COLS; c0 += PART) {
-          float x[PART];
-          scores(c0, x);
-#pragma unroll
-          for (int c1 = 0; c1 < PART; c1 += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int c = c1; c < c1 + 8; c += 2) {
-              const float a = ex2(x[c]), b = ex2(x[c + 1]);
-              l[c0 + c] += a, l[c0 + c + 1] += b;
-              w[(c - c1) >> 1] = pack_bf16x2(a, b);
-            }
-            *reinterpret_cast<uint4*>(smem + L::kP + r * 128 +
-                                      ((((col0 + c0 + c1) >> 3) ^ (r & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int c0 = 0; c0 < COLS; c0 += PART) weigh(c0, 1.f);
+        } else if (fresh) {  // a tile without an entry: no weights
+          uint4* const row = reinterpret_cast<uint4*>(smem + L::kP + r * 128);
+          for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
         }
         tma::fence_proxy_async();
         tc::fence_before();
@@ -498,7 +531,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     // The thread has fragment i of the quarter (8 dims; of the last one four coded dims and
     // four rotary ones) of 16 entries, 8 apart: the same place in the swizzle.
     const int i = lane & 15, key0 = 2 * (warp & 3) + (lane >> 4);
-    constexpr int N = 16, STRIDE = kKeys / N;
+    // Half of them are decoded before their place is free, as far as registers go.
+    constexpr int N = 16, STRIDE = kKeys / N, EARLY = 8;
     // of entry i of the half warp's: its slot (-1: none) and the exponents of the quarter
     int slot = -1;
     uint32_t ex = 0;
@@ -516,7 +550,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
                                                               dsv4::kScaleAt + 4 * (quarter >> 1)));
     };
     // bytes over 134, or a NaN code: the whole warp decodes the long way
-    auto large = [&]() { return (((ex & 0x7f7f7f7fu) + 0x79797979u) & ex & 0x80808080u) != 0; };
+    auto large = [&]() { return ((ex & 0x7f7f7f7fu) + 0x79797979u) & ex; };
+    const Factors f = factors();
     auto hand_over = [&]() {
       tma::fence_proxy_async();
       __syncwarp();
@@ -527,7 +562,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     if (quarter < 3) {
       uint8_t* x_at = smem + L::kX + (2 * quarter + (i >> 3)) * L::kChunk + key0 * 128 +
                       (((i & 7) ^ (key0 & 7)) << 4);
-      const int shift = 16 * (quarter & 1) + (i & 8);  // of the fragment's exponent
+      const uint32_t which = 0x4440 + 2 * (quarter & 1) + (i >> 3);  // the fragment's exponent
       uint2 code[N];
       auto read = [&]() {
 #pragma unroll
@@ -541,16 +576,38 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       read();
       for (int tile = 0; tile < left; ++tile) {
         next_slots(tile + 1);
-        bool odd = large();
+        uint32_t strange = large();
 #pragma unroll
-        for (int k = 0; k < N; ++k) odd |= has_nan(code[k]);
-        odd = __any_sync(kFullMask, odd);
+        for (int k = 0; k < N; ++k)
+          strange = nan_bits(nan_bits(strange, code[k].x, f), code[k].y, f);
+        const bool odd = __any_sync(kFullMask, (strange & 0x80808080u) != 0);
+        auto byte_of = [&](int k) {
+          return prmt(__shfl_sync(kFullMask, ex, (lane & 16) + k), which);
+        };
+        // (two ways with a branch around each: with the choice made entry by entry both
+        // were gone for every one, and a quarter took 2850 cycles instead of 1100)
+        uint4 early[EARLY];
+        if (!odd) {
+#pragma unroll
+          for (int k = 0; k < EARLY; ++k) early[k] = decode8(code[k], byte_of(k), f);
+        } else {
+#pragma unroll
+          for (int k = 0; k < EARLY; ++k)
+            early[k] = dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte_of(k)));
+        }
         if (tile > 0 && !await(kXEmpty + quarter, (tile - 1) & 1)) break;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const uint32_t byte = __shfl_sync(kFullMask, ex, (lane & 16) + k) >> shift & 0xffu;
-          *reinterpret_cast<uint4*>(x_at + STRIDE * k * 128) =
-              odd ? dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte)) : decode8(code[k], byte);
+        for (int k = 0; k < EARLY; ++k)
+          *reinterpret_cast<uint4*>(x_at + STRIDE * k * 128) = early[k];
+        if (!odd) {
+#pragma unroll
+          for (int k = EARLY; k < N; ++k)
+            *reinterpret_cast<uint4*>(x_at + STRIDE * k * 128) = decode8(code[k], byte_of(k), f);
+        } else {
+#pragma unroll
+          for (int k = EARLY; k < N; ++k)
+            *reinterpret_cast<uint4*>(x_at + STRIDE * k * 128) =
+                dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte_of(k)));
         }
         hand_over();
         read_scales();
@@ -576,18 +633,42 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       read();
       for (int tile = 0; tile < left; ++tile) {
         next_slots(tile + 1);
-        bool odd = large();
+        uint32_t strange = large();
 #pragma unroll
-        for (int k = 0; k < N; ++k) odd |= has_nan(make_uint2(code[k], 0));
-        odd = __any_sync(kFullMask, odd);
+        for (int k = 0; k < N; ++k) strange = nan_bits(strange, code[k], f);
+        const bool odd = __any_sync(kFullMask, (strange & 0x80808080u) != 0);
+        auto byte_of = [&](int k) {
+          return prmt(__shfl_sync(kFullMask, ex, (lane & 16) + k), 0x4442);
+        };
+        auto decoded = [&](int k) {
+          const uint4 v = decode8(make_uint2(code[k], 0), byte_of(k), f);
+          return make_uint2(v.x, v.y);
+        };
+        auto decoded_odd = [&](int k) {
+          const uint4 v = dsv4::dequant8(make_uint2(code[k], 0), dsv4::ue8m0_scale(byte_of(k)));
+          return make_uint2(v.x, v.y);
+        };
+        auto put = [&](int k, const uint2& v) {
+          *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128) = v;
+          *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128 + L::kChunk) = rope[k];
+        };
+        uint2 early[EARLY];
+        if (!odd) {
+#pragma unroll
+          for (int k = 0; k < EARLY; ++k) early[k] = decoded(k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < EARLY; ++k) early[k] = decoded_odd(k);
+        }
         if (tile > 0 && !await(kXEmpty + quarter, (tile - 1) & 1)) break;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const uint32_t byte = __shfl_sync(kFullMask, ex, (lane & 16) + k) >> 16 & 0xffu;
-          const uint2 codes = make_uint2(code[k], 0);
-          const uint4 v = odd ? dsv4::dequant8(codes, dsv4::ue8m0_scale(byte)) : decode8(codes, byte);
-          *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128) = make_uint2(v.x, v.y);
-          *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128 + L::kChunk) = rope[k];
+        for (int k = 0; k < EARLY; ++k) put(k, early[k]);
+        if (!odd) {
+#pragma unroll
+          for (int k = EARLY; k < N; ++k) put(k, decoded(k));
+        } else {
+#pragma unroll
+          for (int k = EARLY; k < N; ++k) put(k, decoded_odd(k));
         }
         hand_over();
         read_scales();
