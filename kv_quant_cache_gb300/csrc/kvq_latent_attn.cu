@@ -18,7 +18,9 @@
 //     decode them, four warps to a quarter of the dims: as soon as the second product
 //     of the tile before is done with a quarter, the next tile's takes its place;
 //   * warp 24: issues the matrix instructions;
-//   * warp 25: looks the lists up, up to four tiles ahead.
+//   * warp 25: looks the lists up, up to four tiles ahead;
+//   * warps 26 and 27: copy the queries of a unit as soon as the last scores of the unit
+//     before are done, while its outputs are still to come.
 //
 // With few units a CTA to an SM takes an equal share of all tiles of all lists, from
 // the lists' actual lengths; a unit that falls to several CTAs goes to partials,
@@ -37,7 +39,8 @@ constexpr int kKeys = 128;          // entries of a tile
 constexpr int kQuarters = 4;        // of the dims
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 16;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps, kListWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // (two warps of that group have no work)
+constexpr int kQueryWarp = kListWarp + 1, kQueryWarps = 2;
+constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr int kAhead = 4;  // tiles whose slots are in shared memory
 // (28 warps of 72 registers each.  A softmax warp reads its scores twice, half of its
 // heads at a time, to make do with them.)
@@ -67,7 +70,7 @@ struct LatentParams {
 
 // mbarriers, by index
 enum { kXFull = 0, kXEmpty = 4, kListFull = 8, kListEmpty = 12, kQFull = 16, kSFull = 17,
-       kPFull = 18, kODone = 19, kDrain = 20, kBarriers = 21 };
+       kPFull = 18, kODone = 19, kQEmpty = 20, kDrain = 21, kBarriers = 22 };
 
 template <int NH>
 struct Layout {
@@ -79,7 +82,8 @@ struct Layout {
   static constexpr int kTops = kQ + 8 * kQChunk;        // [4 quadrants of lanes][NH]
   static constexpr int kRef = kTops + 4 * 64 * 4;       // [NH] references, [NH] factors
   static constexpr int kStart = kRef + 2 * 64 * 4;      // [tokens + 1] first tiles
-  static constexpr int kLists = kStart + (kSharedUnits + 8) * 4;  // [kAhead][128] slots
+  static constexpr int kLens = kStart + (kSharedUnits + 8) * 4;  // [tokens] lengths of lists
+  static constexpr int kLists = kLens + (kSharedUnits + 8) * 4;  // [kAhead][128] slots
   static constexpr int kBars = kLists + kAhead * kKeys * 4;
   static constexpr int kEnd = kBars + 24 * 8 + 48;
   static constexpr int kSmem = kEnd + 1024;             // room to align the base
@@ -90,6 +94,13 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  const int bytes = there ? 16 : 0;  // 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes)
+               : "memory");
 }
 
 // Barriers of the softmax warps; vote: whether any thread's flag is set.
@@ -213,7 +224,8 @@ struct Segments {
       at = 0, stop = 1;
     }
   }
-  __device__ __forceinline__ bool next(const LatentParams& p, const int* start) {
+  __device__ __forceinline__ bool next(const LatentParams& p, const int* start,
+                                       const int* lens) {
     at += n;
     if (at >= stop) return false;
     ++count;
@@ -230,7 +242,7 @@ struct Segments {
       block = rest / tiles;
       first = rest - block * tiles;
       n = (int)min((int64_t)(tiles - first), stop - at);
-      len = list_len(p, __ldg(p.lens + token));
+      len = lens[token];
     } else {
       token = (int)blockIdx.x / p.blocks;
       block = (int)blockIdx.x - token * p.blocks;
@@ -256,6 +268,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
   float* refs = reinterpret_cast<float*>(smem + L::kRef);
   float* moves = refs + 64;  // factors of the heads
   int* start = reinterpret_cast<int*>(smem + L::kStart);
+  int* lens = reinterpret_cast<int*>(smem + L::kLens);
   const uint32_t bars = base + L::kBars;
   volatile int* lists = reinterpret_cast<int*>(smem + L::kLists);
   int* shared_state = reinterpret_cast<int*>(smem + L::kBars + 24 * 8);
@@ -273,7 +286,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     for (int i = 0; i < kBarriers; ++i)
       tma::mbar_init(bar(i), i < kXEmpty ? kLoadWarps / kQuarters
                              : i >= kListEmpty && i < kQFull ? kLoadWarps + kSoftmaxWarps + 1
-                             : i == kQFull || i == kPFull ? kSoftmaxWarps : 1);
+                             : i == kQFull ? kQueryWarps : i == kPFull ? kSoftmaxWarps : 1);
     tma::mbar_init_fence();
     *dead = *quit = 0;
   }
@@ -283,7 +296,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     // the first tile of each token, of one block of heads
     for (int t = threadIdx.x; t < p.num_tokens; t += kThreads) {
       const int len = __ldg(p.lens + t);
-      start[t + 1] = list_tiles(list_len(p, len));
+      lens[t] = list_len(p, len);
+      start[t + 1] = list_tiles(lens[t]);
       if (blockIdx.x == 0 && len != list_len(p, len) && p.errors) atomicAdd(p.errors, 1);
     }
     __syncthreads();
@@ -324,32 +338,10 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     const int col0 = half * COLS;  // .. and its first head
     uint32_t done = 0, segs = 0;  // phases of the barriers
     bool ok = true;
-    while (ok && seg.next(p, start)) {
+    while (ok && seg.next(p, start, lens)) {
       const int head0 = seg.block * NH, rows = min(NH, p.num_heads - head0);
-      // Q, swizzled; the products that read the last segment's are done
-      const __nv_bfloat16* q = p.q + (int64_t)seg.token * p.q_stride + (int64_t)head0 * kDim;
-      constexpr int FLIGHT = 8;  // loads of a thread at a time
-#pragma unroll 1
-      for (int i0 = threadIdx.x; i0 < NH * 64; i0 += FLIGHT * 32 * kSoftmaxWarps) {
-        uint4 v[FLIGHT];
-#pragma unroll
-        for (int u = 0; u < FLIGHT; ++u) {
-          const int i = i0 + u * 32 * kSoftmaxWarps;
-          v[u] = make_uint4(0, 0, 0, 0);
-          if (i >> 6 < rows) v[u] = __ldg(reinterpret_cast<const uint4*>(q) + i);
-        }
-#pragma unroll
-        for (int u = 0; u < FLIGHT; ++u) {
-          const int i = i0 + u * 32 * kSoftmaxWarps, h = i >> 6, c = i & 63;
-          if (h < NH)
-            *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * L::kQChunk + h * 128 +
-                                      (((c & 7) ^ (h & 7)) << 4)) = v[u];
-        }
-      }
-      tma::fence_proxy_async();
       if (threadIdx.x < NH) refs[threadIdx.x] = 0.f;
       softmax_sync();
-      if (lane == 0) tc::mbar_arrive(bar(kQFull));
 
       bool fresh = true;  // no entry so far: the references mean nothing
       float l[COLS];
@@ -486,29 +478,28 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
               sum == 0.f ? -INFINITY : refs[threadIdx.x] + log2f(sum);
       }
       softmax_sync();
-      // (short loops: straight code that runs once a unit costs more to fetch than to run)
       const bool whole = seg.whole();
       const int64_t row0 = whole ? (int64_t)seg.token * p.num_heads + head0 : (int64_t)slot_at * NH;
 #pragma unroll 1
-      for (int k = 0; k < kQuarters * COLS / 8; ++k) {
-        const int c0 = col0 + 8 * (k % (COLS / 8)), quarter = k / (COLS / 8);
-        uint32_t o[8];
-        tc::ld8(o, o_tmem + lanes + quarter * NH + c0);
+      for (int k = 0; k < kQuarters; ++k) {
+        uint32_t o[COLS];
+        tc::ld(o, o_tmem + lanes + k * NH + col0);
         tc::wait_ld();
-        const int64_t at = (row0 + c0) * kDim + 128 * quarter + r;
+        const int64_t at = (row0 + col0) * kDim + 128 * k + r;
         if (whole) {
+          __nv_bfloat16* to = p.out + at;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c0 + c < rows)
-              p.out[at + c * kDim] = __float2bfloat16_rn(__uint_as_float(o[c]) * moves[c0 + c]);
+          for (int c = 0; c < COLS; ++c)
+            if (col0 + c < rows)
+              to[c * kDim] = __float2bfloat16_rn(__uint_as_float(o[c]) * moves[col0 + c]);
         } else {
+          float* to = p.part_o + at;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            p.part_o[at + c * kDim] = __uint_as_float(o[c]) * moves[c0 + c];
+          for (int c = 0; c < COLS; ++c) to[c * kDim] = __uint_as_float(o[c]) * moves[col0 + c];
         }
       }
       tc::fence_before();
-      softmax_sync();  // tops, moves, refs and Q may be written again
+      softmax_sync();  // tops, moves and refs may be written again
     }
     // Given up: what this segment and those still to come should have held is marked.
     if (!ok) {
@@ -523,7 +514,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
                 __float2bfloat16_rn(NAN);
           }
         }
-      } while (seg.next(p, start));
+      } while (seg.next(p, start, lens));
     }
   } else if (warp < kMmaWarp) {
     // ---- entries: four warps to a quarter of the dims ------------------------------------
@@ -575,7 +566,6 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       };
       read();
       for (int tile = 0; tile < left; ++tile) {
-        next_slots(tile + 1);
         uint32_t strange = large();
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -610,6 +600,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
                 dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte_of(k)));
         }
         hand_over();
+        next_slots(tile + 1);
         read_scales();
         read();
       }
@@ -632,7 +623,6 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       };
       read();
       for (int tile = 0; tile < left; ++tile) {
-        next_slots(tile + 1);
         uint32_t strange = large();
 #pragma unroll
         for (int k = 0; k < N; ++k) strange = nan_bits(strange, code[k], f);
@@ -671,6 +661,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           for (int k = EARLY; k < N; ++k) put(k, decoded_odd(k));
         }
         hand_over();
+        next_slots(tile + 1);
         read_scales();
         read();
       }
@@ -704,6 +695,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       }
       if (!ok) break;
       tc::commit(bar(kSFull));
+      if (where & 2) tc::commit(bar(kQEmpty));
       ok = await(kPFull, tile & 1);
       if (!ok) break;
       tc::fence_after();
@@ -726,7 +718,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     // ---- the lists ------------------------------------------------------------------------
     bool ok = true, rejected = false;
     uint32_t tile = 0;
-    while (ok && seg.next(p, start)) {
+    while (ok && seg.next(p, start, lens)) {
       const int* list = p.slots + (int64_t)seg.token * p.list_width;
       for (int j = 0; ok && j < seg.n; ++j, ++tile) {
         int slot[kKeys / 32];
@@ -747,6 +739,23 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       }
     }
     if (rejected && p.errors) atomicAdd(p.errors, 1);
+  } else if (warp >= kQueryWarp) {
+    // ---- the queries, swizzled -------------------------------------------------------------
+    for (uint32_t segs = 0; seg.next(p, start, lens); ++segs) {
+      if (segs > 0 && !await(kQEmpty, (segs - 1) & 1)) break;
+      const int head0 = seg.block * NH, rows = min(NH, p.num_heads - head0);
+      const __nv_bfloat16* q = p.q + (int64_t)seg.token * p.q_stride + (int64_t)head0 * kDim;
+      const int c = threadIdx.x & 63;  // the thread's fragment of every row
+      const uint32_t to = base + L::kQ + (c >> 3) * L::kQChunk;
+#pragma unroll 4
+      for (int h = 0; h < NH; ++h)
+        copy16(to + h * 128 + (((c & 7) ^ (h & 7)) << 4), h < rows ? q + h * kDim + 8 * c : p.q,
+               h < rows);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      tma::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kQFull));
+    }
   }
   tc::fence_before();
   __syncthreads();
