@@ -103,6 +103,10 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
                : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(p)) : "memory");
+}
+
 // Barriers of the softmax warps; vote: whether any thread's flag is set.
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
@@ -727,6 +731,16 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           const int at = (seg.first + j) * kKeys + 32 * u + lane;
           slot[u] = at < seg.len ? __ldg(list + at) : -1;
           if (slot[u] < -1 || slot[u] >= p.num_slots) rejected = true, slot[u] = -1;
+        }
+        // into the L2 meanwhile: the loads behind the last tile's are a burst, which from
+        // memory takes as long as the whole tile
+#pragma unroll
+        for (int u = 0; u < kKeys / 32; ++u) {
+          if (slot[u] < 0) continue;
+          const uint8_t* e = p.cache + (int64_t)slot[u] * dsv4::kEntry;
+#pragma unroll
+          for (int b = 0; b < dsv4::kEntry; b += 128) prefetch_l2(e + b);
+          prefetch_l2(e + dsv4::kEntry - 1);
         }
         if (tile >= kAhead) ok = await(kListEmpty + tile % kAhead, list_phase(tile - kAhead));
         if (!ok) break;
