@@ -36,7 +36,7 @@ struct Append4Params {
   uint8_t* cache;
   int num_q, num_kv, num_rows, first_row;
   int rot;
-  int chunks, chunk_rows;  // warps per token, rows each of them takes
+  int chunks;  // warps per token; they take its groups of rows in turn
   int64_t items;
   int64_t max_pos, num_slots;
   int page_size;
@@ -76,40 +76,71 @@ __device__ __forceinline__ uint32_t group_meta(uint32_t lohi) {
   const float lo = __uint_as_float(lohi << 16), hi = -__uint_as_float(lohi & 0xffff0000u);
   const float width = __fsub_rn(hi, lo);
   if (!(width < INFINITY)) return 0x7fc07fc0u;  // NaN, an infinity: the group reads back as NaN
-  const float scale = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(width, 15.f)));
+  // width / 15, correctly rounded: a product, and the exact remainder's share of it
+  float q = __fmul_rn(width, 1.f / 15.f);
+  q = __fmaf_rn(__fmaf_rn(-15.f, q, width), 1.f / 15.f, q);
+  if (width < 0x1p-100f) q = __fdiv_rn(width, 15.f);  // (where the remainder may not be exact)
+  const float scale = __bfloat162float(__float2bfloat16_rn(q));
   return pack_bf16x2(scale, __fadd_rn(lo, __fmul_rn(8.f, scale)));
 }
 
-// The word of codes of a fragment's eight values.
-__device__ __forceinline__ uint32_t codes_of(const uint4& v, uint32_t meta) {
+// Whether the ends of a group may come out past the codes at the ends: only where the
+// roundings of scale and zero make up half a step.
+__device__ __forceinline__ bool past_ends(uint32_t lohi, uint32_t meta) {
+  const float lo = __uint_as_float(lohi << 16), hi = -__uint_as_float(lohi & 0xffff0000u);
+  const float scale = __uint_as_float(meta << 16), zero = __uint_as_float(meta & 0xffff0000u);
+  return scale > 0.f && (hi - zero > 7.49f * scale || lo - zero < -8.49f * scale);
+}
+
+// The word of codes of a fragment's eight values; cut: codes may lie past the ends.
+// Rounding to a whole number is adding 1.5 2^23; the remainder t - c scale is exact, and
+// shows where the product of t and the reciprocal has rounded across the middle of two
+// codes, or from it to the odd one (values of 8 bits lie in the middle often: 3 in
+// 1000).  Four codes are put together as one number, c_0 + 16 c_1 + .., which is exact
+// and keeps to the pipe that the rest of the work leaves free.
+__device__ __forceinline__ uint32_t codes_of(const uint4& v, uint32_t meta, bool cut) {
   const float scale = __uint_as_float(meta << 16), zero = __uint_as_float(meta & 0xffff0000u);
   if (!(scale > 0.f)) return 0x88888888u;  // one value (or NaN): zero alone
-  float x[8];
+  constexpr float kWhole = 12582912.f;
+  float x[8], u[8];  // u: the codes, negative, between -7 and 8
   unpack_bf16x8(v, x);
-  uint32_t w = 0;
-  const bool tiny = scale < 0x1p-100f;  // its reciprocal may overflow
-  const float inv = tiny ? 0.f : __frcp_rn(scale), half = 0.5f * scale;
+  if (scale < 0x1p-100f) {  // its reciprocal may overflow
+    for (int i = 0; i < 8; ++i) u[i] = -rintf(__fdiv_rn(__fsub_rn(x[i], zero), scale));
+    cut = true;
+  } else {
+    float inv;  // (what it is off by, the remainder shows)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+    const float half = 0.5f * scale;
+    float r[8];
+    bool middle = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fsub_rn(x[i], zero);
-    float c;
-    if (tiny) {
-      c = rintf(__fdiv_rn(t, scale));
-    } else {
-      c = rintf(__fmul_rn(t, inv));
-      c = fminf(fmaxf(c, -9.f), 8.f);
-      const float r = fabsf(__fmaf_rn(-c, scale, t));  // exact
-      // the product may have rounded across the middle of two codes, or from it to
-      // the odd one
-      if (r >= half) {
-        const float to = __fmaf_rn(-c, scale, t) > 0.f ? c + 1.f : c - 1.f;
-        if (r > half || ((int)c & 1)) c = to;
+    for (int i = 0; i < 8; ++i) {
+      const float t = __fsub_rn(x[i], zero);
+      u[i] = __fsub_rn(kWhole, __fmaf_rn(t, inv, kWhole));
+      r[i] = __fmaf_rn(u[i], scale, t);
+      middle |= fabsf(r[i]) >= half;
+    }
+    if (middle) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // above half a step by its bits, less the lowest of the whole number: at half, odd
+        const uint32_t odd = __float_as_uint(__fadd_rn(u[i], kWhole)) & 1u;
+        if ((__float_as_uint(r[i]) & 0x7fffffffu) > __float_as_uint(half) - odd)
+          u[i] -= copysignf(1.f, r[i]);
       }
     }
-    const uint32_t code = (uint32_t)(int)(fminf(fmaxf(c, -8.f), 7.f) + 8.f);
-    w |= code << (4 * (i / 2) + 16 * (i & 1));
   }
-  return w;
+  if (cut) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = fminf(fmaxf(u[i], -7.f), 8.f);
+  }
+  constexpr float kBase = 8388608.f + 8.f * (1 + 16 + 256 + 4096);  // 2^23, and 8 to each code
+  uint32_t half_word[2];  // dims of even place, of odd place
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    half_word[h] = __float_as_uint(fmaf(
+        u[6 + h], -4096.f, fmaf(u[4 + h], -256.f, fmaf(u[2 + h], -16.f, kBase - u[h]))));
+  return __byte_perm(half_word[0], half_word[1], 0x5410);
 }
 
 template <int D, bool NEOX, int STEPS>
@@ -124,8 +155,10 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const Append4Param
   const int l = lane % LPR;
   const int64_t t = item / p.chunks;
   const int chunk = (int)(item - t * p.chunks);
-  const int r0 = p.first_row + chunk * p.chunk_rows;
-  const int r1 = min(r0 + p.chunk_rows, p.num_rows);
+  // In turn: key and value rows, which take most of the work, are a token's last (a
+  // stretch of rows to each warp: the last one of a CTA at work alone, 235 us at 32768
+  // tokens).
+  auto first_of = [&](int s) { return p.first_row + (s * p.chunks + chunk) * RPW; };
   const int64_t slot = __ldg(p.slots + t);
   const int64_t pos = p.rot ? __ldg(p.positions + t) : 0;
 
@@ -139,8 +172,8 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const Append4Param
   uint4 xa[STEPS], xb[STEPS];
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    const int r = r0 + s * RPW + lane / LPR;
-    if (r < r1) {
+    const int r = first_of(s) + lane / LPR;
+    if (r < p.num_rows) {
       xa[s] = load_stream(src + (size_t)r * D + oa);
       xb[s] = load_stream(src + (size_t)r * D + ob);
     } else {
@@ -173,70 +206,73 @@ __global__ void __launch_bounds__(kWarps * 32) append4_kernel(const Append4Param
   const int64_t block = (int64_t)p.page_size * kv4::row_bytes(D);
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    const int r = r0 + s * RPW + lane / LPR;
-    if (r0 + s * RPW >= r1) break;  // warp-uniform
+    const int r = first_of(s) + lane / LPR;
+    if (first_of(s) >= p.num_rows) break;  // warp-uniform
     if (rotated && r < p.num_q + p.num_kv) {
       float a[8], b[8];
       unpack_bf16x8(xa[s], a);
       unpack_bf16x8(xb[s], b);
-      const bool key = r >= p.num_q;
-      auto turn = [&](float& u, float& v, float c, float n) {
-        const float x = u, y = v;
-        if (key) {
-          u = exact_rotation(x, c, y, n);
-          v = exact_rotation(y, c, -x, n);
+      auto turn_all = [&](auto turn) {
+        if (NEOX) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) turn(a[i], b[i], cs[i], sn[i]);
         } else {
-          u = fmaf(-y, n, x * c);
-          v = fmaf(x, n, y * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            turn(a[2 * i], a[2 * i + 1], cs[i], sn[i]);
+            turn(b[2 * i], b[2 * i + 1], cs[4 + i], sn[4 + i]);
+          }
         }
       };
-      if (NEOX) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn(a[i], b[i], cs[i], sn[i]);
+      // (one branch around all pairs: with the choice made pair by pair every row went
+      // both ways)
+      if (r < p.num_q) {
+        turn_all([](float& u, float& v, float c, float n) {
+          const float x = u, y = v;
+          u = fmaf(-y, n, x * c);
+          v = fmaf(x, n, y * c);
+        });
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          turn(a[2 * i], a[2 * i + 1], cs[i], sn[i]);
-          turn(b[2 * i], b[2 * i + 1], cs[4 + i], sn[4 + i]);
-        }
+        turn_all([](float& u, float& v, float c, float n) {
+          const float x = u, y = v;
+          u = exact_rotation(x, c, y, n);
+          v = exact_rotation(y, c, -x, n);
+        });
       }
       xa[s] = pack_bf16x8(a);
       xb[s] = pack_bf16x8(b);
     }
-    if (r < p.num_q && r < r1) {
+    if (r < p.num_q) {
       __nv_bfloat16* dst = p.q_out + t * p.q_token_stride + (size_t)r * D;
       store_stream(dst + oa, xa[s]);
       store_stream(dst + ob, xb[s]);
     }
-    if (!store_kv || r0 + s * RPW + RPW <= p.num_q) continue;  // warp-uniform: no key or value
+    if (!store_kv || first_of(s) + RPW <= p.num_q) continue;  // warp-uniform: no key or value
     const uint32_t sa = span(xa[s]), sb = span(xb[s]);
     const int ga = oa / kv4::kGroup, gb = ob / kv4::kGroup;
-    uint32_t meta[GROUPS];
+    uint32_t own = 0;  // of group l % GROUPS
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       constexpr uint32_t none = 0x7f807f80u;  // (+inf, +inf)
       uint32_t m = min2(ga == g ? sa : none, gb == g ? sb : none);
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) m = min2(m, __shfl_xor_sync(kFullMask, m, o));
-      meta[g] = group_meta(m);
+      if (l % GROUPS == g) own = m;
     }
-    if (r < p.num_q || r >= r1) continue;
-    uint32_t ma = meta[0], mb = meta[0];
-#pragma unroll
-    for (int g = 1; g < GROUPS; ++g) {
-      ma = ga == g ? meta[g] : ma;
-      mb = gb == g ? meta[g] : mb;
-    }
+    const uint32_t ends = own;
+    own = group_meta(own);
+    const bool cut = __any_sync(kFullMask, past_ends(ends, own));
+    const uint32_t ma = __shfl_sync(kFullMask, own, lane - l + ga);
+    const uint32_t mb = __shfl_sync(kFullMask, own, lane - l + gb);
+    if (r < p.num_q || r >= p.num_rows) continue;
     // key heads, then value heads, as the page holds them
     uint8_t* to = p.cache + (page * 2 * p.num_kv + (r - p.num_q)) * block;
     uint32_t* codes = reinterpret_cast<uint32_t*>(to + (int64_t)off * (D / 2));
-    codes[oa / 8] = codes_of(xa[s], ma);
-    codes[ob / 8] = codes_of(xb[s], mb);
+    codes[oa / 8] = codes_of(xa[s], ma, cut);
+    codes[ob / 8] = codes_of(xb[s], mb, cut);
     uint32_t* words =
         reinterpret_cast<uint32_t*>(to + (int64_t)p.page_size * (D / 2)) + off * GROUPS;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g)
-      if (l == g) words[g] = meta[g];
+    if (l < GROUPS) words[l] = own;
   }
 }
 
@@ -265,7 +301,6 @@ cudaError_t launch_append4(const AppendArgs& a, cudaStream_t stream) {
   const int rows = p.num_rows - p.first_row;
   const int groups = (rows + RPW - 1) / RPW;
   p.chunks = (groups + STEPS - 1) / STEPS;
-  p.chunk_rows = (groups + p.chunks - 1) / p.chunks * RPW;
   p.items = (int64_t)a.num_tokens * p.chunks;
   const int64_t grid = (p.items + kWarps - 1) / kWarps;
   static std::atomic<int> cache[kMaxDevices];
