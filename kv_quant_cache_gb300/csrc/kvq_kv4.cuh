@@ -21,21 +21,11 @@ constexpr int kGroup = 64;  // dims that share a scale and a zero
 __host__ __device__ constexpr int row_bytes(int head_dim) { return head_dim / 2 + head_dim / 16; }
 
 // Codes i and i + 4 of a word as bf16 pairs 16 + c: the code lands on the upper four
-// bits of the fraction of 16.  `sixteen` is 0x41804180 from a register: an instruction
-// takes one constant, and with two the mask and the bits would be two of them.
+// bits of the fraction of 16.
 template <int I>
-__device__ __forceinline__ uint32_t pair16(uint32_t w, uint32_t sixteen) {
+__device__ __forceinline__ uint32_t pair16(uint32_t w) {
   const uint32_t x = I == 0 ? w << 3 : w >> (4 * I - 3);
-  uint32_t y;
-  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(y) : "r"(x), "r"(sixteen));
-  return y;
-}
-
-// The constant, where the compiler does not know it for one.
-__device__ __forceinline__ uint32_t sixteen_pair() {
-  uint32_t x;
-  asm volatile("mov.b32 %0, 0x41804180;" : "=r"(x));
-  return x;
+  return (x & 0x00780078u) | 0x41804180u;
 }
 
 }  // namespace kv4

@@ -8,10 +8,12 @@
 //   S   = scale sum_j ( s_kj (q_j n_kj) + z_kj sum(q_j) )
 //   O_j = sum_k (P_k s_kj) n_kj + sum_k P_k z_kj
 // so no code is ever multiplied by its scale: codes become bf16 integers by a
-// shift, a mask and a subtraction, two at a time, and go straight into 16x8x16
+// mask and a product, two at a time, and go straight into 16x8x16
 // matrix instructions; K's scales and zeros are applied to S in fp32, V's scales
 // to the weights P, whose product is rounded once to bf16 (the row sum adds the
-// unrounded P), V's zeros to P in fp32.
+// unrounded P), V's zeros to P in fp32.  Every second code comes out as a quarter of
+// n: the other dims of Q are divided by 4 (exact), S multiplied by it, and so are those
+// dims of O.
 //
 // The codes are the first operand of both products, S^T = K Q^T and O^T = V^T P^T:
 // 16 keys (or dims) against 8 rows, so that the 1 to 8 rows that most models have to
@@ -19,11 +21,9 @@
 // padding.  More rows are more second operands to the same codes.  The transposed
 // P takes one matrix transposition in registers.
 //
-// K's codes keep the 16 that the mask leaves in them: the accumulators start from
-// -24 sum(q_j).  V's must not: the sum over a long range would lose in the offset
-// what it is to keep.  The reference of a row's softmax
-// moves only when a score exceeds it by more than 2^8, which spares the exchange
-// of maxima: until then weights above 1 are as exact as those below.
+// The reference of a row's softmax moves only when a score exceeds it by more than
+// 2^8, which spares the exchange of maxima: until then weights above 1 are as exact as
+// those below.
 //
 // A group's codes come in by 16-byte asynchronous copies, three groups ahead, into
 // a ring that only this warp uses, so that there is no CTA barrier in the loop.
@@ -124,11 +124,24 @@ __device__ __forceinline__ uint32_t piece_at(int r, int j) {
   return r * 128 + ((j ^ (r & 3)) << 5);
 }
 
-__device__ __forceinline__ uint32_t less24(uint32_t pair) {  // 16 + c -> c - 8, twice, exact
-  constexpr uint32_t k24 = 0x41c041c0u;
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&pair),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&k24));
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(a), "r"(b));
+  return y;
+}
+
+// The codes in the low four bits of each half, less 8; and those in the next four, less
+// 8, a quarter of that.  128 + c is a mask away; the number whose bits are 16 c is 16 c
+// times the smallest there is, up to 8 bits, and one product with 2^127 mends that.
+// Neither takes a shift.  (`big` is 0x43004300 from a register: an instruction takes one
+// constant, and with two the mask and the bits would be two of them.)
+__device__ __forceinline__ uint32_t low_codes(uint32_t w, uint32_t big) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(x) : "r"(w), "r"(big));
+  return fma2(x, 0x3f803f80u, 0xc308c308u);  // 1, -136
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+  return fma2(w & 0x00f000f0u, 0x7f007f00u, 0xc000c000u);  // 2^127, -2
 }
 
 // Transposes an 8x8 matrix of 16-bit values, two neighbours of a row to a lane.
@@ -259,7 +272,7 @@ attn4_kernel(const Attn4Params p) {
   // ---- Q fragments --------------------------------------------------------------------
   // row 8 n + g; step s of group j: dims 64 j + 16 t + 2 s + {0, 1} and those 8 further
   uint32_t qf[NT][D / 16][2];
-  float qsum[NT][GROUPS][2];  // of rows 8 n + 2 t and the next
+  float qsum[NT][GROUPS][2];  // a quarter of it, of rows 8 n + 2 t and the next
   int sees[NT][2];            // .. and the keys they see
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -278,21 +291,23 @@ attn4_kernel(const Attn4Params p) {
       float sum = 0.f;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        qf[n][4 * j + s][0] = x[s];
-        qf[n][4 * j + s][1] = y[s];
+        // (even steps take whole codes)
+        qf[n][4 * j + s][0] = s & 1 ? x[s] : fma2(x[s], 0x3e803e80u, 0x80008000u);
+        qf[n][4 * j + s][1] = s & 1 ? y[s] : fma2(y[s], 0x3e803e80u, 0x80008000u);
         sum += (low(x[s]) + high(x[s])) + (low(y[s]) + high(y[s]));
       }
       sum += __shfl_xor_sync(kFullMask, sum, 1);
       sum += __shfl_xor_sync(kFullMask, sum, 2);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        qsum[n][j][c] = __shfl_sync(kFullMask, sum, 4 * (2 * t + c));
+        qsum[n][j][c] = 0.25f * __shfl_sync(kFullMask, sum, 4 * (2 * t + c));
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) sees[n][c] = __shfl_sync(kFullMask, len, 8 * n + 2 * t + c);
   }
 
-  const uint32_t sixteen = kv4::sixteen_pair();
+  uint32_t big;
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(big));
   // tile 4 j + e of O^T: its row g is dim 64 j + 8 g + 2 e, row g + 8 the next; columns 2 t
   // and 2 t + 1 are those rows of Q
   float o[NT][D / 16][4];
@@ -337,18 +352,16 @@ attn4_kernel(const Attn4Params p) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) raw[n][k] = -24.f * qsum[n][j][k & 1];
-      auto part = [&](auto index) {
-        constexpr int I = decltype(index)::value;
-        auto pair = [&](uint32_t w) { return kv4::pair16<I>(w, sixteen); };
+        for (int k = 0; k < 4; ++k) raw[n][k] = 0.f;
+      auto part = [&](int i, auto pair) {
         const uint32_t a[4] = {pair(w[0].x), pair(w[1].x), pair(w[0].y), pair(w[1].y)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma(raw[n], a, qf[n][4 * j + I][0], qf[n][4 * j + I][1]);
+        for (int n = 0; n < NT; ++n) mma(raw[n], a, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
       };
-      part(std::integral_constant<int, 0>());
-      part(std::integral_constant<int, 1>());
-      part(std::integral_constant<int, 2>());
-      part(std::integral_constant<int, 3>());
+      part(0, [&](uint32_t x) { return low_codes(x, big); });
+      part(1, [&](uint32_t x) { return high_codes(x); });
+      part(2, [&](uint32_t x) { return low_codes(x >> 8, big); });
+      part(3, [&](uint32_t x) { return high_codes(x >> 8); });
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t meta = km[key_of(h, g) * GROUPS + j];
@@ -370,7 +383,7 @@ attn4_kernel(const Attn4Params p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float& x = s[n][2 * h + c];
-          x *= p.scale_log2;
+          x = 4.f * x * p.scale_log2;
           if (!ALL && key0 + key_of(h, g) >= sees[n][c]) x = -INFINITY;
         }
         // (from -inf on every score exceeds it; -inf itself does not)
@@ -426,29 +439,31 @@ attn4_kernel(const Attn4Params p) {
           b[n][h] = transposed(pack_bf16x2(e[0], e[1]));
         }
       }
-      uint32_t even[2], odd[2];  // codes of two keys each: dims 2 i, dims 2 i + 1 of the word
+      uint2 word[2];  // of keys 2 t and the next, of both halves
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        auto word = [&](int c) {
+        auto of = [&](int c) {
           return *reinterpret_cast<const uint32_t*>(
               vc + piece_at<GROUPS>(key_of(h, 2 * t + c), j) + 4 * g);
         };
-        const uint32_t x = word(0), y = word(1);
-        even[h] = __byte_perm(x, y, 0x5410);
-        odd[h] = __byte_perm(x, y, 0x7632);
+        word[h] = make_uint2(of(0), of(1));
       }
-      auto part = [&](auto index) {
-        constexpr int I = decltype(index)::value;
-        auto pair = [&](uint32_t w) { return kv4::pair16<I>(w, sixteen); };
-        const uint32_t a[4] = {less24(pair(even[0])), less24(pair(odd[0])),
-                               less24(pair(even[1])), less24(pair(odd[1]))};
+      // bytes of the two keys, a code each of dims 2 i (bytes 0, 1) or 2 i + 1 (2, 3)
+      auto both = [&](int h, uint32_t which) { return __byte_perm(word[h].x, word[h].y, which); };
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma(o[n][4 * j + I], a, b[n][0], b[n][1]);
-      };
-      part(std::integral_constant<int, 0>());
-      part(std::integral_constant<int, 1>());
-      part(std::integral_constant<int, 2>());
-      part(std::integral_constant<int, 3>());
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t even0 = both(0, 0x0400 + 0x0101 * i), even1 = both(1, 0x0400 + 0x0101 * i);
+        const uint32_t odd0 = both(0, 0x0602 + 0x0101 * i), odd1 = both(1, 0x0602 + 0x0101 * i);
+        const uint32_t lo[4] = {low_codes(even0, big), low_codes(odd0, big), low_codes(even1, big),
+                                low_codes(odd1, big)};
+        const uint32_t hi[4] = {high_codes(even0), high_codes(odd0), high_codes(even1),
+                                high_codes(odd1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma(o[n][4 * j + 2 * i], lo, b[n][0], b[n][1]);
+          mma(o[n][4 * j + 2 * i + 1], hi, b[n][0], b[n][1]);
+        }
+      }
     }
   };
   for (int i = 0; i < steps; ++i) {
@@ -499,8 +514,9 @@ attn4_kernel(const Attn4Params p) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const float *x = o[n][4 * j + e], *y = o[n][4 * j + e + 1];
-          *reinterpret_cast<float4*>(dst + 64 * j + 2 * e) = make_float4(
-              (x[c] + z) * f, (x[2 + c] + z) * f, (y[c] + z) * f, (y[2 + c] + z) * f);
+          *reinterpret_cast<float4*>(dst + 64 * j + 2 * e) =
+              make_float4((x[c] + z) * f, (x[2 + c] + z) * f, fmaf(4.f, y[c], z) * f,
+                          fmaf(4.f, y[2 + c], z) * f);
         }
       }
       if (warp == 0 && g == 0) part_lse[r] = sum == 0.f ? -INFINITY : ref + log2f(sum);
