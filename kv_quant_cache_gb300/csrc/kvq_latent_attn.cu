@@ -578,6 +578,9 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         auto byte_of = [&](int k) {
           return prmt(__shfl_sync(kFullMask, ex, (lane & 16) + k), which);
         };
+        // not before the last tile's weights are there: the softmax, which everything
+        // waits for, would share its issue slots with all this
+        if (tile > 0 && !await(kPFull, (tile - 1) & 1)) break;
         // (two ways with a branch around each: with the choice made entry by entry both
         // were gone for every one, and a quarter took 2850 cycles instead of 1100)
         uint4 early[EARLY];
@@ -646,6 +649,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128) = v;
           *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128 + L::kChunk) = rope[k];
         };
+        if (tile > 0 && !await(kPFull, (tile - 1) & 1)) break;
         uint2 early[EARLY];
         if (!odd) {
 #pragma unroll
