@@ -63,7 +63,7 @@ struct LatentParams {
   bool shared_out;           // the tiles are shared out
   __nv_bfloat16* out;
   float* part_o;             // [CTAs][2][heads of a unit][512]
-  float* part_lse;           // [CTAs][2][heads of a unit]
+  float2* part_sums;         // [CTAs][2][heads of a unit]: reference, sum of the weights
   int* errors;
   uint32_t wait_polls;       // of a barrier, before the waiter gives up
 };
@@ -356,28 +356,34 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
                            await(kSFull, done & 1);
         if (!ready) *dead = *quit = 1;
         const bool there = ready && lists[done % kAhead * kKeys + r] >= 0;
-        // scores in units of log2, less their heads' references; PART heads at a time
+        // scores in units of log2, less their heads' references if asked for; PART heads
+        // at a time. (The product is rounded before the reference, one of its kind, is
+        // taken off: the entry that it is from has weight 1 however large the scores, and
+        // so have those of the same score in all tiles and parts.)
         constexpr int PART = COLS < 16 ? COLS : 16;
         const float none = there ? 0.f : -INFINITY;
-        auto scores = [&](int c0, float (&x)[PART]) {
+        auto scores = [&](int c0, float (&x)[PART], bool less) {
           uint32_t s[PART];
           __syncwarp();
           tc::ld(s, s_tmem + lanes + col0 + c0);
           tc::wait_ld();
+          auto score = [&](uint32_t y, float ref) {
+            return __fadd_rn(__fmul_rn(__uint_as_float(y), p.scale_log2), less ? none - ref : none);
+          };
 #pragma unroll
           for (int c = 0; c < PART; c += 4) {
             const float4 ref = *reinterpret_cast<const float4*>(refs + col0 + c0 + c);
-            x[c] = fmaf(__uint_as_float(s[c]), p.scale_log2, none - ref.x);
-            x[c + 1] = fmaf(__uint_as_float(s[c + 1]), p.scale_log2, none - ref.y);
-            x[c + 2] = fmaf(__uint_as_float(s[c + 2]), p.scale_log2, none - ref.z);
-            x[c + 3] = fmaf(__uint_as_float(s[c + 3]), p.scale_log2, none - ref.w);
+            x[c] = score(s[c], ref.x);
+            x[c + 1] = score(s[c + 1], ref.y);
+            x[c + 2] = score(s[c + 2], ref.z);
+            x[c + 3] = score(s[c + 3], ref.w);
           }
         };
         // The weights of PART heads, added to (taken off) the sums and handed over; not
         // those of a thread with a score far above its reference.
         auto weigh = [&](int c0, float sign) {
           float x[PART], top = -INFINITY;
-          scores(c0, x);
+          scores(c0, x, true);
 #pragma unroll
           for (int c = 0; c < PART; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
           if (top > kRescaleAt) return true;
@@ -415,17 +421,18 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
             // (what is lost in taking off what was added is lost against larger weights)
             if (!fresh) weigh(c0, -1.f);
             float x[PART];
-            scores(c0, x);
+            scores(c0, x, false);
             const float mine = columns(x, lane, [](float a, float b) { return fmaxf(a, b); });
             if (lane % (32 / PART) == 0) tops[quad * 64 + col0 + c0 + lane / (32 / PART)] = mine;
           }
           softmax_sync();
-          if (threadIdx.x < NH) {  // how far each head's reference moves, and where to
-            float by = fresh ? -INFINITY : 0.f;
-            for (int k = 0; k < 4; ++k) by = fmaxf(by, tops[k * 64 + threadIdx.x]);
-            if (by == -INFINITY) by = 0.f;
-            moves[threadIdx.x] = fresh ? 0.f : ex2(-by);
-            refs[threadIdx.x] += by;
+          if (threadIdx.x < NH) {  // each head's reference becomes the maximum
+            const float old = refs[threadIdx.x];
+            float top = fresh ? -INFINITY : old;
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, tops[k * 64 + threadIdx.x]);
+            if (top == -INFINITY) top = 0.f;
+            moves[threadIdx.x] = ex2(old - top);
+            refs[threadIdx.x] = top;
           }
           const bool rescale = !fresh;
           fresh = false;
@@ -478,8 +485,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         for (int k = 0; k < 4; ++k) sum += tops[k * 64 + threadIdx.x];
         moves[threadIdx.x] = sum == 0.f ? 0.f : 1.f / sum;  // 0: no entry
         if (!seg.whole())
-          p.part_lse[slot_at * NH + threadIdx.x] =
-              sum == 0.f ? -INFINITY : refs[threadIdx.x] + log2f(sum);
+          p.part_sums[slot_at * NH + threadIdx.x] =
+              make_float2(sum == 0.f ? -INFINITY : refs[threadIdx.x], sum);
       }
       softmax_sync();
       const bool whole = seg.whole();
@@ -512,7 +519,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         for (int i = threadIdx.x; i < NH * kDim; i += 32 * kSoftmaxWarps) {
           const int h = i / kDim;
           if (!seg.whole()) {
-            if (i < NH) p.part_lse[(2 * (int)blockIdx.x + (seg.count > 1)) * NH + i] = NAN;
+            if (i < NH)
+              p.part_sums[(2 * (int)blockIdx.x + (seg.count > 1)) * NH + i] = make_float2(0.f, NAN);
           } else if (h < rows) {
             p.out[((int64_t)seg.token * p.num_heads + seg.block * NH) * kDim + i] =
                 __float2bfloat16_rn(NAN);
@@ -796,6 +804,7 @@ constexpr int kJoinWarps = 4;
 
 // One warp per row, the rows of one token to a CTA.  Which CTAs had the row's unit
 // follows from the lists' lengths, as it did for them.
+template <int FLIGHT>
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const JoinParams p) {
   grid_dependency_wait();
   __shared__ int sums[2][kJoinWarps];
@@ -831,29 +840,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Join
     return (int64_t)(2 * (b0 + s) + second) * p.heads + (head - block * p.heads);
   };
   float top = -INFINITY;
-  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.x.part_lse[at(s)]);
+  for (int s = lane; s < parts; s += 32) top = fmaxf(top, p.x.part_sums[at(s)].x);
   top = group_max<32>(top);
   const float ref = top == -INFINITY ? 0.f : top;
   constexpr int V = kDim / 32;  // dims of a lane, four at a time
   float acc[V] = {};
   float sum = 0.f;
-  constexpr int FLIGHT = 4;  // parts whose outputs are loaded together
   for (int s0 = 0; s0 < parts; s0 += FLIGHT) {
-    float w[FLIGHT];
+    float2 w[FLIGHT];
     float4 v[FLIGHT][V / 4];
 #pragma unroll
     for (int u = 0; u < FLIGHT; ++u) {
-      w[u] = -INFINITY;
+      w[u].x = -INFINITY;
       if (s0 + u >= parts) continue;
-      w[u] = p.x.part_lse[at(s0 + u)];
+      w[u] = p.x.part_sums[at(s0 + u)];
       const float4* from = reinterpret_cast<const float4*>(p.x.part_o + at(s0 + u) * kDim) + lane;
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) v[u][k] = from[32 * k];
     }
 #pragma unroll
     for (int u = 0; u < FLIGHT; ++u) {
-      if (w[u] == -INFINITY) continue;  // a part without an entry
-      const float g = exp2f(w[u] - ref);
+      if (w[u].x == -INFINITY) continue;  // a part without an entry
+      const float g = exp2f(w[u].x - ref) * w[u].y;
       sum += g;
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) {
@@ -908,7 +916,7 @@ cudaError_t launch(const LatentParams& p, const Plan& s, cudaStream_t stream) {
 
 int64_t latent_attn_workspace(int64_t num_tokens, int num_heads, int list_width) {
   const Plan s = plan_for(num_tokens, num_heads, list_width);
-  return s.parts ? s.ctas * 2 * s.heads * (kDim + 1) * 4 : 0;
+  return s.parts ? s.ctas * 2 * s.heads * (kDim + 2) * 4 : 0;
 }
 
 cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t stream) {
@@ -930,7 +938,7 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t stream) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   if (s.parts) {
     p.part_o = static_cast<float*>(a.workspace);
-    p.part_lse = p.part_o + s.ctas * 2 * s.heads * kDim;
+    p.part_sums = reinterpret_cast<float2*>(p.part_o + s.ctas * 2 * s.heads * kDim);
   }
   p.errors = a.errors;
   p.wait_polls = tile_wait_limit();
@@ -946,8 +954,11 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t stream) {
   j.ctas = (int)s.ctas;
   j.heads = s.heads;
   const int64_t grid = (int64_t)a.num_tokens * ((a.num_heads + kJoinWarps - 1) / kJoinWarps);
-  return launch_kernel(latent_join_kernel, dim3((unsigned)grid), dim3(kJoinWarps * 32), 0, stream,
-                       j);
+  // Few rows wait for their loads, many for the SMs' registers: 2 x 64 rows 23.8 us with two
+  // parts in flight and 19.9 with eight, 152 x 64 rows 96.3 and 108.1.
+  return launch_kernel((int64_t)a.num_tokens * a.num_heads <= 512 ? latent_join_kernel<8>
+                                                                  : latent_join_kernel<2>,
+                       dim3((unsigned)grid), dim3(kJoinWarps * 32), 0, stream, j);
 }
 
 }  // namespace kvq
