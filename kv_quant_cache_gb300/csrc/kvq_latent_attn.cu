@@ -539,9 +539,12 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     // of entry i of the half warp's: its slot (-1: none) and the exponents of the quarter
     int slot = -1;
     uint32_t ex = 0;
+    bool listed = true;  // (a tile whose list did not come is not handed over)
     auto next_slots = [&](uint32_t tile) {
       slot = -1;
-      if (tile >= (uint32_t)left || !await(kListFull + tile % kAhead, list_phase(tile))) return;
+      if (tile >= (uint32_t)left) return;
+      listed = await(kListFull + tile % kAhead, list_phase(tile));
+      if (!listed) return;
       slot = lists[tile % kAhead * kKeys + key0 + STRIDE * i];
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(kListEmpty + tile % kAhead));
@@ -577,7 +580,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         }
       };
       read();
-      for (int tile = 0; tile < left; ++tile) {
+      for (int tile = 0; listed && tile < left; ++tile) {
         uint32_t strange = large();
 #pragma unroll
         for (int k = 0; k < N; ++k)
@@ -637,7 +640,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         }
       };
       read();
-      for (int tile = 0; tile < left; ++tile) {
+      for (int tile = 0; listed && tile < left; ++tile) {
         uint32_t strange = large();
 #pragma unroll
         for (int k = 0; k < N; ++k) strange = nan_bits(strange, code[k], f);
