@@ -694,15 +694,15 @@ def paged_kv4_gather(kv_cache, slots, k=None, v=None, stream=None, errors=None):
         raise ValueError("slots must be a 1-D int64 tensor")
     shape = (slots.shape[0], Hkv, D)
     dev = _home(kv_cache, slots, k, v, errors)
+    cache_ptr, slots_ptr = _ptr(kv_cache, _U8, dev, "kv_cache"), _ptr(slots, _I64T, dev, "slots")
     if k is None:
         k = _new(shape, _BF16, dev, stream)
     if v is None:
         v = _new(shape, _BF16, dev, stream)
     if k.shape != shape or v.shape != shape:
         raise ValueError("k and v must be [len(slots), Hkv, head_dim]")
-    _launch(dev, stream, (_LIB or lib()).paged_kv4_gather, _ptr(kv_cache, _U8, dev, "kv_cache"),
-            N, Hkv, page, D, _ptr(slots, _I64T, dev, "slots"), shape[0], _ptr(k, _BF16, dev, "k"),
-            _ptr(v, _BF16, dev, "v"), _counted(errors, dev))
+    _launch(dev, stream, (_LIB or lib()).paged_kv4_gather, cache_ptr, N, Hkv, page, D, slots_ptr,
+            shape[0], _ptr(k, _BF16, dev, "k"), _ptr(v, _BF16, dev, "v"), _counted(errors, dev))
     return k, v
 
 
@@ -799,9 +799,9 @@ def set_stage_wait_limit(polls: int) -> int:
 
 
 def set_tile_wait_limit(polls: int) -> int:
-    """Polls of a barrier before a CTA of the shared prefix's tensor-core tiles
-    gives up, and its rows become NaN (0: without a poll); returns the previous
-    limit."""
+    """Polls of a barrier before a CTA of the tensor-core tiles (shared prefix,
+    latent attention) gives up, and its rows become NaN (0: without a poll);
+    returns the previous limit."""
     return lib().kvq_set_tile_wait_limit(int(polls))
 
 
