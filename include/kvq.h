@@ -508,7 +508,8 @@ kvq_status paged_kv4_gather(const void* kv_cache, int64_t num_pages, int num_hea
  * out = softmax(scale q K^T) V per query head, K and V the values that the codes
  * stand for.  Scores, softmax statistics and sums in fp32; the product of a
  * softmax numerator with the scale of V is rounded to bf16 for the product with
- * V's codes, the output once at the end.
+ * V's codes, the output once at the end.  The scale of a group of K times `scale`
+ * and log2(e) has to be finite.
  */
 int64_t paged_kv4_attention_workspace(int64_t num_tokens, int64_t tokens_per_request,
                                       int num_heads_q, int num_heads_kv, int head_dim,

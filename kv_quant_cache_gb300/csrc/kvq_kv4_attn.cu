@@ -1,7 +1,7 @@
 // kvq_kv4_attn.cu -- attention over the paged cache held in 4 bits, for the few
 // query rows of a decode step or a short chunk.
 //
-// One cluster of 1..8 CTAs takes up to 8, 16 or 32 query rows of one request and kv
+// One cluster of 1..8 CTAs takes up to 8, 16, 24 or 32 query rows of one request and kv
 // head (tokens x heads of the group) and the request's keys, its CTAs a part each.
 // A warp works alone on every kWarps-th group of 16 keys, with an online softmax of
 // its own.  With q_j the row's dims of group j of 64, and n = c - 8 the codes:
@@ -9,11 +9,12 @@
 //   O_j = sum_k (P_k s_kj) n_kj + sum_k P_k z_kj
 // so no code is ever multiplied by its scale: codes become bf16 integers by a
 // mask and a product, two at a time, and go straight into 16x8x16
-// matrix instructions; K's scales and zeros are applied to S in fp32, V's scales
-// to the weights P, whose product is rounded once to bf16 (the row sum adds the
-// unrounded P), V's zeros to P in fp32.  Every second code comes out as a quarter of
-// n: the other dims of Q are divided by 4 (exact), S multiplied by it, and so are those
-// dims of O.
+// matrix instructions.  K's scales (times `scale`) are applied to S in fp32; K's zeros,
+// bf16 as they are, meet scale sum(q_j) in three bf16 values (24 bits of it) in one more
+// matrix instruction; V's scales are applied to the weights P, whose product is rounded
+// once to bf16 (the row sum adds the unrounded P), V's zeros to P in fp32.  Every second
+// code comes out as a quarter of n: the other dims of Q are divided by 4 (exact), S
+// multiplied by it, and so are those dims of O.
 //
 // The codes are the first operand of both products, S^T = K Q^T and O^T = V^T P^T:
 // 16 keys (or dims) against 8 rows, so that the 1 to 8 rows that most models have to
@@ -23,7 +24,7 @@
 //
 // The reference of a row's softmax moves only when a score exceeds it by more than
 // 2^8, which spares the exchange of maxima: until then weights above 1 are as exact as
-// those below.
+// those below.  (A row whose first score is infinite, of either sign, becomes NaN.)
 //
 // A group's codes come in by 16-byte asynchronous copies, three groups ahead, into
 // a ring that only this warp uses, so that there is no CTA barrier in the loop.
@@ -71,12 +72,18 @@ struct Attn4Params {
   int trigger_from;
 };
 
+// CTAs of an SM, by the registers of D dims and NT times 8 query rows
+constexpr int ctas_of(int D, int NT) {
+  // (three to an SM, of fewer registers each, were slower at 64 dims and 32 rows, 46 us
+  // for 31, and at 128 and 24, 148 for 91)
+  return D * NT <= 64 ? 5 : D * NT <= 128 ? 4 : 2;
+}
+
 // D dims, NT times 8 query rows.
 template <int D, int NT>
 struct Shape4 {
   static constexpr int kRows = 8 * NT;
-  // CTAs of an SM, by their registers
-  static constexpr int kCtas = D * NT <= 64 ? 5 : D * NT <= 128 ? 4 : 2;
+  static constexpr int kCtas = ctas_of(D, NT);
   static constexpr int kGroups = D / kv4::kGroup;
   static constexpr int kCodes = kStep * D / 2;           // bytes of 16 keys' codes
   static constexpr int kMeta = kStep * kGroups * 4;      // .. scales and zeros
@@ -159,6 +166,25 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The upper halves of two words.
+__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) {
+  return __byte_perm(a, b, 0x7632);
+}
+
+// N words at once
+template <int N>
+__device__ __forceinline__ void words(uint32_t (&w)[N], const uint32_t* from) {
+  if (N == 1) {
+    w[0] = *from;
+  } else if (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(from);
+    w[0] = x.x, w[N > 1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(from);
+    w[0] = x.x, w[N > 1] = x.y, w[N > 2 ? 2 : 0] = x.z, w[N > 2 ? 3 : 0] = x.w;
+  }
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, Shape4<D, NT>::kCtas)
@@ -272,7 +298,9 @@ attn4_kernel(const Attn4Params p) {
   // ---- Q fragments --------------------------------------------------------------------
   // row 8 n + g; step s of group j: dims 64 j + 16 t + 2 s + {0, 1} and those 8 further
   uint32_t qf[NT][D / 16][2];
-  float qsum[NT][GROUPS][2];  // a quarter of it, of rows 8 n + 2 t and the next
+  // sum(q_j) scale / 4 of row 8 n + g in three bf16 values, at the columns of z below (of
+  // one group: values 0 to 2 at columns 0 to 2; of more: value t at 2 t + {0, 1} + {0, 8})
+  uint32_t qz[NT][GROUPS == 4 ? 2 : 1];
   int sees[NT][2];            // .. and the keys they see
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -280,6 +308,7 @@ attn4_kernel(const Attn4Params p) {
     const int u = (row0 + r) / p.group;
     const __nv_bfloat16* src =
         p.q + (t0 + u) * p.q_stride + (int64_t)(kv_head * p.group + row0 + r - u * p.group) * D;
+    qz[n][0] = qz[n][GROUPS / 4] = 0;
 #pragma unroll
     for (int j = 0; j < GROUPS; ++j) {
       uint4 a = make_uint4(0, 0, 0, 0), b = a;
@@ -298,9 +327,18 @@ attn4_kernel(const Attn4Params p) {
       }
       sum += __shfl_xor_sync(kFullMask, sum, 1);
       sum += __shfl_xor_sync(kFullMask, sum, 2);
+      sum *= 0.25f * p.scale_log2;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        qsum[n][j][c] = 0.25f * __shfl_sync(kFullMask, sum, 4 * (2 * t + c));
+      for (int k = 0; k < 3; ++k) {
+        const __nv_bfloat16 x = __float2bfloat16_rn(sum);
+        sum -= __bfloat162float(x);
+        const uint32_t bits = __bfloat16_as_ushort(x);
+        if (GROUPS == 1) {
+          if (t == k / 2) qz[n][0] |= bits << (16 * (k % 2));
+        } else {
+          if (t == k) qz[n][j / 2] |= bits << (16 * (j % 2));
+        }
+      }
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) sees[n][c] = __shfl_sync(kFullMask, len, 8 * n + 2 * t + c);
@@ -337,11 +375,21 @@ attn4_kernel(const Attn4Params p) {
     const int key0 = (first + i * kWarps) * kStep;
 
     // ---- S^T: keys g and g + 8 (of key_of), rows 2 t and 2 t + 1 ---------------------------
-    float s[NT][4];
+    // in quarters, of units of log2; first the zeros' part
+    uint32_t meta[2][GROUPS];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int h = 0; h < 2; ++h) words(meta[h], km + key_of(h, g) * GROUPS);
+    float s[NT][4];
+    const uint32_t z[4] = {highs(meta[0][0], meta[0][GROUPS > 1]),
+                           highs(meta[1][0], meta[1][GROUPS > 1]),
+                           GROUPS == 4 ? highs(meta[0][GROUPS / 2], meta[0][GROUPS - 1]) : 0,
+                           GROUPS == 4 ? highs(meta[1][GROUPS / 2], meta[1][GROUPS - 1]) : 0};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+      mma(s[n], z, qz[n][0], GROUPS == 4 ? qz[n][GROUPS / 4] : 0);
+    }
 #pragma unroll
     for (int j = 0; j < GROUPS; ++j) {
       uint2 w[2];
@@ -364,18 +412,17 @@ attn4_kernel(const Attn4Params p) {
       part(3, [&](uint32_t x) { return high_codes(x >> 8); });
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t meta = km[key_of(h, g) * GROUPS + j];
-        const float sk = low(meta), zk = high(meta);
+        const float sk = low(meta[h][j]) * p.scale_log2;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            s[n][2 * h + c] = fmaf(sk, raw[n][2 * h + c], fmaf(zk, qsum[n][j][c], s[n][2 * h + c]));
+            s[n][2 * h + c] = fmaf(sk, raw[n][2 * h + c], s[n][2 * h + c]);
       }
     }
 
     // ---- softmax, in units of log2 ----------------------------------------------------------
-    bool moved = false;
+    float y[NT][4], above = -INFINITY;  // less the references
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -383,18 +430,18 @@ attn4_kernel(const Attn4Params p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float& x = s[n][2 * h + c];
-          x = 4.f * x * p.scale_log2;
           if (!ALL && key0 + key_of(h, g) >= sees[n][c]) x = -INFINITY;
+          y[n][2 * h + c] = fmaf(4.f, x, -m[n][c]);
         }
         // (from -inf on every score exceeds it; -inf itself does not)
-        moved |= fmaxf(s[n][c], s[n][2 + c]) > m[n][c] + kRescaleAt;
+        above = fmaxf(above, fmaxf(y[n][c], y[n][2 + c]));
       }
-    if (__any_sync(kFullMask, moved)) {
+    if (__any_sync(kFullMask, above > kRescaleAt)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(m[n][c], fmaxf(s[n][c], s[n][2 + c]));
+          float top = fmaxf(m[n][c], 4.f * fmaxf(s[n][c], s[n][2 + c]));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 4));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 8));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 16));
@@ -406,26 +453,31 @@ attn4_kernel(const Attn4Params p) {
           for (int k = 0; k < D / 16; ++k) o[n][k][c] *= f, o[n][k][2 + c] *= f;
 #pragma unroll
           for (int j = 0; j < GROUPS; ++j) zeros[n][j][c] *= f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) y[n][2 * h + c] = fmaf(4.f, s[n][2 * h + c], -top);
         }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float ref = m[n][c] == -INFINITY ? 0.f : m[n][c];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s[n][2 * h + c] = ex2(s[n][2 * h + c] - ref);
+        for (int h = 0; h < 2; ++h) {
+          s[n][2 * h + c] = ex2(y[n][2 * h + c]);
+          if (!ALL && key0 + key_of(h, g) >= sees[n][c]) s[n][2 * h + c] = 0.f;
+        }
         l[n][c] += s[n][c] + s[n][2 + c];
       }
 
     // ---- O^T --------------------------------------------------------------------------------
 #pragma unroll
+    for (int h = 0; h < 2; ++h) words(meta[h], vm + key_of(h, g) * GROUPS);
+#pragma unroll
     for (int j = 0; j < GROUPS; ++j) {
       uint32_t b[NT][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t meta = vm[key_of(h, g) * GROUPS + j];
-        const float sv = low(meta), zv = high(meta);
+        const float sv = low(meta[h][j]), zv = high(meta[h][j]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float e[2];
@@ -594,7 +646,7 @@ attn4_kernel(const Attn4Params p) {
 // ---- launch ------------------------------------------------------------------------------
 
 struct Spread4 {
-  int rows;  // of a tile: 8, 16 or 32
+  int rows;  // of a tile: 8, 16, 24 or 32
   int tiles;
   int64_t units;
   int cluster, splits;
@@ -610,12 +662,12 @@ Spread4 spread4(int64_t num_tokens, int per_request, int num_heads_q, int num_he
                 int head_dim, int page_size, int table_width) {
   Spread4 s;
   const int64_t rows = (int64_t)num_heads_q / num_heads_kv * per_request;
-  s.rows = rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
-  s.tiles = (int)((rows + s.rows - 1) / s.rows);
+  const int limit = head_dim == 256 ? 16 : 32;
+  s.tiles = (int)((rows + limit - 1) / limit);
+  s.rows = (int)((rows + s.tiles * 8 - 1) / (s.tiles * 8)) * 8;
   s.units = num_tokens / per_request * num_heads_kv * s.tiles;
   const int64_t keys = (int64_t)table_width * page_size;
-  const int size = head_dim * (s.rows / 8);
-  const int64_t resident = 152 * (size <= 64 ? 5 : size <= 128 ? 4 : 2);
+  const int64_t resident = 152 * ctas_of(head_dim, s.rows / 8);
   s.cluster = 1, s.part_steps = 0;
   while (s.cluster < kMaxCluster && s.units * s.cluster * 2 <= resident &&
          keys >= (int64_t)s.cluster * 2 * 2 * kStep * kWarps)
@@ -695,9 +747,11 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t stream) {
   switch (x.head_dim + s.rows) {
     case 64 + 8: e = launch4<64, 1>(p, s.units, stream); break;
     case 64 + 16: e = launch4<64, 2>(p, s.units, stream); break;
+    case 64 + 24: e = launch4<64, 3>(p, s.units, stream); break;
     case 64 + 32: e = launch4<64, 4>(p, s.units, stream); break;
     case 128 + 8: e = launch4<128, 1>(p, s.units, stream); break;
     case 128 + 16: e = launch4<128, 2>(p, s.units, stream); break;
+    case 128 + 24: e = launch4<128, 3>(p, s.units, stream); break;
     case 128 + 32: e = launch4<128, 4>(p, s.units, stream); break;
     case 256 + 8: e = launch4<256, 1>(p, s.units, stream); break;
     case 256 + 16: e = launch4<256, 2>(p, s.units, stream); break;
