@@ -679,10 +679,11 @@ const char* kvq_prefix_config_name(int id);
 int kvq_set_prefix_config(int id);
 
 /*
- * Every wait on a barrier inside the tensor-core tiles polls at most `polls`
- * times (default 1 << 24) and for about a second.  Where one runs out, its CTA
- * lets its copies and matrix instructions in flight land (bounded by the clock
- * alone) and ends; the rows that it has not finished become NaN, and something
+ * Every wait on a barrier inside the tensor-core tiles (of the shared prefix, of
+ * dsv4_latent_attention) polls at most `polls` times (default 1 << 24) and for
+ * about a second.  Where one runs out, its CTA lets its copies and matrix
+ * instructions in flight land (bounded by the clock alone) and ends; the rows
+ * that it has not finished become NaN, and something
  * is added to *error_count.  0: the softmax's run out without a poll (tests).
  * Applies to launches enqueued after the call; returns the previous limit.
  * Not synchronised with launches on other threads.
