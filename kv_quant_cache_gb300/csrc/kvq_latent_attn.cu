@@ -895,10 +895,16 @@ struct Plan {
 
 Plan plan_for(int64_t num_tokens, int num_heads, int list_width) {
   Plan s;
+  const int64_t tiles = list_width > kKeys ? (list_width + kKeys - 1) / kKeys : 1;
+  // As many heads to a unit as there are, up to 64, while that leaves less than half of
+  // the SMs idle: fewer are more units, each quicker through its tile's steps (one token of
+  // 64 heads x 2051 entries 18.0 us in 17 tiles, 14.5 in 68 of 16 heads).
   s.heads = num_heads <= 16 ? 16 : num_heads <= 32 ? 32 : 64;
+  while (s.heads > 16 &&
+         num_tokens * ((num_heads + s.heads - 1) / s.heads) * tiles * 2 <= kCtas)
+    s.heads /= 2;
   s.blocks = (num_heads + s.heads - 1) / s.heads;
   const int64_t units = num_tokens * s.blocks;
-  const int64_t tiles = list_width > kKeys ? (list_width + kKeys - 1) / kKeys : 1;
   s.parts = s.shared_out = units <= kSharedUnits && tiles > 1;
   s.ctas = !s.shared_out ? units : units * tiles < kCtas ? units * tiles : kCtas;
   return s;

@@ -26,7 +26,7 @@ def case(T, H, K, seed=1):
     return [q.cuda(), cache.cuda(), slots.cuda(), lens.cuda()], *want
 
 
-@pytest.mark.parametrize("T,H,K", [(3, 64, 1500), (40, 20, 700), (620, 2, 300)])
+@pytest.mark.parametrize("T,H,K", [(3, 64, 1500), (40, 20, 700), (60, 64, 700), (620, 2, 300)])
 def test_rows_of_a_wait_that_ran_out_are_marked(cuda_device, T, H, K):
     """A call ends in time; what a CTA that gave up has not computed becomes NaN and is
     counted, nothing that the workspace held gets out, and the next call is whole.

@@ -191,6 +191,32 @@ def test_latent_tokens_around_what_is_shared_out(cuda_device, T, H, K):
     assert torch.equal(bits(got), bits(kvq.dsv4_latent_attention(*args)))
 
 
+@pytest.mark.parametrize("H", [16, 30, 64, 100])
+def test_latent_lengths_of_many_tokens(cuda_device, H):
+    """Enough tokens that their blocks of heads are as wide as they get: lengths around
+    the tiles' ends, lists with gaps, a token without an entry, and a NaN entry that
+    reaches its readers alone."""
+    ends = [0, 1, 2, 63, 64, 65, 127, 128, 129, 191, 256, 257, 300]
+    T = 6 * len(ends)
+    q, cache, slots, lens = latent_case(T, H, 300, seed=H)
+    lens[:] = torch.tensor(ends * 6, dtype=torch.int32)
+    slots[5] = -1
+    slots[3, :10] = -1
+    slots[8, :128] = -1
+    slots[slots == 77] = 78
+    bad = [17, 38, 77]
+    slots[bad, 0] = 77
+    args = [x.cuda() for x in (q, cache, slots, lens)]
+    want = ref4.latent_attention(q, cache, slots, lens, 512 ** -0.5)
+    ref.check(kvq.dsv4_latent_attention(*args), *want)
+    args[1][77, 0, 130] = 0x7f  # a NaN code
+    got = kvq.dsv4_latent_attention(*args).cpu()
+    seen = torch.zeros(T, dtype=torch.bool)
+    seen[bad] = True
+    assert bool(got[seen].isnan().all())
+    ref.check(got[~seen], want[0][~seen], want[1][~seen])
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("per,G", [(1, 1), (1, 8), (3, 3), (2, 8), (17, 1), (4, 8), (33, 1), (9, 7)])
 def test_rows_of_a_tile(cuda_device, D, per, G):

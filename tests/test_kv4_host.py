@@ -151,7 +151,9 @@ def test_workspace_sizes(L):
     assert f(4, 2, 4, 2, 128, 16, 0) == f(256, 1, 32, 8, 128, 64, 8) == 0
     assert g(4, 4, 0) == g(1, 64, 128) == g(5000, 128, 2048) == 0
     # two partial rows of 512 sums, a reference and a sum of weights per head and CTA
-    assert g(1, 64, 4096) == 32 * 2 * 64 * 514 * 4
+    assert g(1, 64, 4096) == 128 * 2 * 16 * 514 * 4  # of four times 16 heads
+    assert g(2, 64, 4096) == 128 * 2 * 32 * 514 * 4
+    assert g(8, 64, 4096) == 152 * 2 * 64 * 514 * 4
     assert g(64, 64, 2048) == 152 * 2 * 64 * 514 * 4
     assert g(64, 20, 2048) == 152 * 2 * 32 * 514 * 4
 
