@@ -26,6 +26,7 @@
 // the lists' actual lengths; a unit that falls to several CTAs goes to partials,
 // which a second launch joins.  With many units a CTA takes one.
 #include <cstring>
+#include <type_traits>
 
 #include "kvq_dsv4_entry.cuh"
 #include "kvq_paged_attn.cuh"
@@ -260,6 +261,9 @@ struct Segments {
   __device__ __forceinline__ bool whole() const { return n == tiles; }
 };
 
+template <int K>
+using I = std::integral_constant<int, K>;
+
 template <int NH>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_tiles_kernel(const __grid_constant__ LatentParams p) {
@@ -352,7 +356,8 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
 #pragma unroll
       for (int c = 0; c < COLS; ++c) l[c] = 0.f;
       for (int j = 0; j < seg.n; ++j, ++done) {
-        const bool ready = p.wait_polls != 0 && await(kListFull + done % kAhead, list_phase(done)) &&
+        const bool ready = p.wait_polls != 0 &&
+                           await(kListFull + done % kAhead, list_phase(done)) &&
                            await(kSFull, done & 1);
         if (!ready) *dead = *quit = 1;
         const bool there = ready && lists[done % kAhead * kKeys + r] >= 0;
@@ -534,11 +539,17 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     // The thread has fragment i of the quarter (8 dims; of the last one four coded dims and
     // four rotary ones) of 16 entries, 8 apart: the same place in the swizzle.
     const int i = lane & 15, key0 = 2 * (warp & 3) + (lane >> 4);
-    // Half of them are decoded before their place is free, as far as registers go.
-    constexpr int N = 16, STRIDE = kKeys / N, EARLY = 8;
-    // of entry i of the half warp's: its slot (-1: none) and the exponents of the quarter
+    // EARLY of them are decoded before their place is free, as far as registers go; with
+    // many heads as many of the next tile's are read then too: the loads, a burst that
+    // shared memory accesses wait behind, are then not all under way while the softmax is
+    // (16 x 128 heads x 16384 entries 129 -> 115 us; few heads wait for the loads instead,
+    // and with 32 all of it was 2 % slower).
+    constexpr bool AHEAD = NH > 32;
+    constexpr int N = 16, STRIDE = kKeys / N, EARLY = AHEAD ? 4 : 8;
+    // of entry i of the half warp's: its slot (-1: none) and the exponents of the quarter,
+    // those of the next tile as soon as its list is looked up
     int slot = -1;
-    uint32_t ex = 0;
+    uint32_t ex = 0, next_ex = 0;
     bool listed = true;  // (a tile whose list did not come is not handed over)
     auto next_slots = [&](uint32_t tile) {
       slot = -1;
@@ -551,9 +562,9 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     };
     auto slot_of = [&](int k) { return __shfl_sync(kFullMask, slot, (lane & 16) + k); };
     auto read_scales = [&]() {
-      ex = slot < 0 ? 0
-                    : __ldg(reinterpret_cast<const uint32_t*>(p.cache + (int64_t)slot * dsv4::kEntry +
-                                                              dsv4::kScaleAt + 4 * (quarter >> 1)));
+      const uint8_t* e =
+          p.cache + (int64_t)slot * dsv4::kEntry + dsv4::kScaleAt + 4 * (quarter >> 1);
+      next_ex = slot < 0 ? 0 : __ldg(reinterpret_cast<const uint32_t*>(e));
     };
     // bytes over 134, or a NaN code: the whole warp decodes the long way
     auto large = [&]() { return ((ex & 0x7f7f7f7fu) + 0x79797979u) & ex; };
@@ -565,21 +576,22 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
     };
     next_slots(0);
     read_scales();
+    ex = next_ex;
     if (quarter < 3) {
       uint8_t* x_at = smem + L::kX + (2 * quarter + (i >> 3)) * L::kChunk + key0 * 128 +
                       (((i & 7) ^ (key0 & 7)) << 4);
       const uint32_t which = 0x4440 + 2 * (quarter & 1) + (i >> 3);  // the fragment's exponent
       uint2 code[N];
-      auto read = [&]() {
+      auto read = [&](auto from, auto to) {  // the codes of entries from .. to - 1
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
+        for (int k = from.value; k < to.value; ++k) {
           const int of = slot_of(k);
           const uint8_t* e = p.cache + (int64_t)of * dsv4::kEntry + 128 * quarter + 8 * i;
           code[k] = make_uint2(0, 0);
           if (of >= 0) code[k] = __ldg(reinterpret_cast<const uint2*>(e));
         }
       };
-      read();
+      read(I<0>(), I<N>());
       for (int tile = 0; listed && tile < left; ++tile) {
         uint32_t strange = large();
 #pragma unroll
@@ -592,6 +604,10 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         // not before the last tile's weights are there: the softmax, which everything
         // waits for, would share its issue slots with all this
         if (tile > 0 && !await(kPFull, (tile - 1) & 1)) break;
+        if (AHEAD) {
+          next_slots(tile + 1);
+          read_scales();
+        }
         // (two ways with a branch around each: with the choice made entry by entry both
         // were gone for every one, and a quarter took 2850 cycles instead of 1100)
         uint4 early[EARLY];
@@ -603,6 +619,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           for (int k = 0; k < EARLY; ++k)
             early[k] = dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte_of(k)));
         }
+        if (AHEAD) read(I<0>(), I<EARLY>());
         if (tile > 0 && !await(kXEmpty + quarter, (tile - 1) & 1)) break;
 #pragma unroll
         for (int k = 0; k < EARLY; ++k)
@@ -618,18 +635,22 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
                 dsv4::dequant8(code[k], dsv4::ue8m0_scale(byte_of(k)));
         }
         hand_over();
-        next_slots(tile + 1);
-        read_scales();
-        read();
+        if (!AHEAD) {
+          next_slots(tile + 1);
+          read_scales();
+          read(I<0>(), I<EARLY>());
+        }
+        read(I<EARLY>(), I<N>());
+        ex = next_ex;
       }
     } else {
       uint8_t* x_at =
           smem + L::kX + 6 * L::kChunk + key0 * 128 + (((i >> 1) ^ (key0 & 7)) << 4) + 8 * (i & 1);
       uint32_t code[N];
       uint2 rope[N];
-      auto read = [&]() {
+      auto read = [&](auto from, auto to) {  // the codes of entries from .. to - 1
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
+        for (int k = from.value; k < to.value; ++k) {
           const int of = slot_of(k);
           const uint8_t* e = p.cache + (int64_t)of * dsv4::kEntry;
           code[k] = 0, rope[k] = make_uint2(0, 0);
@@ -639,7 +660,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           }
         }
       };
-      read();
+      read(I<0>(), I<N>());
       for (int tile = 0; listed && tile < left; ++tile) {
         uint32_t strange = large();
 #pragma unroll
@@ -661,6 +682,10 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           *reinterpret_cast<uint2*>(x_at + STRIDE * k * 128 + L::kChunk) = rope[k];
         };
         if (tile > 0 && !await(kPFull, (tile - 1) & 1)) break;
+        if (AHEAD) {
+          next_slots(tile + 1);
+          read_scales();
+        }
         uint2 early[EARLY];
         if (!odd) {
 #pragma unroll
@@ -672,6 +697,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
         if (tile > 0 && !await(kXEmpty + quarter, (tile - 1) & 1)) break;
 #pragma unroll
         for (int k = 0; k < EARLY; ++k) put(k, early[k]);
+        if (AHEAD) read(I<0>(), I<EARLY>());
         if (!odd) {
 #pragma unroll
           for (int k = EARLY; k < N; ++k) put(k, decoded(k));
@@ -680,9 +706,13 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
           for (int k = EARLY; k < N; ++k) put(k, decoded_odd(k));
         }
         hand_over();
-        next_slots(tile + 1);
-        read_scales();
-        read();
+        if (!AHEAD) {
+          next_slots(tile + 1);
+          read_scales();
+          read(I<0>(), I<EARLY>());
+        }
+        read(I<EARLY>(), I<N>());
+        ex = next_ex;
       }
     }
   } else if (warp == kMmaWarp) {
