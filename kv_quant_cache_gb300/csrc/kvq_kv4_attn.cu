@@ -653,11 +653,14 @@ struct Spread4 {
   int part_steps;
 };
 
-// CTAs are added while all of them are resident at once and each keeps at least
-// two steps for every warp: first within a cluster, joined in place; beyond that as
-// partials that a second launch joins.  Where there are more row tiles than that, a
-// long range is cut in parts of 2048 keys all the same: lengths differ, and the
-// last tiles of a wave would keep a few SMs busy alone.
+// CTAs are added while all of them are resident at once and each keeps at least two
+// steps for every warp: first within a cluster, joined in place; beyond that as partials
+// that a second launch joins.  Where no more fit, a long range is cut in parts of 2048
+// keys instead (of 4096 where that is six waves of CTAs all the same): lengths differ,
+// and the last tiles of a wave would keep a few SMs busy alone.  What a cluster holds at
+// once is not cut if its CTAs have about as little as that (16 x 8 heads of 16 rows, 8192
+// keys: 56 us in clusters of 2, 67 in parts), unless they leave many places empty (20 x 8
+// heads of 8 rows: 52 us in clusters of 2, 48 in parts).
 Spread4 spread4(int64_t num_tokens, int per_request, int num_heads_q, int num_heads_kv,
                 int head_dim, int page_size, int table_width) {
   Spread4 s;
@@ -672,13 +675,16 @@ Spread4 spread4(int64_t num_tokens, int per_request, int num_heads_q, int num_he
   while (s.cluster < kMaxCluster && s.units * s.cluster * 2 <= resident &&
          keys >= (int64_t)s.cluster * 2 * 2 * kStep * kWarps)
     s.cluster *= 2;
+  const bool full = s.units * s.cluster * 4 >= resident * 3;
   int64_t splits = 1;
   if (s.units * s.cluster * 2 <= resident) {
     while (s.units * s.cluster * (splits + 1) <= resident && keys > s.cluster * splits * 1024)
       ++splits;
-  } else if (keys >= (int64_t)s.cluster * 4096) {
-    s.part_steps = 2048 / kStep;
-    splits = (keys + s.cluster * 2048 - 1) / (s.cluster * 2048);
+  } else if (keys >= 4096 && (keys + 2047) / 2048 > s.cluster * (full && s.cluster > 1 ? 2 : 1)) {
+    s.cluster = 1;
+    const int part = s.units * (keys / 4096) >= 6 * resident ? 4096 : 2048;
+    s.part_steps = part / kStep;
+    splits = (keys + part - 1) / part;
     if (splits > 65535) splits = 65535, s.part_steps = 0;
   }
   s.splits = (int)splits;
