@@ -695,14 +695,20 @@ def paged_kv4_gather(kv_cache, slots, k=None, v=None, stream=None, errors=None):
     shape = (slots.shape[0], Hkv, D)
     dev = _home(kv_cache, slots, k, v, errors)
     cache_ptr, slots_ptr = _ptr(kv_cache, _U8, dev, "kv_cache"), _ptr(slots, _I64T, dev, "slots")
+    if (k is not None and k.shape != shape) or (v is not None and v.shape != shape):
+        raise ValueError("k and v must be [len(slots), Hkv, head_dim]")
     if k is None:
         k = _new(shape, _BF16, dev, stream)
+        k_ptr = k.data_ptr()
+    else:
+        k_ptr = _ptr(k, _BF16, dev, "k")
     if v is None:
         v = _new(shape, _BF16, dev, stream)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("k and v must be [len(slots), Hkv, head_dim]")
+        v_ptr = v.data_ptr()
+    else:
+        v_ptr = _ptr(v, _BF16, dev, "v")
     _launch(dev, stream, (_LIB or lib()).paged_kv4_gather, cache_ptr, N, Hkv, page, D, slots_ptr,
-            shape[0], _ptr(k, _BF16, dev, "k"), _ptr(v, _BF16, dev, "v"), _counted(errors, dev))
+            shape[0], k_ptr, v_ptr, _counted(errors, dev))
     return k, v
 
 
