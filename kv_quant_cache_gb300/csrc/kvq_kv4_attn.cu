@@ -89,6 +89,10 @@ template <int D, int NT>
 struct Shape4 {
   static constexpr int kRows = 8 * NT;
   static constexpr int kCtas = ctas_of(D, NT);
+  // Steps of the loop's body: four make places in the ring constants (64 sequences x 32768
+  // keys 392 -> 384 us, 40 x 8 heads of 64 dims x 8192 keys 60 -> 53), where registers are
+  // left for it (24 rows of 128 dims 71 -> 73, 16 of 256 61 -> 63).
+  static constexpr int kUnroll = D * NT <= 256 && D < 256 ? 4 : D == 256 ? 2 : 1;
   static constexpr int kGroups = D / kv4::kGroup;
   static constexpr int kCodes = kStep * D / 2;           // bytes of 16 keys' codes
   static constexpr int kMeta = kStep * kGroups * 4;      // .. scales and zeros
@@ -523,15 +527,23 @@ attn4_kernel(const Attn4Params p) {
       }
     }
   };
-  for (int i = 0; i < steps; ++i) {
+  auto turn = [&](int i, auto all_seen) {
     issue(i + kStages - 1);
     copy_wait<kStages - 1>();
     __syncwarp();
-    if (outside >> (i & 31) & 1) continue;  // (nothing was copied)
-    if ((first + i * kWarps) * kStep <= least - kStep) step(i, std::true_type());
-    else step(i, std::false_type());
+    if (!(outside >> (i & 31) & 1)) step(i, all_seen);  // (else nothing was copied)
     __syncwarp();  // the stage is read before its next copies start
+  };
+  // the steps of keys that every row sees, then the others
+  const int seen = max(0, min(steps, (least / kStep - first + kWarps - 1) / kWarps));
+  int i = 0;
+#pragma unroll 1
+  for (; i + S::kUnroll <= seen; i += S::kUnroll) {
+#pragma unroll
+    for (int k = 0; k < S::kUnroll; ++k) turn(i + k, std::true_type());
   }
+#pragma unroll 1
+  for (; i < steps; ++i) turn(i, std::false_type());
   copy_wait<0>();
   if (rejected && p.errors) atomicAdd(p.errors, 1);
   auto all_keys = [](float x) {  // the sum over the lanes that hold the same rows
