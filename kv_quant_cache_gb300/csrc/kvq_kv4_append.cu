@@ -14,9 +14,8 @@
 // Minimum and maximum of a group travel together in one register, (lo, -hi) as a
 // bf16 pair.
 // Memory bound: every row is read once, q rows are written as they came, key and
-// value rows in 9/32 of their bytes.  32768 tokens of 32 + 16 heads of 128: 148 us,
-// 4.8 TB/s; half of the issue slots then go to rotation, extrema and rounding, which
-// the loads in flight hide but for that.
+// value rows in 9/32 of their bytes.  32768 tokens of 32 + 16 heads of 128: 143 us,
+// 4.9 TB/s, two thirds of the issue slots busy with rotation, extrema and rounding.
 //
 // Read back.  A lane takes words l and l + D/16 of a row, so that a row's
 // stores are contiguous; all loads of a warp's rows are in flight together.  65536
@@ -29,6 +28,8 @@ namespace kvq {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtas = 7;                            // of an SM, append
+constexpr int64_t kLater = 152 * kCtas / 2 * kWarps;  // warps: half a wave of CTAs
 
 struct Append4Params {
   __nv_bfloat16* qkv;
@@ -148,7 +149,7 @@ __device__ __forceinline__ uint32_t codes_of(const uint4& v, uint32_t meta, bool
 
 template <int D, bool NEOX, int STEPS>
 // (seven CTAs an SM: 32768 tokens 151 us, as many as registers allowed without, 161)
-__global__ void __launch_bounds__(kWarps * 32, 7) append4_kernel(const Append4Params p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) append4_kernel(const Append4Params p) {
   constexpr int LPR = D / 16;    // lanes per row
   constexpr int RPW = 32 / LPR;  // rows per warp step
   constexpr int GROUPS = D / kv4::kGroup;
@@ -183,6 +184,18 @@ __global__ void __launch_bounds__(kWarps * 32, 7) append4_kernel(const Append4Pa
     } else {
       xa[s] = xb[s] = make_uint4(0, 0, 0, 0);
     }
+  }
+  if (STEPS > 1 && item + kLater < p.items) {
+    // rows of a warp that comes later, into the L2: without, a CTA's loads, all issued at
+    // once, take their time from memory before anything can be done (32768 tokens 143
+    // us, 150 without, 144 a whole wave ahead)
+    constexpr int LINES = RPW * D * 2 / 128, PER_ROW = D * 2 / 128;
+    const int64_t later = (item + kLater) / p.chunks;
+    const int its = (int)(item + kLater - later * p.chunks);
+    const int s = lane / LINES, line = lane % LINES;
+    const int r = p.first_row + (s * p.chunks + its) * RPW + line / PER_ROW;
+    if (s < STEPS && r < p.num_rows)
+      prefetch_l2(p.qkv + (later * p.num_rows + r) * D + line % PER_ROW * 64);
   }
   if (p.rot && (pos < 0 || pos >= p.max_pos)) {  // warp-uniform: leave the token as it is
     if (p.errors && chunk == 0 && lane == 0) atomicAdd(p.errors, 1);

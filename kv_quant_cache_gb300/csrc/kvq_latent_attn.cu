@@ -110,10 +110,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
                : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(p)) : "memory");
-}
-
 // Barriers of the softmax warps; vote: whether any thread's flag is set.
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
