@@ -267,7 +267,7 @@ attn4_kernel(const Attn4Params p) {
     }
   };
   look_up(lane, &next_codes, &next_meta);
-  uint32_t outside = 0;  // of the last 32 steps issued: bit i % 32, the page is not there
+  uint32_t outside = 0;  // of the steps in the ring: bit i % kStages, the page is not there
 
   // where the lane's fragments of a step go
   uint32_t place[S::kCodes / 512];
@@ -285,7 +285,7 @@ attn4_kernel(const Attn4Params p) {
     }
     const int64_t codes = __shfl_sync(kFullMask, codes_at, i & 31);
     const int64_t meta = __shfl_sync(kFullMask, meta_at, i & 31);
-    outside = (outside & ~(1u << (i & 31))) | ((codes < 0 ? 1u : 0u) << (i & 31));
+    outside = (outside & ~(1u << i % kStages)) | (codes < 0 ? 1u << i % kStages : 0u);
     if (codes >= 0) {
       const uint8_t* k = cache + codes + 16 * lane;
       const uint8_t* v = k + v_from_k;
@@ -531,7 +531,7 @@ attn4_kernel(const Attn4Params p) {
     issue(i + kStages - 1);
     copy_wait<kStages - 1>();
     __syncwarp();
-    if (!(outside >> (i & 31) & 1)) step(i, all_seen);  // (else nothing was copied)
+    if (!(outside & 1u << i % kStages)) step(i, all_seen);  // (else nothing was copied)
     __syncwarp();  // the stage is read before its next copies start
   };
   // the steps of keys that every row sees, then the others
