@@ -32,9 +32,9 @@
 // keys that a load touches lie in different banks; the matrix instructions may take
 // the keys in any order, and key_of() is one that does for the loads of K and of V.
 //
-// What bounds it: instructions.  A step of 16 keys of 128 dims and up to 8 rows is 390 of
-// a warp (130 decode the codes, 17 are matrix instructions), for 2.3 KB: 64 sequences x 32768
-// keys x 8 heads take 405 us, 4.5 TB/s, with 71 % of the issue slots busy.  With 24 or 32
+// What bounds it: instructions.  A step of 16 keys of 128 dims and up to 8 rows is 359 of
+// a warp (150 decode the codes, 17 are matrix instructions), for 2.3 KB: 64 sequences x 32768
+// keys x 8 heads take 378 us, 4.8 TB/s, with two thirds of the issue slots busy.  With 24 or 32
 // rows it is their latencies: 8 warps to an SM are all that registers allow.
 #include <cooperative_groups.h>
 
