@@ -22,7 +22,7 @@
 //   * warps 26 and 27: copy the queries of a unit as soon as the last scores of the unit
 //     before are done, while its outputs are still to come.
 //
-// What bounds it: shared memory.  A tile of 64 heads is 3072 cycles of operands read by
+// What bounds it: shared memory.  A tile of 64 heads is 3000 cycles of operands read by
 // the matrix instructions (A of 128 KB twice, of 64 heads as B), 1024 of X written, and
 // the entries' loads pass through the same pipe; X has room for one tile, so that its
 // products, the softmax between them and the next tile's decoding follow one another.
