@@ -648,7 +648,7 @@ kvq_status kvq_stage_events(uint64_t* fallbacks, uint64_t* drain_timeouts, int r
  * (griddepcontrol.wait; of a shared prefix's two launches the first waits for
  * all that came before, the second for the first); its one-shot launch shapes
  * then let the next kernel be scheduled (griddepcontrol.launch_dependents), its
- * persistent shapes do not.  Results and stream order are those of ordinary
+ * persistent shapes and dsv4_latent_attention do not.  Results and stream order are those of ordinary
  * launches; only the launch gaps shrink: on GB300 a 32-layer decode step
  * captured in a CUDA graph goes from 2.47 to 1.79 us per launch, a mid-size
  * step gains 3 %, and the 32768-token step is unchanged.  A kernel of the

@@ -6,10 +6,12 @@ The 4-bit cache is a decision per value, so its bytes have to be equal.
 The bound of the attention over it, element by element.  A value is v = z + s n
 with n = c - 8.  With w the exact softmax weights and n_keys keys:
   * a numerator times its key's s is rounded once to bf16: 2^-8 sum_i w_i |s n|_i;
-  * a score is sum over groups of s (q . (16 + c)) + (z - 24 s) sum(q): 64-term
-    fp32 sums of exact products and a few fp32 operations a group, so off by at
-    most ds = (D + 16) 2^-23 |scale| max_i sum_j (31 s + |z - 24 s|) sum_d |q_d|,
-    which is a relative ds of its numerator, and of the row sum again;
+  * a score is the sum over groups of s (q . n) + z sum(q), 64-term fp32 sums of exact
+    products and a few fp32 operations a group: off by at most ds = (D + 16) 2^-23 |scale|
+    max_i sum_j (31 s + |z - 24 s|) sum_d |q_d|, which is a relative ds of its
+    numerator, and of the row sum again.  (Terms are at most (8 s + |z|) |q|, 8/7 of the
+    magnitudes above; products are added sixteen at a time, so roundings are far fewer
+    than D.);
   * additions and rescalings as in the bf16 attention: (2 n_keys + 64) 2^-22;
   * the output is rounded once to bf16: 2^-8 |out|.
 """

@@ -263,3 +263,41 @@ def test_scores_far_apart(cuda_device, D):
             tol[t, h] = (ref4.EPS_BF16 * (sn[:m, 1][top].abs().mean(0) + want[t, h].abs())
                          + 2.0 ** -10 * (sn[:m, 1].abs() + z[:m, 1].abs()).amax(0))
     ref.check(got, want, tol)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 1e-30])
+@pytest.mark.parametrize("D,per", [(64, 3), (128, 1), (256, 2)])
+def test_scales_of_4_bit_scores(cuda_device, D, per, scale):
+    host = kv4_case(3, per, 8, 2, D, 16, 40, seed=D + per)
+    got = kvq.paged_kv4_attention(*(x.cuda() for x in host), tokens_per_request=per, scale=scale)
+    torch.cuda.synchronize()
+    ref.check(got, *ref4.attention(*host, scale, per_request=per))
+
+
+def test_the_largest_pages(cuda_device):
+    """65536 tokens to a page: written, read back and attended to on both sides of the
+    boundary of two pages."""
+    page, Hq, Hkv, D = 65536, 4, 2, 64
+    g = gen(9)
+    raw = ref4.random_cache(g, 3, Hkv, page, D)
+    table = torch.tensor([[2, 0], [1, 2]], dtype=torch.int32)
+    at = torch.tensor([0, 1, page - 1, page, page + 1, 2 * page - 1])
+    slots = table[0].long()[at // page] * page + at % page
+    qkv = normal(g, len(at), (Hq + 2 * Hkv) * D)
+    cache = raw.cuda()
+    kvq.paged_kv4_rope_append(qkv.cuda(), Hq, Hkv, D, None, True, None, slots.cuda(), cache)
+    torch.cuda.synchronize()
+    k, v = qkv.view(-1, Hq + 2 * Hkv, D)[:, Hq:].split(Hkv, 1)
+    codes = ref4.Cache(raw).codes.clone()
+    got = ref4.Cache(cache.cpu())
+    for which, rows in ((0, k), (1, v)):
+        codes[slots // page, which, :, slots % page] = ref4.quantise(rows)[0]
+    assert torch.equal(got.codes, codes)
+    back = kvq.paged_kv4_gather(cache, slots.cuda())
+    for x, want in zip(back, ref4.gather(cache.cpu(), slots)):
+        assert torch.equal(x.cpu(), want)
+    q = normal(g, 6, Hq, D)
+    lens = torch.tensor([page - 1, page, page + 1, 2 * page, 17, 0], dtype=torch.int32)
+    out = kvq.paged_kv4_attention(q.cuda(), cache, table.cuda(), lens.cuda(), tokens_per_request=3)
+    torch.cuda.synchronize()
+    ref.check(out, *ref4.attention(q, cache.cpu(), table, lens, D ** -0.5, per_request=3))
