@@ -34,7 +34,7 @@
 //
 // What bounds it: instructions.  A step of 16 keys of 128 dims and up to 8 rows is 359 of
 // a warp (150 decode the codes, 17 are matrix instructions), for 2.3 KB: 64 sequences x 32768
-// keys x 8 heads take 378 us, 4.8 TB/s, with two thirds of the issue slots busy.  With 24 or 32
+// keys x 8 heads take 366 us, 4.9 TB/s, with two thirds of the issue slots busy.  With 24 or 32
 // rows it is their latencies: 8 warps to an SM are all that registers allow.
 #include <cooperative_groups.h>
 
@@ -93,6 +93,10 @@ struct Shape4 {
   // keys 392 -> 384 us, 40 x 8 heads of 64 dims x 8192 keys 60 -> 53), where registers are
   // left for it (24 rows of 128 dims 71 -> 73, 16 of 256 61 -> 63).
   static constexpr int kUnroll = D * NT <= 256 && D < 256 ? 4 : D == 256 ? 2 : 1;
+  // Two steps at a time where there are few warps to hide a step's latencies, and registers
+  // for it (16 rows of 128 dims 51.5 -> 49.2 us, 24 of 64 24.7 -> 24.0, 8 of 256 105 ->
+  // 104; 32 of 64 the same, 24 of 128 71 -> 74, 32 of 128 111 -> 160).
+  static constexpr bool kPair = D * NT > 128 && D * NT <= 256 && NT < 4;
   static constexpr int kGroups = D / kv4::kGroup;
   static constexpr int kCodes = kStep * D / 2;           // bytes of 16 keys' codes
   static constexpr int kMeta = kStep * kGroups * 4;      // .. scales and zeros
@@ -374,83 +378,93 @@ attn4_kernel(const Attn4Params p) {
     }
   }
 
-  // A step of 16 keys; all: every row sees every one of them.
-  auto step = [&](int i, auto all_seen) {
+  const float q_scale = p.scale_log2;
+  // P steps of 16 keys together; all: every row sees every one of them.
+  auto step = [&](int i, auto all_seen, auto together) {
     constexpr bool ALL = decltype(all_seen)::value;
-    const uint8_t* kc = smem + warp * S::kWarp + i % kStages * S::kStage;
-    const uint8_t* vc = kc + S::kCodes;
-    const uint32_t* km = reinterpret_cast<const uint32_t*>(vc + S::kCodes);
-    const uint32_t* vm = km + kStep * GROUPS;
-    const int key0 = (first + i * kWarps) * kStep;
+    constexpr int P = decltype(together)::value;
+    auto stage = [&](int p) { return smem + warp * S::kWarp + (i + p) % kStages * S::kStage; };
+    auto seen = [&](int p, int h, int n, int c) {
+      return ALL || (first + (i + p) * kWarps) * kStep + key_of(h, g) < sees[n][c];
+    };
 
     // ---- S^T: keys g and g + 8 (of key_of), rows 2 t and 2 t + 1 ---------------------------
     // in quarters, of units of log2; first the zeros' part
-    uint32_t meta[2][GROUPS];
+    float s[P][NT][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) words(meta[h], km + key_of(h, g) * GROUPS);
-    float s[NT][4];
-    const uint32_t z[4] = {highs(meta[0][0], meta[0][GROUPS > 1]),
-                           highs(meta[1][0], meta[1][GROUPS > 1]),
-                           GROUPS == 4 ? highs(meta[0][GROUPS / 2], meta[0][GROUPS - 1]) : 0,
-                           GROUPS == 4 ? highs(meta[1][GROUPS / 2], meta[1][GROUPS - 1]) : 0};
+    for (int p = 0; p < P; ++p) {
+      const uint8_t* kc = stage(p);
+      const uint32_t* km = reinterpret_cast<const uint32_t*>(kc + 2 * S::kCodes);
+      uint32_t meta[2][GROUPS];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      for (int h = 0; h < 2; ++h) words(meta[h], km + key_of(h, g) * GROUPS);
+      const uint32_t z[4] = {highs(meta[0][0], meta[0][GROUPS > 1]),
+                             highs(meta[1][0], meta[1][GROUPS > 1]),
+                             GROUPS == 4 ? highs(meta[0][GROUPS / 2], meta[0][GROUPS - 1]) : 0,
+                             GROUPS == 4 ? highs(meta[1][GROUPS / 2], meta[1][GROUPS - 1]) : 0};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
-      mma(s[n], z, qz[n][0], GROUPS == 4 ? qz[n][GROUPS / 4] : 0);
-    }
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      uint2 w[2];
+        for (int k = 0; k < 4; ++k) s[p][n][k] = 0.f;
+        mma(s[p][n], z, qz[n][0], GROUPS == 4 ? qz[n][GROUPS / 4] : 0);
+      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[h] = *reinterpret_cast<const uint2*>(kc + piece_at<GROUPS>(key_of(h, g), j) + 8 * t);
-      float raw[NT][4];
+      for (int j = 0; j < GROUPS; ++j) {
+        uint2 w[2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) raw[n][k] = 0.f;
-      auto part = [&](int i, auto pair) {
-        const uint32_t a[4] = {pair(w[0].x), pair(w[1].x), pair(w[0].y), pair(w[1].y)};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma(raw[n], a, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
-      };
-      part(0, [&](uint32_t x) { return low_codes(x, big); });
-      part(1, [&](uint32_t x) { return high_codes(x); });
-      part(2, [&](uint32_t x) { return low_codes(x >> 8, big); });
-      part(3, [&](uint32_t x) { return high_codes(x >> 8); });
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float sk = low(meta[h][j]) * p.scale_log2;
+        for (int h = 0; h < 2; ++h)
+          w[h] = *reinterpret_cast<const uint2*>(kc + piece_at<GROUPS>(key_of(h, g), j) + 8 * t);
+        float raw[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            s[n][2 * h + c] = fmaf(sk, raw[n][2 * h + c], s[n][2 * h + c]);
+          for (int k = 0; k < 4; ++k) raw[n][k] = 0.f;
+        auto part = [&](int i, auto pair) {
+          const uint32_t a[4] = {pair(w[0].x), pair(w[1].x), pair(w[0].y), pair(w[1].y)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma(raw[n], a, qf[n][4 * j + i][0], qf[n][4 * j + i][1]);
+        };
+        part(0, [&](uint32_t x) { return low_codes(x, big); });
+        part(1, [&](uint32_t x) { return high_codes(x); });
+        part(2, [&](uint32_t x) { return low_codes(x >> 8, big); });
+        part(3, [&](uint32_t x) { return high_codes(x >> 8); });
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float sk = low(meta[h][j]) * q_scale;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              s[p][n][2 * h + c] = fmaf(sk, raw[n][2 * h + c], s[p][n][2 * h + c]);
+        }
       }
     }
 
     // ---- softmax, in units of log2 ----------------------------------------------------------
-    float y[NT][4], above = -INFINITY;  // less the references
+    float y[P][NT][4], above = -INFINITY;  // less the references
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& x = s[n][2 * h + c];
-          if (!ALL && key0 + key_of(h, g) >= sees[n][c]) x = -INFINITY;
-          y[n][2 * h + c] = fmaf(4.f, x, -m[n][c]);
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[p][n][2 * h + c];
+            if (!seen(p, h, n, c)) x = -INFINITY;
+            y[p][n][2 * h + c] = fmaf(4.f, x, -m[n][c]);
+          }
+          // (from -inf on every score exceeds it; -inf itself does not)
+          above = fmaxf(above, fmaxf(y[p][n][c], y[p][n][2 + c]));
         }
-        // (from -inf on every score exceeds it; -inf itself does not)
-        above = fmaxf(above, fmaxf(y[n][c], y[n][2 + c]));
-      }
     if (__any_sync(kFullMask, above > kRescaleAt)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(m[n][c], 4.f * fmaxf(s[n][c], s[n][2 + c]));
+          float top = m[n][c];
+#pragma unroll
+          for (int p = 0; p < P; ++p) top = fmaxf(top, 4.f * fmaxf(s[p][n][c], s[p][n][2 + c]));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 4));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 8));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 16));
@@ -463,84 +477,116 @@ attn4_kernel(const Attn4Params p) {
 #pragma unroll
           for (int j = 0; j < GROUPS; ++j) zeros[n][j][c] *= f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) y[n][2 * h + c] = fmaf(4.f, s[n][2 * h + c], -top);
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y[p][n][2 * h + c] = fmaf(4.f, s[p][n][2 * h + c], -top);
         }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[n][2 * h + c] = ex2(y[n][2 * h + c]);
-          if (!ALL && key0 + key_of(h, g) >= sees[n][c]) s[n][2 * h + c] = 0.f;
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            s[p][n][2 * h + c] = ex2(y[p][n][2 * h + c]);
+            if (!seen(p, h, n, c)) s[p][n][2 * h + c] = 0.f;
+          }
+          l[n][c] += s[p][n][c] + s[p][n][2 + c];
         }
-        l[n][c] += s[n][c] + s[n][2 + c];
-      }
 
     // ---- O^T --------------------------------------------------------------------------------
 #pragma unroll
-    for (int h = 0; h < 2; ++h) words(meta[h], vm + key_of(h, g) * GROUPS);
+    for (int p = 0; p < P; ++p) {
+      const uint8_t* vc = stage(p) + S::kCodes;
+      const uint32_t* vm =
+          reinterpret_cast<const uint32_t*>(vc + S::kCodes) + kStep * GROUPS;
+      uint32_t meta[2][GROUPS];
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      uint32_t b[NT][2];
+      for (int h = 0; h < 2; ++h) words(meta[h], vm + key_of(h, g) * GROUPS);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float sv = low(meta[h][j]), zv = high(meta[h][j]);
+      for (int j = 0; j < GROUPS; ++j) {
+        uint32_t b[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float e[2];
+        for (int h = 0; h < 2; ++h) {
+          const float sv = low(meta[h][j]), zv = high(meta[h][j]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // (a key that a row does not see may hold anything)
-            const bool seen = ALL || key0 + key_of(h, g) < sees[n][c];
-            e[c] = seen ? s[n][2 * h + c] * sv : 0.f;
-            if (seen) zeros[n][j][c] = fmaf(s[n][2 * h + c], zv, zeros[n][j][c]);
+          for (int n = 0; n < NT; ++n) {
+            float e[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // (a key that a row does not see may hold anything)
+              e[c] = seen(p, h, n, c) ? s[p][n][2 * h + c] * sv : 0.f;
+              if (seen(p, h, n, c))
+                zeros[n][j][c] = fmaf(s[p][n][2 * h + c], zv, zeros[n][j][c]);
+            }
+            b[n][h] = transposed(pack_bf16x2(e[0], e[1]));
           }
-          b[n][h] = transposed(pack_bf16x2(e[0], e[1]));
         }
-      }
-      uint2 word[2];  // of keys 2 t and the next, of both halves
+        uint2 word[2];  // of keys 2 t and the next, of both halves
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        auto of = [&](int c) {
-          return *reinterpret_cast<const uint32_t*>(
-              vc + piece_at<GROUPS>(key_of(h, 2 * t + c), j) + 4 * g);
-        };
-        word[h] = make_uint2(of(0), of(1));
-      }
-      // bytes of the two keys, a code each of dims 2 i (bytes 0, 1) or 2 i + 1 (2, 3)
-      auto both = [&](int h, uint32_t which) { return __byte_perm(word[h].x, word[h].y, which); };
+        for (int h = 0; h < 2; ++h) {
+          auto of = [&](int c) {
+            return *reinterpret_cast<const uint32_t*>(
+                vc + piece_at<GROUPS>(key_of(h, 2 * t + c), j) + 4 * g);
+          };
+          word[h] = make_uint2(of(0), of(1));
+        }
+        // bytes of the two keys, a code each of dims 2 i (bytes 0, 1) or 2 i + 1 (2, 3)
+        auto both = [&](int h, uint32_t which) { return __byte_perm(word[h].x, word[h].y, which); };
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t even0 = both(0, 0x0400 + 0x0101 * i), even1 = both(1, 0x0400 + 0x0101 * i);
-        const uint32_t odd0 = both(0, 0x0602 + 0x0101 * i), odd1 = both(1, 0x0602 + 0x0101 * i);
-        const uint32_t lo[4] = {low_codes(even0, big), low_codes(odd0, big), low_codes(even1, big),
-                                low_codes(odd1, big)};
-        const uint32_t hi[4] = {high_codes(even0), high_codes(odd0), high_codes(even1),
-                                high_codes(odd1)};
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t even0 = both(0, 0x0400 + 0x0101 * i), even1 = both(1, 0x0400 + 0x0101 * i);
+          const uint32_t odd0 = both(0, 0x0602 + 0x0101 * i), odd1 = both(1, 0x0602 + 0x0101 * i);
+          const uint32_t lo[4] = {low_codes(even0, big), low_codes(odd0, big),
+                                  low_codes(even1, big), low_codes(odd1, big)};
+          const uint32_t hi[4] = {high_codes(even0), high_codes(odd0), high_codes(even1),
+                                  high_codes(odd1)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma(o[n][4 * j + 2 * i], lo, b[n][0], b[n][1]);
-          mma(o[n][4 * j + 2 * i + 1], hi, b[n][0], b[n][1]);
+          for (int n = 0; n < NT; ++n) {
+            mma(o[n][4 * j + 2 * i], lo, b[n][0], b[n][1]);
+            mma(o[n][4 * j + 2 * i + 1], hi, b[n][0], b[n][1]);
+          }
         }
       }
     }
   };
+  auto out_of_cache = [&](int i) { return (outside & 1u << i % kStages) != 0; };
+  constexpr std::integral_constant<int, 1> kOne{};
   auto turn = [&](int i, auto all_seen) {
     issue(i + kStages - 1);
     copy_wait<kStages - 1>();
     __syncwarp();
-    if (!(outside & 1u << i % kStages)) step(i, all_seen);  // (else nothing was copied)
+    if (!out_of_cache(i)) step(i, all_seen, kOne);  // (else nothing was copied)
     __syncwarp();  // the stage is read before its next copies start
   };
+  auto turn2 = [&](int i) {  // two steps together
+    issue(i + kStages - 1);
+    copy_wait<kStages - 2>();
+    __syncwarp();
+    if (!out_of_cache(i) && !out_of_cache(i + 1)) {
+      step(i, std::true_type(), std::integral_constant<int, 2>());
+    } else {
+#pragma unroll 1
+      for (int k = i; k < i + 2; ++k)
+        if (!out_of_cache(k)) step(k, std::false_type(), kOne);
+    }
+    __syncwarp();
+    issue(i + kStages);
+  };
   // the steps of keys that every row sees, then the others
-  const int seen = max(0, min(steps, (least / kStep - first + kWarps - 1) / kWarps));
+  const int seen_by_all = max(0, min(steps, (least / kStep - first + kWarps - 1) / kWarps));
   int i = 0;
 #pragma unroll 1
-  for (; i + S::kUnroll <= seen; i += S::kUnroll) {
+  for (; i + S::kUnroll <= seen_by_all; i += S::kUnroll) {
+    if (S::kPair) {
 #pragma unroll
-    for (int k = 0; k < S::kUnroll; ++k) turn(i + k, std::true_type());
+      for (int k = 0; k < S::kUnroll; k += 2) turn2(i + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < S::kUnroll; ++k) turn(i + k, std::true_type());
+    }
   }
 #pragma unroll 1
   for (; i < steps; ++i) turn(i, std::false_type());

@@ -301,3 +301,21 @@ def test_the_largest_pages(cuda_device):
     out = kvq.paged_kv4_attention(q.cuda(), cache, table.cuda(), lens.cuda(), tokens_per_request=3)
     torch.cuda.synchronize()
     ref.check(out, *ref4.attention(q, cache.cpu(), table, lens, D ** -0.5, per_request=3))
+
+
+@pytest.mark.parametrize("D,per,G", [(64, 1, 8), (64, 3, 8), (64, 4, 8), (128, 1, 4), (128, 2, 8),
+                                     (128, 3, 8), (256, 1, 4), (256, 2, 8)])
+def test_pages_outside_the_cache_among_seen_keys(cuda_device, D, per, G):
+    """Every seventh page or so lies outside the cache, behind each other and alone, in
+    long ranges that every row sees: they are left out, and counted."""
+    q, raw, table, lens = kv4_case(2, per, 2 * G, 2, D, 16, 300, seed=D + per)
+    g = gen(10)
+    table[torch.rand(2, 300, generator=g) < 0.15] = raw.shape[0]
+    table[0, 40:48] = -1
+    lens[:] = torch.randint(4600, 4801, (2 * per,), generator=g, dtype=torch.int32)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = kvq.paged_kv4_attention(q.cuda(), raw.cuda(), table.cuda(), lens.cuda(),
+                                  tokens_per_request=per, errors=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) > 0
+    ref.check(got, *ref4.attention(q, raw, table, lens, D ** -0.5, per_request=per))
