@@ -760,11 +760,11 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
       }
       if (where & 2) tc::commit(bar(kODone));
     }
-    if (!ok) {  // nothing may be in flight when the tensor memory goes
-      tc::commit(bar(kDrain));
-      tc::drain(bar(kDrain), 0);
-      __syncwarp();
-    }
+    // Nothing may be in flight when the tensor memory goes: not the last products either,
+    // which nobody waits for where a softmax warp gave up on them.
+    tc::commit(bar(kDrain));
+    tc::drain(bar(kDrain), 0);
+    __syncwarp();
   } else if (warp == kListWarp) {
     // ---- the lists ------------------------------------------------------------------------
     bool ok = true, rejected = false;
