@@ -609,11 +609,11 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         }
       }
     }
-    if (!ok) {  // nothing may be in flight when the tensor memory goes
-      tc::commit(bar(kDrain));
-      tc::drain(bar(kDrain), 0);
-      __syncwarp();
-    }
+    // Nothing may be in flight when the tensor memory goes: not the last products either,
+    // which nobody waits for where a softmax warp gave up on them.
+    tc::commit(bar(kDrain));
+    tc::drain(bar(kDrain), 0);
+    __syncwarp();
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     // ---- the loads: one warp for K, one for V --------------------------------------------
     const int kv = warp - kLoadWarp;
@@ -677,11 +677,11 @@ prefix_tiles_kernel(const __grid_constant__ PrefixParams p) {
         }
       }
     }
-    if (!ok) {  // let the copies in flight land before the CTA may end
-      for (int slot = 0; slot < 2; ++slot) {
-        const int turn = slot ? last[1] : last[0];
-        if (turn >= 0) tc::drain(bar((kv ? kVFull : kKFull) + slot), (turn >> 1) & 1);
-      }
+    // The copies in flight land before the CTA may end: the last ones too, which nobody
+    // waits for where the matrix instructions were given up.
+    for (int slot = 0; slot < 2; ++slot) {
+      const int turn = slot ? last[1] : last[0];
+      if (turn >= 0) tc::drain(bar((kv ? kVFull : kKFull) + slot), (turn >> 1) & 1);
     }
   }
   __syncthreads();

@@ -49,3 +49,26 @@ def latent(T, H, K, seed):
                                    (620, 40, 100)])
 def test_latent_tiles(cuda_device, T, H, K):
     behind_calls_that_give_up(latent(T, H, K, seed=T), latent(150, 64, 256, seed=2))
+
+
+def prefix(D, T, H, keys, seed):
+    g = torch.Generator().manual_seed(seed + D)
+    page, pages = 64, -(-keys // 64)
+    q = torch.randn(T, H, D, generator=g).bfloat16()
+    cache = torch.randn(pages + T, 2, H, page, D, generator=g).bfloat16()
+    ids = torch.randperm(pages + T, generator=g).int()
+    lens = torch.randint(0, 9, (T,), generator=g, dtype=torch.int32)
+    args = [q.cuda(), cache.cuda(), ids[:pages].cuda(), keys, ids[pages:].view(T, 1).cuda(),
+            lens.cuda()]
+    return lambda: kvq.paged_shared_prefix_attention(*args)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefix_tiles(cuda_device, D):
+    """Whole blocks of keys, which the copy engine brings, few and many to a CTA."""
+    old = kvq.set_config("prefix", 1)
+    try:
+        for T, H, keys in ((20, 200, 256), (40, 4, 3000)):
+            behind_calls_that_give_up(prefix(D, T, H, keys, seed=1), prefix(D, 30, 160, 384, seed=2))
+    finally:
+        kvq.set_config("prefix", old)
