@@ -53,6 +53,7 @@ constexpr int kWarps = 4;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 16;   // keys of one step of a warp
 constexpr int kStages = 4;
+constexpr int kWaves = 16;  // of CTAs, into which long ranges are cut at most
 constexpr float kRescaleAt = 8.f;  // log2 by which a score may exceed the reference
 
 struct Attn4Params {
@@ -70,7 +71,7 @@ struct Attn4Params {
   const int* lens;
   float scale_log2;
   int cluster, splits;
-  int part_steps;            // steps of a CTA's part; 0: an equal share
+  int part_steps;            // steps of a CTA's part, at least; 0: an equal share
   __nv_bfloat16* out;
   Partials parts;            // with several splits
   int* errors;
@@ -237,11 +238,21 @@ attn4_kernel(const Attn4Params p) {
   const int most = __reduce_max_sync(kFullMask, len);
   const int least = __reduce_min_sync(kFullMask, lane < rows ? len : most);
 
-  // ---- which keys: an equal share of the request's groups of 16, or a fixed part ---------
+  // ---- which keys: an equal share of the request's groups of 16, or parts of a given size,
+  // of a larger one where so many parts would not reach the end -----------------------------
   const int parts = p.cluster * p.splits;
   const int all_steps = most / kStep + (most % kStep != 0);
-  const int share = p.part_steps ? p.part_steps : (all_steps + parts - 1) / parts;
+  const int share = max(p.part_steps, (all_steps + parts - 1) / parts);
   const int64_t begin = (int64_t)share * (blockIdx.y * p.cluster + rank);
+  // A part past the request's end, for all CTAs of the cluster (the first part, where there is
+  // no key): its sums say so, and the join reads no more of it.  Tables are as wide as the
+  // longest request may get, so most parts may be like this.
+  if (p.splits > 1 && (int64_t)share * blockIdx.y * p.cluster >= all_steps) {
+    if (rank == 0 && threadIdx.x < rows)
+      p.parts.lse[blockIdx.y * p.parts.rows + row_of(threadIdx.x)] = -INFINITY;
+    if (rejected && p.errors) atomicAdd(p.errors, 1);
+    return;
+  }
   const int first = (int)min(begin, (int64_t)all_steps) + warp;
   const int last = (int)min(begin + share, (int64_t)all_steps);
   const int steps = first < last ? (last - first + kWarps - 1) / kWarps : 0;
@@ -720,7 +731,12 @@ struct Spread4 {
 // steps for every warp: first within a cluster, joined in place; beyond that as partials
 // that a second launch joins.  Where no more fit, a long range is cut in parts of 2048
 // keys instead (of 4096 where that is six waves of CTAs all the same): lengths differ,
-// and the last tiles of a wave would keep a few SMs busy alone.  What a cluster holds at
+// and the last tiles of a wave would keep a few SMs busy alone.  The range is the table's,
+// since lengths are known on the device alone.  So that a table much wider than the requests are
+// long costs little, parts are 16 waves of CTAs at most (up to 80 MB of partials), and of more
+// keys in those requests that they would not reach the end of (64 and 256 sequences of 2048
+// keys, 64 query heads, a table for 131072: 52 and 138 us, without a limit and with empty parts
+// that write zeros 120 and 455; with a table for 2048 41 and 128).  What a cluster holds at
 // once is not cut if its CTAs have about as little as that (16 x 8 heads of 16 rows, 8192
 // keys: 56 us in clusters of 2, 67 in parts), unless they leave many places empty (20 x 8
 // heads of 8 rows: 52 us in clusters of 2, 48 in parts).
@@ -748,7 +764,8 @@ Spread4 spread4(int64_t num_tokens, int per_request, int num_heads_q, int num_he
     const int part = s.units * (keys / 4096) >= 6 * resident ? 4096 : 2048;
     s.part_steps = part / kStep;
     splits = (keys + part - 1) / part;
-    if (splits > 65535) splits = 65535, s.part_steps = 0;
+    const int64_t most = kWaves * resident / s.units;
+    if (splits > most) splits = most > 1 ? most : 1;
   }
   s.splits = (int)splits;
   return s;

@@ -93,3 +93,44 @@ def test_bad_pages_and_lengths_in_later_parts(cuda_device):
         torch.cuda.synchronize()
         assert int(err.item()) > 0
         check(out, q, raw, table, lens, 1, torch.tensor([0, 1, 3, 5, 6, 7, 100, 128, 200, 399]))
+
+
+@pytest.mark.parametrize("D,per,G,B,page,count", [(64, 1, 8, 400, 64, 30), (128, 2, 8, 160, 64, 30),
+                                                  (256, 1, 8, 320, 128, 15)])
+def test_a_table_much_wider_than_the_requests(cuda_device, D, per, G, B, page, count):
+    """A table for 131072 keys over requests of a few thousand, and some as long as it: 16
+    waves of parts, which the longest requests fill with larger ones. Parts past a request's
+    end leave their place in the workspace as it was."""
+    width = 131072 // page
+    q, raw, table = case(B, per, G, 1, D, page, width, seed=D + per)
+    assert parts(q, raw, table, per) == count
+    T = B * per
+    g = torch.Generator().manual_seed(9)
+    lens = torch.randint(0, 4097, (T,), generator=g, dtype=torch.int32)
+    some = torch.arange(12) + T // 2
+    lens[some] = torch.tensor([131072, 131071, count * 4096, count * 4096 - 1, 0, 0, 4096, 4096, 60000,
+                               60000, 8, 3000], dtype=torch.int32)
+    if per == 1:
+        lens[T // 3], some = count * 4096 + 1, torch.cat([some, torch.tensor([T // 3])])
+    need = kvq.lib().paged_kv4_attention_workspace(T, per, G, 1, D, page, width)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    args = [x.cuda() for x in (q, raw, table, lens)]
+    out = kvq.paged_kv4_attention(*args, tokens_per_request=per, workspace=ws)
+    torch.cuda.synchronize()
+    check(out, q, raw, table, lens, per, some)
+    assert bool((out[lens.cuda() == 0] == 0).all()) and not bool(out.isnan().any())
+    # rows of requests of up to 4096 keys: the first part's alone are written
+    held = ws.view(torch.int32)[:count * T * G * D].view(count, T, G * D)
+    short = (lens.view(B, per).amax(1) <= 4096).repeat_interleave(per).cuda()
+    assert bool((held[1:, short] == -1).all())
+    # the same requests behind a table that ends with them
+    short = short.nonzero()[:, 0]
+    n = len(short) // per
+    tight = args[2][short[::per] // per, :4096 // page].contiguous()
+    again = kvq.paged_kv4_attention(args[0][short], args[1], tight, args[3][short],
+                                    tokens_per_request=per)
+    assert tight.shape[0] == n
+    want = ref4.attention(q[short.cpu()][:8], raw, table[short.cpu()[:8] // per], lens[short.cpu()[:8]],
+                          D ** -0.5)
+    ref.check(again[:8], *want)
+    ref.check(out[short[:8]], *want)
