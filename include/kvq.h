@@ -508,8 +508,11 @@ kvq_status paged_kv4_gather(const void* kv_cache, int64_t num_pages, int num_hea
  * out = softmax(scale q K^T) V per query head, K and V the values that the codes
  * stand for.  Scores, softmax statistics and sums in fp32; the product of a
  * softmax numerator with the scale of V is rounded to bf16 for the product with
- * V's codes, the output once at the end.  The scale of a group of K times `scale`
- * and log2(e) has to be finite.
+ * V's codes, the output once at the end.
+ * What the arithmetic above has to hold in fp32: the scale of a group of K, and the
+ * sum of 64 dims of q, each times `scale` and log2(e); and numerators of up to 2^8
+ * times V, summed.  A score that overflows weighs nothing where it is -inf (a row
+ * that has no other gets zeros) and makes its row NaN where it is +inf.
  */
 int64_t paged_kv4_attention_workspace(int64_t num_tokens, int64_t tokens_per_request,
                                       int num_heads_q, int num_heads_kv, int head_dim,
@@ -542,7 +545,9 @@ kvq_status paged_kv4_attention(const void* q, int64_t q_stride, int64_t num_toke
  *              q.  A token without any entry gets zeros.
  * An entry's values are those of dsv4_kv_cache_gather.  Scores, softmax statistics
  * and sums in fp32; the softmax numerators are rounded to bf16 for the product
- * with the values, the output once at the end.
+ * with the values, the output once at the end.  Numerators are up to 2^30; their
+ * sums with the values have to stay finite in fp32.  Scores that overflow are
+ * taken as in paged_kv4_attention.
  * No counterpart in the source pages, which end where the entry is written.
  */
 int64_t dsv4_latent_attention_workspace(int64_t num_tokens, int num_heads, int64_t list_width);

@@ -22,9 +22,10 @@
 // padding.  More rows are more second operands to the same codes.  The transposed
 // P takes one matrix transposition in registers.
 //
-// The reference of a row's softmax moves only when a score exceeds it by more than
-// 2^8, which spares the exchange of maxima: until then weights above 1 are as exact as
-// those below.  (A row whose first score is infinite, of either sign, becomes NaN.)
+// The reference of a row's softmax moves only when a score exceeds it by more than 8 in
+// units of log2, a weight of 2^8, which spares the exchange of maxima: until then weights
+// above 1 are as exact as those below.  It starts at the least finite number, so that a score
+// of -inf weighs nothing wherever it comes.
 //
 // A group's codes come in by 16-byte asynchronous copies, three groups ahead, into
 // a ring that only this warp uses, so that there is no CTA barrier in the loop.
@@ -55,6 +56,7 @@ constexpr int kStep = 16;   // keys of one step of a warp
 constexpr int kStages = 4;
 constexpr int kWaves = 16;  // of CTAs, into which long ranges are cut at most
 constexpr float kRescaleAt = 8.f;  // log2 by which a score may exceed the reference
+constexpr float kNone = -3.402823466e38f;  // the reference before the first score
 
 struct Attn4Params {
   const __nv_bfloat16* q;
@@ -383,7 +385,7 @@ attn4_kernel(const Attn4Params p) {
       for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m[n][c] = -INFINITY, l[n][c] = 0.f;
+      m[n][c] = kNone, l[n][c] = 0.f;
 #pragma unroll
       for (int j = 0; j < GROUPS; ++j) zeros[n][j][c] = 0.f;
     }
@@ -465,7 +467,7 @@ attn4_kernel(const Attn4Params p) {
             if (!seen(p, h, n, c)) x = -INFINITY;
             y[p][n][2 * h + c] = fmaf(4.f, x, -m[n][c]);
           }
-          // (from -inf on every score exceeds it; -inf itself does not)
+          // (from kNone on every score exceeds it; -inf does not)
           above = fmaxf(above, fmaxf(y[p][n][c], y[p][n][2 + c]));
         }
     if (__any_sync(kFullMask, above > kRescaleAt)) {
@@ -479,7 +481,6 @@ attn4_kernel(const Attn4Params p) {
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 4));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 8));
           top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 16));
-          // (-inf) - (-inf): no key yet, nothing accumulated, any factor does
           const float f = top == m[n][c] ? 1.f : ex2(m[n][c] - top);
           m[n][c] = top;
           l[n][c] *= f;
@@ -625,10 +626,9 @@ attn4_kernel(const Attn4Params p) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int r = 8 * n + 2 * t + c;
-      float top = -INFINITY, sum = 0.f;
+      float ref = kNone, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, state[w * kRows + r].x);
-      const float ref = top == -INFINITY ? 0.f : top;
+      for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, state[w * kRows + r].x);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         sum += state[w * kRows + r].y * exp2f(state[w * kRows + r].x - ref);
