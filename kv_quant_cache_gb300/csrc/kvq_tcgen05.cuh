@@ -137,9 +137,6 @@ __device__ __forceinline__ void st8(uint32_t addr, const uint32_t (&r)[8]) {
 __device__ __forceinline__ void ld(uint32_t (&r)[32], uint32_t addr) { ld32(r, addr); }
 __device__ __forceinline__ void ld(uint32_t (&r)[16], uint32_t addr) { ld16(r, addr); }
 __device__ __forceinline__ void ld(uint32_t (&r)[8], uint32_t addr) { ld8(r, addr); }
-__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[32]) { st32(addr, r); }
-__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[16]) { st16(addr, r); }
-__device__ __forceinline__ void st(uint32_t addr, const uint32_t (&r)[8]) { st8(addr, r); }
 
 // ---- descriptors -----------------------------------------------------------------
 // Shared-memory matrix of 128-byte rows with the 128-byte swizzle, base
