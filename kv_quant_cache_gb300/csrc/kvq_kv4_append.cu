@@ -13,9 +13,10 @@
 // then to bf16, and the quotient's rounding is decided on the exact remainder.
 // Minimum and maximum of a group travel together in one register, (lo, -hi) as a
 // bf16 pair.
-// Memory bound: every row is read once, q rows are written as they came, key and
-// value rows in 9/32 of their bytes.  32768 tokens of 32 + 16 heads of 128: 143 us,
-// 4.9 TB/s, two thirds of the issue slots busy with rotation, extrema and rounding.
+// Every row is read once, q rows are written as they came, key and value rows in 9/32 of
+// their bytes.  32768 tokens of 32 + 16 heads of 128: 143 us, 4.9 TB/s.  Neither memory (59 %)
+// nor the issue slots (70 %, with rotation, extrema and rounding) are full: loads, arithmetic
+// and stores of a warp follow one another, and registers allow 28 warps to an SM.
 //
 // Read back.  A lane takes words l and l + D/16 of a row, so that a row's
 // stores are contiguous; all loads of a warp's rows are in flight together.  65536
@@ -81,6 +82,7 @@ __device__ __forceinline__ uint32_t group_meta(uint32_t lohi) {
   const float width = __fsub_rn(hi, lo);
   if (!(width < INFINITY)) return 0x7fc07fc0u;  // NaN, an infinity: the group reads back as NaN
   // width / 15, correctly rounded: a product, and the exact remainder's share of it
+  // (Markstein's correction)
   float q = __fmul_rn(width, 1.f / 15.f);
   q = __fmaf_rn(__fmaf_rn(-15.f, q, width), 1.f / 15.f, q);
   if (width < 0x1p-100f) q = __fdiv_rn(width, 15.f);  // (where the remainder may not be exact)

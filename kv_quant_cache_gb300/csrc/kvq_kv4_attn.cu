@@ -33,10 +33,12 @@
 // keys that a load touches lie in different banks; the matrix instructions may take
 // the keys in any order, and key_of() is one that does for the loads of K and of V.
 //
-// What bounds it: instructions.  A step of 16 keys of 128 dims and up to 8 rows is 359 of
-// a warp (150 decode the codes, 17 are matrix instructions), for 2.3 KB: 64 sequences x 32768
-// keys x 8 heads take 366 us, 4.9 TB/s, with two thirds of the issue slots busy.  With 24 or 32
-// rows it is their latencies: 8 warps to an SM are all that registers allow.
+// What bounds it: instructions, and their latencies.  A step of 16 keys of 128 dims and up to
+// 8 rows is 359 of a warp (150 decode the codes, 17 are matrix instructions), for 2.3 KB: 64
+// sequences x 32768 keys x 8 heads take 363 us, 5.0 TB/s.  Nothing is full there: issue slots
+// are 66 % busy, memory 53 %, and the 16 warps to an SM that registers allow wait for results
+// and for the ALU pipe.  With 24 and more rows of 64 dims, 16 of 128 and 8 of 256 they are 8,
+// and latencies weigh more.
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -12,8 +12,9 @@
 // Warps have one role each:
 //   * warps 0-7: the softmax.  A thread has one entry (its tensor-memory lane) and half
 //     of the heads.  The reference of a head moves only when a score exceeds it by
-//     more than 2^30, so that the exchange of maxima between lanes, and the
-//     rescaling of O^T, are rare; weights go to shared memory as rows of heads;
+//     more than 30 in units of log2, a weight of 2^30, so that the exchange of maxima
+//     between lanes, and the rescaling of O^T, are rare; weights, rounded to bf16 for the
+//     product (the sums take them unrounded), go to shared memory as rows of heads;
 //   * warps 8-23: read entries (8 bytes a lane, a whole tile ahead in registers) and
 //     decode them, four warps to a quarter of the dims: as soon as the second product
 //     of the tile before is done with a quarter, the next tile's takes its place;
@@ -22,11 +23,14 @@
 //   * warps 26 and 27: copy the queries of a unit as soon as the last scores of the unit
 //     before are done, while its outputs are still to come.
 //
-// What bounds it: shared memory.  A tile of 64 heads is 3000 cycles of operands read by
-// the matrix instructions (A of 128 KB twice, of 64 heads as B), 1024 of X written, and
-// the entries' loads pass through the same pipe; X has room for one tile, so that its
-// products, the softmax between them and the next tile's decoding follow one another.
-// 16 tokens x 128 heads x 16384 entries 115 us (450 TFLOP/s), 64 x 64 x 2048 49 us.
+// What bounds it: X has room for one tile, so that its products, the softmax between them
+// and the next tile's decoding follow one another, and shared memory, which all of them
+// use.  Of the 9600 cycles of a tile of 64 heads (16 tokens x 128 heads x 16384 entries)
+// its pipe is busy for 6900 at most, by the counters: 3000 of operands that the matrix
+// instructions read (A of 128 KB twice, of 64 heads as B), 3900 of loads and stores (X
+// written, entries and scores, partials).  The next busiest are issue slots, 38 %, and
+// the tensor cores, 21 %.
+// 16 tokens x 128 heads x 16384 entries 112 us (460 TFLOP/s), 64 x 64 x 2048 48 us.
 //
 // With few units a CTA to an SM takes an equal share of all tiles of all lists, from
 // the lists' actual lengths; a unit that falls to several CTAs goes to partials,
@@ -52,7 +56,13 @@ constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr int kAhead = 4;  // tiles whose slots are in shared memory
 // (28 warps of 72 registers each.  A softmax warp reads its scores twice, half of its
 // heads at a time, to make do with them.)
-constexpr int kSharedUnits = 4 * 152;  // up to so many units the tiles are shared out
+// Up to so many units the tiles are shared out.  Both ways measured, lists of half to all of
+// 2048 entries, 64 heads: 76 tokens 54 us (74 as a CTA to a unit), 228 121 (136), 608 281
+// (287), 1024 451 (457): sharing out fills the last wave, and wins little once there are
+// many.  Not so where units fill whole waves (152 tokens 90 (80); 152 of 128 heads 158
+// (145)) and where lists are of few tiles, as partials and their join cost more than they
+// bring (608 tokens of 150 to 300 entries 97 (79)): the host does not know the lengths.
+constexpr int kSharedUnits = 4 * 152;
 constexpr int kCtas = 152;             // .. to so many CTAs
 // log2 by which a score may exceed its reference: weights are as exact above 1 as below
 constexpr float kRescaleAt = 30.f;
