@@ -66,6 +66,7 @@ constexpr int kSharedUnits = 4 * 152;
 constexpr int kCtas = 152;             // .. to so many CTAs
 // log2 by which a score may exceed its reference: weights are as exact above 1 as below
 constexpr float kRescaleAt = 30.f;
+constexpr float kNone = -3.402823466e38f;  // the reference of a head with scores of -inf alone
 
 struct LatentParams {
   const __nv_bfloat16* q;
@@ -448,7 +449,7 @@ latent_tiles_kernel(const __grid_constant__ LatentParams p) {
             const float old = refs[threadIdx.x];
             float top = fresh ? -INFINITY : old;
             for (int k = 0; k < 4; ++k) top = fmaxf(top, tops[k * 64 + threadIdx.x]);
-            if (top == -INFINITY) top = 0.f;
+            top = fmaxf(top, kNone);  // (as -inf less itself is NaN)
             moves[threadIdx.x] = ex2(old - top);
             refs[threadIdx.x] = top;
           }
